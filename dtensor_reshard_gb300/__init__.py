@@ -150,7 +150,7 @@ def _load():
                           "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, vpp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)
-    i64p = ctypes.POINTER(ctypes.c_int64)
+    i64, i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
     sig = {
         "reshard_plan_create": ([i64p, ctypes.c_int32, ctypes.c_int32,
                                  ctypes.POINTER(reshard_mesh_t),
@@ -222,6 +222,16 @@ def _load():
         "reshard_partition_execute": ([vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vpp,
                                        vpp, vp, vp, vp], ctypes.c_int),
         "reshard_partition_destroy": ([vp], ctypes.c_int),
+        "reshard_fp8_quantize": ([vp, ctypes.c_int32, i64, i64, i64, i64, ctypes.c_int32, vp, i64,
+                                  vp, i64, vp], ctypes.c_int),
+        "reshard_fp8_matmul": ([vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp,
+                                ctypes.c_int32, i64, vp], ctypes.c_int),
+        "reshard_sample": ([vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp],
+                           ctypes.c_int),
+        "reshard_balance_loss_workspace": ([i64, i64, i64], i64),
+        "reshard_balance_loss": ([vp, ctypes.c_int32, i64, i64, i64, i64, vp, i64, vp,
+                                  ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, vp, i64, vp],
+                                 ctypes.c_int),
         "reshard_last_error": ([], ctypes.c_char_p),
         "reshard_version": ([], ctypes.c_char_p),
     }
@@ -796,3 +806,76 @@ def nccl_exchange(gpu_rank, send_buf, recv_buf):
                 w.wait()
     return exchange
 
+
+
+# ------------------------------------------------------------- operators beside a refit
+SCORES = {"softmax": 0, "sigmoid": 1}
+MAX_EXPERTS = _DEFINES["RESHARD_MAX_EXPERTS"]
+MAX_VOCAB = _DEFINES["RESHARD_MAX_VOCAB"]
+
+
+def _dtype(d) -> int:
+    return DTYPES[d] if isinstance(d, str) else int(d)
+
+
+def _cdiv(a: int, b: int) -> int:
+    return -(-a // b)
+
+
+def reshard_fp8_quantize(x, q, scale, shape, dtype, block_rows: int = 1, ldx=None, ldq=None,
+                         lds=None, stream=None):
+    """x of ``shape`` ([nmat,] rows, cols) and ``dtype`` -> e4m3 bytes q and float32 scales,
+    one for each block_rows x 128 block.  Pitches default to dense rows."""
+    nmat, rows, cols = shape if len(shape) == 3 else (1, *shape)
+    _check(_lib.reshard_fp8_quantize(
+        _ptr(x), _dtype(dtype), nmat, rows, cols, cols if ldx is None else ldx, block_rows, _ptr(q),
+        cols if ldq is None else ldq, _ptr(scale), _cdiv(cols, 128) if lds is None else lds,
+        _stream(stream)), "reshard_fp8_quantize")
+
+
+def reshard_fp8_matmul(x, xs, w, ws, y, shape, dtype, offsets=None, nexperts: int = 1, ldx=None,
+                       ldw=None, ldxs=None, ldws=None, ldy=None, stream=None):
+    """y [tokens, n] of ``dtype`` = x [tokens, k] times w [nexperts, n, k] transposed, both
+    quantised; ``shape`` = (tokens, n, k).  With ``offsets`` (device int32 [nexperts + 1])
+    each expert's rows are multiplied by its own matrix.  Pitches default to dense rows."""
+    tokens, n, k = shape
+    blocks = _cdiv(k, 128)
+    _check(_lib.reshard_fp8_matmul(
+        _ptr(x), k if ldx is None else ldx, _ptr(xs), blocks if ldxs is None else ldxs, _ptr(w),
+        k if ldw is None else ldw, _ptr(ws), blocks if ldws is None else ldws, _ptr(offsets),
+        nexperts, tokens, n, k, _ptr(y), _dtype(dtype), n if ldy is None else ldy,
+        _stream(stream)), "reshard_fp8_matmul")
+
+
+def reshard_sample(logits, shape, dtype, u, token, logprob=None, temperature=None, top_k=None,
+                   top_p=None, min_p=None, ld=None, stream=None):
+    """token [rows] (int32) drawn from logits of ``shape`` (rows, vocab) with the uniform
+    numbers u [rows], and their log-probabilities.  The settings are device arrays [rows]
+    (top_k int32, the others float32) or None."""
+    rows, vocab = shape
+    _check(_lib.reshard_sample(
+        _ptr(logits), _dtype(dtype), rows, vocab, vocab if ld is None else ld, _ptr(temperature),
+        _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token), _ptr(logprob),
+        _stream(stream)), "reshard_sample")
+
+
+def reshard_balance_loss_workspace(shape) -> int:
+    """Workspace bytes of reshard_balance_loss for ``shape`` = (nseq, seqlen, nexperts)."""
+    return int(_lib.reshard_balance_loss_workspace(*shape))
+
+
+def reshard_balance_loss(logits, shape, dtype, experts, topk: int, coef: float, workspace, counts,
+                         loss=None, dlogits=None, mask=None, score="softmax", grad=None, ld=None,
+                         workspace_bytes: int = 0, stream=None):
+    """Load-balance loss of router logits of ``shape`` (nseq, seqlen, nexperts) with the
+    choices experts [nseq, seqlen, topk]: counts [nseq, nexperts] (int32), loss [1] and
+    dlogits where given.  mask: bytes [nseq, seqlen], 0 for padding; grad: the loss's
+    gradient on the device, None for 1."""
+    nseq, seqlen, nexperts = shape
+    if workspace is not None and not workspace_bytes and hasattr(workspace, "numel"):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(_lib.reshard_balance_loss(
+        _ptr(logits), _dtype(dtype), nseq, seqlen, nexperts, nexperts if ld is None else ld,
+        _ptr(experts), topk, _ptr(mask), SCORES[score] if isinstance(score, str) else int(score),
+        coef, _ptr(grad), _ptr(loss), _ptr(counts), _ptr(dlogits), _ptr(workspace),
+        workspace_bytes, _stream(stream)), "reshard_balance_loss")

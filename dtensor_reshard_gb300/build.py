@@ -1,6 +1,6 @@
 """Build libreshard.so in-tree with nvcc for sm_103a (GB300).
 
-The two translation units (host planner, CUDA kernels) compile in parallel and
+The translation units (host planner, CUDA kernels) compile in parallel and
 link into ``dtensor_reshard_gb300/libreshard.so``; the CUDA runtime is linked
 statically, so the library needs only the driver at run time.
 """
@@ -20,8 +20,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["planner.cpp", "batch.cpp", "kernels.cu", "bulk_fanout.cu", "transpose.cu",
-           "static_scratch.cu", "realign_staged.cu", "refit.cpp", "partition.cpp"]
-HEADERS = ["internal.h", "staging.cuh"]
+           "static_scratch.cu", "realign_staged.cu", "refit.cpp", "partition.cpp",
+           "fp8_quantize.cu", "fp8_matmul.cu", "sample.cu", "balance.cu"]
+HEADERS = ["internal.h", "staging.cuh", "operators.cuh"]
 
 
 def nvcc() -> str:

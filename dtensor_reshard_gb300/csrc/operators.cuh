@@ -1,0 +1,66 @@
+// operators.cuh -- pieces shared by the operators that run beside a refit
+// (fp8_quantize.cu, fp8_matmul.cu, sample.cu, balance.cu): element types,
+// reductions and argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "internal.h"
+
+namespace rs {
+namespace op {
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool float_dtype(int32_t d) {
+  return d == RESHARD_BF16 || d == RESHARD_FP16 || d == RESHARD_FP32;
+}
+inline bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+inline int64_t dtype_size(int32_t d) { return d == RESHARD_FP32 ? 4 : 2; }
+
+// The status of the launch just made.
+inline reshard_status_t launched(const char* what) {
+  const cudaError_t ce = cudaGetLastError();
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(ce));
+  return RESHARD_OK;
+}
+
+// f(T()) with T the element type of a floating dtype.
+template <typename F>
+reshard_status_t by_dtype(int32_t dtype, F&& f) {
+  if (dtype == RESHARD_BF16) return f(__nv_bfloat16());
+  if (dtype == RESHARD_FP16) return f(__half());
+  return f(float());
+}
+
+}  // namespace op
+}  // namespace rs

@@ -752,6 +752,146 @@ reshard_status_t reshard_plan_exclude(reshard_plan_t plan, const int64_t* src_go
 /* Release a plan and its device tables.  Errors: BAD_HANDLE. */
 reshard_status_t reshard_plan_destroy(reshard_plan_t plan);
 
+/*
+ * Operators that run beside a refit of a mixture-of-experts model.  The write-ups
+ * describe the weight transfer only (news.bpdata.com, section "A megkozelites: refit
+ * mint DTensor-to-DTensor reshard": weights go from the trainer's layout to the
+ * layout of the ranks that generate); these are the computations that the two ends
+ * run on what is transferred:
+ *   reshard_fp8_quantize   weights or activations to 8-bit floating point in scaled
+ *                          blocks (a plan of dtype u8 then moves half of bf16's bytes);
+ *   reshard_fp8_matmul     the product of such matrices, dense or per expert;
+ *   reshard_sample         the next token of every request from its logits;
+ *   reshard_balance_loss   the router's load-balance loss, the tokens each expert
+ *                          got, and the gradient in the router's logits.
+ * All matrices are row-major with a row pitch ("ld") in elements.  All of them follow
+ * the conventions above: work is enqueued on `stream`, nothing is synchronised,
+ * allocated or kept between calls, every call can be captured into a CUDA graph, and
+ * an output must not overlap an input.  A call without rows or columns launches nothing
+ * (the loss of no token is written as 0).
+ * Sums do not depend on the order in which the GPU runs: equal inputs give equal bits.
+ */
+
+/* Scores of reshard_balance_loss. */
+typedef enum reshard_score {
+  RESHARD_SCORE_SOFTMAX = 0, /* p = exp(l) / sum exp(l) */
+  RESHARD_SCORE_SIGMOID = 1  /* p = sigmoid(l) / sum sigmoid(l) */
+} reshard_score_t;
+
+/*
+ * Quantise nmat matrices of rows x cols to 8-bit floating point (e4m3: 3 mantissa
+ * bits, largest value 448) with one float32 scale for every block_rows x 128 block:
+ *   scale = max(max|x| / 448, 2^-126),   q = e4m3(x / scale)
+ * in float32, rounded to nearest even and clamped to +-448.  Blocks at the right and
+ * lower edges are short.  Matrix i starts rows * ldx elements after matrix i - 1
+ * (q: rows * ldq bytes; scale: ceil(rows / block_rows) * lds floats).  A NaN gives a
+ * NaN and does not change its block's scale; an infinity makes its block's scale
+ * infinite (its own value NaN, the block's other values 0).
+ *
+ * x [nmat][rows][ldx] of dtype BF16, FP16 or FP32; block_rows 1 (activations) or
+ * 128 (weights); q [nmat][rows][ldq] bytes, of which cols are written; scale
+ * [nmat][ceil(rows / block_rows)][lds], of which ceil(cols / 128) are written.  Any
+ * alignment is accepted; rows that start on 16 bytes (x) and 8 bytes (q) are faster.
+ * Errors: INVALID_ARG (null pointer, unknown or integer dtype, negative size, pitch
+ * too small, block_rows), CUDA.
+ */
+reshard_status_t reshard_fp8_quantize(const void* x, int32_t dtype, int64_t nmat, int64_t rows,
+                                      int64_t cols, int64_t ldx, int32_t block_rows, void* q,
+                                      int64_t ldq, float* scale, int64_t lds, void* stream);
+
+/* Most weight matrices of one reshard_fp8_matmul. */
+#define RESHARD_MAX_EXPERTS 4096
+
+/*
+ * Product of two quantised matrices (reshard_fp8_quantize: x in 1x128 blocks, w in
+ * 128x128 blocks), for every token t of expert e and output feature n:
+ *   y[t][n] = sum_b xs[t][b] * ws[e][n / 128][b] * sum_{k in block b} x[t][k] * w[e][n][k]
+ * The sum over a block of 128 is one float32 tensor-core accumulation, the sum over
+ * blocks is float32, and y is rounded once.
+ *
+ * offsets == NULL: one weight matrix (nexperts 1) for all tokens.  Else rows are
+ * sorted by expert and offsets[nexperts + 1] (device memory, not decreasing, within
+ * 0..tokens) gives expert e the rows offsets[e] .. offsets[e + 1] - 1; rows of no
+ * expert are not written.  Offsets outside 0..tokens are clamped to it.
+ *
+ * x [tokens][ldx] bytes, xs [tokens][ldxs]; w [nexperts][n][ldw] bytes, ws
+ * [nexperts][ceil(n / 128)][ldws]; y [tokens][ldy] of ydtype BF16, FP16 or FP32.
+ * x and w must be 16-byte aligned and ldx, ldw multiples of 16 (bytes beyond k are not
+ * used); scales and y are aligned to their type.
+ * Errors: INVALID_ARG (null pointer, dtype, negative size, pitch too small, misaligned
+ * x, w or pitch, nexperts without offsets), UNSUPPORTED (nexperts > RESHARD_MAX_EXPERTS,
+ * a size of 2^31 or more), CUDA.
+ */
+reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const float* xs, int64_t ldxs,
+                                    const void* w, int64_t ldw, const float* ws, int64_t ldws,
+                                    const int32_t* offsets, int64_t nexperts, int64_t tokens,
+                                    int64_t n, int64_t k, void* y, int32_t ydtype, int64_t ldy,
+                                    void* stream);
+
+/* Largest vocabulary reshard_sample accepts. */
+#define RESHARD_MAX_VOCAB (1 << 20)
+
+/*
+ * One token for each row of logits, from one given uniform number a row.  With
+ * l = logits[r], T = temperature[r], m = max l and z_i = (l_i - m) * (1 / T), token i
+ * has weight w_i = round(2^40 * exp(z_i)), a whole number, so that every sum below is
+ * exact.  Tokens are ranked by logit, ties to the lowest index, and token i is kept if
+ *   its rank is below top_k[r]  (top_k <= 0: all are),
+ *   the weights of these tokens ranked before it sum to less than top_p[r] times the
+ *     sum over all of these tokens, or it is ranked first  (top_p >= 1: all are),
+ *   exp(z_i) >= min(min_p[r], 1).
+ * token[r] is the kept token of lowest index at which the running sum of kept weights
+ * in index order passes u[r] times their sum.  T <= 0 (or NaN) takes the token ranked
+ * first.  logprob[r] is the token's log-probability z - ln(sum_i exp(z_i)) over ALL
+ * tokens, before top-k, top-p and min-p, at temperature T (at 1 where T <= 0).
+ * Logits of -inf, and NaN, have weight 0, and so has a logit whose difference from m
+ * overflows to -inf (any other one where m is +inf); a row of -inf and NaN alone gives
+ * token -1 and logprob -inf.  u is meant to be in [0, 1): below 0 (or NaN) counts as 0, and at 1 or
+ * above the last kept token with a weight is taken.
+ *
+ * logits [rows][ld] of dtype BF16, FP16 or FP32 and any alignment.  temperature,
+ * top_k, top_p, min_p: [rows] in device memory, each may be NULL (1, all, 1, 0).
+ * token [rows]; logprob [rows] or NULL.
+ * Errors: INVALID_ARG (null pointer, dtype, negative size, pitch too small),
+ * UNSUPPORTED (vocab > RESHARD_MAX_VOCAB, 2^31 rows or more), CUDA.
+ */
+reshard_status_t reshard_sample(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                int64_t ld, const float* temperature, const int32_t* top_k,
+                                const float* top_p, const float* min_p, const float* u,
+                                int32_t* token, float* logprob, void* stream);
+
+/* Workspace bytes of reshard_balance_loss for these sizes (0 for invalid ones). */
+int64_t reshard_balance_loss_workspace(int64_t nseq, int64_t seqlen, int64_t nexperts);
+
+/*
+ * Load-balance loss of a router that sends each token to topk of E = nexperts experts.
+ * Sequence s has n_s tokens with mask != 0 (all, when mask is NULL); S' sequences have
+ * any.  With p_t the scores of token t (reshard_score_t), and over tokens with mask,
+ *   counts[s][e] = how many choices experts[s][t][j] equal e
+ *   f[s][e]      = counts[s][e] * E / (topk * n_s)
+ *   loss         = coef / S' * sum_s 1 / n_s * sum_t sum_e f[s][e] * p[t][e]
+ *   dlogits[t]   = grad * dloss / dlogits[t]   (f is constant; 0 where mask is 0)
+ * For a loss over the whole batch pass it as one sequence.  f depends on the choices
+ * alone, so loss and gradient come from one pass over the logits.  Choices outside
+ * 0..E - 1 are dropped ones and count for no expert.  A token with no score above
+ * 0 in float32 (all its logits -inf) has p = 0.  No token: loss 0.
+ *
+ * logits [nseq][seqlen][ld] of dtype BF16, FP16 or FP32; experts [nseq][seqlen][topk];
+ * mask [nseq][seqlen] bytes or NULL; grad: device pointer to the gradient of the loss,
+ * or NULL for 1; loss: one float, or NULL; counts [nseq][nexperts]; dlogits
+ * [nseq][seqlen][ld] of dtype, or NULL; workspace: reshard_balance_loss_workspace bytes
+ * of device memory, 16-byte aligned, contents irrelevant before and after.
+ * Errors: INVALID_ARG (null pointer, dtype, score, negative size, topk < 1, pitch too
+ * small, workspace too small or misaligned), UNSUPPORTED (nexperts > RESHARD_MAX_EXPERTS,
+ * nseq * seqlen * topk of 2^31 or more), CUDA.
+ */
+reshard_status_t reshard_balance_loss(const void* logits, int32_t dtype, int64_t nseq,
+                                      int64_t seqlen, int64_t nexperts, int64_t ld,
+                                      const int32_t* experts, int64_t topk, const uint8_t* mask,
+                                      int32_t score, float coef, const float* grad, float* loss,
+                                      int32_t* counts, void* dlogits, void* workspace,
+                                      int64_t workspace_bytes, void* stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* reshard_last_error(void);
 
