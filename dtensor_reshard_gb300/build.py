@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["planner.cpp", "batch.cpp", "kernels.cu", "bulk_fanout.cu", "transpose.cu",
            "static_scratch.cu", "realign_staged.cu", "refit.cpp", "partition.cpp",
            "fp8_quantize.cu", "fp8_matmul.cu", "sample.cu", "balance.cu"]
-HEADERS = ["internal.h", "staging.cuh", "operators.cuh"]
+HEADERS = ["internal.h", "staging.cuh", "operators.cuh", "tensor_core.cuh"]
 
 
 def nvcc() -> str:

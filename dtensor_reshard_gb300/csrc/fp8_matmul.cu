@@ -1,42 +1,655 @@
 // fp8_matmul.cu -- reshard_fp8_matmul: the product of e4m3 matrices with a float32
 // scale for each block of 128, dense or one weight matrix for each expert.
+//
+// The scales change every 128 steps of k, so no tensor-core accumulator can run through
+// them: the matrix instructions of one block of 128 write a fresh accumulator in tensor
+// memory, and the threads that own its rows add scale * accumulator to float32 sums in
+// registers while the next block is multiplied into another accumulator.
+//
+// Two kernels, which differ in what lies in the accumulator's 128 lanes (its rows):
+//   wide    256 tokens x 256 features a CTA pair: tokens in the lanes, so a thread has one
+//           token scale and one weight scale a block;
+//   narrow  128 features x NT tokens a CTA: weights in the lanes, so that few tokens
+//           (MMA N down to 16) still use whole instructions; bound by reading w.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
 #include "operators.cuh"
+#include "tensor_core.cuh"
 
 namespace rs {
 namespace {
 
 using namespace op;
+using staging::mbar_arrive_expect;
+using staging::mbar_init;
 
-__device__ __forceinline__ float e4m3(uint8_t v) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+constexpr int kBlock = 128;           // values of k that share a scale, bytes of a tile row
+constexpr int kRows = 128;            // rows of a loaded tile
+constexpr int kTileBytes = kRows * kBlock;
+
+// Codes for the device status word (staging.cuh has 1 to 4).
+enum : unsigned int {
+  kStatusLoadWait = 5,    // the loading warp gave up waiting for a free stage
+  kStatusMatrixWait = 6,  // the matrix warp gave up waiting for data or an accumulator
+  kStatusSumWait = 7      // a summing warp gave up waiting for an accumulator
+};
+
+struct MatmulArgs {
+  const float *xs, *ws;
+  int64_t ldxs, ldws;
+  const int32_t* offsets;
+  int32_t nexperts, tokens, n, blocks;  // blocks of k
+  int32_t ntiles, col_blocks;           // tiles and scale blocks along n
+  void* y;
+  int64_t ldy;
+  uint32_t* status;
+  int32_t aligned_y;  // every row of y starts on 16 bytes
+};
+
+// Each expert's first row and first tile, in shared memory: start[e], tiles[e] for
+// e <= nexperts.  `rows` rows make a tile along the tokens, ntiles tiles lie along n.
+struct ExpertTable {
+  int *start, *tiles;
+  __device__ ExpertTable(char* smem, int nexperts)
+      : start(reinterpret_cast<int*>(smem)), tiles(start + nexperts + 1) {}
+  static size_t bytes(int64_t nexperts) { return size_t(8 * (nexperts + 1)); }
+
+  __device__ void build(const MatmulArgs& a, int rows) {
+    const int lane = threadIdx.x & 31;
+    if (a.offsets == nullptr) {
+      if (threadIdx.x == 0) {
+        start[0] = tiles[0] = 0;
+        start[1] = a.tokens;
+        tiles[1] = (a.tokens + rows - 1) / rows * a.ntiles;
+      }
+      return;
+    }
+    for (int i = threadIdx.x; i <= a.nexperts; i += blockDim.x)
+      start[i] = min(max(a.offsets[i], 0), a.tokens);
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    int most = 0, sum = 0;  // an offset below an earlier one counts as that one
+    for (int base = 0; base <= a.nexperts; base += 32) {
+      const int i = base + lane;
+      int v = max(i <= a.nexperts ? start[i] : 0, most);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, w);
+      }
+      if (i <= a.nexperts) start[i] = v;
+      most = __shfl_sync(0xffffffffu, v, 31);
+    }
+    __syncwarp();
+    for (int base = 0; base < a.nexperts; base += 32) {
+      const int i = base + lane;
+      int v = i < a.nexperts ? (start[i + 1] - start[i] + rows - 1) / rows * a.ntiles : 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+      }
+      if (i < a.nexperts) tiles[i + 1] = sum + v;
+      sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) tiles[0] = 0;
+  }
+};
+
+// One tile: rows [row, end) of expert e (at most a tile's), features from n0.
+struct Tile {
+  int e, row, end, n0;
+  __device__ Tile(const ExpertTable& t, int nexperts, int index, int rows, int cols) {
+    int lo = 0, hi = nexperts - 1;  // the last expert whose first tile is not after index
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.tiles[mid] <= index) lo = mid;
+      else hi = mid - 1;
+    }
+    e = lo;
+    const int per_col = (t.start[e + 1] - t.start[e] + rows - 1) / rows;
+    const int i = index - t.tiles[e];
+    row = t.start[e] + i % per_col * rows;
+    end = t.start[e + 1];
+    n0 = i / per_col * cols;
+  }
+};
+
+constexpr size_t kTableMost = 8 * (RESHARD_MAX_EXPERTS + 1);  // ExpertTable::bytes
+constexpr size_t kSmemMost = 227 * 1024;                      // shared memory of a CTA
+
+// After a wait ran out: time for this thread's copies and matrix instructions to land
+// before shared and tensor memory are given back.
+__device__ __noinline__ void give_up(uint32_t* status, uint32_t code) {
+  atomicExch(status, code);
+  for (int i = 0; i < 64; ++i) __nanosleep(100000);
 }
 
-// One warp an output: lanes share each block's products.
+// ------------------------------------------------------------------------------- wide
+// Ten warps a CTA, two CTAs a pair.  Each CTA loads its own 128 tokens and half of the
+// 256 features of every block (32 KiB a stage); the first CTA's matrix warp multiplies
+// for both (256 x 256 x 128 a block), which halves what each CTA has to load of w; each
+// CTA sums its own 128 tokens' lanes, two warps a lane quarter, 128 columns each.
+constexpr int kWideStages = 5;
+constexpr int kWideStageBytes = 2 * kTileBytes;
+constexpr int kWideCols = 256;
+constexpr int kWideSumWarps = 8;
+constexpr int kWideThreads = 32 * (kWideSumWarps + 2);
+constexpr int kOutRow = 64;              // bytes of an output row staged at a time
+constexpr int kOutPitch = kOutRow + 16;  // no bank conflicts where rows are written
+constexpr int kOutBytes = 32 * kOutPitch;
+
+struct WideSmem {
+  alignas(1024) unsigned char stages[kWideStages][kWideStageBytes];
+  alignas(16) unsigned char out[kWideSumWarps][kOutBytes];
+  uint64_t full[kWideStages], empty[kWideStages], sum_full[2], sum_empty[2];
+  uint32_t tmem;
+};
+static_assert(sizeof(WideSmem) + kTableMost <= kSmemMost, "shared memory");
+
 template <typename Y>
-__global__ void __launch_bounds__(256)
-    matmul_kernel(const uint8_t* x, int64_t ldx, const float* xs, int64_t ldxs, const uint8_t* w,
-                  int64_t ldw, const float* ws, int64_t ldws, const int32_t* offsets,
-                  int64_t nexperts, int64_t tokens, int64_t n, int64_t k, Y* y, int64_t ldy) {
-  const int64_t o = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (o >= tokens * n) return;
-  const int64_t t = o / n, j = o % n;
-  int64_t e = 0;
-  if (offsets != nullptr) {
-    while (e < nexperts && !(offsets[e] <= t && t < offsets[e + 1])) ++e;
-    if (e == nexperts) return;
+__global__ void __launch_bounds__(kWideThreads, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ MatmulArgs a) {
+  extern __shared__ __align__(1024) unsigned char dynamic[];
+  WideSmem& sm = *reinterpret_cast<WideSmem*>(dynamic);
+  ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(WideSmem)), a.nexperts);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    tc::prefetch_map(&map_x);
+    tc::prefetch_map(&map_w);
+    for (int i = 0; i < kWideStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.sum_full[i], 1);
+      mbar_init(&sm.sum_empty[i], 2 * kWideSumWarps);
+    }
+    tc::fence_barrier_init();
   }
-  const uint8_t* xr = x + t * ldx;
-  const uint8_t* wr = w + (e * n + j) * ldw;
-  const float* wsr = ws + (e * ((n + 127) / 128) + j / 128) * ldws;
-  float sum = 0.0f;
-  for (int64_t b = 0; b * 128 < k; ++b) {
-    float part = 0.0f;
-    for (int64_t i = b * 128 + lane; i < k && i < b * 128 + 128; i += 32)
-      part += e4m3(xr[i]) * e4m3(wr[i]);
-    sum += warp_sum(part) * (xs[t * ldxs + b] * wsr[b]);
+  if (warp == kWideSumWarps + 1) tc::tmem_alloc<true>(&sm.tmem, 512);
+  table.build(a, 2 * kRows);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  const int total = table.tiles[a.nexperts];
+
+  if (warp == kWideSumWarps) {  // loads
+    uint32_t stage = 0, parity = 1;
+    bool ok = true;
+    for (int t = pair; ok && t < total; t += pairs) {
+      const Tile tile(table, a.nexperts, t, 2 * kRows, kWideCols);
+      for (int b = 0; b < a.blocks; ++b) {
+        if (!(ok = tc::wait_cluster(&sm.empty[stage], parity))) break;
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect(&sm.full[stage], 2 * kWideStageBytes);
+          const uint32_t bar = tc::in_cta(staging::smem_addr(&sm.full[stage]), 0);
+          const uint32_t dst = staging::smem_addr(sm.stages[stage]);
+          tc::load_box_pair(dst, &map_x, bar, b * kBlock, tile.row + int(rank) * kRows, 0);
+          tc::load_box_pair(dst + kTileBytes, &map_w, bar, b * kBlock, tile.n0 + int(rank) * kRows,
+                            tile.e);
+        }
+        __syncwarp();
+        if (++stage == kWideStages) stage = 0, parity ^= 1;
+      }
+    }
+    // every matrix instruction has let go of its stage before this CTA may end
+    for (int i = 0; ok && i < kWideStages; ++i) {
+      ok = tc::wait_cluster(&sm.empty[stage], parity);
+      if (++stage == kWideStages) stage = 0, parity ^= 1;
+    }
+    if (!ok && lane == 0) give_up(a.status, kStatusLoadWait);
+  } else if (warp == kWideSumWarps + 1) {  // matrix instructions, by the first CTA
+    if (rank == 0) {
+      constexpr uint32_t instruction = tc::e4m3_instruction(2 * kRows, kWideCols);
+      uint32_t stage = 0, parity = 0, buf = 0, buf_parity = 1;
+      bool ok = true;
+      for (int t = pair; ok && t < total; t += pairs) {
+        for (int b = 0; b < a.blocks; ++b) {
+          if (!(ok = tc::wait_cluster(&sm.sum_empty[buf], buf_parity))) break;
+          if (!(ok = tc::wait_cluster(&sm.full[stage], parity))) break;
+          tc::fence_after_sync();
+          if (lane == 0) {
+            const uint32_t src = staging::smem_addr(sm.stages[stage]);
+            const uint64_t dx = tc::tile_desc(src), dw = tc::tile_desc(src + kTileBytes);
+            for (int k = 0; k < 4; ++k)  // 32 bytes of k an instruction
+              tc::mma_e4m3<true>(tmem + buf * kWideCols, dx + 2 * k, dw + 2 * k, instruction, k > 0);
+            tc::mma_commit<true>(staging::smem_addr(&sm.empty[stage]));
+            tc::mma_commit<true>(staging::smem_addr(&sm.sum_full[buf]));
+          }
+          __syncwarp();
+          if (++stage == kWideStages) stage = 0, parity ^= 1;
+          if (++buf == 2) buf = 0, buf_parity ^= 1;
+        }
+      }
+      if (!ok && lane == 0) give_up(a.status, kStatusMatrixWait);
+    }
+  } else {  // sums
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + half * 128;
+    unsigned char* out = sm.out[warp];
+    uint32_t buf = 0, parity = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < total; t += pairs) {
+      const Tile tile(table, a.nexperts, t, 2 * kRows, kWideCols);
+      const int row0 = tile.row + int(rank) * kRows + quarter * 32;
+      const int col0 = tile.n0 + half * 128;
+      const float* xs = a.xs + int64_t(min(row0 + lane, a.tokens - 1)) * a.ldxs;
+      const float* ws =
+          a.ws + (int64_t(tile.e) * a.col_blocks + min(col0 / kBlock, a.col_blocks - 1)) * a.ldws;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      float sx = xs[0], sw = ws[0];
+      for (int b = 0; b < a.blocks; ++b) {
+        const uint32_t s = __float_as_uint(sx * sw);
+        const uint64_t scale = tc::pack2(s, s);
+        if (b + 1 < a.blocks) {
+          sx = xs[b + 1];
+          sw = ws[b + 1];
+        }
+        if (!(ok = tc::wait_cluster(&sm.sum_full[buf], parity))) break;
+        tc::fence_after_sync();
+        const uint32_t from = lanes + buf * kWideCols;
+        uint32_t v[2][16];
+        tc::tmem_load16(from, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          tc::tmem_wait(v[c & 1]);
+          if (c < 7) tc::tmem_load16(from + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc[8 * c + i] =
+                tc::fma2(tc::pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), scale, acc[8 * c + i]);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::arrive_cluster(tc::in_cta(staging::smem_addr(&sm.sum_empty[buf]), 0));
+        if (++buf == 2) buf = 0, parity ^= 1;
+      }
+      if (!ok) break;
+      // through shared memory, so that neighbouring lanes store neighbouring columns
+      constexpr int kChunk = kOutRow / int(sizeof(Y));  // columns of a round
+      constexpr int kVec = 16 / int(sizeof(Y));
+      Y* y = static_cast<Y*>(a.y);
+#pragma unroll
+      for (int round = 0; round < 128 / kChunk; ++round) {
+#pragma unroll
+        for (int j = 0; j < kOutRow / 16; ++j) {
+          __align__(16) Y vec[kVec];
+#pragma unroll
+          for (int i = 0; i < kVec / 2; ++i) {
+            const float2 f = tc::unpack2(acc[(round * kChunk + j * kVec) / 2 + i]);
+            vec[2 * i] = from_float<Y>(f.x);
+            vec[2 * i + 1] = from_float<Y>(f.y);
+          }
+          *reinterpret_cast<uint4*>(out + lane * kOutPitch + j * 16) =
+              *reinterpret_cast<const uint4*>(vec);
+        }
+        __syncwarp();
+        const int c0 = col0 + round * kChunk;
+        if (a.aligned_y) {
+#pragma unroll
+          for (int i = 0; i < kOutRow / 16; ++i) {
+            constexpr int kLanes = kOutRow / 16;  // lanes of a row
+            const int r = i * (32 / kLanes) + lane / kLanes, c = c0 + lane % kLanes * kVec;
+            const uint4 v = *reinterpret_cast<const uint4*>(out + r * kOutPitch + lane % kLanes * 16);
+            if (row0 + r < tile.end && c < a.n) {
+              Y* to = y + int64_t(row0 + r) * a.ldy + c;
+              if (c + kVec <= a.n) {
+                *reinterpret_cast<uint4*>(to) = v;
+              } else {
+                const Y* e = reinterpret_cast<const Y*>(&v);
+                for (int k = 0; k < a.n - c; ++k) to[k] = e[k];
+              }
+            }
+          }
+        } else {
+          for (int r = 0; r < 32 && row0 + r < tile.end; ++r)
+            for (int c = lane; c < kChunk && c0 + c < a.n; c += 32)
+              y[int64_t(row0 + r) * a.ldy + c0 + c] =
+                  *reinterpret_cast<const Y*>(out + r * kOutPitch + c * sizeof(Y));
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) give_up(a.status, kStatusSumWait);
   }
-  if (lane == 0) y[t * ldy + j] = from_float<Y>(sum);
+  __syncwarp();
+  tc::fence_before_sync();
+  tc::cluster_sync();
+  if (warp == kWideSumWarps + 1) tc::tmem_free<true>(tmem, 512);
+}
+
+// ----------------------------------------------------------------------------- narrow
+// Six warps a CTA, one tile of 128 features x NT tokens a CTA.  `split` CTAs of a cluster
+// take a share of the blocks of k each and add their sums through distributed shared
+// memory in rank order.
+template <int NT>
+struct NarrowShape {
+  static constexpr int kStageBytes = kTileBytes + NT * kBlock;
+  // two CTAs an SM where that leaves them three stages each
+  static constexpr int kStages = NT <= 16 ? 5 : NT <= 32 ? 4 : 3;
+  static constexpr int kBufs = NT <= 64 ? 4 : 2;  // accumulators
+  static constexpr int kColumns = kBufs * NT;     // of tensor memory: 64, 128, 256, 256
+};
+constexpr int kNarrowThreads = 32 * 6;
+
+template <int NT>
+struct NarrowSmem {
+  using S = NarrowShape<NT>;
+  alignas(1024) unsigned char stages[S::kStages][S::kStageBytes];
+  alignas(16) float sums[NT][kRows];
+  alignas(16) float scales[4][2][NT];
+  uint64_t full[S::kStages], empty[S::kStages], sum_full[S::kBufs], sum_empty[S::kBufs];
+  uint32_t tmem;
+};
+static_assert(sizeof(NarrowSmem<128>) + kTableMost <= kSmemMost, "shared memory");
+
+template <int NT, typename Y>
+__global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
+    narrow_kernel(const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ CUtensorMap map_w, const __grid_constant__ MatmulArgs a,
+                  const int split) {
+  using S = NarrowShape<NT>;
+  extern __shared__ __align__(1024) unsigned char dynamic[];
+  NarrowSmem<NT>& sm = *reinterpret_cast<NarrowSmem<NT>*>(dynamic);
+  ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(NarrowSmem<NT>)), a.nexperts);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(blockIdx.x) % split, index = int(blockIdx.x) / split;
+
+  table.build(a, NT);
+  __syncthreads();
+  if (index >= table.tiles[a.nexperts]) return;  // the whole cluster
+  if (threadIdx.x == 0) {
+    tc::prefetch_map(&map_x);
+    tc::prefetch_map(&map_w);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < S::kBufs; ++i) {
+      mbar_init(&sm.sum_full[i], 1);
+      mbar_init(&sm.sum_empty[i], 4);
+    }
+    tc::fence_barrier_init();
+  }
+  if (warp == 5) tc::tmem_alloc<false>(&sm.tmem, S::kColumns);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  const Tile tile(table, a.nexperts, index, NT, kRows);
+  const int b0 = int(int64_t(a.blocks) * rank / split);
+  const int b1 = int(int64_t(a.blocks) * (rank + 1) / split);
+  const int cols = min(NT, tile.end - tile.row);
+
+  if (warp == 4) {  // loads
+    uint32_t stage = 0, parity = 1;
+    bool ok = true;
+    for (int b = b0; b < b1; ++b) {
+      if (!(ok = tc::wait_cluster(&sm.empty[stage], parity))) break;
+      if (lane == 0) {
+        mbar_arrive_expect(&sm.full[stage], S::kStageBytes);
+        const uint32_t bar = staging::smem_addr(&sm.full[stage]);
+        const uint32_t dst = staging::smem_addr(sm.stages[stage]);
+        tc::load_box(dst, &map_w, bar, b * kBlock, tile.n0, tile.e);
+        tc::load_box(dst + kTileBytes, &map_x, bar, b * kBlock, tile.row, 0);
+      }
+      __syncwarp();
+      if (++stage == S::kStages) stage = 0, parity ^= 1;
+    }
+    // every matrix instruction has let go of its stage before this CTA may end
+    for (int i = 0; ok && i < S::kStages; ++i) {
+      ok = tc::wait_cluster(&sm.empty[stage], parity);
+      if (++stage == S::kStages) stage = 0, parity ^= 1;
+    }
+    if (!ok && lane == 0) give_up(a.status, kStatusLoadWait);
+  } else if (warp == 5) {  // matrix instructions
+    constexpr uint32_t instruction = tc::e4m3_instruction(kRows, NT);
+    uint32_t stage = 0, parity = 0, buf = 0, buf_parity = 1;
+    bool ok = true;
+    for (int b = b0; b < b1; ++b) {
+      if (!(ok = tc::wait_cluster(&sm.sum_empty[buf], buf_parity))) break;
+      if (!(ok = tc::wait_cluster(&sm.full[stage], parity))) break;
+      tc::fence_after_sync();
+      if (lane == 0) {
+        const uint32_t src = staging::smem_addr(sm.stages[stage]);
+        const uint64_t dw = tc::tile_desc(src), dx = tc::tile_desc(src + kTileBytes);
+        for (int k = 0; k < 4; ++k)
+          tc::mma_e4m3<false>(tmem + buf * NT, dw + 2 * k, dx + 2 * k, instruction, k > 0);
+        tc::mma_commit<false>(staging::smem_addr(&sm.empty[stage]));
+        tc::mma_commit<false>(staging::smem_addr(&sm.sum_full[buf]));
+      }
+      __syncwarp();
+      if (++stage == S::kStages) stage = 0, parity ^= 1;
+      if (++buf == S::kBufs) buf = 0, buf_parity ^= 1;
+    }
+    if (!ok && lane == 0) give_up(a.status, kStatusMatrixWait);
+  } else {  // sums: a thread has one feature of every token
+    const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
+    const float* ws = a.ws + (int64_t(tile.e) * a.col_blocks + tile.n0 / kBlock) * a.ldws;
+    constexpr int kPer = (NT + 31) / 32;
+    const float* xs[kPer];
+    float next[kPer], sw = 0.0f;
+    for (int i = 0; i < kPer; ++i) {
+      xs[i] = a.xs + int64_t(min(tile.row + i * 32 + lane, a.tokens - 1)) * a.ldxs;
+      next[i] = b0 < b1 ? xs[i][b0] : 0.0f;
+    }
+    if (b0 < b1) sw = ws[b0];
+    uint64_t acc[NT / 2];
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) acc[i] = 0;
+    uint32_t buf = 0, parity = 0;
+    bool ok = true;
+    for (int b = b0; b < b1; ++b) {
+      float* scales = sm.scales[warp][b & 1];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (NT >= 32 || lane < NT) scales[i * 32 + lane] = next[i] * sw;
+        if (b + 1 < b1) next[i] = xs[i][b + 1];
+      }
+      if (b + 1 < b1) sw = ws[b + 1];
+      __syncwarp();
+      if (!(ok = tc::wait_cluster(&sm.sum_full[buf], parity))) break;
+      tc::fence_after_sync();
+      const uint32_t from = lanes + buf * NT;
+      uint32_t v[2][16];
+      tc::tmem_load16(from, v[0]);
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        tc::tmem_wait(v[c & 1]);
+        if (c + 1 < NT / 16) tc::tmem_load16(from + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 s = reinterpret_cast<const ulonglong2*>(scales)[c * 4 + i];
+          acc[c * 8 + 2 * i] = tc::fma2(tc::pack2(v[c & 1][4 * i], v[c & 1][4 * i + 1]), s.x,
+                                        acc[c * 8 + 2 * i]);
+          acc[c * 8 + 2 * i + 1] = tc::fma2(tc::pack2(v[c & 1][4 * i + 2], v[c & 1][4 * i + 3]), s.y,
+                                            acc[c * 8 + 2 * i + 1]);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) staging::mbar_arrive(&sm.sum_empty[buf]);
+      if (++buf == S::kBufs) buf = 0, parity ^= 1;
+    }
+    if (!ok && lane == 0) give_up(a.status, kStatusSumWait);
+    const int feature = warp * 32 + lane;
+    Y* y = static_cast<Y*>(a.y) + int64_t(tile.row) * a.ldy + tile.n0 + feature;
+    if (split == 1) {
+      if (ok && tile.n0 + feature < a.n) {
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+          const float2 f = tc::unpack2(acc[i]);
+          if (2 * i < cols) y[2 * i * a.ldy] = from_float<Y>(f.x);
+          if (2 * i + 1 < cols) y[(2 * i + 1) * a.ldy] = from_float<Y>(f.y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) {
+        const float2 f = tc::unpack2(acc[i]);
+        if (2 * i < cols) sm.sums[2 * i][feature] = f.x;
+        if (2 * i + 1 < cols) sm.sums[2 * i + 1][feature] = f.y;
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    tc::cluster_sync();
+    if (warp < 4 && tile.n0 + int(threadIdx.x) < a.n) {
+      Y* y = static_cast<Y*>(a.y) + int64_t(tile.row) * a.ldy + tile.n0 + threadIdx.x;
+      for (int c = rank; c < cols; c += split) {
+        const uint32_t at = staging::smem_addr(&sm.sums[c][threadIdx.x]);
+        float sum = 0.0f;
+        for (int r = 0; r < split; ++r) sum += tc::load_cluster(tc::in_cta(at, r));
+        y[int64_t(c) * a.ldy] = from_float<Y>(sum);
+      }
+    }
+    __syncwarp();
+    tc::cluster_sync();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) tc::tmem_free<false>(tmem, S::kColumns);
+}
+
+// An inner size of zero: the rows of experts get zeros.
+template <typename Y>
+__global__ void zero_kernel(const MatmulArgs a) {
+  int first = 0, end = a.tokens;
+  if (a.offsets != nullptr) {
+    first = min(max(a.offsets[0], 0), a.tokens);
+    end = min(a.offsets[a.nexperts], a.tokens);
+  }
+  for (int r = first + int(blockIdx.x); r < end; r += int(gridDim.x))
+    for (int c = threadIdx.x; c < a.n; c += blockDim.x)
+      static_cast<Y*>(a.y)[int64_t(r) * a.ldy + c] = from_float<Y>(0.0f);
+}
+
+// ------------------------------------------------------------------------------- host
+// [planes][rows][pitch] bytes, of which k a row count; boxes of 128 bytes x box_rows rows,
+// zeros beyond every edge.
+reshard_status_t tile_map(CUtensorMap* map, const void* base, int64_t k, int64_t rows, int64_t planes,
+                          int64_t pitch, int box_rows) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> entry{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 encode = entry.load(std::memory_order_acquire);
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t ce =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (ce != cudaSuccess || found != cudaDriverEntryPointSuccess || !fn)
+      return fail(RESHARD_ERR_CUDA, std::string("cuTensorMapEncodeTiled: ") + cudaGetErrorString(ce));
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    entry.store(encode, std::memory_order_release);
+  }
+  const cuuint64_t dims[3] = {cuuint64_t(k), cuuint64_t(rows), cuuint64_t(planes)};
+  const cuuint64_t strides[2] = {cuuint64_t(pitch), cuuint64_t(pitch) * cuuint64_t(rows)};
+  const cuuint32_t box[3] = {kBlock, cuuint32_t(box_rows), 1}, steps[3] = {1, 1, 1};
+  const CUresult r =
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(RESHARD_ERR_CUDA, "cuTensorMapEncodeTiled: error " + std::to_string(int(r)));
+  return RESHARD_OK;
+}
+
+reshard_status_t launch(const void* kernel, unsigned grid, unsigned threads, size_t smem, int cluster,
+                        cudaStream_t stream, void** args) {
+  cudaError_t ce =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (ce == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    ce = cudaLaunchKernelExC(&cfg, kernel, args);
+  }
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("reshard_fp8_matmul: ") + cudaGetErrorString(ce));
+  return RESHARD_OK;
+}
+
+struct Operands {
+  const void *x, *w;
+  int64_t ldx, ldw, k;
+};
+
+template <typename Y>
+reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int sms, cudaStream_t stream) {
+  CUtensorMap map_x, map_w;
+  reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, kRows);
+  if (st == RESHARD_OK) st = tile_map(&map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows);
+  if (st != RESHARD_OK) return st;
+  a.ntiles = int32_t(cdiv(a.n, kWideCols));
+  // an expert's last tile may be short, so experts add at most one row of tiles each
+  const int64_t most = a.ntiles * (cdiv(a.tokens, 2 * kRows) + (a.nexperts > 1 ? a.nexperts : 0));
+  const int64_t pairs = most < sms / 2 ? most : sms / 2;
+  void* args[] = {&map_x, &map_w, &a};
+  return launch(reinterpret_cast<const void*>(wide_kernel<Y>), unsigned(2 * pairs), kWideThreads,
+                sizeof(WideSmem) + ExpertTable::bytes(a.nexperts), 2, stream, args);
+}
+
+template <int NT, typename Y>
+reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int sms, cudaStream_t stream) {
+  CUtensorMap map_x, map_w;
+  reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, NT);
+  if (st == RESHARD_OK) st = tile_map(&map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows);
+  if (st != RESHARD_OK) return st;
+  a.ntiles = int32_t(cdiv(a.n, kRows));
+  int64_t tiles = a.ntiles * cdiv(a.tokens, NT);
+  if (a.offsets) tiles = a.ntiles * (a.tokens / NT + (a.nexperts < a.tokens ? a.nexperts : a.tokens));
+  int split = 1;
+  while (split < 8 && tiles * split < 2 * sms && a.blocks >= 4 * split) split *= 2;
+  if (tiles * split >= int64_t(1) << 31)
+    return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
+  void* args[] = {&map_x, &map_w, &a, &split};
+  return launch(reinterpret_cast<const void*>(narrow_kernel<NT, Y>), unsigned(tiles * split),
+                kNarrowThreads, sizeof(NarrowSmem<NT>) + ExpertTable::bytes(a.nexperts), split, stream,
+                args);
+}
+
+template <typename Y>
+reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t stream) {
+  if (a.blocks == 0) {
+    zero_kernel<Y><<<unsigned(a.tokens < 1024 ? a.tokens : 1024), 256, 0, stream>>>(a);
+    return launched("reshard_fp8_matmul");
+  }
+  int dev = 0, sms = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
+  reshard_status_t st = device_status_word(&a.status);
+  if (st != RESHARD_OK) return st;
+  const int64_t each = cdiv(a.tokens, a.nexperts);  // tokens of an expert, on average
+  if (!a.offsets) {
+    if (each <= 16) return launch_narrow<16, Y>(a, o, sms, stream);
+    if (each <= 32) return launch_narrow<32, Y>(a, o, sms, stream);
+    if (each <= 64) return launch_narrow<64, Y>(a, o, sms, stream);
+    if (each <= 128) return launch_narrow<128, Y>(a, o, sms, stream);
+  } else {
+    if (each <= 4) return launch_narrow<16, Y>(a, o, sms, stream);
+    if (each <= 8) return launch_narrow<32, Y>(a, o, sms, stream);
+    if (each <= 16) return launch_narrow<64, Y>(a, o, sms, stream);
+    if (each <= 64) return launch_narrow<128, Y>(a, o, sms, stream);
+  }
+  return launch_wide<Y>(a, o, sms, stream);
 }
 
 }  // namespace
@@ -58,9 +671,9 @@ extern "C" reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const
   if (!offsets && nexperts != 1)
     return fail(RESHARD_ERR_INVALID_ARG, "several experts need offsets");
   if (nexperts > RESHARD_MAX_EXPERTS) return fail(RESHARD_ERR_UNSUPPORTED, "too many experts");
-  constexpr int64_t kMost = int64_t(1) << 31;
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1024;  // rounding up to tiles stays in 32 bits
   if (tokens >= kMost || n >= kMost || k >= kMost || nexperts * n >= kMost)
-    return fail(RESHARD_ERR_UNSUPPORTED, "size of 2^31 or more");
+    return fail(RESHARD_ERR_UNSUPPORTED, "size of nearly 2^31 or more");
   if (tokens == 0 || n == 0) return RESHARD_OK;
   const int64_t blocks = rs::op::cdiv(k, 128);
   if (ldx < k || ldw < k || ldxs < blocks || ldws < blocks || ldy < n)
@@ -72,12 +685,22 @@ extern "C" reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const
   if (!rs::op::aligned(xs, 4) || !rs::op::aligned(ws, 4) || !rs::op::aligned(offsets, 4) ||
       !rs::op::aligned(y, rs::op::dtype_size(ydtype)))
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
+  rs::MatmulArgs a = {};
+  a.xs = xs;
+  a.ws = ws;
+  a.ldxs = ldxs;
+  a.ldws = ldws;
+  a.offsets = offsets;
+  a.nexperts = int32_t(nexperts);
+  a.tokens = int32_t(tokens);
+  a.n = int32_t(n);
+  a.blocks = int32_t(blocks);
+  a.col_blocks = int32_t(rs::op::cdiv(n, 128));
+  a.y = y;
+  a.ldy = ldy;
+  a.aligned_y = rs::op::aligned(y, 16) && ldy * rs::op::dtype_size(ydtype) % 16 == 0;
+  const rs::Operands o = {x, w, ldx, ldw, k};
   return rs::op::by_dtype(ydtype, [&](auto t) {
-    using Y = decltype(t);
-    rs::matmul_kernel<Y><<<unsigned(rs::op::cdiv(tokens * n, 8)), 256, 0,
-                           static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint8_t*>(x), ldx, xs, ldxs, static_cast<const uint8_t*>(w), ldw, ws,
-        ldws, offsets, nexperts, tokens, n, k, static_cast<Y*>(y), ldy);
-    return rs::op::launched("reshard_fp8_matmul");
+    return rs::launch_matmul<decltype(t)>(a, o, static_cast<cudaStream_t>(stream));
   });
 }

@@ -337,8 +337,9 @@ reshard_status_t gather_broadcast_execute(reshard_plan_t plan, const void* const
  * failure detection of this library).  The TMA-staged fan-out kernel bounds
  * every wait on its shared-memory barriers; a wait that runs out (which a
  * correct run never does) records a nonzero code here instead of hanging or
- * trapping, and the kernel returns.  Codes: 0 none, 1 producer wait, 2 consumer
- * wait, 3 self-test.  Synchronous (reads device memory with cudaMemcpy);
+ * trapping, and the kernel returns.  reshard_fp8_matmul's waits are bounded the same
+ * way.  Codes: 0 none, 1 producer wait, 2 consumer wait, 3 self-test, 5, 6, 7
+ * reshard_fp8_matmul's loading, matrix and summing warps.  Synchronous (reads device memory with cudaMemcpy);
  * `clear` != 0 resets the word to 0 after reading.  Errors: INVALID_ARG, CUDA.
  */
 reshard_status_t reshard_device_status(int32_t clear, uint32_t* status);
@@ -820,7 +821,7 @@ reshard_status_t reshard_fp8_quantize(const void* x, int32_t dtype, int64_t nmat
  * used); scales and y are aligned to their type.
  * Errors: INVALID_ARG (null pointer, dtype, negative size, pitch too small, misaligned
  * x, w or pitch, nexperts without offsets), UNSUPPORTED (nexperts > RESHARD_MAX_EXPERTS,
- * a size of 2^31 or more), CUDA.
+ * a size within 1024 of 2^31 or more), CUDA.
  */
 reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const float* xs, int64_t ldxs,
                                     const void* w, int64_t ldw, const float* ws, int64_t ldws,
