@@ -24,6 +24,7 @@ namespace {
 using namespace op;
 using staging::mbar_arrive_expect;
 using staging::mbar_init;
+using staging::mbar_wait;
 
 constexpr int kBlock = 128;           // values of k that share a scale, bytes of a tile row
 constexpr int kRows = 128;            // rows of a loaded tile
@@ -54,7 +55,7 @@ struct ExpertTable {
   int *start, *tiles;
   __device__ ExpertTable(char* smem, int nexperts)
       : start(reinterpret_cast<int*>(smem)), tiles(start + nexperts + 1) {}
-  static size_t bytes(int64_t nexperts) { return size_t(8 * (nexperts + 1)); }
+  __host__ __device__ static constexpr size_t bytes(int64_t nexperts) { return size_t(8 * (nexperts + 1)); }
 
   __device__ void build(const MatmulArgs& a, int rows) {
     const int lane = threadIdx.x & 31;
@@ -99,6 +100,7 @@ struct ExpertTable {
 // One tile: rows [row, end) of expert e (at most a tile's), features from n0.
 struct Tile {
   int e, row, end, n0;
+  __device__ Tile() : e(0), row(0), end(0), n0(0) {}
   __device__ Tile(const ExpertTable& t, int nexperts, int index, int rows, int cols) {
     int lo = 0, hi = nexperts - 1;  // the last expert whose first tile is not after index
     while (lo < hi) {
@@ -126,52 +128,71 @@ __device__ __noinline__ void give_up(uint32_t* status, uint32_t code) {
 }
 
 // ------------------------------------------------------------------------------- wide
-// Ten warps a CTA, two CTAs a pair.  Each CTA loads its own 128 tokens and half of the
-// 256 features of every block (32 KiB a stage); the first CTA's matrix warp multiplies
-// for both (256 x 256 x 128 a block), which halves what each CTA has to load of w; each
-// CTA sums its own 128 tokens' lanes, two warps a lane quarter, 128 columns each.
-constexpr int kWideStages = 5;
-constexpr int kWideStageBytes = 2 * kTileBytes;
+// Twelve warps a CTA, two CTAs a cluster, which take 256 tokens x 256 features: each CTA
+// loads its own 128 tokens and half of the features of every block (32 KiB of a 48 KiB
+// stage), the halves going to both CTAs, and multiplies and sums its own 128 tokens, two
+// warps a lane quarter, 128 columns each.  (One cta_group::2 instruction for both CTAs
+// loads as little but hands accumulators over between SMs: 416 us against XXX us for
+// 8192 x 14336 x 4096.)
+constexpr int kWideStages = 4;  // 3 where the expert table needs the room
+constexpr int kWideStageBytes = 3 * kTileBytes;
 constexpr int kWideCols = 256;
 constexpr int kWideSumWarps = 8;
-constexpr int kWideThreads = 32 * (kWideSumWarps + 2);
+constexpr int kWideWarpCols = kWideCols / (kWideSumWarps / 4);
+constexpr int kWideThreads = 32 * (kWideSumWarps + 4);
 constexpr int kOutRow = 64;              // bytes of an output row staged at a time
 constexpr int kOutPitch = kOutRow + 16;  // no bank conflicts where rows are written
 constexpr int kOutBytes = 32 * kOutPitch;
 
+// A summing warp fetches the scales of its 32 rows for 8 blocks at a time, a sector a
+// row, and keeps the products of both scales in shared memory (one word a lane and block:
+// reading xs where it lies would touch 32 lines for each block).
+constexpr int kScaleBlocks = 8;
+constexpr int kScalePitch = kScaleBlocks + 1;
+
+// Shares of the register file, a warp: 8 * 224 + 4 * 56 = 12 * 168 at launch.
+constexpr int kWideSumRegisters = 224, kWideOtherRegisters = 56;
+
+// What lies before the stages in shared memory.
 struct WideSmem {
-  alignas(1024) unsigned char stages[kWideStages][kWideStageBytes];
   alignas(16) unsigned char out[kWideSumWarps][kOutBytes];
+  float scales[kWideSumWarps][32 * kScalePitch];
   uint64_t full[kWideStages], empty[kWideStages], sum_full[2], sum_empty[2];
   uint32_t tmem;
 };
-static_assert(sizeof(WideSmem) + kTableMost <= kSmemMost, "shared memory");
+// Offset of the stages: behind WideSmem and the table, on a swizzle atom.
+__host__ __device__ constexpr size_t wide_stages_at(size_t table_bytes) {
+  return (sizeof(WideSmem) + table_bytes + 1023) / 1024 * 1024;
+}
+static_assert(wide_stages_at(kTableMost) + 3 * kWideStageBytes <= kSmemMost, "shared memory");
 
 template <typename Y>
 __global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                const __grid_constant__ MatmulArgs a) {
+                const __grid_constant__ MatmulArgs a, const int stages) {
   extern __shared__ __align__(1024) unsigned char dynamic[];
   WideSmem& sm = *reinterpret_cast<WideSmem*>(dynamic);
   ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(WideSmem)), a.nexperts);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t data =
+      staging::smem_addr(dynamic) + uint32_t(wide_stages_at(ExpertTable::bytes(a.nexperts)));
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_x);
     tc::prefetch_map(&map_w);
-    for (int i = 0; i < kWideStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);  // both CTAs write into a stage
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sum_full[i], 1);
-      mbar_init(&sm.sum_empty[i], 2 * kWideSumWarps);
+      mbar_init(&sm.sum_empty[i], kWideSumWarps);
     }
     tc::fence_barrier_init();
   }
-  if (warp == kWideSumWarps + 1) tc::tmem_alloc<true>(&sm.tmem, 512);
+  if (warp == kWideSumWarps + 1) tc::tmem_alloc(&sm.tmem, 512);
   table.build(a, 2 * kRows);
   tc::fence_before_sync();
   __syncthreads();
@@ -181,88 +202,111 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int total = table.tiles[a.nexperts];
 
   if (warp == kWideSumWarps) {  // loads
+    tc::registers_down<kWideOtherRegisters>();
     uint32_t stage = 0, parity = 1;
     bool ok = true;
     for (int t = pair; ok && t < total; t += pairs) {
       const Tile tile(table, a.nexperts, t, 2 * kRows, kWideCols);
       for (int b = 0; b < a.blocks; ++b) {
-        if (!(ok = tc::wait_cluster(&sm.empty[stage], parity))) break;
+        if (!(ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls))) break;
         if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect(&sm.full[stage], 2 * kWideStageBytes);
-          const uint32_t bar = tc::in_cta(staging::smem_addr(&sm.full[stage]), 0);
-          const uint32_t dst = staging::smem_addr(sm.stages[stage]);
-          tc::load_box_pair(dst, &map_x, bar, b * kBlock, tile.row + int(rank) * kRows, 0);
-          tc::load_box_pair(dst + kTileBytes, &map_w, bar, b * kBlock, tile.n0 + int(rank) * kRows,
-                            tile.e);
+          mbar_arrive_expect(&sm.full[stage], kWideStageBytes);
+          const uint32_t bar = staging::smem_addr(&sm.full[stage]);
+          const uint32_t dst = data + stage * kWideStageBytes;
+          tc::load_box(dst, &map_x, bar, b * kBlock, tile.row + int(rank) * kRows, 0);
+          tc::load_box_both(dst + (1 + rank) * kTileBytes, &map_w, bar, b * kBlock,
+                            tile.n0 + int(rank) * kRows, tile.e);
         }
         __syncwarp();
-        if (++stage == kWideStages) stage = 0, parity ^= 1;
+        if (++stage == uint32_t(stages)) stage = 0, parity ^= 1;
       }
     }
     // every matrix instruction has let go of its stage before this CTA may end
-    for (int i = 0; ok && i < kWideStages; ++i) {
-      ok = tc::wait_cluster(&sm.empty[stage], parity);
-      if (++stage == kWideStages) stage = 0, parity ^= 1;
+    for (int i = 0; ok && i < stages; ++i) {
+      ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls);
+      if (++stage == uint32_t(stages)) stage = 0, parity ^= 1;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusLoadWait);
-  } else if (warp == kWideSumWarps + 1) {  // matrix instructions, by the first CTA
-    if (rank == 0) {
-      constexpr uint32_t instruction = tc::e4m3_instruction(2 * kRows, kWideCols);
-      uint32_t stage = 0, parity = 0, buf = 0, buf_parity = 1;
+  } else if (warp > kWideSumWarps) {
+    tc::registers_down<kWideOtherRegisters>();
+    if (warp <= kWideSumWarps + 2) {  // matrix instructions
+      constexpr uint32_t instruction = tc::e4m3_instruction(kRows, kWideCols);
+      const uint32_t buf = warp - (kWideSumWarps + 1);  // this warp's accumulator: every other block
+      const int count = pair < total ? ((total - 1 - pair) / pairs + 1) * a.blocks : 0;
+      uint32_t stage = buf, parity = 0, buf_parity = 1;
       bool ok = true;
-      for (int t = pair; ok && t < total; t += pairs) {
-        for (int b = 0; b < a.blocks; ++b) {
-          if (!(ok = tc::wait_cluster(&sm.sum_empty[buf], buf_parity))) break;
-          if (!(ok = tc::wait_cluster(&sm.full[stage], parity))) break;
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint32_t src = staging::smem_addr(sm.stages[stage]);
-            const uint64_t dx = tc::tile_desc(src), dw = tc::tile_desc(src + kTileBytes);
-            for (int k = 0; k < 4; ++k)  // 32 bytes of k an instruction
-              tc::mma_e4m3<true>(tmem + buf * kWideCols, dx + 2 * k, dw + 2 * k, instruction, k > 0);
-            tc::mma_commit<true>(staging::smem_addr(&sm.empty[stage]));
-            tc::mma_commit<true>(staging::smem_addr(&sm.sum_full[buf]));
-          }
-          __syncwarp();
-          if (++stage == kWideStages) stage = 0, parity ^= 1;
-          if (++buf == 2) buf = 0, buf_parity ^= 1;
+      for (int i = buf; i < count; i += 2) {
+        if (!(ok = mbar_wait(&sm.sum_empty[buf], buf_parity, staging::kWaitPolls))) break;
+        if (!(ok = mbar_wait(&sm.full[stage], parity, staging::kWaitPolls))) break;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint32_t src = data + stage * kWideStageBytes;
+          const uint64_t dx = tc::tile_desc(src), dw = tc::tile_desc(src + kTileBytes);
+          for (int k = 0; k < 4; ++k)  // 32 bytes of k an instruction
+            tc::mma_e4m3(tmem + buf * kWideCols, dx + 2 * k, dw + 2 * k, instruction, k > 0);
+          tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
+          tc::mma_commit_both(staging::smem_addr(&sm.empty[stage]));
         }
+        __syncwarp();
+        stage += 2;
+        if (stage >= uint32_t(stages)) stage -= stages, parity ^= 1;
+        buf_parity ^= 1;
       }
       if (!ok && lane == 0) give_up(a.status, kStatusMatrixWait);
     }
   } else {  // sums
-    const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + half * 128;
+    tc::registers_up<kWideSumRegisters>();
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + part * kWideWarpCols;
     unsigned char* out = sm.out[warp];
+    float* scales = sm.scales[warp];
+    float next_x[8], next_w = 0.0f;  // scales of the 8 blocks to come
+    auto fetch = [&](const Tile& tile, int b0) {
+      const int b = b0 + lane % kScaleBlocks;
+      const int row0 = tile.row + int(rank) * kRows + quarter * 32 + lane / kScaleBlocks;
+      const int block = min((tile.n0 + part * kWideWarpCols) / kBlock, a.col_blocks - 1);
+      if (b >= a.blocks) return;
+      next_w = a.ws[(int64_t(tile.e) * a.col_blocks + block) * a.ldws + b];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        next_x[i] = a.xs[int64_t(min(row0 + 4 * i, a.tokens - 1)) * a.ldxs + b];
+    };
     uint32_t buf = 0, parity = 0;
     bool ok = true;
+    Tile tile;
+    if (pair < total) {
+      tile = Tile(table, a.nexperts, pair, 2 * kRows, kWideCols);
+      fetch(tile, 0);
+    }
     for (int t = pair; ok && t < total; t += pairs) {
-      const Tile tile(table, a.nexperts, t, 2 * kRows, kWideCols);
+      const Tile following(table, a.nexperts, min(t + pairs, total - 1), 2 * kRows, kWideCols);
       const int row0 = tile.row + int(rank) * kRows + quarter * 32;
-      const int col0 = tile.n0 + half * 128;
-      const float* xs = a.xs + int64_t(min(row0 + lane, a.tokens - 1)) * a.ldxs;
-      const float* ws =
-          a.ws + (int64_t(tile.e) * a.col_blocks + min(col0 / kBlock, a.col_blocks - 1)) * a.ldws;
-      uint64_t acc[64];
+      const int col0 = tile.n0 + part * kWideWarpCols;
+      uint64_t acc[kWideWarpCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float sx = xs[0], sw = ws[0];
+      for (int i = 0; i < kWideWarpCols / 2; ++i) acc[i] = 0;
       for (int b = 0; b < a.blocks; ++b) {
-        const uint32_t s = __float_as_uint(sx * sw);
-        const uint64_t scale = tc::pack2(s, s);
-        if (b + 1 < a.blocks) {
-          sx = xs[b + 1];
-          sw = ws[b + 1];
+        if (b % kScaleBlocks == 0) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            scales[(4 * i + lane / kScaleBlocks) * kScalePitch + lane % kScaleBlocks] =
+                next_x[i] * next_w;
+          __syncwarp();
+          const bool last = b + kScaleBlocks >= a.blocks;
+          fetch(last ? following : tile, last ? 0 : b + kScaleBlocks);
         }
-        if (!(ok = tc::wait_cluster(&sm.sum_full[buf], parity))) break;
+        const uint32_t s = __float_as_uint(scales[lane * kScalePitch + b % kScaleBlocks]);
+        const uint64_t scale = tc::pack2(s, s);
+        if (!(ok = mbar_wait(&sm.sum_full[buf], parity, staging::kWaitPolls))) break;
         tc::fence_after_sync();
         const uint32_t from = lanes + buf * kWideCols;
         uint32_t v[2][16];
         tc::tmem_load16(from, v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kWideWarpCols / 16; ++c) {
           tc::tmem_wait(v[c & 1]);
-          if (c < 7) tc::tmem_load16(from + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < kWideWarpCols / 16) tc::tmem_load16(from + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             acc[8 * c + i] =
@@ -270,7 +314,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::arrive_cluster(tc::in_cta(staging::smem_addr(&sm.sum_empty[buf]), 0));
+        if (lane == 0) staging::mbar_arrive(&sm.sum_empty[buf]);
         if (++buf == 2) buf = 0, parity ^= 1;
       }
       if (!ok) break;
@@ -279,7 +323,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       constexpr int kVec = 16 / int(sizeof(Y));
       Y* y = static_cast<Y*>(a.y);
 #pragma unroll
-      for (int round = 0; round < 128 / kChunk; ++round) {
+      for (int round = 0; round < kWideWarpCols / kChunk; ++round) {
 #pragma unroll
         for (int j = 0; j < kOutRow / 16; ++j) {
           __align__(16) Y vec[kVec];
@@ -318,13 +362,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         __syncwarp();
       }
+      tile = following;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusSumWait);
   }
   __syncwarp();
   tc::fence_before_sync();
   tc::cluster_sync();
-  if (warp == kWideSumWarps + 1) tc::tmem_free<true>(tmem, 512);
+  if (warp == kWideSumWarps + 1) tc::tmem_free(tmem, 512);
 }
 
 // ----------------------------------------------------------------------------- narrow
@@ -380,7 +425,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
     }
     tc::fence_barrier_init();
   }
-  if (warp == 5) tc::tmem_alloc<false>(&sm.tmem, S::kColumns);
+  if (warp == 5) tc::tmem_alloc(&sm.tmem, S::kColumns);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -394,7 +439,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
     uint32_t stage = 0, parity = 1;
     bool ok = true;
     for (int b = b0; b < b1; ++b) {
-      if (!(ok = tc::wait_cluster(&sm.empty[stage], parity))) break;
+      if (!(ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls))) break;
       if (lane == 0) {
         mbar_arrive_expect(&sm.full[stage], S::kStageBytes);
         const uint32_t bar = staging::smem_addr(&sm.full[stage]);
@@ -407,7 +452,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
     }
     // every matrix instruction has let go of its stage before this CTA may end
     for (int i = 0; ok && i < S::kStages; ++i) {
-      ok = tc::wait_cluster(&sm.empty[stage], parity);
+      ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls);
       if (++stage == S::kStages) stage = 0, parity ^= 1;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusLoadWait);
@@ -416,16 +461,16 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
     uint32_t stage = 0, parity = 0, buf = 0, buf_parity = 1;
     bool ok = true;
     for (int b = b0; b < b1; ++b) {
-      if (!(ok = tc::wait_cluster(&sm.sum_empty[buf], buf_parity))) break;
-      if (!(ok = tc::wait_cluster(&sm.full[stage], parity))) break;
+      if (!(ok = mbar_wait(&sm.sum_empty[buf], buf_parity, staging::kWaitPolls))) break;
+      if (!(ok = mbar_wait(&sm.full[stage], parity, staging::kWaitPolls))) break;
       tc::fence_after_sync();
       if (lane == 0) {
         const uint32_t src = staging::smem_addr(sm.stages[stage]);
         const uint64_t dw = tc::tile_desc(src), dx = tc::tile_desc(src + kTileBytes);
         for (int k = 0; k < 4; ++k)
-          tc::mma_e4m3<false>(tmem + buf * NT, dw + 2 * k, dx + 2 * k, instruction, k > 0);
-        tc::mma_commit<false>(staging::smem_addr(&sm.empty[stage]));
-        tc::mma_commit<false>(staging::smem_addr(&sm.sum_full[buf]));
+          tc::mma_e4m3(tmem + buf * NT, dw + 2 * k, dx + 2 * k, instruction, k > 0);
+        tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
+        tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
       }
       __syncwarp();
       if (++stage == S::kStages) stage = 0, parity ^= 1;
@@ -457,7 +502,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
       }
       if (b + 1 < b1) sw = ws[b + 1];
       __syncwarp();
-      if (!(ok = tc::wait_cluster(&sm.sum_full[buf], parity))) break;
+      if (!(ok = mbar_wait(&sm.sum_full[buf], parity, staging::kWaitPolls))) break;
       tc::fence_after_sync();
       const uint32_t from = lanes + buf * NT;
       uint32_t v[2][16];
@@ -518,7 +563,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 5) tc::tmem_free<false>(tmem, S::kColumns);
+  if (warp == 5) tc::tmem_free(tmem, S::kColumns);
 }
 
 // An inner size of zero: the rows of experts get zeros.
@@ -600,9 +645,11 @@ reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int sms, cudaStre
   // an expert's last tile may be short, so experts add at most one row of tiles each
   const int64_t most = a.ntiles * (cdiv(a.tokens, 2 * kRows) + (a.nexperts > 1 ? a.nexperts : 0));
   const int64_t pairs = most < sms / 2 ? most : sms / 2;
-  void* args[] = {&map_x, &map_w, &a};
+  const size_t at = wide_stages_at(ExpertTable::bytes(a.nexperts));
+  int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : kWideStages - 1;
+  void* args[] = {&map_x, &map_w, &a, &stages};
   return launch(reinterpret_cast<const void*>(wide_kernel<Y>), unsigned(2 * pairs), kWideThreads,
-                sizeof(WideSmem) + ExpertTable::bytes(a.nexperts), 2, stream, args);
+                at + size_t(stages) * kWideStageBytes, 2, stream, args);
 }
 
 template <int NT, typename Y>

@@ -1,14 +1,37 @@
 // sample.cu -- reshard_sample: one token a row of logits, with temperature, top-k,
 // top-p and min-p, from one given uniform number a row.
+//
+// A cluster of CTAs takes a row and keeps it in shared memory (a slice a CTA), so that
+// the row is read from HBM once however many questions are asked of it:
+//   1. the largest logit;
+//   2. the weights' sum, and for top-k and top-p a histogram of how far below the
+//      largest each token lies: counts and weights in 2048 bins of 1/128 in ln p;
+//   3. the bin in which the last kept token lies, from the histograms' sums; the tokens of
+//      that one bin are listed and ranked by (logit, index), which gives the last kept
+//      token exactly;
+//   4. the kept weights' sums, and the token whose running sum passes the target.
+// Weights are whole numbers (2^-40 of the largest), so sums are exact and neither the
+// order of atomics nor the split over warps and CTAs can change a result.
+#include <algorithm>
+
 #include "operators.cuh"
+#include "tensor_core.cuh"
 
 namespace rs {
 namespace {
 
 using namespace op;
+using staging::smem_addr;
+using tc::cluster_sync;
+using tc::in_cta;
 
-constexpr int kThreads = 1024;
-constexpr uint64_t kOne = uint64_t(1) << 40;  // weight of the most likely token
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;
+constexpr float kBinsPerNat = 128.0f;
+constexpr float kHistogramNats = kBins / kBinsPerNat;  // 16
+constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
 
 struct SampleArgs {
   const void* logits;
@@ -21,178 +44,642 @@ struct SampleArgs {
 
 // A logit as it is ranked: NaN as -inf, -0 as +0.
 __device__ __forceinline__ float clean(float l) { return l == l ? l + 0.0f : -INFINITY; }
-// Whole numbers in the order of the floats.
+// Whole numbers in the order of the floats, and back.
 __device__ __forceinline__ uint32_t key_of(float l) {
   const uint32_t b = __float_as_uint(l);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
-__device__ __forceinline__ float scaled(float l, float top, float inv) {
-  return l == top ? 0.0f : (l - top) * inv;
-}
-__device__ __forceinline__ float prob_of(float l, float top, float inv) {
-  return l == top ? 1.0f : l - top == -INFINITY ? 0.0f : expf((l - top) * inv);
-}
-__device__ __forceinline__ uint64_t weight_of(float e) {
-  return uint64_t(__float2ll_rn(e * float(kOne)));
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ uint64_t block_sum(uint64_t v, uint64_t* part) {
+// The row's scale: z = ln of a token's probability relative to the largest.
+struct Scale {
+  float top, inv;
+  __device__ float z(float l) const { return l == top ? 0.0f : __fmul_rn(__fsub_rn(l, top), inv); }
+  // exp(z); 0 where the difference is -inf
+  __device__ float e(float l) const {
+    const float d = __fsub_rn(l, top);
+    return l == top ? 1.0f : d == -INFINITY ? 0.0f : expf(__fmul_rn(d, inv));
+  }
+};
+
+// round(2^40 e), e in [0, 1], as high * 2^22 + low: adding 48 = 1.5 * 2^5 leaves e's
+// multiples of 2^-18 in the sum's low bits, adding 1.5 * 2^-17 to what is left those of
+// 2^-40 (without contraction, so that e is what is split); both halves of 256 weights add up in 32 bits.
+struct Weight {
+  int high, low;
+  __device__ explicit Weight(float e) {
+    const float a = __fadd_rn(e, 48.0f);
+    const float b = __fadd_rn(__fsub_rn(e, __fsub_rn(a, 48.0f)), 0x1.8p-17f);
+    high = int(__float_as_uint(a) - __float_as_uint(48.0f));
+    low = int(__float_as_uint(b) - __float_as_uint(0x1.8p-17f));
+  }
+  __device__ static uint64_t join(int high, int low) {
+    return uint64_t((int64_t(high) << 22) + low);
+  }
+  __device__ uint64_t value() const { return join(high, low); }
+};
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-  for (int i = 0; i < kThreads / 32; ++i) v += part[i];
   return v;
 }
-// Sum over the threads before this one.
-__device__ uint64_t block_before(uint64_t v, uint64_t* part) {
-  uint64_t run = v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {  // inclusive
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t w = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += w;
+    const uint64_t w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
   }
-  __syncthreads();
-  if (lane == 31) part[warp] = run;
-  __syncthreads();
-  for (int i = 0; i < warp; ++i) run += part[i];
-  return run - v;
+  return v;
 }
 
-// One CTA a row; the row is read again for every question asked of it.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a) {
-  __shared__ uint64_t part[kThreads / 32];
-  __shared__ float tops[kThreads / 32];
-  __shared__ int32_t found;
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-  const int vocab = int(a.vocab), tid = threadIdx.x;
-  // every thread owns consecutive tokens
-  const int each = (vocab + kThreads - 1) / kThreads;
-  const int i0 = min(vocab, tid * each), i1 = min(vocab, i0 + each);
+__device__ __forceinline__ void store_cluster(T* at, uint32_t rank, T value) {
+  const uint32_t to = in_cta(smem_addr(at), rank);
+  if (sizeof(T) == 8)
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(uint64_t(value)) : "memory");
+  else
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(uint32_t(value)) : "memory");
+}
+__device__ __forceinline__ uint4 load_cluster16(const void* at, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(in_cta(smem_addr(at), rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add_cluster(uint32_t* at, uint32_t rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "r"(in_cta(smem_addr(at), rank)), "r"(v)
+               : "memory");
+  return old;
+}
 
+// The last kept token: those with a larger key are kept, and with this key those up to
+// this index.
+struct Cut {
+  uint32_t key, index;
+};
+
+enum Step : uint32_t { kList, kHistogram, kBisect, kCut };
+// What every CTA does next, as the first one has decided.
+struct Order {
+  uint32_t step, bin, from;  // kList: that bin of the histogram from `from` nats on
+  Cut cut;
+};
+
+constexpr int kListMost = 3072;  // listed tokens: 8 bytes each in the histogram's place
+
+struct SampleSmem {
+  union {
+    struct {
+      alignas(16) uint64_t mass[kBins];
+      alignas(16) uint32_t count[kBins];
+    };
+    struct {
+      uint32_t key[kListMost], index[kListMost];
+    };
+  };
+  uint64_t warp_mass[kWarps];
+  uint64_t cta_mass[2][kMaxCluster];   // written by the other CTAs: sums of a pass,
+  uint32_t cta_count[2][kMaxCluster];  // counts (or lowest index of the largest logit)
+  uint32_t cta_top[kMaxCluster];
+  uint64_t scan_mass[kWarps];
+  uint32_t scan_count[kWarps];
+  uint32_t listed;
+  Order order;
+  uint64_t best_mass;
+  uint32_t best;
+};
+static_assert(sizeof(uint32_t) * 2 * kListMost <= 12 * kBins, "the list lies in the histogram");
+
+// This CTA's slice of a row, in granules of 16 aligned bytes; what lies outside the row
+// in the first and last granule reads as -inf.
+template <typename T, bool RESIDENT>
+struct Slice {
+  static constexpr int kPer = 16 / int(sizeof(T));
+  const T* row;
+  unsigned char* smem;
+  int vocab, skew;  // elements of the first granule that lie before the row
+  int g0, g1;       // granules of the CTA
+  int w0, w1;       // granules of the warp
+
+  __device__ int first(int g) const { return g * kPer - skew; }  // index of its first element
+  __device__ uint4 fetch(int g) const {
+    const int i = first(g);
+    if (i >= 0 && i + kPer <= vocab) return __ldg(reinterpret_cast<const uint4*>(row + i));
+    __align__(16) T v[kPer];
+    for (int j = 0; j < kPer; ++j)
+      v[j] = i + j >= 0 && i + j < vocab ? row[i + j] : from_float<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(v);
+  }
+  __device__ void keep(int g, const uint4& v) const {
+    if (RESIDENT) *reinterpret_cast<uint4*>(smem + size_t(g - g0) * 16) = v;
+  }
+  __device__ uint4 granule(int g) const {
+    return RESIDENT ? *reinterpret_cast<const uint4*>(smem + size_t(g - g0) * 16) : fetch(g);
+  }
+  __device__ static float at(const uint4& v, int j) {
+    return clean(to_float(reinterpret_cast<const T*>(&v)[j]));
+  }
+  // visit(index, logit) for every element of the warp's part, a lane at a time its own
+  template <typename F>
+  __device__ void each(F&& visit) const {
+    for (int g = w0 + int(threadIdx.x & 31); g < w1; g += 32) {
+      const uint4 v = granule(g);
+      const int i = first(g);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) visit(i + j, at(v, j));
+    }
+  }
+};
+
+template <typename T, bool RESIDENT>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  SampleSmem& sm = *reinterpret_cast<SampleSmem*>(dynamic);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t ctas;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const uint32_t rank = tc::cluster_rank();
+  const int64_t r = blockIdx.x / ctas;
+
+  tc::cluster_arrive();  // every CTA of the cluster runs before another one writes to it
+
+  Slice<T, RESIDENT> s;
+  s.row = static_cast<const T*>(a.logits) + r * a.ld;
+  s.smem = dynamic + (sizeof(SampleSmem) + 15) / 16 * 16;
+  s.vocab = int(a.vocab);
+  s.skew = int(reinterpret_cast<uintptr_t>(s.row) % 16 / sizeof(T));
+  const int granules = (s.vocab + s.skew + s.kPer - 1) / s.kPer;
+  s.g0 = int(int64_t(granules) * rank / ctas);
+  s.g1 = int(int64_t(granules) * (rank + 1) / ctas);
+  const int per_warp = (s.g1 - s.g0 + kWarps - 1) / kWarps;
+  s.w0 = min(s.g1, s.g0 + warp * per_warp);
+  s.w1 = min(s.g1, s.w0 + per_warp);
+
+  const float temperature = a.temperature ? a.temperature[r] : 1.0f;
+  const bool greedy = !(temperature > 0.0f);
+  float p = a.top_p ? a.top_p[r] : 1.0f;
+  int k = a.top_k ? a.top_k[r] : 0;
+  const float floor_e = fminf(a.min_p ? a.min_p[r] : 0.0f, 1.0f);
+  const float u = fmaxf(a.u[r], 0.0f);  // NaN: 0
+  if (!(p > 0.0f)) k = 1, p = 1.0f;     // only the first
+  const bool by_count = !greedy && k > 0 && k < s.vocab;
+  const bool by_mass = !greedy && p < 1.0f;
+
+  // 1. the slice, and the largest logit
+  if (by_count || by_mass)
+    for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
   float top = -INFINITY;
-  for (int i = tid; i < vocab; i += kThreads) top = fmaxf(top, clean(to_float(x[i])));
-  top = warp_max(top);
-  if ((tid & 31) == 0) tops[tid >> 5] = top;
-  if (tid == 0) found = vocab;
+  for (int g = s.w0 + lane; g < s.w1; g += 32) {
+    const uint4 v = s.fetch(g);
+    s.keep(g, v);
+#pragma unroll
+    for (int j = 0; j < s.kPer; ++j) top = fmaxf(top, to_float(reinterpret_cast<const T*>(&v)[j]));
+  }
+  top = warp_max(top + 0.0f);  // a NaN loses against any number
+  if (lane == 0) sm.scan_count[warp] = key_of(top);
   __syncthreads();
-  for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, tops[i]);
-  if (top == -INFINITY) {
-    if (tid == 0) {
-      a.token[row] = -1;
-      if (a.logprob) a.logprob[row] = -INFINITY;
+  tc::cluster_wait();
+  if (tid < int(ctas)) {
+    uint32_t most = 0;
+    for (int i = 0; i < kWarps; ++i) most = max(most, sm.scan_count[i]);
+    store_cluster(&sm.cta_top[rank], tid, most);
+  }
+  cluster_sync();
+  uint32_t top_key = 0;
+  for (uint32_t i = 0; i < ctas; ++i) top_key = max(top_key, sm.cta_top[i]);
+  Scale scale;
+  scale.top = logit_of(top_key);
+  scale.inv = greedy ? 1.0f : 1.0f / temperature;
+  if (scale.top == -INFINITY) {
+    if (rank == 0 && tid == 0) {
+      a.token[r] = -1;
+      if (a.logprob) a.logprob[r] = -INFINITY;
     }
     return;
   }
-  const float temp = a.temperature ? a.temperature[row] : 1.0f;
-  const bool greedy = !(temp > 0.0f);
-  const float inv = greedy ? 1.0f : 1.0f / temp;
-  auto weight = [&](float l) { return weight_of(prob_of(l, top, inv)); };
-  uint64_t total = 0;
-  for (int i = tid; i < vocab; i += kThreads) total += weight(clean(to_float(x[i])));
-  total = block_sum(total, part);
 
+  // 2. weights, and the histogram from `from` nats below the largest on
+  auto bin_of = [&](float l, float from) {  // not below 0 and not above kBins
+    const float d = __fmul_rn(__fsub_rn(-scale.z(l), from), kBinsPerNat);
+    return d < float(kBins) ? (d >= 0.0f ? int(d) : -1) : kBins;
+  };
+  auto tally = [&](float l, uint64_t w, float from) {
+    const int bin = bin_of(l, from);
+    if (bin >= 0 && bin < kBins) {
+      atomicAdd(&sm.count[bin], 1u);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[bin]), (unsigned long long)w);
+    }
+  };
+  int high = 0, low = 0;
+  uint32_t lowest = 0xffffffffu;
   if (greedy) {
-    for (int i = i0; i < i1; ++i)
-      if (clean(to_float(x[i])) == top) {
-        atomicMin(&found, i);
-        break;
-      }
+    s.each([&](int i, float l) {
+      const Weight w(scale.e(l));
+      high += w.high, low += w.low;
+      if (l == scale.top) lowest = min(lowest, uint32_t(i));
+    });
+  } else if (by_count || by_mass) {
+    s.each([&](int, float l) {
+      const Weight w(scale.e(l));
+      high += w.high, low += w.low;
+      tally(l, w.value(), 0.0f);
+    });
   } else {
-    // kept so far: keys above `cut`, and the first `ties` tokens with that key
-    uint32_t cut = 0;
-    uint64_t ties = uint64_t(vocab);
-    auto sum_from = [&](uint32_t key, bool mass) {
-      uint64_t v = 0;
-      for (int i = tid; i < vocab; i += kThreads) {
-        const float l = clean(to_float(x[i]));
-        if (key_of(l) >= key) v += mass ? weight(l) : 1;
-      }
-      return block_sum(v, part);
-    };
-    const int k = a.top_k ? a.top_k[row] : 0;
-    if (k > 0 && k < vocab) {
-      for (int b = 31; b >= 0; --b)
-        if (sum_from(cut | (1u << b), false) >= uint64_t(k)) cut |= 1u << b;
-      ties = uint64_t(k) - (cut == 0xffffffffu ? 0 : sum_from(cut + 1, false));
+    s.each([&](int, float l) {
+      const float e = scale.e(l);
+      const Weight w(e);
+      high += w.high, low += w.low;
+    });
+  }
+  // Sums over the warp, the CTA and (slot) the cluster; returns the cluster's.
+  uint32_t slot = 0;
+  auto publish = [&](uint64_t mass, uint32_t count, bool lowest_of) {
+    mass = warp_sum64(mass);
+    for (int o = 16; o; o >>= 1) {
+      const uint32_t c = __shfl_xor_sync(0xffffffffu, count, o);
+      count = lowest_of ? min(count, c) : count + c;
     }
-    auto tie_weight = [&](uint32_t key) {
-      const float l = __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
-      return key == 0 ? 0 : weight(l);
-    };
-    const float p = a.top_p ? a.top_p[row] : 1.0f;
-    if (!(p >= 1.0f)) {
-      // the weights of the kept tokens with at least this key
-      auto mass_from = [&](uint32_t key) {
-        if (key <= cut && ties < uint64_t(vocab))
-          return sum_from(cut + 1, true) + ties * tie_weight(cut);
-        return sum_from(key, true);
-      };
-      const double mass = double(p) * double(mass_from(0));
-      uint32_t pcut = 0;
-      for (int b = 31; b >= 0; --b)
-        if (double(mass_from(pcut | (1u << b))) >= mass) pcut |= 1u << b;
-      const uint32_t first = key_of(top);
-      if (!(mass > 0.0) || pcut > first) pcut = first;
-      const uint64_t above = pcut == first ? 0 : mass_from(pcut + 1);
-      const uint64_t w = tie_weight(pcut);
-      uint64_t most = pcut == cut ? ties : sum_from(pcut, false) - sum_from(pcut + 1, false);
-      uint64_t lo = pcut == first ? 1 : 0, hi = most;  // ties kept: the largest t with
-      while (lo < hi) {                                // double(above + (t - 1) w) < mass
-        const uint64_t t = (lo + hi + 1) / 2;
-        if (double(above + (t - 1) * w) < mass) lo = t;
-        else hi = t - 1;
+    __syncthreads();
+    if (lane == 0) sm.warp_mass[warp] = mass, sm.scan_count[warp] = count;
+    __syncthreads();
+    if (tid < int(ctas)) {
+      uint64_t m = 0;
+      uint32_t c = lowest_of ? 0xffffffffu : 0u;
+      for (int i = 0; i < kWarps; ++i) {
+        m += sm.warp_mass[i];
+        c = lowest_of ? min(c, sm.scan_count[i]) : c + sm.scan_count[i];
       }
-      cut = pcut;
-      ties = lo;
+      store_cluster(&sm.cta_mass[slot][rank], tid, m);
+      store_cluster(&sm.cta_count[slot][rank], tid, c);
     }
-    const float floor_p = fminf(a.min_p ? a.min_p[row] : 0.0f, 1.0f);
-    uint64_t tied = 0;
-    for (int i = i0; i < i1; ++i) tied += key_of(clean(to_float(x[i]))) == cut;
-    const uint64_t tied_before = block_before(tied, part);
-    auto walk = [&](auto&& visit) {
-      uint64_t seen = tied_before;
-      for (int i = i0; i < i1; ++i) {
-        const float l = clean(to_float(x[i]));
-        const uint32_t key = key_of(l);
-        const bool in = key > cut || (key == cut && seen < ties);
-        seen += key == cut;
-        const float e = prob_of(l, top, inv);
-        if (in && !(e < floor_p)) {
-          if (visit(i, weight_of(e))) return;
+    cluster_sync();
+  };
+  publish(Weight::join(high, low), lowest, true);
+  uint64_t total = 0;
+  for (uint32_t i = 0; i < ctas; ++i) total += sm.cta_mass[slot][i];
+  auto answer = [&](int i, float l) {
+    a.token[r] = i;
+    if (a.logprob)
+      a.logprob[r] = scale.z(l) - log1pf(float(double(total - kOne) / double(kOne)));
+  };
+  if (greedy) {
+    if (rank == 0 && tid == 0) {
+      uint32_t i = 0xffffffffu;
+      for (uint32_t c = 0; c < ctas; ++c) i = min(i, sm.cta_count[slot][c]);
+      answer(int(i), scale.top);
+    }
+    return;
+  }
+
+  // 3. the last kept token
+  Cut cut = {0, 0xffffffffu};
+  if (by_count || by_mass) {
+    // sums over the cluster of what `of(index, logit)` gives, for the bisection
+    auto sums = [&](auto&& of, uint64_t* mass, uint32_t* count) {
+      int h = 0, l = 0;
+      uint32_t c = 0;
+      s.each([&](int i, float v) {
+        if (!of(i, key_of(v))) return;
+        const Weight w(scale.e(v));
+        h += w.high, l += w.low, ++c;
+      });
+      slot ^= 1;
+      publish(Weight::join(h, l), c, false);
+      *mass = 0, *count = 0;
+      for (uint32_t i = 0; i < ctas; ++i)
+        *mass += sm.cta_mass[slot][i], *count += sm.cta_count[slot][i];
+    };
+    // The first CTA's view: the histograms' sums (four bins a thread) and what lies before.
+    uint32_t counts[4] = {}, count_before = 0;
+    uint64_t masses[4] = {}, mass_before = 0;
+    uint32_t skipped_count = 0;   // tokens above the histogram's range
+    uint64_t skipped_mass = 0;
+    float from = 0.0f;
+    bool count_open = by_count;   // top-k still to be resolved, else top-p
+    uint64_t kept_mass = total;   // of the tokens that top-k keeps
+    auto gather = [&] {
+      for (int j = 0; j < 4; ++j) counts[j] = 0, masses[j] = 0;
+      for (uint32_t c = 0; c < ctas; ++c) {
+        const uint4 n = load_cluster16(&sm.count[4 * tid], c);
+        const uint4 m0 = load_cluster16(&sm.mass[4 * tid], c);
+        const uint4 m1 = load_cluster16(&sm.mass[4 * tid + 2], c);
+        counts[0] += n.x, counts[1] += n.y, counts[2] += n.z, counts[3] += n.w;
+        masses[0] += m0.x | uint64_t(m0.y) << 32, masses[1] += m0.z | uint64_t(m0.w) << 32;
+        masses[2] += m1.x | uint64_t(m1.y) << 32, masses[3] += m1.z | uint64_t(m1.w) << 32;
+      }
+      const uint32_t cn = counts[0] + counts[1] + counts[2] + counts[3];
+      const uint64_t mn = masses[0] + masses[1] + masses[2] + masses[3];
+      uint64_t ci = warp_scan64(cn, lane), mi = warp_scan64(mn, lane);
+      __syncthreads();
+      if (lane == 31) sm.scan_count[warp] = uint32_t(ci), sm.scan_mass[warp] = mi;
+      __syncthreads();
+      count_before = skipped_count + uint32_t(ci) - cn;
+      mass_before = skipped_mass + mi - mn;
+      for (int i = 0; i < warp; ++i)
+        count_before += sm.scan_count[i], mass_before += sm.scan_mass[i];
+    };
+    // Orders the bin in which the last kept token lies to be listed.
+    auto choose = [&] {
+      if (tid == 0) sm.order.step = kHistogram;
+      __syncthreads();
+      const double mass = double(p) * double(kept_mass);
+      uint32_t c = count_before;
+      uint64_t m = mass_before;
+      for (int j = 0; j < 4; ++j) {
+        const bool inside = count_open ? c < uint32_t(k) && c + counts[j] >= uint32_t(k)
+                                       : double(m) < mass && double(m + masses[j]) >= mass;
+        if (inside) {
+          sm.order.step = kList;
+          sm.order.bin = 4 * tid + j;
+          sm.scan_count[0] = c;
+          sm.scan_mass[0] = m;
+        }
+        c += counts[j], m += masses[j];
+      }
+      if (tid == kThreads - 1) sm.scan_count[1] = c, sm.scan_mass[1] = m;
+      __syncthreads();
+    };
+    auto send = [&] {  // sm.order to every CTA
+      __syncthreads();
+      if (tid < int(ctas) && tid > 0) {
+        store_cluster(&sm.order.step, tid, sm.order.step);
+        store_cluster(&sm.order.bin, tid, sm.order.bin);
+        store_cluster(&sm.order.from, tid, sm.order.from);
+        store_cluster(&sm.order.cut.key, tid, sm.order.cut.key);
+        store_cluster(&sm.order.cut.index, tid, sm.order.cut.index);
+      }
+    };
+    uint32_t bin_count = 0;
+    uint64_t bin_mass = 0;
+    auto decide = [&] {
+      choose();
+      if (sm.order.step == kHistogram) {
+        // beyond this histogram: the next 16 nats; beyond 32 every weight is 0
+        skipped_count = sm.scan_count[1], skipped_mass = sm.scan_mass[1];
+        if (from > 0.0f) {
+          if (count_open && by_mass) {
+            count_open = false;
+            from = 0.0f, skipped_count = 0, skipped_mass = 0;
+          } else {
+            __syncthreads();
+            if (tid == 0) sm.order.step = kCut, sm.order.cut = {0, 0xffffffffu};
+            return;
+          }
+        } else {
+          from = kHistogramNats;
+        }
+        __syncthreads();
+        if (tid == 0) sm.order.from = uint32_t(from);
+      } else {
+        bin_count = sm.scan_count[0];
+        bin_mass = sm.scan_mass[0];
+        __syncthreads();
+        if (tid == 0) sm.order.from = uint32_t(from), sm.listed = 0;
+      }
+    };
+    // Ranks the listed tokens by (logit, index) and takes the last kept one.
+    auto resolve = [&] {
+      const uint32_t n = sm.listed;
+      if (n > uint32_t(kListMost)) {
+        __syncthreads();
+        if (tid == 0) sm.order.step = kBisect;
+        return;
+      }
+      const double mass = double(p) * double(kept_mass);
+      for (uint32_t i = tid; i < n; i += kThreads) {
+        const uint32_t key = sm.key[i], index = sm.index[i];
+        uint32_t before = bin_count;
+        uint64_t m = bin_mass;
+        uint32_t last_key = key;
+        uint64_t w = Weight(scale.e(logit_of(key))).value();
+        const uint64_t own = w;
+        for (uint32_t j = 0; j < n; ++j) {
+          const uint32_t kj = sm.key[j];
+          if (kj > key || (kj == key && sm.index[j] < index)) {
+            if (kj != last_key) w = Weight(scale.e(logit_of(kj))).value(), last_key = kj;
+            ++before, m += w;
+          }
+        }
+        const bool last = count_open ? before + 1 == uint32_t(k)
+                                     : double(m) < mass && double(m + own) >= mass;
+        if (last) {
+          sm.order.cut = {key, index};
+          sm.best_mass = m + own;
         }
       }
+      __syncthreads();
+      if (count_open && by_mass) {  // top-p among what top-k keeps
+        kept_mass = sm.best_mass;
+        count_open = false;
+        cut = sm.order.cut;
+        __syncthreads();
+        if (tid == 0) sm.order.step = kHistogram;  // decided below
+      } else if (tid == 0) {
+        sm.order.step = kCut;
+      }
     };
-    uint64_t mine = 0;
-    walk([&](int, uint64_t w) {
-      mine += w;
-      return false;
-    });
-    uint64_t run = block_before(mine, part);
-    const uint64_t all = block_sum(mine, part);
-    const double target = double(fmaxf(a.u[row], 0.0f)) * double(all);
-    // the first token at which the sum passes the target; if none does, the last one
-    // with a weight
-    if (double(run + mine) > target || (run + mine == all && mine > 0)) {
-      int at = vocab;
-      walk([&](int i, uint64_t w) {
-        run += w;
-        if (w > 0) at = i;
-        return double(run) > target;
-      });
-      atomicMin(&found, at);
+
+    if (rank == 0) {
+      gather();
+      decide();
+      send();
+    }
+    for (;;) {
+      cluster_sync();
+      const Order order = sm.order;
+      if (order.step == kCut || order.step == kBisect) break;
+      const float begin = float(order.from);
+      if (order.step == kHistogram) {
+        for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
+        __syncthreads();
+        s.each([&](int, float l) { tally(l, Weight(scale.e(l)).value(), begin); });
+        cluster_sync();
+        if (rank == 0) {
+          gather();
+          decide();
+          send();
+        }
+      } else {
+        s.each([&](int i, float l) {
+          if (bin_of(l, begin) != int(order.bin)) return;
+          const uint32_t at = add_cluster(&sm.listed, 0, 1);
+          if (at >= uint32_t(kListMost)) return;
+          store_cluster(&sm.key[at], 0, key_of(l));
+          store_cluster(&sm.index[at], 0, uint32_t(i));
+        });
+        cluster_sync();
+        if (rank == 0) {
+          const bool count_was_open = count_open;
+          resolve();
+          __syncthreads();
+          if (sm.order.step == kHistogram && count_was_open) {
+            // top-p: its bin is in the histogram that the registers still hold, or above it
+            if (from == 0.0f) {
+              decide();
+            } else {
+              from = 0.0f, skipped_count = 0, skipped_mass = 0;
+              if (tid == 0) sm.order.from = 0;
+            }
+          }
+          send();
+        }
+      }
+    }
+    const Order order = sm.order;
+    if (order.step == kCut) {
+      cut = order.cut;
+    } else {
+      // Too many tokens in one bin: the cut's key by bisection over its bits, then its
+      // index, every CTA over its slice.
+      uint64_t mass;
+      uint32_t count;
+      cut = {0, 0xffffffffu};
+      auto last_index = [&](uint32_t key, uint32_t ties) {  // of the first `ties` with this key
+        uint32_t lo = 0, hi = uint32_t(s.vocab - 1);
+        while (lo < hi) {
+          const uint32_t mid = (lo + hi) / 2;
+          sums([&](int i, uint32_t q) { return q == key && uint32_t(i) <= mid; }, &mass, &count);
+          if (count >= ties) hi = mid;
+          else lo = mid + 1;
+        }
+        return lo;
+      };
+      auto kept = [&](int i, uint32_t q) {
+        return q > cut.key || (q == cut.key && uint32_t(i) <= cut.index);
+      };
+      uint64_t all = total;
+      if (by_count) {
+        uint32_t key = 0;
+        for (int b = 31; b >= 0; --b) {
+          sums([&](int i, uint32_t q) { return q >= (key | 1u << b) && i >= 0 && i < s.vocab; },
+               &mass, &count);
+          if (count >= uint32_t(k)) key |= 1u << b;
+        }
+        sums([&](int i, uint32_t q) { return q > key && i >= 0 && i < s.vocab; }, &mass, &count);
+        const uint64_t above = mass;
+        const uint32_t ties = uint32_t(k) - count;
+        cut = {key, last_index(key, ties)};
+        all = above + ties * Weight(scale.e(logit_of(key))).value();
+      }
+      if (by_mass) {
+        const double target = double(p) * double(all);
+        uint32_t key = 0;
+        for (int b = 31; b >= 0; --b) {
+          sums([&](int i, uint32_t q) { return q >= (key | 1u << b) && kept(i, q); }, &mass, &count);
+          if (double(mass) >= target) key |= 1u << b;
+        }
+        sums([&](int i, uint32_t q) { return q > key && kept(i, q); }, &mass, &count);
+        const uint64_t above = mass, w = Weight(scale.e(logit_of(key))).value();
+        sums([&](int i, uint32_t q) { return q == key && kept(i, q); }, &mass, &count);
+        uint32_t lo = 1, hi = count;  // ties kept: the most t with above + (t - 1) w < target
+        while (lo < hi) {
+          const uint32_t t = lo + (hi - lo + 1) / 2;
+          if (double(above + (t - 1) * w) < target) lo = t;
+          else hi = t - 1;
+        }
+        cut = {key, last_index(key, lo)};
+      }
     }
   }
-  __syncthreads();
-  if (tid == 0) {
-    a.token[row] = found;
-    if (a.logprob)
-      a.logprob[row] = scaled(clean(to_float(x[found])), top, inv) -
-                       log1pf(float(double(total - kOne) / double(kOne)));
+
+  // 4. the token
+  const bool filtered = by_count || by_mass || floor_e > 0.0f;
+  auto weight = [&](int i, float l) {  // 0 for a token that is not kept
+    const uint32_t key = key_of(l);
+    if (key < cut.key || (key == cut.key && uint32_t(i) > cut.index)) return Weight(0.0f);
+    const float e = scale.e(l);
+    return Weight(e < floor_e ? 0.0f : e);
+  };
+  uint64_t all = total;
+  if (filtered) {
+    int h = 0, l = 0;
+    s.each([&](int i, float v) {
+      const Weight w = weight(i, v);
+      h += w.high, l += w.low;
+    });
+    slot ^= 1;
+    publish(Weight::join(h, l), 0, false);
+    all = 0;
+    for (uint32_t i = 0; i < ctas; ++i) all += sm.cta_mass[slot][i];
   }
+  const double target = double(u) * double(all);
+  // the first token at which the sum passes the target; none does for u >= 1: the last
+  // one with a weight, at which the sum is complete
+  auto passes = [&](uint64_t sum) { return double(sum) > target || sum == all; };
+  uint64_t run = 0;
+  for (uint32_t i = 0; i < rank; ++i) run += sm.cta_mass[slot][i];
+  for (int i = 0; i < warp; ++i) run += sm.warp_mass[i];
+  if (passes(run) || !passes(run + sm.warp_mass[warp])) return;
+  for (int g = s.w0 + lane; ; g += 32) {  // ends: the warp's sum passes
+    uint64_t mine = 0;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (g < s.w1) {
+      v = s.granule(g);
+      for (int j = 0; j < s.kPer; ++j) mine += weight(s.first(g) + j, s.at(v, j)).value();
+    }
+    const uint64_t upto = run + warp_scan64(mine, lane);
+    const uint32_t found = __ballot_sync(0xffffffffu, passes(upto));
+    if (found) {
+      if (lane == __ffs(int(found)) - 1) {
+        uint64_t sum = upto - mine;
+        for (int j = 0; j < s.kPer; ++j) {
+          const int i = s.first(g) + j;
+          const float l = s.at(v, j);
+          sum += weight(i, l).value();
+          if (passes(sum)) {
+            answer(i, l);
+            break;
+          }
+        }
+      }
+      return;
+    }
+    run = __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
+template <typename T>
+reshard_status_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
+  const int64_t bytes = (a.vocab + 16 / int64_t(sizeof(T))) * int64_t(sizeof(T));
+  // CTAs a row: slices of at most 32 KiB; smaller ones while SMs would stay without a CTA
+  int ctas = 1;
+  while (ctas < kMaxCluster && (bytes > ctas * 32768 || (rows * ctas < sms && bytes > ctas * 4096)))
+    ctas *= 2;
+  const int64_t slice = (cdiv(cdiv(bytes, 16) + 1, ctas) + 1) * 16;
+  const size_t fixed = (sizeof(SampleSmem) + 15) / 16 * 16;
+  const bool resident = fixed + size_t(slice) <= 227 * 1024;
+  const size_t smem = fixed + (resident ? size_t(slice) : 0);
+  const void* kernel = resident ? reinterpret_cast<const void*>(sample_kernel<T, true>)
+                                : reinterpret_cast<const void*>(sample_kernel<T, false>);
+  ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (ce == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(rows * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(ctas), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<SampleArgs*>(&a)};
+    ce = cudaLaunchKernelExC(&cfg, kernel, args);
+  }
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("reshard_sample: ") + cudaGetErrorString(ce));
+  return RESHARD_OK;
 }
 
 }  // namespace
@@ -210,7 +697,7 @@ extern "C" reshard_status_t reshard_sample(const void* logits, int32_t dtype, in
     return fail(RESHARD_ERR_INVALID_ARG, "dtype must be BF16, FP16 or FP32");
   if (rows < 0 || vocab < 0) return fail(RESHARD_ERR_INVALID_ARG, "negative size");
   if (vocab > RESHARD_MAX_VOCAB) return fail(RESHARD_ERR_UNSUPPORTED, "vocabulary too large");
-  if (rows >= int64_t(1) << 31) return fail(RESHARD_ERR_UNSUPPORTED, "2^31 rows or more");
+  if (rows >= int64_t(1) << 28) return fail(RESHARD_ERR_UNSUPPORTED, "2^28 rows or more");
   if (rows == 0 || vocab == 0) return RESHARD_OK;
   if (ld < vocab) return fail(RESHARD_ERR_INVALID_ARG, "row pitch smaller than a row");
   if (!logits || !u || !token) return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
@@ -220,8 +707,6 @@ extern "C" reshard_status_t reshard_sample(const void* logits, int32_t dtype, in
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
   rs::SampleArgs a = {logits, vocab, ld, temperature, top_p, min_p, u, top_k, token, logprob};
   return rs::op::by_dtype(dtype, [&](auto t) {
-    rs::sample_kernel<decltype(t)>
-        <<<unsigned(rows), rs::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return rs::op::launched("reshard_sample");
+    return rs::launch_sample<decltype(t)>(a, rows, static_cast<cudaStream_t>(stream));
   });
 }

@@ -22,6 +22,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// cluster_sync() in two halves; what a thread did before its arrival is not published.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // The address of `addr` (a shared address of this CTA) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -37,23 +44,6 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
 __device__ __forceinline__ void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// As staging::mbar_wait, for barriers that other CTAs of the cluster arrive at.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < staging::kWaitPolls; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
-        "selp.u32 %0, 1, 0, p; }"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
-  return false;
-}
 
 // ---------------------------------------------------------------------------- TMA loads
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -68,13 +58,13 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// The same inside a CTA pair: `bar` may be the other CTA's.
-__device__ __forceinline__ void load_box_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+// The same to that place of both CTAs of a cluster of two; the bytes count on each one's `bar`.
+__device__ __forceinline__ void load_box_both(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                               int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(uint16_t(3))
       : "memory");
 }
 
@@ -89,62 +79,39 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
 __host__ __device__ constexpr uint32_t e4m3_instruction(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
-// PAIR: one instruction for the tensor cores of both CTAs of a pair (cta_group::2).
-template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t instruction,
                                          bool add) {
-  if (PAIR)
-    asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0; "
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(instruction), "r"(uint32_t(add))
-        : "memory");
-  else
-    asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0; "
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(instruction), "r"(uint32_t(add))
-        : "memory");
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(instruction), "r"(uint32_t(add))
+      : "memory");
 }
-// One arrival at `bar` (PAIR: at that barrier of both CTAs) once the matrix instructions
-// issued so far are done.
-template <bool PAIR>
+// One arrival at `bar` once the matrix instructions issued so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  if (PAIR)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(bar),
-        "h"(uint16_t(3))
-        : "memory");
-  else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+// The same at that barrier of both CTAs of a cluster of two.
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(uint16_t(3))
+      : "memory");
 }
 
 // ------------------------------------------------------------------------- tensor memory
-// By one whole warp (PAIR: of each CTA of the pair); the address goes to *slot.
-template <bool PAIR>
+// By one whole warp; the address goes to *slot.
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t columns) {
-  if (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(slot)),
-                 "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(slot)),
-                 "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(slot)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
-template <bool PAIR>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-  if (PAIR)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
-  else
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 // 16 columns of this warp's 32 lanes, a lane a thread; complete after tmem_wait().
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
@@ -170,6 +137,17 @@ __device__ __forceinline__ void fence_before_sync() {
 }
 __device__ __forceinline__ void fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// ------------------------------------------------------------- shares of the register file
+// By every warp of a warpgroup (four warps from a multiple of four).
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // -------------------------------------------------------------------- packed float32 pairs

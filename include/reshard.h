@@ -854,7 +854,7 @@ reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const float* xs,
  * top_k, top_p, min_p: [rows] in device memory, each may be NULL (1, all, 1, 0).
  * token [rows]; logprob [rows] or NULL.
  * Errors: INVALID_ARG (null pointer, dtype, negative size, pitch too small),
- * UNSUPPORTED (vocab > RESHARD_MAX_VOCAB, 2^31 rows or more), CUDA.
+ * UNSUPPORTED (vocab > RESHARD_MAX_VOCAB, 2^28 rows or more), CUDA.
  */
 reshard_status_t reshard_sample(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                                 int64_t ld, const float* temperature, const int32_t* top_k,
