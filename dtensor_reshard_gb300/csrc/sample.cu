@@ -5,7 +5,7 @@
 // the row is read from HBM once however many questions are asked of it:
 //   1. the largest logit;
 //   2. the weights' sum, and for top-k and top-p a histogram of how far below the
-//      largest each token lies: counts and weights in 2048 bins of 1/128 in ln p;
+//      largest each token lies: counts and weights in 1024 bins of 1/64 in ln p;
 //   3. the bin in which the last kept token lies, from the histograms' sums; the tokens of
 //      that one bin are listed and ranked by (logit, index), which gives the last kept
 //      token exactly;
@@ -25,12 +25,11 @@ using staging::smem_addr;
 using tc::cluster_sync;
 using tc::in_cta;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
-constexpr float kBinsPerNat = 128.0f;
-constexpr float kHistogramNats = kBins / kBinsPerNat;  // 16
+constexpr int kBins = 1024;
+constexpr float kBinsPerNat = 64.0f;  // a histogram covers 16 nats
 constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
 
 struct SampleArgs {
@@ -53,33 +52,78 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// The row's scale: z = ln of a token's probability relative to the largest.
+// Two float32 operations at once, each rounded on its own (and never contracted).
+__device__ __forceinline__ float2 add2(float2 a, float b) {
+  uint64_t d, x = tc::pack2(__float_as_uint(a.x), __float_as_uint(a.y));
+  const uint64_t y = tc::pack2(__float_as_uint(b), __float_as_uint(b));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return tc::unpack2(d);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  uint64_t d;
+  const uint64_t x = tc::pack2(__float_as_uint(a.x), __float_as_uint(a.y));
+  const uint64_t y = tc::pack2(__float_as_uint(-b.x), __float_as_uint(-b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return tc::unpack2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+  uint64_t d, x = tc::pack2(__float_as_uint(a.x), __float_as_uint(a.y));
+  const uint64_t y = tc::pack2(__float_as_uint(b), __float_as_uint(b));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return tc::unpack2(d);
+}
+
+// The row's scale: z = ln of a token's probability relative to the largest.  top is
+// finite, and so is inv; z of -inf, of a difference that overflows and of NaN has weight 0
+// (-inf, or NaN where inv is 0).
 struct Scale {
   float top, inv;
-  __device__ float z(float l) const { return l == top ? 0.0f : __fmul_rn(__fsub_rn(l, top), inv); }
-  // exp(z); 0 where the difference is -inf
-  __device__ float e(float l) const {
-    const float d = __fsub_rn(l, top);
-    return l == top ? 1.0f : d == -INFINITY ? 0.0f : expf(__fmul_rn(d, inv));
-  }
+  __device__ float2 z(float l0, float l1) const { return mul2(add2(make_float2(l0, l1), -top), inv); }
+  __device__ float z(float l) const { return z(l, l).x; }
+  __device__ static float e(float z) { return fmaxf(expf(z), 0.0f); }
 };
 
 // round(2^40 e), e in [0, 1], as high * 2^22 + low: adding 48 = 1.5 * 2^5 leaves e's
 // multiples of 2^-18 in the sum's low bits, adding 1.5 * 2^-17 to what is left those of
-// 2^-40 (without contraction, so that e is what is split); both halves of 256 weights add up in 32 bits.
-struct Weight {
-  int high, low;
-  __device__ explicit Weight(float e) {
-    const float a = __fadd_rn(e, 48.0f);
-    const float b = __fadd_rn(__fsub_rn(e, __fsub_rn(a, 48.0f)), 0x1.8p-17f);
-    high = int(__float_as_uint(a) - __float_as_uint(48.0f));
-    low = int(__float_as_uint(b) - __float_as_uint(0x1.8p-17f));
+// 2^-40.  The bits of both sums are added up as they are, in 32 bits (both halves of 256
+// weights fit), and their constant parts taken off at the end.
+struct Weights {
+  uint32_t high = 0, low = 0, n = 0;
+  __device__ void add(float e0, float e1) {
+    const float2 a = add2(make_float2(e0, e1), 48.0f);
+    const float2 b = add2(sub2(make_float2(e0, e1), add2(a, -48.0f)), 0x1.8p-17f);
+    high += __float_as_uint(a.x) + __float_as_uint(a.y);
+    low += __float_as_uint(b.x) + __float_as_uint(b.y);
+    n += 2;
   }
-  __device__ static uint64_t join(int high, int low) {
-    return uint64_t((int64_t(high) << 22) + low);
+  __device__ uint64_t sum() const {
+    const int h = int(high - n * __float_as_uint(48.0f));
+    const int l = int(low - n * __float_as_uint(0x1.8p-17f));
+    return uint64_t((int64_t(h) << 22) + l);
   }
-  __device__ uint64_t value() const { return join(high, low); }
 };
+__device__ __forceinline__ uint64_t weight_of(float e) {
+  Weights w;
+  w.add(e, 0.0f);
+  return w.sum();
+}
+
+// The histogram bin of a token, from 0 at the largest logit on, in whole steps of
+// 1 / kBinsPerNat: the low bits of 2^23 + steps.  Grows as the logit falls; beyond any
+// histogram for weight 0.
+__device__ __forceinline__ uint32_t bin_of(float z) {
+  return __float_as_uint(__fmaf_rn(z, -kBinsPerNat, 8388608.0f)) - 0x4b000000u;
+}
+
+// The smallest whole number that is not below x as a float64 (above: that is above x).
+// Comparing sums with it replaces comparing their float64s with x.
+__device__ uint64_t threshold(double x, bool above) {
+  if (!(x < 0x1p60)) return ~uint64_t(0);
+  uint64_t s = __double2ull_ru(x) + 64;  // sums below 2^60 round by at most 64
+  for (uint64_t o = 64; o; o >>= 1)
+    if (s >= o && (above ? double(s - o) > x : double(s - o) >= x)) s -= o;
+  return s;
+}
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -127,11 +171,11 @@ struct Cut {
 enum Step : uint32_t { kList, kHistogram, kBisect, kCut };
 // What every CTA does next, as the first one has decided.
 struct Order {
-  uint32_t step, bin, from;  // kList: that bin of the histogram from `from` nats on
+  uint32_t step, bin;  // kList: the tokens of that bin; kHistogram: one from that bin on
   Cut cut;
 };
 
-constexpr int kListMost = 3072;  // listed tokens: 8 bytes each in the histogram's place
+constexpr int kListMost = 1536;  // listed tokens: 8 bytes each in the histogram's place
 
 struct SampleSmem {
   union {
@@ -151,8 +195,7 @@ struct SampleSmem {
   uint32_t scan_count[kWarps];
   uint32_t listed;
   Order order;
-  uint64_t best_mass;
-  uint32_t best;
+  uint64_t limit, best_mass;
 };
 static_assert(sizeof(uint32_t) * 2 * kListMost <= 12 * kBins, "the list lies in the histogram");
 
@@ -166,39 +209,35 @@ struct Slice {
   int vocab, skew;  // elements of the first granule that lie before the row
   int g0, g1;       // granules of the CTA
   int w0, w1;       // granules of the warp
+  bool infinite;    // the largest logit is +inf: only such tokens have a weight
 
   __device__ int first(int g) const { return g * kPer - skew; }  // index of its first element
   __device__ uint4 fetch(int g) const {
     const int i = first(g);
     if (i >= 0 && i + kPer <= vocab) return __ldg(reinterpret_cast<const uint4*>(row + i));
     __align__(16) T v[kPer];
+#pragma unroll
     for (int j = 0; j < kPer; ++j)
       v[j] = i + j >= 0 && i + j < vocab ? row[i + j] : from_float<T>(-INFINITY);
     return *reinterpret_cast<const uint4*>(v);
   }
-  __device__ void keep(int g, const uint4& v) const {
-    if (RESIDENT) *reinterpret_cast<uint4*>(smem + size_t(g - g0) * 16) = v;
+  __device__ uint4* place(int g) const { return reinterpret_cast<uint4*>(smem + size_t(g - g0) * 16); }
+  // +inf as 0, all others as -inf
+  __device__ static uint4 flattened(uint4 v) {
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) e[j] = from_float<T>(to_float(e[j]) == INFINITY ? 0.0f : -INFINITY);
+    return v;
   }
   __device__ uint4 granule(int g) const {
-    return RESIDENT ? *reinterpret_cast<const uint4*>(smem + size_t(g - g0) * 16) : fetch(g);
+    if (RESIDENT) return *place(g);
+    return infinite ? flattened(fetch(g)) : fetch(g);
   }
-  __device__ static float at(const uint4& v, int j) {
-    return clean(to_float(reinterpret_cast<const T*>(&v)[j]));
-  }
-  // visit(index, logit) for every element of the warp's part, a lane at a time its own
-  template <typename F>
-  __device__ void each(F&& visit) const {
-    for (int g = w0 + int(threadIdx.x & 31); g < w1; g += 32) {
-      const uint4 v = granule(g);
-      const int i = first(g);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) visit(i + j, at(v, j));
-    }
-  }
+  __device__ static float at(const uint4& v, int j) { return to_float(reinterpret_cast<const T*>(&v)[j]); }
 };
 
 template <typename T, bool RESIDENT>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   SampleSmem& sm = *reinterpret_cast<SampleSmem*>(dynamic);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -206,21 +245,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const uint32_t rank = tc::cluster_rank();
   const int64_t r = blockIdx.x / ctas;
-
   tc::cluster_arrive();  // every CTA of the cluster runs before another one writes to it
 
   Slice<T, RESIDENT> s;
+  constexpr int kPer = s.kPer;
   s.row = static_cast<const T*>(a.logits) + r * a.ld;
   s.smem = dynamic + (sizeof(SampleSmem) + 15) / 16 * 16;
   s.vocab = int(a.vocab);
   s.skew = int(reinterpret_cast<uintptr_t>(s.row) % 16 / sizeof(T));
-  const int granules = (s.vocab + s.skew + s.kPer - 1) / s.kPer;
+  const int granules = (s.vocab + s.skew + kPer - 1) / kPer;
   s.g0 = int(int64_t(granules) * rank / ctas);
   s.g1 = int(int64_t(granules) * (rank + 1) / ctas);
   const int per_warp = (s.g1 - s.g0 + kWarps - 1) / kWarps;
   s.w0 = min(s.g1, s.g0 + warp * per_warp);
   s.w1 = min(s.g1, s.w0 + per_warp);
 
+  // 1. the slice, and the largest logit
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int g = s.w0 + lane; g < s.w1; g += 32) {
+    const uint4 v = s.fetch(g);
+    if (RESIDENT) *s.place(g) = v;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) top = fmaxf(top, s.at(v, j));  // a NaN loses
+  }
   const float temperature = a.temperature ? a.temperature[r] : 1.0f;
   const bool greedy = !(temperature > 0.0f);
   float p = a.top_p ? a.top_p[r] : 1.0f;
@@ -230,18 +278,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (!(p > 0.0f)) k = 1, p = 1.0f;     // only the first
   const bool by_count = !greedy && k > 0 && k < s.vocab;
   const bool by_mass = !greedy && p < 1.0f;
-
-  // 1. the slice, and the largest logit
   if (by_count || by_mass)
     for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
-  float top = -INFINITY;
-  for (int g = s.w0 + lane; g < s.w1; g += 32) {
-    const uint4 v = s.fetch(g);
-    s.keep(g, v);
-#pragma unroll
-    for (int j = 0; j < s.kPer; ++j) top = fmaxf(top, to_float(reinterpret_cast<const T*>(&v)[j]));
-  }
-  top = warp_max(top + 0.0f);  // a NaN loses against any number
+  const float mine_top = top;
+  top = warp_max(top + 0.0f);
   if (lane == 0) sm.scan_count[warp] = key_of(top);
   __syncthreads();
   tc::cluster_wait();
@@ -255,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   for (uint32_t i = 0; i < ctas; ++i) top_key = max(top_key, sm.cta_top[i]);
   Scale scale;
   scale.top = logit_of(top_key);
-  scale.inv = greedy ? 1.0f : 1.0f / temperature;
+  scale.inv = greedy ? 1.0f : fminf(1.0f / temperature, 0x1.fffffep127f);
   if (scale.top == -INFINITY) {
     if (rank == 0 && tid == 0) {
       a.token[r] = -1;
@@ -263,48 +303,57 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     return;
   }
+  s.infinite = scale.top == INFINITY;
+  const bool holds_top = mine_top == scale.top;
+  if (s.infinite) {
+    scale.top = 0.0f;
+    if (RESIDENT)
+      for (int g = s.w0 + lane; g < s.w1; g += 32) *s.place(g) = s.flattened(*s.place(g));
+  }
 
-  // 2. weights, and the histogram from `from` nats below the largest on
-  auto bin_of = [&](float l, float from) {  // not below 0 and not above kBins
-    const float d = __fmul_rn(__fsub_rn(-scale.z(l), from), kBinsPerNat);
-    return d < float(kBins) ? (d >= 0.0f ? int(d) : -1) : kBins;
-  };
-  auto tally = [&](float l, uint64_t w, float from) {
-    const int bin = bin_of(l, from);
-    if (bin >= 0 && bin < kBins) {
+  // 2. weights, and the histogram of the 16 nats below the largest
+  auto tally = [&](float z, float e, uint32_t begin) {
+    const uint32_t bin = bin_of(z) - begin;
+    if (bin < uint32_t(kBins)) {
       atomicAdd(&sm.count[bin], 1u);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[bin]), (unsigned long long)w);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[bin]), (unsigned long long)weight_of(e));
     }
   };
-  int high = 0, low = 0;
+  Weights sums;
   uint32_t lowest = 0xffffffffu;
-  if (greedy) {
-    s.each([&](int i, float l) {
-      const Weight w(scale.e(l));
-      high += w.high, low += w.low;
-      if (l == scale.top) lowest = min(lowest, uint32_t(i));
-    });
-  } else if (by_count || by_mass) {
-    s.each([&](int, float l) {
-      const Weight w(scale.e(l));
-      high += w.high, low += w.low;
-      tally(l, w.value(), 0.0f);
-    });
+  if (by_count || by_mass) {
+    for (int g = s.w0 + lane; g < s.w1; g += 32) {
+      const uint4 v = s.granule(g);
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
+        const float e0 = scale.e(z.x), e1 = scale.e(z.y);
+        sums.add(e0, e1);
+        tally(z.x, e0, 0);
+        tally(z.y, e1, 0);
+      }
+    }
   } else {
-    s.each([&](int, float l) {
-      const float e = scale.e(l);
-      const Weight w(e);
-      high += w.high, low += w.low;
-    });
+    for (int g = s.w0 + lane; g < s.w1; g += 32) {
+      const uint4 v = s.granule(g);
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
+        sums.add(scale.e(z.x), scale.e(z.y));
+      }
+    }
+    if (greedy && holds_top)
+      for (int g = s.w0 + lane; g < s.w1 && lowest == 0xffffffffu; g += 32) {
+        const uint4 v = s.granule(g);
+        for (int j = kPer - 1; j >= 0; --j)
+          if (s.at(v, j) == scale.top) lowest = uint32_t(s.first(g) + j);
+      }
   }
-  // Sums over the warp, the CTA and (slot) the cluster; returns the cluster's.
+  // Sums over the warp, the CTA and (slot) the cluster.
   uint32_t slot = 0;
   auto publish = [&](uint64_t mass, uint32_t count, bool lowest_of) {
     mass = warp_sum64(mass);
-    for (int o = 16; o; o >>= 1) {
-      const uint32_t c = __shfl_xor_sync(0xffffffffu, count, o);
-      count = lowest_of ? min(count, c) : count + c;
-    }
+    count = lowest_of ? __reduce_min_sync(0xffffffffu, count) : __reduce_add_sync(0xffffffffu, count);
     __syncthreads();
     if (lane == 0) sm.warp_mass[warp] = mass, sm.scan_count[warp] = count;
     __syncthreads();
@@ -320,9 +369,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     cluster_sync();
   };
-  publish(Weight::join(high, low), lowest, true);
-  uint64_t total = 0;
-  for (uint32_t i = 0; i < ctas; ++i) total += sm.cta_mass[slot][i];
+  auto cluster_mass = [&] {
+    uint64_t m = 0;
+    for (uint32_t i = 0; i < ctas; ++i) m += sm.cta_mass[slot][i];
+    return m;
+  };
+  publish(sums.sum(), lowest, true);
+  const uint64_t total = cluster_mass();
   auto answer = [&](int i, float l) {
     a.token[r] = i;
     if (a.logprob)
@@ -339,32 +392,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
   // 3. the last kept token
   Cut cut = {0, 0xffffffffu};
+  auto kept = [&](uint32_t key, int i) {
+    return key > cut.key || (key == cut.key && uint32_t(i) <= cut.index);
+  };
   if (by_count || by_mass) {
-    // sums over the cluster of what `of(index, logit)` gives, for the bisection
-    auto sums = [&](auto&& of, uint64_t* mass, uint32_t* count) {
-      int h = 0, l = 0;
-      uint32_t c = 0;
-      s.each([&](int i, float v) {
-        if (!of(i, key_of(v))) return;
-        const Weight w(scale.e(v));
-        h += w.high, l += w.low, ++c;
-      });
-      slot ^= 1;
-      publish(Weight::join(h, l), c, false);
-      *mass = 0, *count = 0;
-      for (uint32_t i = 0; i < ctas; ++i)
-        *mass += sm.cta_mass[slot][i], *count += sm.cta_count[slot][i];
-    };
     // The first CTA's view: the histograms' sums (four bins a thread) and what lies before.
     uint32_t counts[4] = {}, count_before = 0;
     uint64_t masses[4] = {}, mass_before = 0;
     uint32_t skipped_count = 0;   // tokens above the histogram's range
     uint64_t skipped_mass = 0;
-    float from = 0.0f;
+    uint32_t begin = 0;           // the histogram's first bin
     bool count_open = by_count;   // top-k still to be resolved, else top-p
     uint64_t kept_mass = total;   // of the tokens that top-k keeps
+    uint32_t bin_count = 0;       // tokens and weights before the listed bin
+    uint64_t bin_mass = 0;
     auto gather = [&] {
       for (int j = 0; j < 4; ++j) counts[j] = 0, masses[j] = 0;
+#pragma unroll 4
       for (uint32_t c = 0; c < ctas; ++c) {
         const uint4 n = load_cluster16(&sm.count[4 * tid], c);
         const uint4 m0 = load_cluster16(&sm.mass[4 * tid], c);
@@ -384,19 +428,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       for (int i = 0; i < warp; ++i)
         count_before += sm.scan_count[i], mass_before += sm.scan_mass[i];
     };
-    // Orders the bin in which the last kept token lies to be listed.
-    auto choose = [&] {
-      if (tid == 0) sm.order.step = kHistogram;
+    // Orders the bin in which the last kept token lies to be listed; where it lies beyond
+    // the histogram, a histogram of the next 16 nats; beyond 32 nats every weight is 0.
+    auto decide = [&] {
+      if (tid == 0) {
+        sm.order.step = kHistogram;
+        sm.limit = threshold(double(p) * double(kept_mass), false);
+      }
       __syncthreads();
-      const double mass = double(p) * double(kept_mass);
+      const uint64_t limit = sm.limit;
       uint32_t c = count_before;
       uint64_t m = mass_before;
       for (int j = 0; j < 4; ++j) {
         const bool inside = count_open ? c < uint32_t(k) && c + counts[j] >= uint32_t(k)
-                                       : double(m) < mass && double(m + masses[j]) >= mass;
+                                       : m < limit && m + masses[j] >= limit;
         if (inside) {
           sm.order.step = kList;
-          sm.order.bin = 4 * tid + j;
+          sm.order.bin = begin + 4 * tid + j;
           sm.scan_count[0] = c;
           sm.scan_mass[0] = m;
         }
@@ -404,235 +452,227 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
       if (tid == kThreads - 1) sm.scan_count[1] = c, sm.scan_mass[1] = m;
       __syncthreads();
+      const bool list = sm.order.step == kList;
+      if (list) {
+        bin_count = sm.scan_count[0], bin_mass = sm.scan_mass[0];
+        if (tid == 0) sm.listed = 0;
+        return;
+      }
+      skipped_count = sm.scan_count[1], skipped_mass = sm.scan_mass[1];
+      __syncthreads();
+      if (begin == 0) {
+        begin = kBins;
+      } else if (count_open && by_mass) {
+        count_open = false;
+        begin = 0, skipped_count = 0, skipped_mass = 0;
+      } else if (tid == 0) {
+        sm.order.step = kCut, sm.order.cut = {0, 0xffffffffu};
+      }
+      if (tid == 0) sm.order.bin = begin;
+    };
+    // Ranks the listed tokens by (logit, index) and takes the last kept one.
+    auto resolve = [&] {
+      const uint32_t n = sm.listed;
+      if (n > uint32_t(kListMost)) {
+        if (tid == 0) sm.order.step = kBisect;
+        return;
+      }
+      const uint64_t limit = sm.limit;
+      for (uint32_t i = tid; i < n; i += kThreads) {
+        const uint32_t key = sm.key[i], index = sm.index[i];
+        uint32_t before = bin_count, last_key = key;
+        const uint64_t own = weight_of(scale.e(scale.z(logit_of(key))));
+        uint64_t m = bin_mass, w = own;
+        for (uint32_t j = 0; j < n; ++j) {
+          const uint32_t kj = sm.key[j];
+          if (kj > key || (kj == key && sm.index[j] < index)) {
+            if (kj != last_key) w = weight_of(scale.e(scale.z(logit_of(kj)))), last_key = kj;
+            ++before, m += w;
+          }
+        }
+        if (count_open ? before + 1 == uint32_t(k) : m < limit && m + own >= limit) {
+          sm.order.cut = {key, index};
+          sm.best_mass = m + own;
+        }
+      }
+      __syncthreads();
+      if (!(count_open && by_mass)) {
+        if (tid == 0) sm.order.step = kCut;
+        return;
+      }
+      kept_mass = sm.best_mass;  // now top-p among what top-k keeps
+      count_open = false;
+      if (begin == 0) {          // its bin is in the histogram that the registers still hold
+        decide();
+      } else {
+        begin = 0, skipped_count = 0, skipped_mass = 0;
+        if (tid == 0) sm.order.step = kHistogram, sm.order.bin = 0;
+      }
     };
     auto send = [&] {  // sm.order to every CTA
       __syncthreads();
       if (tid < int(ctas) && tid > 0) {
         store_cluster(&sm.order.step, tid, sm.order.step);
         store_cluster(&sm.order.bin, tid, sm.order.bin);
-        store_cluster(&sm.order.from, tid, sm.order.from);
         store_cluster(&sm.order.cut.key, tid, sm.order.cut.key);
         store_cluster(&sm.order.cut.index, tid, sm.order.cut.index);
       }
     };
-    uint32_t bin_count = 0;
-    uint64_t bin_mass = 0;
-    auto decide = [&] {
-      choose();
-      if (sm.order.step == kHistogram) {
-        // beyond this histogram: the next 16 nats; beyond 32 every weight is 0
-        skipped_count = sm.scan_count[1], skipped_mass = sm.scan_mass[1];
-        if (from > 0.0f) {
-          if (count_open && by_mass) {
-            count_open = false;
-            from = 0.0f, skipped_count = 0, skipped_mass = 0;
-          } else {
-            __syncthreads();
-            if (tid == 0) sm.order.step = kCut, sm.order.cut = {0, 0xffffffffu};
-            return;
-          }
-        } else {
-          from = kHistogramNats;
-        }
-        __syncthreads();
-        if (tid == 0) sm.order.from = uint32_t(from);
-      } else {
-        bin_count = sm.scan_count[0];
-        bin_mass = sm.scan_mass[0];
-        __syncthreads();
-        if (tid == 0) sm.order.from = uint32_t(from), sm.listed = 0;
-      }
-    };
-    // Ranks the listed tokens by (logit, index) and takes the last kept one.
-    auto resolve = [&] {
-      const uint32_t n = sm.listed;
-      if (n > uint32_t(kListMost)) {
-        __syncthreads();
-        if (tid == 0) sm.order.step = kBisect;
-        return;
-      }
-      const double mass = double(p) * double(kept_mass);
-      for (uint32_t i = tid; i < n; i += kThreads) {
-        const uint32_t key = sm.key[i], index = sm.index[i];
-        uint32_t before = bin_count;
-        uint64_t m = bin_mass;
-        uint32_t last_key = key;
-        uint64_t w = Weight(scale.e(logit_of(key))).value();
-        const uint64_t own = w;
-        for (uint32_t j = 0; j < n; ++j) {
-          const uint32_t kj = sm.key[j];
-          if (kj > key || (kj == key && sm.index[j] < index)) {
-            if (kj != last_key) w = Weight(scale.e(logit_of(kj))).value(), last_key = kj;
-            ++before, m += w;
-          }
-        }
-        const bool last = count_open ? before + 1 == uint32_t(k)
-                                     : double(m) < mass && double(m + own) >= mass;
-        if (last) {
-          sm.order.cut = {key, index};
-          sm.best_mass = m + own;
-        }
-      }
-      __syncthreads();
-      if (count_open && by_mass) {  // top-p among what top-k keeps
-        kept_mass = sm.best_mass;
-        count_open = false;
-        cut = sm.order.cut;
-        __syncthreads();
-        if (tid == 0) sm.order.step = kHistogram;  // decided below
-      } else if (tid == 0) {
-        sm.order.step = kCut;
-      }
-    };
 
-    if (rank == 0) {
-      gather();
-      decide();
-      send();
-    }
+    bool fresh = true;  // the histograms have just been made
+    Order order;
     for (;;) {
-      cluster_sync();
-      const Order order = sm.order;
-      if (order.step == kCut || order.step == kBisect) break;
-      const float begin = float(order.from);
-      if (order.step == kHistogram) {
-        for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
-        __syncthreads();
-        s.each([&](int, float l) { tally(l, Weight(scale.e(l)).value(), begin); });
-        cluster_sync();
-        if (rank == 0) {
+      if (rank == 0) {
+        if (fresh) {
           gather();
           decide();
-          send();
-        }
-      } else {
-        s.each([&](int i, float l) {
-          if (bin_of(l, begin) != int(order.bin)) return;
-          const uint32_t at = add_cluster(&sm.listed, 0, 1);
-          if (at >= uint32_t(kListMost)) return;
-          store_cluster(&sm.key[at], 0, key_of(l));
-          store_cluster(&sm.index[at], 0, uint32_t(i));
-        });
-        cluster_sync();
-        if (rank == 0) {
-          const bool count_was_open = count_open;
+        } else {
           resolve();
-          __syncthreads();
-          if (sm.order.step == kHistogram && count_was_open) {
-            // top-p: its bin is in the histogram that the registers still hold, or above it
-            if (from == 0.0f) {
-              decide();
-            } else {
-              from = 0.0f, skipped_count = 0, skipped_mass = 0;
-              if (tid == 0) sm.order.from = 0;
+        }
+        send();
+      }
+      cluster_sync();
+      order = sm.order;
+      if (order.step == kCut || order.step == kBisect) break;
+      fresh = order.step == kHistogram;
+      if (fresh) {
+        for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
+        __syncthreads();
+      }
+      for (int g = s.w0 + lane; g < s.w1; g += 32) {
+        const uint4 v = s.granule(g);
+#pragma unroll
+        for (int j = 0; j < kPer; j += 2) {
+          const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
+          if (fresh) {
+            tally(z.x, scale.e(z.x), order.bin);
+            tally(z.y, scale.e(z.y), order.bin);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (bin_of(h ? z.y : z.x) != order.bin) continue;
+              const uint32_t to = add_cluster(&sm.listed, 0, 1);
+              if (to >= uint32_t(kListMost)) continue;
+              store_cluster(&sm.key[to], 0, key_of(clean(s.at(v, j + h))));
+              store_cluster(&sm.index[to], 0, uint32_t(s.first(g) + j + h));
             }
           }
-          send();
         }
       }
+      cluster_sync();
     }
-    const Order order = sm.order;
     if (order.step == kCut) {
       cut = order.cut;
     } else {
       // Too many tokens in one bin: the cut's key by bisection over its bits, then its
       // index, every CTA over its slice.
-      uint64_t mass;
-      uint32_t count;
-      cut = {0, 0xffffffffu};
-      auto last_index = [&](uint32_t key, uint32_t ties) {  // of the first `ties` with this key
-        uint32_t lo = 0, hi = uint32_t(s.vocab - 1);
+      uint64_t mass;   // of the tokens inside the cut that are not ranked behind
+      uint32_t count;  // (key, index)
+      auto sums_to = [&](uint32_t key, uint32_t index) {
+        uint64_t m = 0;
+        uint32_t c = 0;
+#pragma unroll 1
+        for (int g = s.w0 + lane; g < s.w1; g += 32) {
+          const uint4 v = s.granule(g);
+#pragma unroll 1
+          for (int j = 0; j < kPer; ++j) {
+            const int i = s.first(g) + j;
+            const float l = clean(s.at(v, j));
+            const uint32_t q = key_of(l);
+            if (uint32_t(i) >= uint32_t(s.vocab) || !kept(q, i)) continue;
+            if (q < key || (q == key && uint32_t(i) > index)) continue;
+            m += weight_of(scale.e(scale.z(l))), ++c;
+          }
+        }
+        slot ^= 1;
+        publish(m, c, false);
+        mass = cluster_mass(), count = 0;
+        for (uint32_t i = 0; i < ctas; ++i) count += sm.cta_count[slot][i];
+      };
+      constexpr uint32_t kAll = 0xffffffffu;
+      bool open = by_count;
+      uint64_t limit = by_count ? uint64_t(k) : threshold(double(p) * double(total), false);
+#pragma unroll 1
+      for (;;) {
+        uint32_t key = 0;  // the largest for which the sum reaches the limit
+#pragma unroll 1
+        for (int b = 31; b >= 0; --b) {
+          sums_to(key | 1u << b, kAll);
+          if ((open ? uint64_t(count) : mass) >= limit) key |= 1u << b;
+        }
+        uint32_t lo = 0, hi = uint32_t(s.vocab - 1);  // the first index for which it does
         while (lo < hi) {
           const uint32_t mid = (lo + hi) / 2;
-          sums([&](int i, uint32_t q) { return q == key && uint32_t(i) <= mid; }, &mass, &count);
-          if (count >= ties) hi = mid;
+          sums_to(key, mid);
+          if ((open ? uint64_t(count) : mass) >= limit) hi = mid;
           else lo = mid + 1;
         }
-        return lo;
-      };
-      auto kept = [&](int i, uint32_t q) {
-        return q > cut.key || (q == cut.key && uint32_t(i) <= cut.index);
-      };
-      uint64_t all = total;
-      if (by_count) {
-        uint32_t key = 0;
-        for (int b = 31; b >= 0; --b) {
-          sums([&](int i, uint32_t q) { return q >= (key | 1u << b) && i >= 0 && i < s.vocab; },
-               &mass, &count);
-          if (count >= uint32_t(k)) key |= 1u << b;
-        }
-        sums([&](int i, uint32_t q) { return q > key && i >= 0 && i < s.vocab; }, &mass, &count);
-        const uint64_t above = mass;
-        const uint32_t ties = uint32_t(k) - count;
-        cut = {key, last_index(key, ties)};
-        all = above + ties * Weight(scale.e(logit_of(key))).value();
-      }
-      if (by_mass) {
-        const double target = double(p) * double(all);
-        uint32_t key = 0;
-        for (int b = 31; b >= 0; --b) {
-          sums([&](int i, uint32_t q) { return q >= (key | 1u << b) && kept(i, q); }, &mass, &count);
-          if (double(mass) >= target) key |= 1u << b;
-        }
-        sums([&](int i, uint32_t q) { return q > key && kept(i, q); }, &mass, &count);
-        const uint64_t above = mass, w = Weight(scale.e(logit_of(key))).value();
-        sums([&](int i, uint32_t q) { return q == key && kept(i, q); }, &mass, &count);
-        uint32_t lo = 1, hi = count;  // ties kept: the most t with above + (t - 1) w < target
-        while (lo < hi) {
-          const uint32_t t = lo + (hi - lo + 1) / 2;
-          if (double(above + (t - 1) * w) < target) lo = t;
-          else hi = t - 1;
-        }
-        cut = {key, last_index(key, lo)};
+        sums_to(key, lo);
+        cut = {key, lo};
+        if (!open || !by_mass) break;
+        open = false;
+        limit = threshold(double(p) * double(mass), false);
       }
     }
   }
 
   // 4. the token
-  const bool filtered = by_count || by_mass || floor_e > 0.0f;
-  auto weight = [&](int i, float l) {  // 0 for a token that is not kept
-    const uint32_t key = key_of(l);
-    if (key < cut.key || (key == cut.key && uint32_t(i) > cut.index)) return Weight(0.0f);
-    const float e = scale.e(l);
-    return Weight(e < floor_e ? 0.0f : e);
+  const float cut_logit = cut.key == 0 ? -INFINITY : logit_of(cut.key);
+  auto chance = [&](float l, float z, int i) {  // 0 for a token that is not kept
+    const float e = scale.e(z);
+    if (!(l >= cut_logit) || (l == cut_logit && uint32_t(i) > cut.index) || e < floor_e) return 0.0f;
+    return e;
+  };
+  auto granule_sum = [&](const uint4& v, int g) {
+    Weights w;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) {
+      const float l0 = s.at(v, j), l1 = s.at(v, j + 1);
+      const float2 z = scale.z(l0, l1);
+      w.add(chance(l0, z.x, s.first(g) + j), chance(l1, z.y, s.first(g) + j + 1));
+    }
+    return w.sum();
   };
   uint64_t all = total;
-  if (filtered) {
-    int h = 0, l = 0;
-    s.each([&](int i, float v) {
-      const Weight w = weight(i, v);
-      h += w.high, l += w.low;
-    });
+  if (by_count || by_mass || floor_e > 0.0f) {
+    uint64_t mine = 0;
+    for (int g = s.w0 + lane; g < s.w1; g += 32) {
+      const uint4 v = s.granule(g);
+      float most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) most = fmaxf(most, s.at(v, j));
+      if (most >= cut_logit) mine += granule_sum(v, g);
+    }
     slot ^= 1;
-    publish(Weight::join(h, l), 0, false);
-    all = 0;
-    for (uint32_t i = 0; i < ctas; ++i) all += sm.cta_mass[slot][i];
+    publish(mine, 0, false);
+    all = cluster_mass();
   }
-  const double target = double(u) * double(all);
-  // the first token at which the sum passes the target; none does for u >= 1: the last
+  // the first token at which the sum passes u times all; none does for u >= 1: the last
   // one with a weight, at which the sum is complete
-  auto passes = [&](uint64_t sum) { return double(sum) > target || sum == all; };
+  if (tid == 0) sm.limit = min(threshold(double(u) * double(all), true), all);
+  __syncthreads();
+  const uint64_t limit = sm.limit;
   uint64_t run = 0;
   for (uint32_t i = 0; i < rank; ++i) run += sm.cta_mass[slot][i];
   for (int i = 0; i < warp; ++i) run += sm.warp_mass[i];
-  if (passes(run) || !passes(run + sm.warp_mass[warp])) return;
-  for (int g = s.w0 + lane; ; g += 32) {  // ends: the warp's sum passes
-    uint64_t mine = 0;
+  if (run >= limit || run + sm.warp_mass[warp] < limit) return;
+  for (int g = s.w0 + lane;; g += 32) {  // ends: the warp's sum reaches the limit
     uint4 v = make_uint4(0, 0, 0, 0);
+    uint64_t mine = 0;
     if (g < s.w1) {
       v = s.granule(g);
-      for (int j = 0; j < s.kPer; ++j) mine += weight(s.first(g) + j, s.at(v, j)).value();
+      mine = granule_sum(v, g);
     }
     const uint64_t upto = run + warp_scan64(mine, lane);
-    const uint32_t found = __ballot_sync(0xffffffffu, passes(upto));
+    const uint32_t found = __ballot_sync(0xffffffffu, upto >= limit);
     if (found) {
       if (lane == __ffs(int(found)) - 1) {
         uint64_t sum = upto - mine;
-        for (int j = 0; j < s.kPer; ++j) {
+        for (int j = 0; j < kPer; ++j) {
           const int i = s.first(g) + j;
-          const float l = s.at(v, j);
-          sum += weight(i, l).value();
-          if (passes(sum)) {
+          const float l = s.at(v, j), z = scale.z(l);
+          sum += weight_of(chance(l, z, i));
+          if (sum >= limit) {
             answer(i, l);
             break;
           }

@@ -834,7 +834,8 @@ reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const float* xs,
 
 /*
  * One token for each row of logits, from one given uniform number a row.  With
- * l = logits[r], T = temperature[r], m = max l and z_i = (l_i - m) * (1 / T), token i
+ * l = logits[r], T = temperature[r], m = max l and z_i = (l_i - m) * (1 / T) (1 / T at
+ * most the largest float32; z_i = 0 where l_i = m), token i
  * has weight w_i = round(2^40 * exp(z_i)), a whole number, so that every sum below is
  * exact.  Tokens are ranked by logit, ties to the lowest index, and token i is kept if
  *   its rank is below top_k[r]  (top_k <= 0: all are),
