@@ -794,7 +794,7 @@ typedef enum reshard_score {
  * [nmat][ceil(rows / block_rows)][lds], of which ceil(cols / 128) are written.  Any
  * alignment is accepted; rows that start on 16 bytes (x) and 8 bytes (q) are faster.
  * Errors: INVALID_ARG (null pointer, unknown or integer dtype, negative size, pitch
- * too small, block_rows), CUDA.
+ * too small, block_rows), UNSUPPORTED (2^31 blocks or more), CUDA.
  */
 reshard_status_t reshard_fp8_quantize(const void* x, int32_t dtype, int64_t nmat, int64_t rows,
                                       int64_t cols, int64_t ldx, int32_t block_rows, void* q,
