@@ -95,6 +95,7 @@ struct Eight {
     for (int i = 0; i < kGranules; ++i)
       v[i] = staging::funnel16(v[i], i + 1 < kGranules ? v[i + 1] : next, skew / 4,
                                0x3210u + 0x1111u * (skew % 4));
+    if (left >= 8) return;
     T* e = reinterpret_cast<T*>(v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = i < left ? e[i] : from_float<T>(0.0f);
@@ -143,23 +144,45 @@ __device__ __forceinline__ float Eight<__half>::largest() const {
 }
 
 // Eight bytes a lane from sixteen neighbouring lanes to a row's `count` bytes (at most 128)
-// at any alignment: each lane stores the aligned eight bytes that end in its own.
+// at any alignment: each lane stores the aligned eight bytes that end in its own, and what
+// is left at both ends goes out in the widest stores that are aligned.
 __device__ __forceinline__ void store_row(uint8_t* row, uint2 q, int count) {
   const int lane = threadIdx.x % 16;
-  const int skew = int(reinterpret_cast<uintptr_t>(row) % 8);
-  const uint64_t own = q.x | uint64_t(q.y) << 32;
-  const uint64_t before = __shfl_up_sync(0xffffffffu, own, 1, 16);
-  const uint64_t word = skew ? own << (8 * skew) | before >> (64 - 8 * skew) : own;
-  const int from = 8 * lane - skew;  // of the row's bytes
-  if (from >= 0 && from + 8 <= count) {
-    *reinterpret_cast<uint64_t*>(row + from) = word;
+  const uint32_t skew = uint32_t(reinterpret_cast<uintptr_t>(row) % 8);
+  uint8_t* to = row + 8 * lane;
+  if (__all_sync(0xffffffffu, count == 128)) {
+    const uint32_t before_x = __shfl_up_sync(0xffffffffu, q.x, 1, 16);
+    const uint32_t before_y = __shfl_up_sync(0xffffffffu, q.y, 1, 16);
+    const uint64_t own = q.x | uint64_t(q.y) << 32, before = before_x | uint64_t(before_y) << 32;
+    if (lane > 0 || skew == 0)
+      *reinterpret_cast<uint64_t*>(to - skew) = skew ? own << (8 * skew) | before >> (64 - 8 * skew) : own;
+    if (skew != 0 && (lane == 0 || lane == 15)) {
+      // lane 0: up to the next aligned eight bytes; lane 15: the last `skew` bytes
+      const bool head = lane == 0;
+      uint32_t i = head ? 0 : 8 - skew;
+      auto step = [&](uint32_t n) {
+        const uint64_t v = own >> (8 * i);
+        if (n == 4) *reinterpret_cast<uint32_t*>(to + i) = uint32_t(v);
+        if (n == 2) *reinterpret_cast<uint16_t*>(to + i) = uint16_t(v);
+        if (n == 1) to[i] = uint8_t(v);
+        i += n;
+      };
+      const uint32_t n = head ? 8 - skew : skew;
+      if (head) {
+        if (n & 1) step(1);
+        if (n & 2) step(2);
+        if (n & 4) step(4);
+      } else {
+        if (n & 4) step(4);
+        if (n & 2) step(2);
+        if (n & 1) step(1);
+      }
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (from + i >= 0 && from + i < count) row[from + i] = uint8_t(word >> (8 * i));
+      if (8 * lane + i < count) to[i] = uint8_t((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
   }
-  if (lane == 15)
-    for (int i = 128 - skew; i < count; ++i) row[i] = uint8_t(own >> (8 * (i - 120)));
 }
 
 __device__ __forceinline__ float scale_of(float largest) {
