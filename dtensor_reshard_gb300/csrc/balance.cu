@@ -1,13 +1,23 @@
 // balance.cu -- reshard_balance_loss: the router's load-balance loss, the tokens each
 // expert got, and the gradient in the router's logits.
+//
+// The loss is linear in each token's scores with weights f that depend on the choices
+// alone, so with d_t = sum_e f_e p_te it is a sum of d_t, and the gradient needs d_t and
+// the token's own scores: once the choices are counted, one pass over the logits gives
+// both, and nothing of the size of the experts is summed over tokens.  Two kernels: the
+// counts (a cluster a sequence, or several), and the pass, whose first logits are loaded
+// while the counts are still being made.
 #include "operators.cuh"
+#include "tensor_core.cuh"
 
 namespace rs {
 namespace {
 
 using namespace op;
 
-constexpr int kChunk = 64;  // tokens of one CTA
+constexpr int kChunk = 8;           // a pass's CTA takes whole multiples of this many tokens
+constexpr int kCountCluster = 8;
+constexpr int kCountThreads = 1024;
 
 struct BalanceArgs {
   const void* logits;
@@ -18,103 +28,397 @@ struct BalanceArgs {
   float* loss;
   int32_t* counts;
   void* dlogits;
-  int32_t* tokens;  // [nseq]: tokens with mask (workspace)
-  float* parts;     // [nseq * chunks]: sums over tokens (workspace)
-  int64_t nseq, seqlen, topk, chunks;
+  int32_t* tokens;  // workspace: [nseq] tokens with mask
+  float* parts;     // [nseq * chunks] the pass's sums over tokens
+  uint32_t* done;   // CTAs of the pass that have written theirs
+  int32_t nseq, seqlen, topk;
+  int32_t chunk, chunks;            // tokens of a pass's CTA, CTAs of a sequence
+  int32_t clusters;                 // of the counts of a sequence
   int32_t nexperts, score;
   float coef;
 };
 
-__global__ void __launch_bounds__(256) count_kernel(BalanceArgs a) {
-  const int64_t s = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
-  const int64_t t0 = c * kChunk, t1 = t0 + kChunk < a.seqlen ? t0 + kChunk : a.seqlen;
-  for (int64_t i = t0 * a.topk + threadIdx.x; i < t1 * a.topk; i += blockDim.x) {
-    const int64_t t = s * a.seqlen + i / a.topk;
+// The next kernel of the stream may start as far as it does not need this one.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Counts a sequence's choices: every CTA of a cluster counts its share of the tokens in
+// shared memory, then adds up the cluster's counts of its share of the experts.  With one
+// cluster a sequence the sums are the result; several add theirs to zeros.
+__global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_constant__ BalanceArgs a) {
+  extern __shared__ int32_t counted[];  // [nexperts + 1]: the last one counts tokens
+  let_next_start();
+  const int bins = a.nexperts + 1;
+  for (int i = threadIdx.x; i < bins; i += kCountThreads) counted[i] = 0;
+  __syncthreads();
+  const uint32_t rank = tc::cluster_rank();
+  uint32_t ctas;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int part = blockIdx.x % (ctas * a.clusters), s = blockIdx.x / (ctas * a.clusters);
+  const int parts = int(ctas) * a.clusters;
+  const int t0 = int(int64_t(a.seqlen) * part / parts), t1 = int(int64_t(a.seqlen) * (part + 1) / parts);
+  const bool fours = a.topk % 4 == 0 && reinterpret_cast<uintptr_t>(a.experts) % 16 == 0;
+  auto count = [&](int e) {
+    if (uint32_t(e) < uint32_t(a.nexperts)) atomicAdd(&counted[e], 1);
+  };
+  int live = 0;
+  for (int i = t0 + int(threadIdx.x); i < t1; i += kCountThreads) {
+    const int64_t t = int64_t(s) * a.seqlen + i;
     if (a.mask && !a.mask[t]) continue;
-    if (i % a.topk == 0) atomicAdd(&a.tokens[s], 1);
-    const int32_t e = a.experts[s * a.seqlen * a.topk + i];
-    if (e >= 0 && e < a.nexperts) atomicAdd(&a.counts[s * a.nexperts + e], 1);
+    ++live;
+    const int32_t* e = a.experts + t * a.topk;
+    if (fours) {
+      for (int j = 0; j < a.topk; j += 4) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(e + j));
+        count(v.x), count(v.y), count(v.z), count(v.w);
+      }
+    } else {
+      for (int j = 0; j < a.topk; ++j) count(e[j]);
+    }
+  }
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (threadIdx.x % 32 == 0) atomicAdd(&counted[a.nexperts], live);
+  __syncthreads();
+  tc::cluster_sync();
+  for (int i = int(rank * kCountThreads + threadIdx.x); i < bins; i += int(ctas) * kCountThreads) {
+    const uint32_t at = staging::smem_addr(&counted[i]);
+    int sum = 0;
+    for (uint32_t r = 0; r < ctas; ++r)
+      sum += __float_as_int(tc::load_cluster(tc::in_cta(at, r)));
+    int32_t* to = i < a.nexperts ? &a.counts[int64_t(s) * a.nexperts + i] : &a.tokens[s];
+    if (a.clusters == 1) *to = sum;
+    else if (sum) atomicAdd(to, sum);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+  __syncthreads();
+  tc::cluster_sync();  // no CTA's shared memory goes away under a reader
+}
+
+// A token's scores before they are divided by their sum, two at a time: exp(l - top), or
+// 1 / (1 + exp(-l)).  Exponentials are 2^x, x rounded to float32: off by 2^-24 |x| and 2
+// units in the last place (expf spends five times the instructions on less).
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t both(float v) {
+  return tc::pack2(__float_as_uint(v), __float_as_uint(v));
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return tc::pack2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  const float2 f = tc::unpack2(v);
+  return f.x + f.y;
+}
+template <int SCORE>
+struct Score {
+  __device__ static uint64_t of(float l0, float l1, float top) {
+    if (SCORE == RESHARD_SCORE_SOFTMAX) {
+      const float2 x = tc::unpack2(mul2(add2(pair(l0, l1), both(-top)), both(kLog2E)));
+      return pair(exp2_of(x.x), exp2_of(x.y));
+    }
+    const float2 x = tc::unpack2(mul2(pair(l0, l1), both(-kLog2E)));
+    const float2 d = tc::unpack2(add2(pair(exp2_of(x.x), exp2_of(x.y)), both(1.0f)));
+    float r0, r1;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
+    return pair(r0, r1);
+  }
+  // the score's own slope: p (softmax) or p (1 - a)
+  __device__ static uint64_t slope(uint64_t v) {
+    return SCORE == RESHARD_SCORE_SOFTMAX ? v : mul2(v, tc::fma2(v, both(-1.0f), both(1.0f)));
+  }
+};
+
+// What a CTA of the pass needs of the counts: f[e] in shared memory, and the loss's share
+// of a token.
+struct Weighting {
+  float share, inv_tokens;
+  __device__ void make(const BalanceArgs& a, int s, float* f) {
+    __shared__ int live;
+    if (threadIdx.x == 0) live = 0;
+    __syncthreads();
+    int mine = 0;
+    for (int i = threadIdx.x; i < a.nseq; i += blockDim.x) mine += a.tokens[i] > 0;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (threadIdx.x % 32 == 0 && mine) atomicAdd(&live, mine);
+    const int n = max(a.tokens[s], 1);
+    const float per_count = float(a.nexperts) / (float(a.topk) * float(n));
+    for (int e = threadIdx.x; e < a.nexperts; e += blockDim.x)
+      f[e] = float(a.counts[int64_t(s) * a.nexperts + e]) * per_count;
+    __syncthreads();
+    inv_tokens = 1.0f / float(n);
+    share = a.coef / float(max(live, 1)) / float(n) * (a.grad ? *a.grad : 1.0f);
+  }
+};
+
+// The CTA's sum over its tokens, and in the last CTA of the launch the loss: all parts in
+// one fixed order.
+__device__ void finish(const BalanceArgs& a, float sum, float inv_tokens) {
+  __shared__ float sums[8];
+  __shared__ double total[8];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) sums[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) sum += sums[w];
+    a.parts[blockIdx.x] = sum * inv_tokens;
+    __threadfence();
+    last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last || !a.loss) return;
+  __threadfence();
+  double mine = 0.0;
+  for (uint32_t i = threadIdx.x; i < gridDim.x; i += 256) mine += double(__ldcg(a.parts + i));
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  int live = 0;
+  for (int i = threadIdx.x; i < a.nseq; i += 256) live += a.tokens[i] > 0;
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) total[warp] = mine, sums[warp] = float(live);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) mine += total[w], live += int(sums[w]);
+    *a.loss = float(mine * double(a.coef) / double(max(live, 1)));
   }
 }
 
-__device__ __forceinline__ float score_of(float l, float top, int score) {
-  return score == RESHARD_SCORE_SOFTMAX ? expf(l - top) : 1.0f / (1.0f + expf(-l));
+// A token's logits as a lane holds them: N values, read 16 bytes at a time (VEC: every row
+// starts on 16 bytes and ends with a vector) or element by element, neighbouring lanes
+// next to each other either way.  Values beyond the experts are -inf, whose score is 0.
+template <typename T, bool VEC, int N>
+struct Logits {
+  static constexpr int kPer = VEC ? 16 / int(sizeof(T)) : 1;
+  alignas(16) T v[N];
+  // the expert of value i
+  __device__ static int expert(int i, int lane, int lanes) {
+    return (lane + i / kPer * lanes) * kPer + i % kPer;
+  }
+  __device__ void load(const T* row, bool on, int lane, int lanes, int experts) {
+#pragma unroll
+    for (int i = 0; i < N; i += kPer) {
+      const int e = expert(i, lane, lanes);
+      if (VEC) {
+        if (on && e < experts)
+          *reinterpret_cast<uint4*>(v + i) = __ldcs(reinterpret_cast<const uint4*>(row + e));
+      } else {
+        if (on && e < experts) v[i] = row[e];
+      }
+    }
+  }
+  __device__ void clear(int lane, int lanes, int experts) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = from_float<T>(-INFINITY);
+  }
+  __device__ void store(T* row, int lane, int lanes, int experts) const {
+#pragma unroll
+    for (int i = 0; i < N; i += kPer) {
+      const int e = expert(i, lane, lanes);
+      if (e >= experts) continue;
+      if (VEC) __stcs(reinterpret_cast<uint4*>(row + e), *reinterpret_cast<const uint4*>(v + i));
+      else row[e] = v[i];
+    }
+  }
+};
+
+// The pass: a token a group of `lanes` lanes, N logits a lane in registers; the next
+// token's are loaded while this one's are worked on.
+template <typename T, int SCORE, bool VEC, int N>
+__global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
+    balance_kernel(const __grid_constant__ BalanceArgs a, const int lanes) {
+  using L = Logits<T, VEC, N>;
+  extern __shared__ float f_smem[];
+  const int s = blockIdx.x / a.chunks;
+  const int first = blockIdx.x % a.chunks * a.chunk;
+  const int end = min(a.seqlen, first + a.chunk);
+  const int lane = threadIdx.x & (lanes - 1), groups = 256 / lanes;
+  const int64_t row0 = int64_t(s) * a.seqlen;
+  const T* logits = static_cast<const T*>(a.logits) + row0 * a.ld;
+  T* dlogits = a.dlogits ? static_cast<T*>(a.dlogits) + row0 * a.ld : nullptr;
+  auto live = [&](int t) { return t < end && (!a.mask || a.mask[row0 + t] != 0); };
+  int t = first + int(threadIdx.x) / lanes;
+  L next;
+  next.clear(lane, lanes, a.nexperts);
+  bool on = live(t);
+  next.load(logits + int64_t(t) * a.ld, on, lane, lanes, a.nexperts);
+  wait_for_previous();
+  Weighting w;
+  w.make(a, s, f_smem);
+  uint64_t f[N / 2];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const int e0 = L::expert(i, lane, lanes), e1 = L::expert(i + 1, lane, lanes);
+    f[i / 2] = pair(e0 < a.nexperts ? f_smem[e0] : 0.0f, e1 < a.nexperts ? f_smem[e1] : 0.0f);
+  }
+  float sum = 0.0f;
+  // the groups of a warp walk together: the shuffles need all lanes
+  for (int base = first; base < end; base += groups, t += groups) {
+    const L now = next;
+    const bool counts = on;
+    on = live(t + groups);
+    next.load(logits + int64_t(t + groups) * a.ld, on, lane, lanes, a.nexperts);
+    L grad;
+    if (__any_sync(0xffffffffu, counts)) {
+      uint64_t p[N / 2], total2 = both(0.0f), dot2 = both(0.0f);
+      float top = 0.0f;
+      if (SCORE == RESHARD_SCORE_SOFTMAX) {
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, to_float(now.v[i]));
+        for (int o = lanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top == -INFINITY) top = 0.0f;  // all scores 0
+      }
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        p[i / 2] = Score<SCORE>::of(to_float(now.v[i]), to_float(now.v[i + 1]), top);
+        total2 = add2(total2, p[i / 2]);
+        dot2 = tc::fma2(p[i / 2], f[i / 2], dot2);
+      }
+      float total = sum2(total2), dot = sum2(dot2);
+      for (int o = lanes / 2; o; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      }
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      dot *= inv;
+      if (counts && lane == 0) sum += dot;
+      const uint64_t scale = both(w.share * inv), minus_dot = both(-dot);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 g = tc::unpack2(
+            mul2(mul2(scale, Score<SCORE>::slope(p[i / 2])), add2(f[i / 2], minus_dot)));
+        grad.v[i] = from_float<T>(counts ? g.x : 0.0f);
+        grad.v[i + 1] = from_float<T>(counts ? g.y : 0.0f);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) grad.v[i] = from_float<T>(0.0f);
+    }
+    if (dlogits && t < end) grad.store(dlogits + int64_t(t) * a.ld, lane, lanes, a.nexperts);
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  finish(a, sum, w.inv_tokens);
 }
 
-// One warp a token.
-template <typename T>
-__global__ void __launch_bounds__(256) balance_kernel(BalanceArgs a) {
-  __shared__ float sums[8];
-  __shared__ int live_s;
-  const int64_t s = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
+// The pass for more experts than a warp's registers hold: a warp a token, the row read
+// again for each question.
+template <typename T, int SCORE>
+__global__ void __launch_bounds__(256) balance_many_kernel(const __grid_constant__ BalanceArgs a) {
+  extern __shared__ float f_smem[];
+  const int s = blockIdx.x / a.chunks;
+  const int first = blockIdx.x % a.chunks * a.chunk;
+  const int end = min(a.seqlen, first + a.chunk);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) live_s = 0;
-  __syncthreads();
-  for (int64_t i = threadIdx.x; i < a.nseq; i += blockDim.x)
-    if (a.tokens[i] > 0) atomicAdd(&live_s, 1);
-  __syncthreads();
-  const float n = float(a.tokens[s] > 0 ? a.tokens[s] : 1);
-  const float per_count = float(a.nexperts) / (float(a.topk) * n);
-  const float share = a.coef / float(live_s > 0 ? live_s : 1) / n * (a.grad ? *a.grad : 1.0f);
-  const int32_t* counts = a.counts + s * a.nexperts;
-  const T* logits = static_cast<const T*>(a.logits);
-  T* dlogits = static_cast<T*>(a.dlogits);
+  wait_for_previous();
+  Weighting w;
+  w.make(a, s, f_smem);
   float sum = 0.0f;
-  for (int64_t i = c * kChunk + warp; i < (c + 1) * kChunk && i < a.seqlen; i += 8) {
-    const int64_t t = s * a.seqlen + i;
-    const T* l = logits + t * a.ld;
-    T* d = dlogits ? dlogits + t * a.ld : nullptr;
+  for (int i = first + warp; i < end; i += 8) {
+    const int64_t t = int64_t(s) * a.seqlen + i;
+    const T* l = static_cast<const T*>(a.logits) + t * a.ld;
+    T* d = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.ld : nullptr;
     if (a.mask && !a.mask[t]) {
       if (d)
         for (int e = lane; e < a.nexperts; e += 32) d[e] = from_float<T>(0.0f);
       continue;
     }
-    float top = -INFINITY, total = 0.0f, dot = 0.0f;
-    for (int e = lane; e < a.nexperts; e += 32) top = fmaxf(top, to_float(l[e]));
-    top = warp_max(top);
-    const bool none = top == -INFINITY;
+    float top = 0.0f, total = 0.0f, dot = 0.0f;
+    if (SCORE == RESHARD_SCORE_SOFTMAX) {
+      top = -INFINITY;
+      for (int e = lane; e < a.nexperts; e += 32) top = fmaxf(top, to_float(l[e]));
+      top = warp_max(top);
+      if (top == -INFINITY) top = 0.0f;  // all scores 0
+    }
     for (int e = lane; e < a.nexperts; e += 32) {
-      const float v = none ? 0.0f : score_of(to_float(l[e]), top, a.score);
+      const float v = tc::unpack2(Score<SCORE>::of(to_float(l[e]), 0.0f, top)).x;
       total += v;
-      dot += v * (float(counts[e]) * per_count);
+      dot = fmaf(v, f_smem[e], dot);
     }
     total = warp_sum(total);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     dot = warp_sum(dot) * inv;
     sum += dot;
     if (!d) continue;
+    const float scale = w.share * inv;
     for (int e = lane; e < a.nexperts; e += 32) {
-      const float v = none ? 0.0f : score_of(to_float(l[e]), top, a.score);
-      const float slope = v * inv * (a.score == RESHARD_SCORE_SOFTMAX ? 1.0f : 1.0f - v);
-      d[e] = from_float<T>(share * slope * (float(counts[e]) * per_count - dot));
+      const uint64_t v = Score<SCORE>::of(to_float(l[e]), 0.0f, top);
+      d[e] = from_float<T>(scale * tc::unpack2(Score<SCORE>::slope(v)).x * (f_smem[e] - dot));
     }
   }
-  if (lane == 0) sums[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) sum += sums[w];
-    a.parts[blockIdx.x] = sum / n;
-  }
+  finish(a, lane == 0 ? sum : 0.0f, w.inv_tokens);
 }
 
-__global__ void __launch_bounds__(256) loss_kernel(BalanceArgs a) {
-  __shared__ double sums[256];
-  __shared__ int live_s;
-  if (threadIdx.x == 0) live_s = 0;
-  __syncthreads();
-  for (int64_t i = threadIdx.x; i < a.nseq; i += 256)
-    if (a.tokens[i] > 0) atomicAdd(&live_s, 1);
-  double sum = 0.0;
-  for (int64_t i = threadIdx.x; i < a.nseq * a.chunks; i += 256) sum += double(a.parts[i]);
-  sums[threadIdx.x] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 256; ++i) sum += sums[i];
-    *a.loss = float(sum * double(a.coef) / double(live_s > 0 ? live_s : 1));
+int64_t header_bytes(int64_t nseq) { return cdiv(nseq * 4 + 4, 16) * 16; }  // tokens, done
+
+reshard_status_t launch_in(const void* kernel, int64_t grid, int threads, size_t smem, int cluster,
+                           bool early, cudaStream_t stream, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (early) {  // before the kernel in front of it has ended
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
   }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t ce = cudaLaunchKernelExC(&cfg, kernel, args);
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
+  return RESHARD_OK;
 }
 
-int64_t tokens_bytes(int64_t nseq) { return cdiv(nseq * 4, 16) * 16; }
+template <typename T, int SCORE, bool VEC>
+const void* pass_kernel(int values) {
+  return values <= 8    ? reinterpret_cast<const void*>(balance_kernel<T, SCORE, VEC, 8>)
+         : values <= 16 ? reinterpret_cast<const void*>(balance_kernel<T, SCORE, VEC, 16>)
+                        : reinterpret_cast<const void*>(balance_kernel<T, SCORE, VEC, 32>);
+}
+
+template <typename T, int SCORE>
+reshard_status_t launch_pass(BalanceArgs& a, int64_t sms, cudaStream_t stream) {
+  constexpr int kPer = 16 / int(sizeof(T));
+  const bool vec = a.nexperts % kPer == 0 && a.ld % kPer == 0 && aligned(a.logits, 16) &&
+                   aligned(a.dlogits, 16);
+  // 16 logits a lane (fewer shuffles a logit than with 8: XXX) while a warp is enough,
+  // 8 where the row is short, up to 32
+  int lanes = 1;
+  while (lanes < 32 && lanes * 16 < a.nexperts) lanes *= 2;
+  const int values = int(cdiv(cdiv(a.nexperts, vec ? kPer : 1), lanes)) * (vec ? kPer : 1);
+  // as many CTAs as are on the GPU at a time
+  const void* kernel = values > 32 ? reinterpret_cast<const void*>(balance_many_kernel<T, SCORE>)
+                       : vec       ? pass_kernel<T, SCORE, true>(values)
+                                   : pass_kernel<T, SCORE, false>(values);
+  const int64_t target = sms * (values > 32 ? 8 : values > 16 ? 2 : 3);
+  a.chunk = int32_t(cdiv(cdiv(int64_t(a.nseq) * a.seqlen, target), kChunk) * kChunk);
+  a.chunks = int32_t(cdiv(a.seqlen, a.chunk));
+  void* args[] = {&a, &lanes};
+  return launch_in(kernel, int64_t(a.nseq) * a.chunks, 256, sizeof(float) * size_t(a.nexperts), 1, true,
+                   stream, args);
+}
 
 }  // namespace
 }  // namespace rs
@@ -123,7 +427,7 @@ using rs::fail;
 
 extern "C" int64_t reshard_balance_loss_workspace(int64_t nseq, int64_t seqlen, int64_t nexperts) {
   if (nseq < 0 || seqlen < 0 || nexperts < 0) return 0;
-  return rs::tokens_bytes(nseq) + 4 * nseq * rs::op::cdiv(seqlen, rs::kChunk);
+  return rs::header_bytes(nseq) + 4 * nseq * rs::op::cdiv(seqlen, rs::kChunk);
 }
 
 extern "C" reshard_status_t reshard_balance_loss(
@@ -155,6 +459,19 @@ extern "C" reshard_status_t reshard_balance_loss(
       !rs::op::aligned(counts, 4) || !rs::op::aligned(loss, 4) || !rs::op::aligned(grad, 4))
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (none) {
+    cudaError_t ce = cudaSuccess;
+    if (nseq > 0 && nexperts > 0) ce = cudaMemsetAsync(counts, 0, size_t(4 * nseq * nexperts), st);
+    if (ce == cudaSuccess && loss) ce = cudaMemsetAsync(loss, 0, 4, st);
+    if (ce != cudaSuccess)
+      return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
+    return RESHARD_OK;
+  }
+  int dev = 0, sms = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
   rs::BalanceArgs a = {};
   a.logits = logits;
   a.ld = ld;
@@ -165,27 +482,34 @@ extern "C" reshard_status_t reshard_balance_loss(
   a.counts = counts;
   a.dlogits = dlogits;
   a.tokens = static_cast<int32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + rs::tokens_bytes(nseq));
-  a.nseq = nseq;
-  a.seqlen = seqlen;
-  a.topk = topk;
-  a.chunks = rs::op::cdiv(seqlen, rs::kChunk);
+  a.done = static_cast<uint32_t*>(workspace) + nseq;
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + rs::header_bytes(nseq));
+  a.nseq = int32_t(nseq);
+  a.seqlen = int32_t(seqlen);
+  a.topk = int32_t(topk);
   a.nexperts = int32_t(nexperts);
   a.score = score;
   a.coef = coef;
-  cudaError_t ce = cudaMemsetAsync(counts, 0, size_t(4 * nseq * nexperts), st);
-  if (ce == cudaSuccess) ce = cudaMemsetAsync(a.tokens, 0, size_t(4 * nseq), st);
-  if (ce != cudaSuccess)
-    return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
+  // the counts: a cluster a sequence, more of them for choices beyond 4096 a CTA while there
+  // are SMs for them; a short sequence takes one CTA
+  const int64_t choices = seqlen * topk;
+  const int cluster = choices <= 2048 ? 1 : rs::kCountCluster;
+  const int64_t useful = rs::op::cdiv(choices, 4096 * cluster), room = sms / (nseq * cluster);
+  a.clusters = int32_t(useful < 1 || room < 1 ? 1 : useful < room ? useful : room);
+  if (a.clusters > 1) {
+    ce = cudaMemsetAsync(counts, 0, size_t(4 * nseq * nexperts), st);
+    if (ce == cudaSuccess) ce = cudaMemsetAsync(a.tokens, 0, size_t(4 * nseq), st);
+    if (ce != cudaSuccess)
+      return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
+  }
+  void* args[] = {&a};
+  reshard_status_t status =
+      rs::launch_in(reinterpret_cast<const void*>(rs::count_kernel), nseq * a.clusters * cluster,
+                    rs::kCountThreads, sizeof(int32_t) * size_t(nexperts + 1), cluster, false, st, args);
+  if (status != RESHARD_OK || !(loss || dlogits)) return status;
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    const unsigned grid = none ? 0 : unsigned(a.nseq * a.chunks);
-    if (none) a.chunks = 0;
-    if (grid > 0) {
-      rs::count_kernel<<<grid, 256, 0, st>>>(a);
-      if (loss || dlogits) rs::balance_kernel<T><<<grid, 256, 0, st>>>(a);
-    }
-    if (loss) rs::loss_kernel<<<1, 256, 0, st>>>(a);
-    return rs::op::launched("reshard_balance_loss");
+    return score == RESHARD_SCORE_SOFTMAX ? rs::launch_pass<T, RESHARD_SCORE_SOFTMAX>(a, sms, st)
+                                          : rs::launch_pass<T, RESHARD_SCORE_SIGMOID>(a, sms, st);
   });
 }
