@@ -100,11 +100,12 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
 
 // A token's scores before they are divided by their sum, two at a time: exp(l - top), or
 // 1 / (1 + exp(-l)).  Exponentials are 2^x, x rounded to float32: off by 2^-24 |x| and 2
-// units in the last place (expf spends five times the instructions on less).
+// units in the last place (expf spends five times the instructions on less); scores below
+// 2^-126 are 0.
 constexpr float kLog2E = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint64_t both(float v) {
@@ -137,8 +138,8 @@ struct Score {
     const float2 x = tc::unpack2(mul2(pair(l0, l1), both(-kLog2E)));
     const float2 d = tc::unpack2(add2(pair(exp2_of(x.x), exp2_of(x.y)), both(1.0f)));
     float r0, r1;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
     return pair(r0, r1);
   }
   // the score's own slope: p (softmax) or p (1 - a)
@@ -201,9 +202,40 @@ __device__ void finish(const BalanceArgs& a, float sum, float inv_tokens) {
   }
 }
 
+// The largest of N values (a NaN loses against any number), and two values at once.
+template <int N>
+__device__ __forceinline__ float largest_of(const float (&v)[N]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);
+  return m;
+}
+template <int N>
+__device__ __forceinline__ float largest_of(const __nv_bfloat16 (&v)[N]) {
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(v);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(v + i));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <int N>
+__device__ __forceinline__ float largest_of(const __half (&v)[N]) {
+  __half2 m = *reinterpret_cast<const __half2*>(v);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) m = __hmax2(m, *reinterpret_cast<const __half2*>(v + i));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ void set_pair(float* to, float2 x) { to[0] = x.x, to[1] = x.y; }
+__device__ __forceinline__ void set_pair(__nv_bfloat16* to, float2 x) {
+  *reinterpret_cast<__nv_bfloat162*>(to) = __float22bfloat162_rn(x);
+}
+__device__ __forceinline__ void set_pair(__half* to, float2 x) {
+  *reinterpret_cast<__half2*>(to) = __float22half2_rn(x);
+}
+
 // A token's logits as a lane holds them: N values, read 16 bytes at a time (VEC: every row
 // starts on 16 bytes and ends with a vector) or element by element, neighbouring lanes
-// next to each other either way.  Values beyond the experts are -inf, whose score is 0.
+// next to each other either way.  Values beyond the experts, and all of a token that does
+// not count, are -inf: scores and gradients 0.
 template <typename T, bool VEC, int N>
 struct Logits {
   static constexpr int kPer = VEC ? 16 / int(sizeof(T)) : 1;
@@ -214,20 +246,17 @@ struct Logits {
   }
   __device__ void load(const T* row, bool on, int lane, int lanes, int experts) {
 #pragma unroll
-    for (int i = 0; i < N; i += kPer) {
+    for (int i = 0; i < N; ++i) {
       const int e = expert(i, lane, lanes);
-      if (VEC) {
-        if (on && e < experts)
-          *reinterpret_cast<uint4*>(v + i) = __ldcs(reinterpret_cast<const uint4*>(row + e));
-      } else {
-        if (on && e < experts) v[i] = row[e];
-      }
+      if (on && e < experts) v[i] = row[e];
     }
   }
-  __device__ void clear(int lane, int lanes, int experts) {
+  __device__ void clear() {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = from_float<T>(-INFINITY);
   }
+  __device__ float largest() const { return largest_of(v); }
+  __device__ void set(int i, float2 x) { set_pair(v + i, x); }  // values i and i + 1
   __device__ void store(T* row, int lane, int lanes, int experts) const {
 #pragma unroll
     for (int i = 0; i < N; i += kPer) {
@@ -239,13 +268,14 @@ struct Logits {
   }
 };
 
-// The pass: a token a group of `lanes` lanes, N logits a lane in registers; the next
-// token's are loaded while this one's are worked on.
+// The pass: a token a group of `lanes` lanes, N logits a lane in registers.  While a token
+// is worked on the kAhead next ones are on their way (32 KiB a CTA: registers alone kept
+// too little of the memory busy), one where rows are not aligned.
+constexpr int kAhead = 4;
 template <typename T, int SCORE, bool VEC, int N>
 __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
     balance_kernel(const __grid_constant__ BalanceArgs a, const int lanes) {
   using L = Logits<T, VEC, N>;
-  extern __shared__ float f_smem[];
   const int s = blockIdx.x / a.chunks;
   const int first = blockIdx.x % a.chunks * a.chunk;
   const int end = min(a.seqlen, first + a.chunk);
@@ -255,10 +285,36 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
   T* dlogits = a.dlogits ? static_cast<T*>(a.dlogits) + row0 * a.ld : nullptr;
   auto live = [&](int t) { return t < end && (!a.mask || a.mask[row0 + t] != 0); };
   int t = first + int(threadIdx.x) / lanes;
+  // VEC: a ring of kAhead tokens' vectors in shared memory, each thread's own
+  extern __shared__ __align__(16) float dynamic[];
+  constexpr int kVectors = VEC ? N / L::kPer : 1;
+  uint4* ring = reinterpret_cast<uint4*>(dynamic) + threadIdx.x;  // [kAhead][kVectors][256]
+  float* f_smem = dynamic + (VEC ? kAhead * kVectors * 256 * 4 : 0);
+  auto fetch = [&](int t, bool on, int slot) {
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      const int e = L::expert(i * L::kPer, lane, lanes);
+      if (on && e < a.nexperts)
+        staging::cp_async16(ring + (slot * kVectors + i) * 256, logits + int64_t(t) * a.ld + e);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   L next;
-  next.clear(lane, lanes, a.nexperts);
-  bool on = live(t);
-  next.load(logits + int64_t(t) * a.ld, on, lane, lanes, a.nexperts);
+  next.clear();
+  bool on = live(t);       // whether token t counts, and (VEC) the kAhead ones after it
+  uint32_t ahead = 0;
+  bool coming = false;     // the one after those: read an iteration before it is needed
+  if (VEC) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const bool counts = live(t + d * groups);
+      ahead |= uint32_t(counts) << d;
+      fetch(t + d * groups, counts, d);
+    }
+    coming = live(t + kAhead * groups);
+  } else {
+    next.load(logits + int64_t(t) * a.ld, on, lane, lanes, a.nexperts);
+  }
   wait_for_previous();
   Weighting w;
   w.make(a, s, f_smem);
@@ -269,20 +325,33 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
     f[i / 2] = pair(e0 < a.nexperts ? f_smem[e0] : 0.0f, e1 < a.nexperts ? f_smem[e1] : 0.0f);
   }
   float sum = 0.0f;
+  int slot = 0;
   // the groups of a warp walk together: the shuffles need all lanes
   for (int base = first; base < end; base += groups, t += groups) {
-    const L now = next;
-    const bool counts = on;
-    on = live(t + groups);
-    next.load(logits + int64_t(t + groups) * a.ld, on, lane, lanes, a.nexperts);
+    L now = next;
+    bool counts = on;
+    if (VEC) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      counts = ahead & 1;
+#pragma unroll
+      for (int i = 0; i < kVectors; ++i)
+        if (counts && L::expert(i * L::kPer, lane, lanes) < a.nexperts)
+          *reinterpret_cast<uint4*>(now.v + i * L::kPer) = ring[(slot * kVectors + i) * 256];
+      fetch(t + kAhead * groups, coming, slot);
+      ahead = ahead >> 1 | uint32_t(coming) << (kAhead - 1);
+      coming = live(t + (kAhead + 1) * groups);
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
+    } else {
+      on = live(t + groups);
+      next.clear();
+      next.load(logits + int64_t(t + groups) * a.ld, on, lane, lanes, a.nexperts);
+    }
     L grad;
     if (__any_sync(0xffffffffu, counts)) {
       uint64_t p[N / 2], total2 = both(0.0f), dot2 = both(0.0f);
       float top = 0.0f;
       if (SCORE == RESHARD_SCORE_SOFTMAX) {
-        top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < N; ++i) top = fmaxf(top, to_float(now.v[i]));
+        top = now.largest();
         for (int o = lanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (top == -INFINITY) top = 0.0f;  // all scores 0
       }
@@ -305,8 +374,7 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
       for (int i = 0; i < N; i += 2) {
         const float2 g = tc::unpack2(
             mul2(mul2(scale, Score<SCORE>::slope(p[i / 2])), add2(f[i / 2], minus_dot)));
-        grad.v[i] = from_float<T>(counts ? g.x : 0.0f);
-        grad.v[i + 1] = from_float<T>(counts ? g.y : 0.0f);
+        grad.set(i, g);
       }
     } else {
 #pragma unroll
@@ -413,11 +481,19 @@ reshard_status_t launch_pass(BalanceArgs& a, int64_t sms, cudaStream_t stream) {
                        : vec       ? pass_kernel<T, SCORE, true>(values)
                                    : pass_kernel<T, SCORE, false>(values);
   const int64_t target = sms * (values > 32 ? 8 : values > 16 ? 2 : 3);
-  a.chunk = int32_t(cdiv(cdiv(int64_t(a.nseq) * a.seqlen, target), kChunk) * kChunk);
+  const int64_t per_seq = target / a.nseq > 1 ? target / a.nseq : 1;
+  a.chunk = int32_t(cdiv(cdiv(a.seqlen, per_seq), kChunk) * kChunk);
   a.chunks = int32_t(cdiv(a.seqlen, a.chunk));
   void* args[] = {&a, &lanes};
-  return launch_in(kernel, int64_t(a.nseq) * a.chunks, 256, sizeof(float) * size_t(a.nexperts), 1, true,
-                   stream, args);
+  size_t smem = sizeof(float) * size_t(a.nexperts);
+  if (vec && values <= 32) smem += kAhead * sizeof(T) * 256 * (values <= 8 ? 8 : values <= 16 ? 16 : 32);
+  if (smem > 48 * 1024) {
+    const cudaError_t ce =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (ce != cudaSuccess)
+      return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
+  }
+  return launch_in(kernel, int64_t(a.nseq) * a.chunks, 256, smem, 1, true, stream, args);
 }
 
 }  // namespace
