@@ -24,7 +24,6 @@ namespace {
 using namespace op;
 using staging::mbar_arrive_expect;
 using staging::mbar_init;
-using staging::mbar_wait;
 
 constexpr int kBlock = 128;           // values of k that share a scale, bytes of a tile row
 constexpr int kRows = 128;            // rows of a loaded tile
@@ -134,7 +133,7 @@ __device__ __noinline__ void give_up(uint32_t* status, uint32_t code) {
 // warps a lane quarter, 128 columns each.  (One cta_group::2 instruction for both CTAs
 // loads as little but hands accumulators over between SMs: 416 us against XXX us for
 // 8192 x 14336 x 4096.)
-constexpr int kWideStages = 4;  // 3 where the expert table needs the room
+constexpr int kWideStages = 4;  // 2 where the expert table needs the room
 constexpr int kWideStageBytes = 3 * kTileBytes;
 constexpr int kWideCols = 256;
 constexpr int kWideSumWarps = 8;
@@ -164,7 +163,7 @@ struct WideSmem {
 __host__ __device__ constexpr size_t wide_stages_at(size_t table_bytes) {
   return (sizeof(WideSmem) + table_bytes + 1023) / 1024 * 1024;
 }
-static_assert(wide_stages_at(kTableMost) + 3 * kWideStageBytes <= kSmemMost, "shared memory");
+static_assert(wide_stages_at(kTableMost) + 2 * kWideStageBytes <= kSmemMost, "shared memory");
 
 template <typename Y>
 __global__ void __launch_bounds__(kWideThreads, 1)
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int t = pair; ok && t < total; t += pairs) {
       const Tile tile(table, a.nexperts, t, 2 * kRows, kWideCols);
       for (int b = 0; b < a.blocks; ++b) {
-        if (!(ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls))) break;
+        if (!(ok = tc::warp_wait(&sm.empty[stage], parity))) break;
         if (lane == 0) {
           mbar_arrive_expect(&sm.full[stage], kWideStageBytes);
           const uint32_t bar = staging::smem_addr(&sm.full[stage]);
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     // every matrix instruction has let go of its stage before this CTA may end
     for (int i = 0; ok && i < stages; ++i) {
-      ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls);
+      ok = tc::warp_wait(&sm.empty[stage], parity);
       if (++stage == uint32_t(stages)) stage = 0, parity ^= 1;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusLoadWait);
@@ -231,13 +230,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::registers_down<kWideOtherRegisters>();
     if (warp <= kWideSumWarps + 2) {  // matrix instructions
       constexpr uint32_t instruction = tc::e4m3_instruction(kRows, kWideCols);
-      const uint32_t buf = warp - (kWideSumWarps + 1);  // this warp's accumulator: every other block
+      // This warp's accumulator, for every other block; the stages are two or four, so that
+      // each is one warp's too (a barrier's phases are told apart by parity, which only holds
+      // for a warp that sees all of them).
+      const uint32_t buf = warp - (kWideSumWarps + 1);
       const int count = pair < total ? ((total - 1 - pair) / pairs + 1) * a.blocks : 0;
       uint32_t stage = buf, parity = 0, buf_parity = 1;
       bool ok = true;
       for (int i = buf; i < count; i += 2) {
-        if (!(ok = mbar_wait(&sm.sum_empty[buf], buf_parity, staging::kWaitPolls))) break;
-        if (!(ok = mbar_wait(&sm.full[stage], parity, staging::kWaitPolls))) break;
+        if (!(ok = tc::warp_wait(&sm.sum_empty[buf], buf_parity))) break;
+        if (!(ok = tc::warp_wait(&sm.full[stage], parity))) break;
         tc::fence_after_sync();
         if (lane == 0) {
           const uint32_t src = data + stage * kWideStageBytes;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         const uint32_t s = __float_as_uint(scales[lane * kScalePitch + b % kScaleBlocks]);
         const uint64_t scale = tc::pack2(s, s);
-        if (!(ok = mbar_wait(&sm.sum_full[buf], parity, staging::kWaitPolls))) break;
+        if (!(ok = tc::warp_wait(&sm.sum_full[buf], parity))) break;
         tc::fence_after_sync();
         const uint32_t from = lanes + buf * kWideCols;
         uint32_t v[2][16];
@@ -355,10 +357,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
         } else {
-          for (int r = 0; r < 32 && row0 + r < tile.end; ++r)
-            for (int c = lane; c < kChunk && c0 + c < a.n; c += 32)
+#pragma unroll 8
+          for (int i = lane; i < 32 * kChunk; i += 32) {
+            const int r = i / kChunk, c = i % kChunk;
+            if (row0 + r < tile.end && c0 + c < a.n)
               y[int64_t(row0 + r) * a.ldy + c0 + c] =
                   *reinterpret_cast<const Y*>(out + r * kOutPitch + c * sizeof(Y));
+          }
         }
         __syncwarp();
       }
@@ -373,136 +378,156 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 }
 
 // ----------------------------------------------------------------------------- narrow
-// Six warps a CTA, one tile of 128 features x NT tokens a CTA.  `split` CTAs of a cluster
-// take a share of the blocks of k each and add their sums through distributed shared
-// memory in rank order.
-template <int NT>
-struct NarrowShape {
-  static constexpr int kStageBytes = kTileBytes + NT * kBlock;
-  // two CTAs an SM where that leaves them three stages each
-  static constexpr int kStages = NT <= 16 ? 5 : NT <= 32 ? 4 : 3;
-  static constexpr int kBufs = NT <= 64 ? 4 : 2;  // accumulators
-  static constexpr int kColumns = kBufs * NT;     // of tensor memory: 64, 128, 256, 256
-};
-constexpr int kNarrowThreads = 32 * 6;
+// One tile of 128 features x NT tokens a CTA: four summing warps, a loading warp and two
+// matrix warps.  `split` CTAs of a cluster take a share of the blocks of k each and send
+// their sums through distributed shared memory to the CTA that adds up the column, in rank
+// order.
+constexpr int kMatrixWarps = 2;
+constexpr int kMostSplit = 8;
+constexpr int kNarrowThreads = 32 * (5 + kMatrixWarps);
+constexpr int kNarrowStages = 4, kNarrowBufs = 4;
+static_assert(kNarrowStages % kMatrixWarps == 0 && kNarrowBufs % kMatrixWarps == 0,
+              "a stage and an accumulator belong to one matrix warp each");
 
 template <int NT>
 struct NarrowSmem {
-  using S = NarrowShape<NT>;
-  alignas(1024) unsigned char stages[S::kStages][S::kStageBytes];
-  alignas(16) float sums[NT][kRows];
-  alignas(16) float scales[4][2][NT];
-  uint64_t full[S::kStages], empty[S::kStages], sum_full[S::kBufs], sum_empty[S::kBufs];
+  static constexpr int kStageBytes = kTileBytes + NT * kBlock;
+  alignas(1024) unsigned char stages[kNarrowStages][kStageBytes];
+  alignas(16) float scales[2][kScaleBlocks][NT + 4];  // no bank conflicts where they are written
+  uint64_t full[kNarrowStages], empty[kNarrowStages], sum_full[kNarrowBufs], sum_empty[kNarrowBufs];
   uint32_t tmem;
+  // behind it: the expert table and, with several CTAs a tile, float sums[NT, rounded up to
+  // whole splits][kRows]
+  __host__ __device__ static constexpr size_t sums_at(size_t table_bytes) {
+    return (sizeof(NarrowSmem) + table_bytes + 15) / 16 * 16;
+  }
 };
-static_assert(sizeof(NarrowSmem<128>) + kTableMost <= kSmemMost, "shared memory");
+static_assert(NarrowSmem<64>::sums_at(kTableMost) + (64 + kMostSplit) * kRows * 4 <= kSmemMost, "shared memory");
 
 template <int NT, typename Y>
-__global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kNarrowThreads, 2)
     narrow_kernel(const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_w, const __grid_constant__ MatmulArgs a,
                   const int split) {
-  using S = NarrowShape<NT>;
+  using S = NarrowSmem<NT>;
   extern __shared__ __align__(1024) unsigned char dynamic[];
   NarrowSmem<NT>& sm = *reinterpret_cast<NarrowSmem<NT>*>(dynamic);
   ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(NarrowSmem<NT>)), a.nexperts);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float(*sums)[kRows] = reinterpret_cast<float(*)[kRows]>(
+      dynamic + NarrowSmem<NT>::sums_at(ExpertTable::bytes(a.nexperts)));
   const int rank = int(blockIdx.x) % split, index = int(blockIdx.x) / split;
 
-  table.build(a, NT);
-  __syncthreads();
-  if (index >= table.tiles[a.nexperts]) return;  // the whole cluster
-  if (threadIdx.x == 0) {
+  if (split > 1) tc::cluster_arrive();  // the others run before this CTA writes to them
+  if (threadIdx.x == 128) {
     tc::prefetch_map(&map_x);
     tc::prefetch_map(&map_w);
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
-    }
-    for (int i = 0; i < S::kBufs; ++i) {
-      mbar_init(&sm.sum_full[i], 1);
-      mbar_init(&sm.sum_empty[i], 4);
-    }
-    tc::fence_barrier_init();
   }
-  if (warp == 5) tc::tmem_alloc(&sm.tmem, S::kColumns);
-  tc::fence_before_sync();
+  table.build(a, NT);
   __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = sm.tmem;
+  if (index >= table.tiles[a.nexperts]) {  // the whole cluster
+    if (split > 1) tc::cluster_wait();
+    return;
+  }
   const Tile tile(table, a.nexperts, index, NT, kRows);
   const int b0 = int(int64_t(a.blocks) * rank / split);
   const int b1 = int(int64_t(a.blocks) * (rank + 1) / split);
   const int cols = min(NT, tile.end - tile.row);
+  auto load = [&](int b, uint32_t stage) {
+    mbar_arrive_expect(&sm.full[stage], S::kStageBytes);
+    const uint32_t bar = staging::smem_addr(&sm.full[stage]);
+    const uint32_t dst = staging::smem_addr(sm.stages[stage]);
+    tc::load_box(dst, &map_w, bar, b * kBlock, tile.n0, tile.e);
+    tc::load_box(dst + kTileBytes, &map_x, bar, b * kBlock, tile.row, 0);
+  };
+  if (warp == 4 && lane == 0) {  // the first loads wait for nothing else
+    for (int i = 0; i < kNarrowStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < kNarrowBufs; ++i) {
+      mbar_init(&sm.sum_full[i], 1);
+      mbar_init(&sm.sum_empty[i], 4);
+    }
+    tc::fence_barrier_init();
+    for (int i = 0; i < kNarrowStages && b0 + i < b1; ++i) load(b0 + i, i);
+  }
+  __syncwarp();
+  if (warp == 5) tc::tmem_alloc(&sm.tmem, kNarrowBufs * NT);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (split > 1) tc::cluster_wait();
+  const uint32_t tmem = sm.tmem;
 
   if (warp == 4) {  // loads
-    uint32_t stage = 0, parity = 1;
+    uint32_t stage = 0, parity = 0;
     bool ok = true;
-    for (int b = b0; b < b1; ++b) {
-      if (!(ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls))) break;
-      if (lane == 0) {
-        mbar_arrive_expect(&sm.full[stage], S::kStageBytes);
-        const uint32_t bar = staging::smem_addr(&sm.full[stage]);
-        const uint32_t dst = staging::smem_addr(sm.stages[stage]);
-        tc::load_box(dst, &map_w, bar, b * kBlock, tile.n0, tile.e);
-        tc::load_box(dst + kTileBytes, &map_x, bar, b * kBlock, tile.row, 0);
-      }
+    for (int b = b0 + kNarrowStages; b < b1; ++b) {
+      if (!(ok = tc::warp_wait(&sm.empty[stage], parity))) break;
+      if (lane == 0) load(b, stage);
       __syncwarp();
-      if (++stage == S::kStages) stage = 0, parity ^= 1;
+      if (++stage == kNarrowStages) stage = 0, parity ^= 1;
     }
     // every matrix instruction has let go of its stage before this CTA may end
-    for (int i = 0; ok && i < S::kStages; ++i) {
-      ok = mbar_wait(&sm.empty[stage], parity, staging::kWaitPolls);
-      if (++stage == S::kStages) stage = 0, parity ^= 1;
+    for (int i = 0; ok && i < kNarrowStages && i < b1 - b0; ++i) {
+      ok = tc::warp_wait(&sm.empty[stage], parity);
+      if (++stage == kNarrowStages) stage = 0, parity ^= 1;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusLoadWait);
-  } else if (warp == 5) {  // matrix instructions
+  } else if (warp >= 5) {  // matrix instructions, every other block
     constexpr uint32_t instruction = tc::e4m3_instruction(kRows, NT);
-    uint32_t stage = 0, parity = 0, buf = 0, buf_parity = 1;
     bool ok = true;
-    for (int b = b0; b < b1; ++b) {
-      if (!(ok = mbar_wait(&sm.sum_empty[buf], buf_parity, staging::kWaitPolls))) break;
-      if (!(ok = mbar_wait(&sm.full[stage], parity, staging::kWaitPolls))) break;
+    for (int i = warp - 5; i < b1 - b0; i += kMatrixWarps) {
+      const uint32_t stage = i % kNarrowStages, buf = i % kNarrowBufs;
+      if (!(ok = tc::warp_wait(&sm.sum_empty[buf], (i / kNarrowBufs & 1) ^ 1))) break;
+      if (!(ok = tc::warp_wait(&sm.full[stage], i / kNarrowStages & 1))) break;
       tc::fence_after_sync();
       if (lane == 0) {
         const uint32_t src = staging::smem_addr(sm.stages[stage]);
         const uint64_t dw = tc::tile_desc(src), dx = tc::tile_desc(src + kTileBytes);
         for (int k = 0; k < 4; ++k)
           tc::mma_e4m3(tmem + buf * NT, dw + 2 * k, dx + 2 * k, instruction, k > 0);
-        tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
         tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
+        tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
       }
       __syncwarp();
-      if (++stage == S::kStages) stage = 0, parity ^= 1;
-      if (++buf == S::kBufs) buf = 0, buf_parity ^= 1;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusMatrixWait);
   } else {  // sums: a thread has one feature of every token
     const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
     const float* ws = a.ws + (int64_t(tile.e) * a.col_blocks + tile.n0 / kBlock) * a.ldws;
-    constexpr int kPer = (NT + 31) / 32;
-    const float* xs[kPer];
-    float next[kPer], sw = 0.0f;
-    for (int i = 0; i < kPer; ++i) {
-      xs[i] = a.xs + int64_t(min(tile.row + i * 32 + lane, a.tokens - 1)) * a.ldxs;
-      next[i] = b0 < b1 ? xs[i][b0] : 0.0f;
-    }
-    if (b0 < b1) sw = ws[b0];
+    // The four warps fetch the scales of every token for 8 blocks at a time, a sector a
+    // token, and share the products of both scales in shared memory.
+    float next_x[NT / 16], next_w = 0.0f;
+    auto fetch = [&](int begin) {
+      const int b = begin + lane % kScaleBlocks;
+      if (b >= b1) return;
+      next_w = ws[b];
+#pragma unroll
+      for (int i = 0; i < NT / 16; ++i)
+        next_x[i] =
+            a.xs[int64_t(min(tile.row + 16 * i + int(threadIdx.x) / kScaleBlocks, a.tokens - 1)) * a.ldxs + b];
+    };
+    fetch(b0);
     uint64_t acc[NT / 2];
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) acc[i] = 0;
     uint32_t buf = 0, parity = 0;
     bool ok = true;
     for (int b = b0; b < b1; ++b) {
-      float* scales = sm.scales[warp][b & 1];
+      const int step = b - b0;
+      if (step % kScaleBlocks == 0) {
+        float(*to)[NT + 4] = sm.scales[step / kScaleBlocks & 1];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (NT >= 32 || lane < NT) scales[i * 32 + lane] = next[i] * sw;
-        if (b + 1 < b1) next[i] = xs[i][b + 1];
+        for (int i = 0; i < NT / 16; ++i)
+          to[lane % kScaleBlocks][16 * i + threadIdx.x / kScaleBlocks] = next_x[i] * next_w;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        fetch(b + kScaleBlocks);
       }
-      if (b + 1 < b1) sw = ws[b + 1];
-      __syncwarp();
-      if (!(ok = mbar_wait(&sm.sum_full[buf], parity, staging::kWaitPolls))) break;
+      const float* scales = sm.scales[step / kScaleBlocks & 1][step % kScaleBlocks];
+      // no way out of the loop before its end: the other warps wait at the barrier above
+      ok = ok && tc::warp_wait(&sm.sum_full[buf], parity);
       tc::fence_after_sync();
       const uint32_t from = lanes + buf * NT;
       uint32_t v[2][16];
@@ -523,7 +548,7 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) staging::mbar_arrive(&sm.sum_empty[buf]);
-      if (++buf == S::kBufs) buf = 0, parity ^= 1;
+      if (++buf == kNarrowBufs) buf = 0, parity ^= 1;
     }
     if (!ok && lane == 0) give_up(a.status, kStatusSumWait);
     const int feature = warp * 32 + lane;
@@ -538,11 +563,18 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
         }
       }
     } else {
+      // column c to CTA c % split
+      const uint32_t at = staging::smem_addr(&sums[rank][feature]);
 #pragma unroll
       for (int i = 0; i < NT / 2; ++i) {
         const float2 f = tc::unpack2(acc[i]);
-        if (2 * i < cols) sm.sums[2 * i][feature] = f.x;
-        if (2 * i + 1 < cols) sm.sums[2 * i + 1][feature] = f.y;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = 2 * i + h;
+          if (c < cols)
+            tc::store_cluster(tc::in_cta(at + c / split * split * int(sizeof(sums[0])), c % split),
+                              h ? f.y : f.x);
+        }
       }
     }
   }
@@ -551,19 +583,20 @@ __global__ void __launch_bounds__(kNarrowThreads, NT <= 64 ? 2 : 1)
     tc::cluster_sync();
     if (warp < 4 && tile.n0 + int(threadIdx.x) < a.n) {
       Y* y = static_cast<Y*>(a.y) + int64_t(tile.row) * a.ldy + tile.n0 + threadIdx.x;
+#pragma unroll 2
       for (int c = rank; c < cols; c += split) {
-        const uint32_t at = staging::smem_addr(&sm.sums[c][threadIdx.x]);
         float sum = 0.0f;
-        for (int r = 0; r < split; ++r) sum += tc::load_cluster(tc::in_cta(at, r));
+#pragma unroll
+        for (int r = 0; r < kMostSplit; ++r)
+          if (r < split) sum += sums[c - rank + r][threadIdx.x];
         y[int64_t(c) * a.ldy] = from_float<Y>(sum);
       }
     }
     __syncwarp();
-    tc::cluster_sync();
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 5) tc::tmem_free(tmem, S::kColumns);
+  if (warp == 5) tc::tmem_free(tmem, kNarrowBufs * NT);
 }
 
 // An inner size of zero: the rows of experts get zeros.
@@ -646,7 +679,7 @@ reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int sms, cudaStre
   const int64_t most = a.ntiles * (cdiv(a.tokens, 2 * kRows) + (a.nexperts > 1 ? a.nexperts : 0));
   const int64_t pairs = most < sms / 2 ? most : sms / 2;
   const size_t at = wide_stages_at(ExpertTable::bytes(a.nexperts));
-  int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : kWideStages - 1;
+  int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : 2;
   void* args[] = {&map_x, &map_w, &a, &stages};
   return launch(reinterpret_cast<const void*>(wide_kernel<Y>), unsigned(2 * pairs), kWideThreads,
                 at + size_t(stages) * kWideStageBytes, 2, stream, args);
@@ -661,14 +694,19 @@ reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int sms, cudaSt
   a.ntiles = int32_t(cdiv(a.n, kRows));
   int64_t tiles = a.ntiles * cdiv(a.tokens, NT);
   if (a.offsets) tiles = a.ntiles * (a.tokens / NT + (a.nexperts < a.tokens ? a.nexperts : a.tokens));
+  // as many CTAs a tile as are on the GPU at a time (two an SM, one with 64 tokens' sums),
+  // with two blocks each: a second wave would cost more than longer shares
+  const int64_t room = sms * (NT <= 32 ? 2 : 1);
   int split = 1;
-  while (split < 8 && tiles * split < 2 * sms && a.blocks >= 4 * split) split *= 2;
+  while (split < kMostSplit && tiles * (split + 1) <= room && a.blocks >= 2 * (split + 1)) ++split;
   if (tiles * split >= int64_t(1) << 31)
     return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
+  const size_t table = ExpertTable::bytes(a.nexperts);
+  const size_t smem = split > 1 ? NarrowSmem<NT>::sums_at(table) + sizeof(float) * kRows * size_t(cdiv(NT, split) * split)
+                                : sizeof(NarrowSmem<NT>) + table;
   void* args[] = {&map_x, &map_w, &a, &split};
   return launch(reinterpret_cast<const void*>(narrow_kernel<NT, Y>), unsigned(tiles * split),
-                kNarrowThreads, sizeof(NarrowSmem<NT>) + ExpertTable::bytes(a.nexperts), split, stream,
-                args);
+                kNarrowThreads, smem, split, stream, args);
 }
 
 template <typename Y>
@@ -688,13 +726,11 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
   if (!a.offsets) {
     if (each <= 16) return launch_narrow<16, Y>(a, o, sms, stream);
     if (each <= 32) return launch_narrow<32, Y>(a, o, sms, stream);
-    if (each <= 64) return launch_narrow<64, Y>(a, o, sms, stream);
-    if (each <= 128) return launch_narrow<128, Y>(a, o, sms, stream);
+    if (each <= 128) return launch_narrow<64, Y>(a, o, sms, stream);
   } else {
     if (each <= 4) return launch_narrow<16, Y>(a, o, sms, stream);
     if (each <= 8) return launch_narrow<32, Y>(a, o, sms, stream);
-    if (each <= 16) return launch_narrow<64, Y>(a, o, sms, stream);
-    if (each <= 64) return launch_narrow<128, Y>(a, o, sms, stream);
+    if (each <= 64) return launch_narrow<64, Y>(a, o, sms, stream);
   }
   return launch_wide<Y>(a, o, sms, stream);
 }
