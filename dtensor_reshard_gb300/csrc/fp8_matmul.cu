@@ -28,6 +28,7 @@ using staging::mbar_init;
 constexpr int kBlock = 128;           // values of k that share a scale, bytes of a tile row
 constexpr int kRows = 128;            // rows of a loaded tile
 constexpr int kTileBytes = kRows * kBlock;
+constexpr int kMostSplit = 8;         // CTAs of a cluster that share the blocks of k
 
 // Codes for the device status word (staging.cuh has 1 to 4).
 enum : unsigned int {
@@ -45,7 +46,7 @@ struct MatmulArgs {
   void* y;
   int64_t ldy;
   uint32_t* status;
-  int32_t aligned_y;  // every row of y starts on 16 bytes
+  int32_t aligned_y;  // every row of y starts on 32 or 16 bytes, or 0
 };
 
 // Each expert's first row and first tile, in shared memory: start[e], tiles[e] for
@@ -165,7 +166,18 @@ __host__ __device__ constexpr size_t wide_stages_at(size_t table_bytes) {
 }
 static_assert(wide_stages_at(kTableMost) + 2 * kWideStageBytes <= kSmemMost, "shared memory");
 
-template <typename Y>
+// SPLIT: for fewer tokens than fill the GPU that way, a tile of 128 tokens x 256 features a
+// cluster, of which each CTA takes a share of the blocks of k; the sums of 16 columns at a
+// time go to the CTA that adds them up, in rank order, through distributed shared memory
+// (in the place of the stages).
+constexpr int kSplitChunk = 16;  // columns
+constexpr int kSplitChunkBytes = kRows * kSplitChunk * 4;
+// Chunks that a CTA receives at most, from all CTAs of a split.
+__host__ __device__ constexpr int split_chunks(int split) {
+  return (kWideCols / kSplitChunk + split - 1) / split * split;
+}
+
+template <typename Y, bool SPLIT>
 __global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ MatmulArgs a, const int stages) {
@@ -174,7 +186,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(WideSmem)), a.nexperts);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  uint32_t ctas = 2;
+  if (SPLIT) asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int unit = blockIdx.x / ctas, units = gridDim.x / ctas;
+  constexpr int kTileRows = SPLIT ? kRows : 2 * kRows;
+  const int first_row = SPLIT ? 0 : int(rank) * kRows;  // of this CTA in a tile
+  const int b0 = SPLIT ? int(int64_t(a.blocks) * rank / ctas) : 0;
+  const int b1 = SPLIT ? int(int64_t(a.blocks) * (rank + 1) / ctas) : a.blocks;
   const uint32_t data =
       staging::smem_addr(dynamic) + uint32_t(wide_stages_at(ExpertTable::bytes(a.nexperts)));
 
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::prefetch_map(&map_w);
     for (int i = 0; i < stages; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 2);  // both CTAs write into a stage
+      mbar_init(&sm.empty[i], SPLIT ? 1 : 2);  // both CTAs of a pair write into a stage
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sum_full[i], 1);
@@ -192,7 +210,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::fence_barrier_init();
   }
   if (warp == kWideSumWarps + 1) tc::tmem_alloc(&sm.tmem, 512);
-  table.build(a, 2 * kRows);
+  table.build(a, kTileRows);
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();
@@ -204,17 +222,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::registers_down<kWideOtherRegisters>();
     uint32_t stage = 0, parity = 1;
     bool ok = true;
-    for (int t = pair; ok && t < total; t += pairs) {
-      const Tile tile(table, a.nexperts, t, 2 * kRows, kWideCols);
-      for (int b = 0; b < a.blocks; ++b) {
+    for (int t = unit; ok && t < total; t += units) {
+      const Tile tile(table, a.nexperts, t, kTileRows, kWideCols);
+      for (int b = b0; b < b1; ++b) {
         if (!(ok = tc::warp_wait(&sm.empty[stage], parity))) break;
         if (lane == 0) {
           mbar_arrive_expect(&sm.full[stage], kWideStageBytes);
           const uint32_t bar = staging::smem_addr(&sm.full[stage]);
           const uint32_t dst = data + stage * kWideStageBytes;
-          tc::load_box(dst, &map_x, bar, b * kBlock, tile.row + int(rank) * kRows, 0);
-          tc::load_box_both(dst + (1 + rank) * kTileBytes, &map_w, bar, b * kBlock,
-                            tile.n0 + int(rank) * kRows, tile.e);
+          tc::load_box(dst, &map_x, bar, b * kBlock, tile.row + first_row, 0);
+          if (SPLIT) {
+            tc::load_box(dst + kTileBytes, &map_w, bar, b * kBlock, tile.n0, tile.e);
+            tc::load_box(dst + 2 * kTileBytes, &map_w, bar, b * kBlock, tile.n0 + kRows, tile.e);
+          } else {
+            tc::load_box_both(dst + (1 + rank) * kTileBytes, &map_w, bar, b * kBlock,
+                              tile.n0 + int(rank) * kRows, tile.e);
+          }
         }
         __syncwarp();
         if (++stage == uint32_t(stages)) stage = 0, parity ^= 1;
@@ -234,7 +257,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // each is one warp's too (a barrier's phases are told apart by parity, which only holds
       // for a warp that sees all of them).
       const uint32_t buf = warp - (kWideSumWarps + 1);
-      const int count = pair < total ? ((total - 1 - pair) / pairs + 1) * a.blocks : 0;
+      const int count = unit < total ? ((total - 1 - unit) / units + 1) * (b1 - b0) : 0;
       uint32_t stage = buf, parity = 0, buf_parity = 1;
       bool ok = true;
       for (int i = buf; i < count; i += 2) {
@@ -247,7 +270,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           for (int k = 0; k < 4; ++k)  // 32 bytes of k an instruction
             tc::mma_e4m3(tmem + buf * kWideCols, dx + 2 * k, dw + 2 * k, instruction, k > 0);
           tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
-          tc::mma_commit_both(staging::smem_addr(&sm.empty[stage]));
+          if (SPLIT) tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
+          else tc::mma_commit_both(staging::smem_addr(&sm.empty[stage]));
         }
         __syncwarp();
         stage += 2;
@@ -265,9 +289,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     float next_x[8], next_w = 0.0f;  // scales of the 8 blocks to come
     auto fetch = [&](const Tile& tile, int b0) {
       const int b = b0 + lane % kScaleBlocks;
-      const int row0 = tile.row + int(rank) * kRows + quarter * 32 + lane / kScaleBlocks;
+      const int row0 = tile.row + first_row + quarter * 32 + lane / kScaleBlocks;
       const int block = min((tile.n0 + part * kWideWarpCols) / kBlock, a.col_blocks - 1);
-      if (b >= a.blocks) return;
+      if (b >= b1) return;
       next_w = a.ws[(int64_t(tile.e) * a.col_blocks + block) * a.ldws + b];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -276,29 +300,30 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint32_t buf = 0, parity = 0;
     bool ok = true;
     Tile tile;
-    if (pair < total) {
-      tile = Tile(table, a.nexperts, pair, 2 * kRows, kWideCols);
-      fetch(tile, 0);
+    if (unit < total) {
+      tile = Tile(table, a.nexperts, unit, kTileRows, kWideCols);
+      fetch(tile, b0);
     }
-    for (int t = pair; ok && t < total; t += pairs) {
-      const Tile following(table, a.nexperts, min(t + pairs, total - 1), 2 * kRows, kWideCols);
-      const int row0 = tile.row + int(rank) * kRows + quarter * 32;
+    for (int t = unit; ok && t < total; t += units) {
+      const Tile following(table, a.nexperts, min(t + units, total - 1), kTileRows, kWideCols);
+      const int row0 = tile.row + first_row + quarter * 32;
       const int col0 = tile.n0 + part * kWideWarpCols;
       uint64_t acc[kWideWarpCols / 2];
 #pragma unroll
       for (int i = 0; i < kWideWarpCols / 2; ++i) acc[i] = 0;
-      for (int b = 0; b < a.blocks; ++b) {
-        if (b % kScaleBlocks == 0) {
+      for (int b = b0; b < b1; ++b) {
+        const int step = b - b0;
+        if (step % kScaleBlocks == 0) {
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             scales[(4 * i + lane / kScaleBlocks) * kScalePitch + lane % kScaleBlocks] =
                 next_x[i] * next_w;
           __syncwarp();
-          const bool last = b + kScaleBlocks >= a.blocks;
-          fetch(last ? following : tile, last ? 0 : b + kScaleBlocks);
+          const bool last = b + kScaleBlocks >= b1;
+          fetch(last ? following : tile, last ? b0 : b + kScaleBlocks);
         }
-        const uint32_t s = __float_as_uint(scales[lane * kScalePitch + b % kScaleBlocks]);
+        const uint32_t s = __float_as_uint(scales[lane * kScalePitch + step % kScaleBlocks]);
         const uint64_t scale = tc::pack2(s, s);
         if (!(ok = tc::warp_wait(&sm.sum_full[buf], parity))) break;
         tc::fence_after_sync();
@@ -319,24 +344,96 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (lane == 0) staging::mbar_arrive(&sm.sum_empty[buf]);
         if (++buf == 2) buf = 0, parity ^= 1;
       }
+      if (SPLIT && ctas > 1) {  // one tile a cluster
+        tc::cluster_sync();     // every CTA is done with its stages
+        // [slot of a chunk][CTA][4 columns][row][4]: a warp's store is 512 bytes in a row
+        const uint32_t at = data + rank * kSplitChunkBytes + (quarter * 32 + lane) * 16;
+        const int chunk0 = part * (kWideWarpCols / kSplitChunk);
+        uint32_t owner = chunk0 % ctas, to = at + chunk0 / ctas * ctas * kSplitChunkBytes;
+        const bool any = row0 < tile.end;
+#pragma unroll
+        for (int i = 0; i < kWideWarpCols / kSplitChunk; ++i) {
+          const uint32_t there = tc::in_cta(to, owner);
+          if (any) {
+#pragma unroll
+            for (int j = 0; j < kSplitChunk / 4; ++j)
+              tc::store_cluster16(there + j * (kRows * 16), acc[i * (kSplitChunk / 2) + 2 * j],
+                                  acc[i * (kSplitChunk / 2) + 2 * j + 1]);
+          }
+          if (++owner == ctas) owner = 0, to += ctas * kSplitChunkBytes;
+        }
+        tc::cluster_sync();
+        const float4* sums = reinterpret_cast<const float4*>(
+            dynamic + wide_stages_at(ExpertTable::bytes(a.nexperts)));
+        Y* y = static_cast<Y*>(a.y) + int64_t(tile.row) * a.ldy + tile.n0;
+        const int rows = ok ? min(tile.end - tile.row, kRows) : 0, cols = a.n - tile.n0;
+        for (int chunk = int(rank), slot = 0; chunk < kWideCols / kSplitChunk; chunk += ctas, slot += ctas) {
+          const float4* chunks = sums + slot * (kSplitChunkBytes / 16);
+          if (a.aligned_y && (chunk + 1) * kSplitChunk <= cols) {  // 8 columns of a row a thread
+            const int r = threadIdx.x % kRows, h = threadIdx.x / kRows * 8;
+            float sum[8] = {};
+            const float4* from = chunks + h / 4 * kRows + r;
+            for (int q = 0; q < int(ctas); ++q, from += kSplitChunkBytes / 16) {
+              const float4 lo = from[0], hi = from[kRows];
+              sum[0] += lo.x, sum[1] += lo.y, sum[2] += lo.z, sum[3] += lo.w;
+              sum[4] += hi.x, sum[5] += hi.y, sum[6] += hi.z, sum[7] += hi.w;
+            }
+            __align__(16) Y v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = from_float<Y>(sum[j]);
+            uint4* to = reinterpret_cast<uint4*>(y + int64_t(r) * a.ldy + chunk * kSplitChunk + h);
+            if (r < rows) {
+#pragma unroll
+              for (int j = 0; j < int(sizeof(Y)) / 2; ++j) to[j] = reinterpret_cast<const uint4*>(v)[j];
+            }
+          } else {  // neighbouring lanes on neighbouring columns
+            const int c = threadIdx.x % kSplitChunk, col = chunk * kSplitChunk + c;
+            for (int r = threadIdx.x / kSplitChunk; r < rows; r += 32 * kWideSumWarps / kSplitChunk) {
+              const float* from = reinterpret_cast<const float*>(chunks + c / 4 * kRows + r) + c % 4;
+              float sum = 0.0f;
+              for (int q = 0; q < int(ctas); ++q) sum += from[q * (kSplitChunkBytes / 4)];
+              if (col < cols) y[int64_t(r) * a.ldy + col] = from_float<Y>(sum);
+            }
+          }
+        }
+        break;
+      }
       if (!ok) break;
+      if (a.aligned_y == 32 && col0 + kWideWarpCols <= a.n) {
+        // whole sectors from every lane: few instructions, which are new to the SM at the end
+        // of its first tile
+        if (row0 + lane < tile.end) {
+          Y* to = static_cast<Y*>(a.y) + int64_t(row0 + lane) * a.ldy + col0;
+          constexpr int kVec = 32 / int(sizeof(Y));
+#pragma unroll
+          for (int j = 0; j < kWideWarpCols / kVec; ++j) tc::store32(to + j * kVec, acc + j * (kVec / 2));
+        }
+        tile = following;
+        continue;
+      }
       // through shared memory, so that neighbouring lanes store neighbouring columns
       constexpr int kChunk = kOutRow / int(sizeof(Y));  // columns of a round
       constexpr int kVec = 16 / int(sizeof(Y));
+      static_assert(32 % kChunk == 0, "a lane keeps its column");
       Y* y = static_cast<Y*>(a.y);
-#pragma unroll
+      // (whose code is there once for all rounds)
+#pragma unroll 1
       for (int round = 0; round < kWideWarpCols / kChunk; ++round) {
 #pragma unroll
-        for (int j = 0; j < kOutRow / 16; ++j) {
-          __align__(16) Y vec[kVec];
+        for (int rr = 0; rr < kWideWarpCols / kChunk; ++rr) {
+          if (rr != round) continue;
 #pragma unroll
-          for (int i = 0; i < kVec / 2; ++i) {
-            const float2 f = tc::unpack2(acc[(round * kChunk + j * kVec) / 2 + i]);
-            vec[2 * i] = from_float<Y>(f.x);
-            vec[2 * i + 1] = from_float<Y>(f.y);
+          for (int j = 0; j < kOutRow / 16; ++j) {
+            __align__(16) Y vec[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) {
+              const float2 f = tc::unpack2(acc[(rr * kChunk + j * kVec) / 2 + i]);
+              vec[2 * i] = from_float<Y>(f.x);
+              vec[2 * i + 1] = from_float<Y>(f.y);
+            }
+            *reinterpret_cast<uint4*>(out + lane * kOutPitch + j * 16) =
+                *reinterpret_cast<const uint4*>(vec);
           }
-          *reinterpret_cast<uint4*>(out + lane * kOutPitch + j * 16) =
-              *reinterpret_cast<const uint4*>(vec);
         }
         __syncwarp();
         const int c0 = col0 + round * kChunk;
@@ -357,12 +454,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
         } else {
-#pragma unroll 8
-          for (int i = lane; i < 32 * kChunk; i += 32) {
-            const int r = i / kChunk, c = i % kChunk;
-            if (row0 + r < tile.end && c0 + c < a.n)
-              y[int64_t(row0 + r) * a.ldy + c0 + c] =
-                  *reinterpret_cast<const Y*>(out + r * kOutPitch + c * sizeof(Y));
+          // eight loads, then eight stores: a store to y would hold up loads behind it
+          for (int i0 = lane; i0 < 32 * kChunk; i0 += 8 * 32) {
+            Y v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int e = i0 + 32 * i;
+              v[i] = *reinterpret_cast<const Y*>(out + e / kChunk * kOutPitch + e % kChunk * sizeof(Y));
+            }
+            Y* to = y + int64_t(row0 + i0 / kChunk) * a.ldy + c0 + i0 % kChunk;
+            const bool inside = c0 + i0 % kChunk < a.n;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (inside && row0 + (i0 + 32 * i) / kChunk < tile.end)
+                to[int64_t(32 / kChunk * i) * a.ldy] = v[i];
           }
         }
         __syncwarp();
@@ -372,6 +477,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (!ok && lane == 0) give_up(a.status, kStatusSumWait);
   }
   __syncwarp();
+  if (SPLIT && ctas > 1 && unit < total && warp >= kWideSumWarps) {  // as the summing warps
+    tc::cluster_sync();
+    tc::cluster_sync();
+  }
   tc::fence_before_sync();
   tc::cluster_sync();
   if (warp == kWideSumWarps + 1) tc::tmem_free(tmem, 512);
@@ -383,7 +492,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // their sums through distributed shared memory to the CTA that adds up the column, in rank
 // order.
 constexpr int kMatrixWarps = 2;
-constexpr int kMostSplit = 8;
 constexpr int kNarrowThreads = 32 * (5 + kMatrixWarps);
 constexpr int kNarrowStages = 4, kNarrowBufs = 4;
 static_assert(kNarrowStages % kMatrixWarps == 0 && kNarrowBufs % kMatrixWarps == 0,
@@ -641,6 +749,37 @@ reshard_status_t tile_map(CUtensorMap* map, const void* base, int64_t k, int64_t
   return RESHARD_OK;
 }
 
+// How many clusters of `split` CTAs are on the device at a time: fewer than its SMs divided
+// by the split, since a cluster lies in one part of the GPU (8 CTAs of an SM each: 16, not
+// 19).  Asked for once a device.
+template <typename Kernel>
+int resident_clusters(Kernel* kernel, int dev, unsigned threads, size_t smem, int split) {
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][kMostSplit + 1];
+  if (dev < kDevices) {
+    const int n = known[dev][split].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(split));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {unsigned(split), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // an estimate is not worth an error: the launch reports its own
+    return 1;
+  }
+  if (dev < kDevices) known[dev][split].store(n, std::memory_order_relaxed);
+  return n > 0 ? n : 1;
+}
+
 reshard_status_t launch(const void* kernel, unsigned grid, unsigned threads, size_t smem, int cluster,
                         cudaStream_t stream, void** args) {
   cudaError_t ce =
@@ -668,25 +807,27 @@ struct Operands {
   int64_t ldx, ldw, k;
 };
 
-template <typename Y>
-reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int sms, cudaStream_t stream) {
+// SPLIT: `split` CTAs a tile of 128 tokens (with several of them, a cluster for each of at
+// most `units` tiles); else two CTAs a tile of 256 tokens.
+template <typename Y, bool SPLIT>
+reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, int split,
+                             cudaStream_t stream) {
   CUtensorMap map_x, map_w;
   reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, kRows);
   if (st == RESHARD_OK) st = tile_map(&map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows);
   if (st != RESHARD_OK) return st;
   a.ntiles = int32_t(cdiv(a.n, kWideCols));
-  // an expert's last tile may be short, so experts add at most one row of tiles each
-  const int64_t most = a.ntiles * (cdiv(a.tokens, 2 * kRows) + (a.nexperts > 1 ? a.nexperts : 0));
-  const int64_t pairs = most < sms / 2 ? most : sms / 2;
   const size_t at = wide_stages_at(ExpertTable::bytes(a.nexperts));
   int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : 2;
   void* args[] = {&map_x, &map_w, &a, &stages};
-  return launch(reinterpret_cast<const void*>(wide_kernel<Y>), unsigned(2 * pairs), kWideThreads,
-                at + size_t(stages) * kWideStageBytes, 2, stream, args);
+  return launch(reinterpret_cast<const void*>(wide_kernel<Y, SPLIT>), unsigned(units * split),
+                kWideThreads, at + size_t(stages) * kWideStageBytes, split, stream, args);
 }
+static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
 
 template <int NT, typename Y>
-reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int sms, cudaStream_t stream) {
+reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int dev, int64_t sms,
+                               cudaStream_t stream) {
   CUtensorMap map_x, map_w;
   reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, NT);
   if (st == RESHARD_OK) st = tile_map(&map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows);
@@ -694,19 +835,24 @@ reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int sms, cudaSt
   a.ntiles = int32_t(cdiv(a.n, kRows));
   int64_t tiles = a.ntiles * cdiv(a.tokens, NT);
   if (a.offsets) tiles = a.ntiles * (a.tokens / NT + (a.nexperts < a.tokens ? a.nexperts : a.tokens));
-  // as many CTAs a tile as are on the GPU at a time (two an SM, one with 64 tokens' sums),
-  // with two blocks each: a second wave would cost more than longer shares
-  const int64_t room = sms * (NT <= 32 ? 2 : 1);
+  // As many CTAs a tile as keep to one wave, with two blocks each: a second wave would cost
+  // more than longer shares.
+  const size_t table = ExpertTable::bytes(a.nexperts);
+  auto smem_of = [&](int split) {
+    return split > 1 ? NarrowSmem<NT>::sums_at(table) + sizeof(float) * kRows * size_t(cdiv(NT, split) * split)
+                     : sizeof(NarrowSmem<NT>) + table;
+  };
   int split = 1;
-  while (split < kMostSplit && tiles * (split + 1) <= room && a.blocks >= 2 * (split + 1)) ++split;
+  for (int s = kMostSplit; s > 1 && split == 1; --s)
+    if (a.blocks >= 2 * s && tiles * s <= 2 * sms &&
+        tiles <= resident_clusters(narrow_kernel<NT, Y>, dev, kNarrowThreads,
+                                   NarrowSmem<NT>::sums_at(0) + sizeof(float) * kRows * (NT + kMostSplit), s))
+      split = s;
   if (tiles * split >= int64_t(1) << 31)
     return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
-  const size_t table = ExpertTable::bytes(a.nexperts);
-  const size_t smem = split > 1 ? NarrowSmem<NT>::sums_at(table) + sizeof(float) * kRows * size_t(cdiv(NT, split) * split)
-                                : sizeof(NarrowSmem<NT>) + table;
   void* args[] = {&map_x, &map_w, &a, &split};
   return launch(reinterpret_cast<const void*>(narrow_kernel<NT, Y>), unsigned(tiles * split),
-                kNarrowThreads, smem, split, stream, args);
+                kNarrowThreads, smem_of(split), split, stream, args);
 }
 
 template <typename Y>
@@ -722,17 +868,48 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
     return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
   reshard_status_t st = device_status_word(&a.status);
   if (st != RESHARD_OK) return st;
-  const int64_t each = cdiv(a.tokens, a.nexperts);  // tokens of an expert, on average
-  if (!a.offsets) {
-    if (each <= 16) return launch_narrow<16, Y>(a, o, sms, stream);
-    if (each <= 32) return launch_narrow<32, Y>(a, o, sms, stream);
-    if (each <= 128) return launch_narrow<64, Y>(a, o, sms, stream);
-  } else {
-    if (each <= 4) return launch_narrow<16, Y>(a, o, sms, stream);
-    if (each <= 8) return launch_narrow<32, Y>(a, o, sms, stream);
-    if (each <= 64) return launch_narrow<64, Y>(a, o, sms, stream);
+  // Few tokens (of an expert, on average; experts differ): reading w is all that counts.
+  const int64_t each = cdiv(a.tokens, a.nexperts);
+  if (each <= (a.offsets ? 4 : 16)) return launch_narrow<16, Y>(a, o, dev, sms, stream);
+  if (each <= (a.offsets ? 8 : 32)) return launch_narrow<32, Y>(a, o, dev, sms, stream);
+
+  // Otherwise the least of these estimates in ns, fitted to 20 sizes from 64 x 7168 x 7168 to
+  // 4096 x 4096 x 4096 within 15%: a kernel's start and end, and a time for each block of k
+  // that the CTAs of an SM go through one after the other (w from HBM costs all the same).
+  const int64_t experts = !a.offsets ? 0 : a.nexperts < a.tokens ? a.nexperts : a.tokens;
+  // Tiles of `rows` tokens: an expert's last one may be short, half of one on average.
+  auto tiles = [&](int64_t rows, int64_t cols) {
+    return cdiv(a.n, cols) * cdiv(2 * cdiv(a.tokens, rows) + experts, 2);
+  };
+  const int64_t blocks = a.blocks, stray = a.aligned_y == 32 ? 0 : 6000;  // rows off the sectors
+  const int64_t small = tiles(64, kRows), large = tiles(2 * kRows, kWideCols);
+  const int64_t middle = tiles(kRows, kWideCols);
+  int64_t best = 5500 + cdiv(small, 2 * sms) * blocks * (small > sms ? 650 : 450);
+  int split = 0;  // 0: narrow, -1: pairs, else CTAs a tile of 128 tokens
+  const int64_t pairs = sms / 2;
+  const int64_t pair_cost = 8000 + cdiv(large, pairs) * (blocks * 430 + 1500 + stray);
+  if (pair_cost < best) best = pair_cost, split = -1;
+  const bool room =
+      wide_stages_at(ExpertTable::bytes(a.nexperts)) + kWideStages * kWideStageBytes <= kSmemMost;
+  for (int s = 1; s <= kMostSplit; ++s) {
+    if (s > 1 && (!room || blocks < 2 * s || middle * s > sms ||
+                  middle > resident_clusters(wide_kernel<Y, true>, dev, kWideThreads, kSmemMost, s)))
+      continue;
+    const int64_t cost = s == 1 ? 7500 + cdiv(middle, sms) * (blocks * 540 + 1500 + stray)
+                                : 10500 + cdiv(blocks, s) * 500;
+    if (cost < best) best = cost, split = s;
   }
-  return launch_wide<Y>(a, o, sms, stream);
+  if (split == 0) return launch_narrow<64, Y>(a, o, dev, sms, stream);
+  auto most = [&](int64_t rows) {
+    return cdiv(a.n, kWideCols) * (a.offsets ? a.tokens / rows + experts : cdiv(a.tokens, rows));
+  };
+  if (split > 0) {
+    int64_t units = most(kRows);
+    if (split == 1 && units > sms) units = sms;
+    return launch_wide<Y, true>(a, o, units, split, stream);
+  }
+  const int64_t units = most(2 * kRows) < pairs ? most(2 * kRows) : pairs;
+  return launch_wide<Y, false>(a, o, units, 2, stream);
 }
 
 }  // namespace
@@ -781,7 +958,10 @@ extern "C" reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const
   a.col_blocks = int32_t(rs::op::cdiv(n, 128));
   a.y = y;
   a.ldy = ldy;
-  a.aligned_y = rs::op::aligned(y, 16) && ldy * rs::op::dtype_size(ydtype) % 16 == 0;
+  const int64_t pitch = ldy * rs::op::dtype_size(ydtype);
+  a.aligned_y = rs::op::aligned(y, 32) && pitch % 32 == 0   ? 32
+                : rs::op::aligned(y, 16) && pitch % 16 == 0 ? 16
+                                                            : 0;
   const rs::Operands o = {x, w, ldx, ldw, k};
   return rs::op::by_dtype(ydtype, [&](auto t) {
     return rs::launch_matmul<decltype(t)>(a, o, static_cast<cudaStream_t>(stream));

@@ -4,6 +4,8 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "staging.cuh"
 
@@ -42,6 +44,10 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
 }
 __device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// Four float32 values, as two pairs.
+__device__ __forceinline__ void store_cluster16(uint32_t addr, uint64_t a, uint64_t b) {
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
 }
 // Barrier inits visible to the async proxy and the cluster.
 __device__ __forceinline__ void fence_barrier_init() {
@@ -173,6 +179,36 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
+}
+
+// 32 bytes of float32 pairs, rounded to the type of `to` (32-byte aligned).
+__device__ __forceinline__ void store32(float* to, const uint64_t* p) {
+  asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(to), "l"(p[0]), "l"(p[1]), "l"(p[2]),
+               "l"(p[3])
+               : "memory");
+}
+__device__ __forceinline__ void store32_words(void* to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void store32(__nv_bfloat16* to, const uint64_t* p) {
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(unpack2(p[i]));
+    v[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  store32_words(to, v);
+}
+__device__ __forceinline__ void store32(__half* to, const uint64_t* p) {
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2 h = __float22half2_rn(unpack2(p[i]));
+    v[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  store32_words(to, v);
 }
 
 }  // namespace tc
