@@ -5,11 +5,14 @@
 // the row is read from HBM once however many questions are asked of it:
 //   1. the largest logit;
 //   2. the weights' sum, and for top-k and top-p a histogram of how far below the
-//      largest each token lies: counts and weights in 1024 bins of 1/64 in ln p;
-//   3. the bin in which the last kept token lies, from the histograms' sums; the tokens of
-//      that one bin are listed and ranked by (logit, index), which gives the last kept
-//      token exactly;
-//   4. the kept weights' sums, and the token whose running sum passes the target.
+//      largest each token lies: counts and weights in 512 bins of 1/64 in ln p (8 nats;
+//      few tokens lie so high, which keeps atomics rare; further ones if the cut is below);
+//   3. the bin in which the last kept token lies, from the histograms' sums.  Where no more
+//      than 256 tokens lie as high, these are listed and the first CTA finishes the row
+//      with them; else the tokens of that one bin are listed and ranked by (logit, index),
+//      which gives the last kept token exactly, and
+//   4. the kept weights' sums, and the token whose running sum passes the target, come from
+//      one more pass over the slices.
 // Weights are whole numbers (2^-40 of the largest), so sums are exact and neither the
 // order of atomics nor the split over warps and CTAs can change a result.
 #include <algorithm>
@@ -28,8 +31,10 @@ using tc::in_cta;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 1024;
-constexpr float kBinsPerNat = 64.0f;  // a histogram covers 16 nats
+constexpr int kBins = 512;
+constexpr float kBinsPerNat = 64.0f;  // a histogram covers 8 nats
+constexpr uint32_t kLastBin = 4 * kBins;  // beyond 32 nats every weight is 0
+constexpr uint32_t kFew = kThreads;       // tokens that the first CTA resolves on its own
 constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
 
 struct SampleArgs {
@@ -153,6 +158,29 @@ __device__ __forceinline__ uint4 load_cluster16(const void* at, uint32_t rank) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ uint2 load_cluster8(const void* at, uint32_t rank) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(in_cta(smem_addr(at), rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sum_cluster(uint64_t* at, uint32_t rank, uint64_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(in_cta(smem_addr(at), rank)),
+               "l"(v)
+               : "memory");
+}
+__device__ __forceinline__ void sum_cluster(uint32_t* at, uint32_t rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(in_cta(smem_addr(at), rank)),
+               "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ void max_cluster(uint32_t* at, uint32_t rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(in_cta(smem_addr(at), rank)),
+               "r"(v)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t add_cluster(uint32_t* at, uint32_t rank, uint32_t v) {
   uint32_t old;
   asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
@@ -168,34 +196,36 @@ struct Cut {
   uint32_t key, index;
 };
 
-enum Step : uint32_t { kList, kHistogram, kBisect, kCut };
+enum Step : uint32_t { kList, kListFew, kHistogram, kBisect, kCut };
 // What every CTA does next, as the first one has decided.
 struct Order {
-  uint32_t step, bin;  // kList: the tokens of that bin; kHistogram: one from that bin on
+  uint32_t step, bin;  // kList: that bin's tokens; kListFew: up to it; kHistogram: from it on
   Cut cut;
 };
 
-constexpr int kListMost = 1536;  // listed tokens: 8 bytes each in the histogram's place
+constexpr int kListMost = 768;  // listed tokens: 8 bytes each in the histogram's place
 
 struct SampleSmem {
   union {
     struct {
       alignas(16) uint64_t mass[kBins];
-      alignas(16) uint32_t count[kBins];
+      alignas(16) uint32_t counts[kBins];
     };
     struct {
       uint32_t key[kListMost], index[kListMost];
     };
   };
   uint64_t warp_mass[kWarps];
-  uint64_t cta_mass[2][kMaxCluster];   // written by the other CTAs: sums of a pass,
-  uint32_t cta_count[2][kMaxCluster];  // counts (or lowest index of the largest logit)
-  uint32_t cta_top[kMaxCluster];
+  uint64_t cta_mass[2][kMaxCluster];  // added to by every warp of the cluster: each CTA's
+  uint32_t count[2];                  // sums of a pass, and the cluster's count
+  uint32_t top_key;                   // the largest logit
+  uint32_t rising;                    // ~ the lowest index of the largest logit
   uint64_t scan_mass[kWarps];
   uint32_t scan_count[kWarps];
   uint32_t listed;
   Order order;
   uint64_t limit, best_mass;
+  uint64_t few_mass[kFew];
 };
 static_assert(sizeof(uint32_t) * 2 * kListMost <= 12 * kBins, "the list lies in the histogram");
 
@@ -237,7 +267,7 @@ struct Slice {
 };
 
 template <typename T, bool RESIDENT>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   SampleSmem& sm = *reinterpret_cast<SampleSmem*>(dynamic);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -245,7 +275,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const uint32_t rank = tc::cluster_rank();
   const int64_t r = blockIdx.x / ctas;
-  tc::cluster_arrive();  // every CTA of the cluster runs before another one writes to it
+  if (tid < 2 * kMaxCluster) sm.cta_mass[tid / kMaxCluster][tid % kMaxCluster] = 0;
+  if (tid < 2) sm.count[tid] = 0;
+  if (tid == 0) sm.top_key = 0, sm.rising = 0;
+  tc::cluster_arrive();  // before another CTA adds to these
 
   Slice<T, RESIDENT> s;
   constexpr int kPer = s.kPer;
@@ -279,20 +312,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
   const bool by_count = !greedy && k > 0 && k < s.vocab;
   const bool by_mass = !greedy && p < 1.0f;
   if (by_count || by_mass)
-    for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.counts[i] = 0;
   const float mine_top = top;
   top = warp_max(top + 0.0f);
-  if (lane == 0) sm.scan_count[warp] = key_of(top);
-  __syncthreads();
-  tc::cluster_wait();
-  if (tid < int(ctas)) {
-    uint32_t most = 0;
-    for (int i = 0; i < kWarps; ++i) most = max(most, sm.scan_count[i]);
-    store_cluster(&sm.cta_top[rank], tid, most);
-  }
+  tc::cluster_wait();  // the other CTAs have set their sums to 0
+  if (lane < int(ctas)) max_cluster(&sm.top_key, lane, key_of(top));
   cluster_sync();
-  uint32_t top_key = 0;
-  for (uint32_t i = 0; i < ctas; ++i) top_key = max(top_key, sm.cta_top[i]);
+  const uint32_t top_key = sm.top_key;
   Scale scale;
   scale.top = logit_of(top_key);
   scale.inv = greedy ? 1.0f : fminf(1.0f / temperature, 0x1.fffffep127f);
@@ -311,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       for (int g = s.w0 + lane; g < s.w1; g += 32) *s.place(g) = s.flattened(*s.place(g));
   }
 
-  // 2. weights, and the histogram of the 16 nats below the largest
+  // 2. weights, and the histogram of the nats below the largest
   auto tally = [&](float z, float e, uint32_t begin) {
     const uint32_t bin = bin_of(z) - begin;
     if (bin < uint32_t(kBins)) {
-      atomicAdd(&sm.count[bin], 1u);
+      atomicAdd(&sm.counts[bin], 1u);
       atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[bin]), (unsigned long long)weight_of(e));
     }
   };
@@ -349,23 +375,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
           if (s.at(v, j) == scale.top) lowest = uint32_t(s.first(g) + j);
       }
   }
-  // Sums over the warp, the CTA and (slot) the cluster.
+  // Adds the threads' values to every CTA's sums (of the given slot, which are 0 before).
   uint32_t slot = 0;
-  auto publish = [&](uint64_t mass, uint32_t count, bool lowest_of) {
+  auto publish = [&](uint64_t mass, uint32_t count) {
     mass = warp_sum64(mass);
-    count = lowest_of ? __reduce_min_sync(0xffffffffu, count) : __reduce_add_sync(0xffffffffu, count);
-    __syncthreads();
-    if (lane == 0) sm.warp_mass[warp] = mass, sm.scan_count[warp] = count;
-    __syncthreads();
-    if (tid < int(ctas)) {
-      uint64_t m = 0;
-      uint32_t c = lowest_of ? 0xffffffffu : 0u;
-      for (int i = 0; i < kWarps; ++i) {
-        m += sm.warp_mass[i];
-        c = lowest_of ? min(c, sm.scan_count[i]) : c + sm.scan_count[i];
-      }
-      store_cluster(&sm.cta_mass[slot][rank], tid, m);
-      store_cluster(&sm.cta_count[slot][rank], tid, c);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 0) sm.warp_mass[warp] = mass;
+    if (lane < int(ctas)) {
+      sum_cluster(&sm.cta_mass[slot][rank], lane, mass);
+      if (count) sum_cluster(&sm.count[slot], lane, count);
     }
     cluster_sync();
   };
@@ -374,7 +392,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     for (uint32_t i = 0; i < ctas; ++i) m += sm.cta_mass[slot][i];
     return m;
   };
-  publish(sums.sum(), lowest, true);
+  // The other slot, for the next sums; the one just read is set to 0 for those after them
+  // (their CTAs add to it only after the cluster has met once more).
+  auto next_slot = [&] {
+    __syncthreads();
+    if (tid < kMaxCluster) sm.cta_mass[slot][tid] = 0;
+    if (tid == 0) sm.count[slot] = 0;
+    slot ^= 1;
+  };
+  if (greedy) {
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+    if (lane == 0 && lowest != 0xffffffffu) max_cluster(&sm.rising, 0, ~lowest);
+  }
+  publish(sums.sum(), 0);
   const uint64_t total = cluster_mass();
   auto answer = [&](int i, float l) {
     a.token[r] = i;
@@ -382,11 +412,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       a.logprob[r] = scale.z(l) - log1pf(float(double(total - kOne) / double(kOne)));
   };
   if (greedy) {
-    if (rank == 0 && tid == 0) {
-      uint32_t i = 0xffffffffu;
-      for (uint32_t c = 0; c < ctas; ++c) i = min(i, sm.cta_count[slot][c]);
-      answer(int(i), scale.top);
-    }
+    if (rank == 0 && tid == 0) answer(int(~sm.rising), scale.top);
     return;
   }
 
@@ -396,9 +422,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     return key > cut.key || (key == cut.key && uint32_t(i) <= cut.index);
   };
   if (by_count || by_mass) {
-    // The first CTA's view: the histograms' sums (four bins a thread) and what lies before.
-    uint32_t counts[4] = {}, count_before = 0;
-    uint64_t masses[4] = {}, mass_before = 0;
+    // The first CTA's view: the histograms' sums (two bins a thread) and what lies before.
+    static_assert(kBins == 2 * kThreads, "two bins a thread");
+    uint32_t counts[2] = {}, count_before = 0;
+    uint64_t masses[2] = {}, mass_before = 0;
     uint32_t skipped_count = 0;   // tokens above the histogram's range
     uint64_t skipped_mass = 0;
     uint32_t begin = 0;           // the histogram's first bin
@@ -407,18 +434,16 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     uint32_t bin_count = 0;       // tokens and weights before the listed bin
     uint64_t bin_mass = 0;
     auto gather = [&] {
-      for (int j = 0; j < 4; ++j) counts[j] = 0, masses[j] = 0;
+      counts[0] = counts[1] = 0, masses[0] = masses[1] = 0;
 #pragma unroll 4
       for (uint32_t c = 0; c < ctas; ++c) {
-        const uint4 n = load_cluster16(&sm.count[4 * tid], c);
-        const uint4 m0 = load_cluster16(&sm.mass[4 * tid], c);
-        const uint4 m1 = load_cluster16(&sm.mass[4 * tid + 2], c);
-        counts[0] += n.x, counts[1] += n.y, counts[2] += n.z, counts[3] += n.w;
-        masses[0] += m0.x | uint64_t(m0.y) << 32, masses[1] += m0.z | uint64_t(m0.w) << 32;
-        masses[2] += m1.x | uint64_t(m1.y) << 32, masses[3] += m1.z | uint64_t(m1.w) << 32;
+        const uint2 n = load_cluster8(&sm.counts[2 * tid], c);
+        const uint4 m = load_cluster16(&sm.mass[2 * tid], c);
+        counts[0] += n.x, counts[1] += n.y;
+        masses[0] += m.x | uint64_t(m.y) << 32, masses[1] += m.z | uint64_t(m.w) << 32;
       }
-      const uint32_t cn = counts[0] + counts[1] + counts[2] + counts[3];
-      const uint64_t mn = masses[0] + masses[1] + masses[2] + masses[3];
+      const uint32_t cn = counts[0] + counts[1];
+      const uint64_t mn = masses[0] + masses[1];
       uint64_t ci = warp_scan64(cn, lane), mi = warp_scan64(mn, lane);
       __syncthreads();
       if (lane == 31) sm.scan_count[warp] = uint32_t(ci), sm.scan_mass[warp] = mi;
@@ -429,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         count_before += sm.scan_count[i], mass_before += sm.scan_mass[i];
     };
     // Orders the bin in which the last kept token lies to be listed; where it lies beyond
-    // the histogram, a histogram of the next 16 nats; beyond 32 nats every weight is 0.
+    // the histogram, a histogram of the next nats.
     auto decide = [&] {
       if (tid == 0) {
         sm.order.step = kHistogram;
@@ -439,12 +464,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       const uint64_t limit = sm.limit;
       uint32_t c = count_before;
       uint64_t m = mass_before;
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const bool inside = count_open ? c < uint32_t(k) && c + counts[j] >= uint32_t(k)
                                        : m < limit && m + masses[j] >= limit;
         if (inside) {
-          sm.order.step = kList;
-          sm.order.bin = begin + 4 * tid + j;
+          sm.order.step = c + counts[j] <= kFew ? kListFew : kList;
+          sm.order.bin = begin + 2 * tid + j;
           sm.scan_count[0] = c;
           sm.scan_mass[0] = m;
         }
@@ -452,16 +477,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       }
       if (tid == kThreads - 1) sm.scan_count[1] = c, sm.scan_mass[1] = m;
       __syncthreads();
-      const bool list = sm.order.step == kList;
-      if (list) {
+      if (sm.order.step != kHistogram) {
         bin_count = sm.scan_count[0], bin_mass = sm.scan_mass[0];
         if (tid == 0) sm.listed = 0;
         return;
       }
       skipped_count = sm.scan_count[1], skipped_mass = sm.scan_mass[1];
       __syncthreads();
-      if (begin == 0) {
-        begin = kBins;
+      if (begin + kBins < kLastBin) {
+        begin += kBins;
       } else if (count_open && by_mass) {
         count_open = false;
         begin = 0, skipped_count = 0, skipped_mass = 0;
@@ -509,6 +533,49 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         if (tid == 0) sm.order.step = kHistogram, sm.order.bin = 0;
       }
     };
+    // The whole rest, with all tokens that may be kept in the list: a token a thread.
+    auto finish_few = [&] {
+      const uint32_t n = sm.listed;
+      const bool mine = tid < int(n);
+      const uint32_t key = mine ? sm.key[tid] : 0, index = mine ? sm.index[tid] : 0;
+      const float e = mine ? scale.e(scale.z(logit_of(key))) : 0.0f;
+      const uint64_t own = weight_of(e);
+      sm.few_mass[tid] = own;
+      __syncthreads();
+      uint32_t before = 0;
+      uint64_t m = 0;
+      for (uint32_t j = 0; mine && j < n; ++j) {
+        const uint32_t kj = sm.key[j];
+        if (kj > key || (kj == key && sm.index[j] < index)) ++before, m += sm.few_mass[j];
+      }
+      Cut last = {0, 0xffffffffu};
+      if (count_open) {  // else top-k has been resolved, or keeps all that has a weight
+        if (mine && before + 1 == uint32_t(k)) sm.order.cut = {key, index}, sm.best_mass = m + own;
+        __syncthreads();
+        last = sm.order.cut, kept_mass = sm.best_mass;
+        __syncthreads();
+      }
+      if (by_mass) {
+        if (tid == 0) sm.limit = threshold(double(p) * double(kept_mass), false);
+        __syncthreads();
+        if (mine && m < sm.limit && m + own >= sm.limit) sm.order.cut = {key, index};
+        __syncthreads();
+        last = sm.order.cut;
+      }
+      const bool kept = mine && !(e < floor_e) &&
+                        (key > last.key || (key == last.key && index <= last.index));
+      sm.few_mass[tid] = kept ? own : 0;
+      __syncthreads();
+      uint64_t all = 0, upto = 0;
+      for (uint32_t j = 0; j < n; ++j) {
+        const uint64_t w = sm.few_mass[j];
+        all += w;
+        if (sm.index[j] <= index) upto += w;
+      }
+      if (tid == 0) sm.limit = min(threshold(double(u) * double(all), true), all);
+      __syncthreads();
+      if (kept && upto >= sm.limit && upto - own < sm.limit) answer(int(index), logit_of(key));
+    };
     auto send = [&] {  // sm.order to every CTA
       __syncthreads();
       if (tid < int(ctas) && tid > 0) {
@@ -535,8 +602,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       order = sm.order;
       if (order.step == kCut || order.step == kBisect) break;
       fresh = order.step == kHistogram;
+      const uint32_t lowest_bin = order.step == kListFew ? 0 : order.bin;
       if (fresh) {
-        for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.count[i] = 0;
+        for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.counts[i] = 0;
         __syncthreads();
       }
       for (int g = s.w0 + lane; g < s.w1; g += 32) {
@@ -550,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (bin_of(h ? z.y : z.x) != order.bin) continue;
+              const uint32_t bin = bin_of(h ? z.y : z.x);
+              if (bin < lowest_bin || bin > order.bin) continue;
               const uint32_t to = add_cluster(&sm.listed, 0, 1);
               if (to >= uint32_t(kListMost)) continue;
               store_cluster(&sm.key[to], 0, key_of(clean(s.at(v, j + h))));
@@ -560,6 +629,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         }
       }
       cluster_sync();
+      if (order.step == kListFew) {
+        if (rank == 0) finish_few();
+        return;
+      }
     }
     if (order.step == kCut) {
       cut = order.cut;
@@ -584,10 +657,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
             m += weight_of(scale.e(scale.z(l))), ++c;
           }
         }
-        slot ^= 1;
-        publish(m, c, false);
-        mass = cluster_mass(), count = 0;
-        for (uint32_t i = 0; i < ctas; ++i) count += sm.cta_count[slot][i];
+        next_slot();
+        publish(m, c);
+        mass = cluster_mass(), count = sm.count[slot];
       };
       constexpr uint32_t kAll = 0xffffffffu;
       bool open = by_count;
@@ -643,8 +715,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       for (int j = 0; j < kPer; ++j) most = fmaxf(most, s.at(v, j));
       if (most >= cut_logit) mine += granule_sum(v, g);
     }
-    slot ^= 1;
-    publish(mine, 0, false);
+    next_slot();
+    publish(mine, 0);
     all = cluster_mass();
   }
   // the first token at which the sum passes u times all; none does for u >= 1: the last
