@@ -5,8 +5,9 @@
 // the row is read from HBM once however many questions are asked of it:
 //   1. the largest logit;
 //   2. the weights' sum, and for top-k and top-p a histogram of how far below the
-//      largest each token lies: counts and weights in 512 bins of 1/64 in ln p (8 nats;
-//      few tokens lie so high, which keeps atomics rare; further ones if the cut is below);
+//      largest each token lies: counts and weights in 512 bins of ln p (for top-p of 1/64,
+//      8 nats at a time: few tokens lie so high, which keeps atomics rare; for top-k of 1/16,
+//      without the tokens that the lanes' largest logits rule out);
 //   3. the bin in which the last kept token lies, from the histograms' sums.  Where no more
 //      than 256 tokens lie as high, these are listed and the first CTA finishes the row
 //      with them; else the tokens of that one bin are listed and ranked by (logit, index),
@@ -32,8 +33,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;
-constexpr float kBinsPerNat = 64.0f;  // a histogram covers 8 nats
-constexpr uint32_t kLastBin = 4 * kBins;  // beyond 32 nats every weight is 0
+// Bins of 1/64 nat, a histogram of 8 nats at a time, for top-p alone; bins of 1/16 nat, all
+// 32 nats beyond which every weight is 0, for top-k, whose histogram leaves out most tokens.
+constexpr int kBinsPerNat = 64, kWideBinsPerNat = 16;
+constexpr int kNats = 32;
+static_assert(kBins == kNats * kWideBinsPerNat, "one histogram for top-k");
 constexpr uint32_t kFew = kThreads;       // tokens that the first CTA resolves on its own
 constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
 
@@ -114,10 +118,10 @@ __device__ __forceinline__ uint64_t weight_of(float e) {
 }
 
 // The histogram bin of a token, from 0 at the largest logit on, in whole steps of
-// 1 / kBinsPerNat: the low bits of 2^23 + steps.  Grows as the logit falls; beyond any
+// 1 / per_nat: the low bits of 2^23 + steps.  Grows as the logit falls; beyond any
 // histogram for weight 0.
-__device__ __forceinline__ uint32_t bin_of(float z) {
-  return __float_as_uint(__fmaf_rn(z, -kBinsPerNat, 8388608.0f)) - 0x4b000000u;
+__device__ __forceinline__ uint32_t bin_of(float z, float per_nat) {
+  return __float_as_uint(__fmaf_rn(z, -per_nat, 8388608.0f)) - 0x4b000000u;
 }
 
 // The smallest whole number that is not below x as a float64 (above: that is above x).
@@ -141,6 +145,8 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {  // incl
   }
   return v;
 }
+
+__device__ __forceinline__ int cdiv_int(int a, int b) { return (a - 1) / b + 1; }
 
 template <typename T>
 __device__ __forceinline__ void store_cluster(T* at, uint32_t rank, T value) {
@@ -220,6 +226,7 @@ struct SampleSmem {
   uint32_t count[2];                  // sums of a pass, and the cluster's count
   uint32_t top_key;                   // the largest logit
   uint32_t rising;                    // ~ the lowest index of the largest logit
+  uint32_t below;                     // ~ the key below which no token is among the top k
   uint64_t scan_mass[kWarps];
   uint32_t scan_count[kWarps];
   uint32_t listed;
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   const int64_t r = blockIdx.x / ctas;
   if (tid < 2 * kMaxCluster) sm.cta_mass[tid / kMaxCluster][tid % kMaxCluster] = 0;
   if (tid < 2) sm.count[tid] = 0;
-  if (tid == 0) sm.top_key = 0, sm.rising = 0;
+  if (tid == 0) sm.top_key = 0, sm.rising = 0, sm.below = 0;
   tc::cluster_arrive();  // before another CTA adds to these
 
   Slice<T, RESIDENT> s;
@@ -317,6 +324,17 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   top = warp_max(top + 0.0f);
   tc::cluster_wait();  // the other CTAs have set their sums to 0
   if (lane < int(ctas)) max_cluster(&sm.top_key, lane, key_of(top));
+  if (by_count) {
+    // If each of the cluster's warps holds `most` tokens not below a logit, at least k tokens
+    // are not: the least over the warps of the most-th largest of their lanes' largest ones.
+    const int most = int(cdiv_int(k, kWarps * int(ctas)));
+    uint32_t left = key_of(mine_top + 0.0f), bound = 0;
+    for (int i = 0; i < most && most <= 32; ++i) {
+      bound = __reduce_max_sync(0xffffffffu, left);
+      if (lane == __ffs(int(__ballot_sync(0xffffffffu, left == bound))) - 1) left = 0;
+    }
+    if (lane < int(ctas)) max_cluster(&sm.below, lane, ~bound);
+  }
   cluster_sync();
   const uint32_t top_key = sm.top_key;
   Scale scale;
@@ -338,9 +356,14 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   }
 
   // 2. weights, and the histogram of the nats below the largest
+  const float per_nat = float(by_count ? kWideBinsPerNat : kBinsPerNat);
+  // top-k: the bins of tokens that may be among the k
+  uint32_t bins = kBins;
+  if (by_count && ~sm.below != 0 && !s.infinite)
+    bins = min(bins, bin_of(scale.z(logit_of(~sm.below)), per_nat) + 1);
   auto tally = [&](float z, float e, uint32_t begin) {
-    const uint32_t bin = bin_of(z) - begin;
-    if (bin < uint32_t(kBins)) {
+    const uint32_t bin = bin_of(z, per_nat) - begin;
+    if (bin < bins) {
       atomicAdd(&sm.counts[bin], 1u);
       atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[bin]), (unsigned long long)weight_of(e));
     }
@@ -484,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
       }
       skipped_count = sm.scan_count[1], skipped_mass = sm.scan_mass[1];
       __syncthreads();
-      if (begin + kBins < kLastBin) {
+      if (begin + kBins < uint32_t(kNats) * uint32_t(per_nat)) {
         begin += kBins;
       } else if (count_open && by_mass) {
         count_open = false;
@@ -618,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t bin = bin_of(h ? z.y : z.x);
+              const uint32_t bin = bin_of(h ? z.y : z.x, per_nat);
               if (bin < lowest_bin || bin > order.bin) continue;
               const uint32_t to = add_cluster(&sm.listed, 0, 1);
               if (to >= uint32_t(kListMost)) continue;
