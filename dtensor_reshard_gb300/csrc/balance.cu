@@ -202,28 +202,7 @@ __device__ void finish(const BalanceArgs& a, float sum, float inv_tokens) {
   }
 }
 
-// The largest of N values (a NaN loses against any number), and two values at once.
-template <int N>
-__device__ __forceinline__ float largest_of(const float (&v)[N]) {
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);
-  return m;
-}
-template <int N>
-__device__ __forceinline__ float largest_of(const __nv_bfloat16 (&v)[N]) {
-  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(v);
-#pragma unroll
-  for (int i = 2; i < N; i += 2) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(v + i));
-  return fmaxf(__low2float(m), __high2float(m));
-}
-template <int N>
-__device__ __forceinline__ float largest_of(const __half (&v)[N]) {
-  __half2 m = *reinterpret_cast<const __half2*>(v);
-#pragma unroll
-  for (int i = 2; i < N; i += 2) m = __hmax2(m, *reinterpret_cast<const __half2*>(v + i));
-  return fmaxf(__low2float(m), __high2float(m));
-}
+// Two values at once.
 __device__ __forceinline__ void set_pair(float* to, float2 x) { to[0] = x.x, to[1] = x.y; }
 __device__ __forceinline__ void set_pair(__nv_bfloat16* to, float2 x) {
   *reinterpret_cast<__nv_bfloat162*>(to) = __float22bfloat162_rn(x);

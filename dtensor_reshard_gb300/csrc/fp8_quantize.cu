@@ -43,6 +43,22 @@ struct Divisor {
   }
 };
 
+__device__ __forceinline__ float largest_magnitude(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+// 16-bit values two at a time, with the signs taken off.
+template <typename T>
+__device__ __forceinline__ float largest_magnitude(const T (&v)[8]) {
+  alignas(4) T a[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<uint32_t*>(a)[i] = reinterpret_cast<const uint32_t*>(v)[i] & 0x7fff7fffu;
+  return fmaxf(largest_of(a), 0.0f);
+}
+
 // Eight values of a row, as they lie in memory.
 template <typename T>
 struct Eight {
@@ -104,11 +120,8 @@ struct Eight {
     const T* e = reinterpret_cast<const T*>(v);
     return make_float2(to_float(e[2 * i]), to_float(e[2 * i + 1]));
   }
-  __device__ float largest() const {  // a NaN loses against any number
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(pair(i).x), fabsf(pair(i).y)));
-    return m;
+  __device__ float largest() const {  // in magnitude; a NaN loses against any number
+    return largest_magnitude(reinterpret_cast<const T(&)[8]>(v));
   }
   __device__ uint2 quotients(float s) const {
     uint32_t out[4];
@@ -126,23 +139,6 @@ struct Eight {
     return make_uint2(out[0] | out[1] << 16, out[2] | out[3] << 16);
   }
 };
-template <>
-__device__ __forceinline__ float Eight<__nv_bfloat16>::largest() const {
-  __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
-  const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(e[i]));
-  return fmaxf(__low2float(m), __high2float(m));
-}
-template <>
-__device__ __forceinline__ float Eight<__half>::largest() const {
-  __half2 m = __float2half2_rn(0.0f);
-  const __half2* e = reinterpret_cast<const __half2*>(v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(e[i]));
-  return fmaxf(__low2float(m), __high2float(m));
-}
-
 // Eight bytes a lane from sixteen neighbouring lanes to a row's `count` bytes (at most 128)
 // at any alignment: each lane stores the aligned eight bytes that end in its own, and what
 // is left at both ends goes out in the widest stores that are aligned.

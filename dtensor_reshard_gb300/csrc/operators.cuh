@@ -39,6 +39,29 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The largest of N values (a NaN loses against any number).
+template <int N>
+__device__ __forceinline__ float largest_of(const float (&v)[N]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, v[i]);
+  return m;
+}
+template <int N>
+__device__ __forceinline__ float largest_of(const __nv_bfloat16 (&v)[N]) {
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(v);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(v + i));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <int N>
+__device__ __forceinline__ float largest_of(const __half (&v)[N]) {
+  __half2 m = *reinterpret_cast<const __half2*>(v);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) m = __hmax2(m, *reinterpret_cast<const __half2*>(v + i));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool float_dtype(int32_t d) {
   return d == RESHARD_BF16 || d == RESHARD_FP16 || d == RESHARD_FP32;

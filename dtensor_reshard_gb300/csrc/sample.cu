@@ -270,6 +270,7 @@ struct Slice {
     if (RESIDENT) return *place(g);
     return infinite ? flattened(fetch(g)) : fetch(g);
   }
+  __device__ static float largest(const uint4& v) { return op::largest_of(reinterpret_cast<const T(&)[kPer]>(v)); }
   __device__ static float at(const uint4& v, int j) { return to_float(reinterpret_cast<const T*>(&v)[j]); }
 };
 
@@ -306,8 +307,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   for (int g = s.w0 + lane; g < s.w1; g += 32) {
     const uint4 v = s.fetch(g);
     if (RESIDENT) *s.place(g) = v;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) top = fmaxf(top, s.at(v, j));  // a NaN loses
+    top = fmaxf(top, s.largest(v));
   }
   const float temperature = a.temperature ? a.temperature[r] : 1.0f;
   const bool greedy = !(temperature > 0.0f);
@@ -630,24 +630,32 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
         for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.counts[i] = 0;
         __syncthreads();
       }
-      for (int g = s.w0 + lane; g < s.w1; g += 32) {
-        const uint4 v = s.granule(g);
+      if (fresh) {
+        for (int g = s.w0 + lane; g < s.w1; g += 32) {
+          const uint4 v = s.granule(g);
 #pragma unroll
-        for (int j = 0; j < kPer; j += 2) {
-          const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
-          if (fresh) {
+          for (int j = 0; j < kPer; j += 2) {
+            const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
             tally(z.x, scale.e(z.x), order.bin);
             tally(z.y, scale.e(z.y), order.bin);
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t bin = bin_of(h ? z.y : z.x, per_nat);
-              if (bin < lowest_bin || bin > order.bin) continue;
-              const uint32_t to = add_cluster(&sm.listed, 0, 1);
-              if (to >= uint32_t(kListMost)) continue;
-              store_cluster(&sm.key[to], 0, key_of(clean(s.at(v, j + h))));
-              store_cluster(&sm.index[to], 0, uint32_t(s.first(g) + j + h));
-            }
+          }
+        }
+      } else {
+        // no token of these bins lies below this (all rounding goes that way)
+        const float lowest_logit = __fsub_rd(
+            scale.top, __fdiv_ru(__fdiv_ru(float(order.bin + 1), per_nat), scale.inv));
+        for (int g = s.w0 + lane; g < s.w1; g += 32) {
+          const uint4 v = s.granule(g);
+          if (!(s.largest(v) >= lowest_logit)) continue;
+#pragma unroll 1
+          for (int j = 0; j < kPer; ++j) {
+            const float l = clean(s.at(v, j));
+            const uint32_t bin = bin_of(scale.z(l), per_nat);
+            if (bin < lowest_bin || bin > order.bin) continue;
+            const uint32_t to = add_cluster(&sm.listed, 0, 1);
+            if (to >= uint32_t(kListMost)) continue;
+            store_cluster(&sm.key[to], 0, key_of(l));
+            store_cluster(&sm.index[to], 0, uint32_t(s.first(g) + j));
           }
         }
       }
@@ -733,10 +741,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
     uint64_t mine = 0;
     for (int g = s.w0 + lane; g < s.w1; g += 32) {
       const uint4 v = s.granule(g);
-      float most = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) most = fmaxf(most, s.at(v, j));
-      if (most >= cut_logit) mine += granule_sum(v, g);
+      if (s.largest(v) >= cut_logit) mine += granule_sum(v, g);
     }
     next_slot();
     publish(mine, 0);
