@@ -16,7 +16,7 @@
 //      one more pass over the slices.
 // Weights are whole numbers (2^-40 of the largest), so sums are exact and neither the
 // order of atomics nor the split over warps and CTAs can change a result.
-#include <algorithm>
+#include <type_traits>
 
 #include "operators.cuh"
 #include "tensor_core.cuh"
@@ -38,7 +38,7 @@ constexpr int kBins = 512;
 constexpr int kBinsPerNat = 64, kWideBinsPerNat = 16;
 constexpr int kNats = 32;
 static_assert(kBins == kNats * kWideBinsPerNat, "one histogram for top-k");
-constexpr uint32_t kFew = kThreads;       // tokens that the first CTA resolves on its own
+constexpr uint32_t kFew = kThreads;  // tokens with which the first CTA finishes a row on its own
 constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
 
 struct SampleArgs {
@@ -156,14 +156,6 @@ __device__ __forceinline__ void store_cluster(T* at, uint32_t rank, T value) {
   else
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(uint32_t(value)) : "memory");
 }
-__device__ __forceinline__ uint4 load_cluster16(const void* at, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(in_cta(smem_addr(at), rank))
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ uint2 load_cluster8(const void* at, uint32_t rank) {
   uint2 v;
   asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
@@ -209,16 +201,17 @@ struct Order {
   Cut cut;
 };
 
-constexpr int kListMost = 768;  // listed tokens: 8 bytes each in the histogram's place
+constexpr int kListMost = 512;  // listed tokens, in the histogram's place
 
 struct SampleSmem {
   union {
     struct {
-      alignas(16) uint64_t mass[kBins];
+      alignas(16) uint32_t mass[3][kBins];  // 14 bits of the weights each
       alignas(16) uint32_t counts[kBins];
     };
     struct {
       uint32_t key[kListMost], index[kListMost];
+      uint64_t weight[kListMost];
     };
   };
   uint64_t warp_mass[kWarps];
@@ -232,9 +225,8 @@ struct SampleSmem {
   uint32_t listed;
   Order order;
   uint64_t limit, best_mass;
-  uint64_t few_mass[kFew];
 };
-static_assert(sizeof(uint32_t) * 2 * kListMost <= 12 * kBins, "the list lies in the histogram");
+static_assert(16 * kListMost <= 16 * kBins, "the list lies in the histogram");
 
 // This CTA's slice of a row, in granules of 16 aligned bytes; what lies outside the row
 // in the first and last granule reads as -inf.
@@ -319,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   const bool by_count = !greedy && k > 0 && k < s.vocab;
   const bool by_mass = !greedy && p < 1.0f;
   if (by_count || by_mass)
-    for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.counts[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) sm.mass[0][i] = sm.mass[1][i] = sm.mass[2][i] = 0, sm.counts[i] = 0;
   const float mine_top = top;
   top = warp_max(top + 0.0f);
   tc::cluster_wait();  // the other CTAs have set their sums to 0
@@ -365,7 +357,10 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
     const uint32_t bin = bin_of(z, per_nat) - begin;
     if (bin < bins) {
       atomicAdd(&sm.counts[bin], 1u);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sm.mass[bin]), (unsigned long long)weight_of(e));
+      const uint64_t w = weight_of(e);
+      atomicAdd(&sm.mass[0][bin], uint32_t(w) & 0x3fffu);
+      atomicAdd(&sm.mass[1][bin], uint32_t(w >> 14) & 0x3fffu);
+      atomicAdd(&sm.mass[2][bin], uint32_t(w >> 28));
     }
   };
   Weights sums;
@@ -461,9 +456,12 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
 #pragma unroll 4
       for (uint32_t c = 0; c < ctas; ++c) {
         const uint2 n = load_cluster8(&sm.counts[2 * tid], c);
-        const uint4 m = load_cluster16(&sm.mass[2 * tid], c);
+        const uint2 m0 = load_cluster8(&sm.mass[0][2 * tid], c);
+        const uint2 m1 = load_cluster8(&sm.mass[1][2 * tid], c);
+        const uint2 m2 = load_cluster8(&sm.mass[2][2 * tid], c);
         counts[0] += n.x, counts[1] += n.y;
-        masses[0] += m.x | uint64_t(m.y) << 32, masses[1] += m.z | uint64_t(m.w) << 32;
+        masses[0] += m0.x + (uint64_t(m1.x) << 14) + (uint64_t(m2.x) << 28);
+        masses[1] += m0.y + (uint64_t(m1.y) << 14) + (uint64_t(m2.y) << 28);
       }
       const uint32_t cn = counts[0] + counts[1];
       const uint64_t mn = masses[0] + masses[1];
@@ -525,17 +523,17 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
         return;
       }
       const uint64_t limit = sm.limit;
+      for (uint32_t i = tid; i < n; i += kThreads)
+        sm.weight[i] = weight_of(scale.e(scale.z(logit_of(sm.key[i]))));
+      __syncthreads();
       for (uint32_t i = tid; i < n; i += kThreads) {
         const uint32_t key = sm.key[i], index = sm.index[i];
-        uint32_t before = bin_count, last_key = key;
-        const uint64_t own = weight_of(scale.e(scale.z(logit_of(key))));
-        uint64_t m = bin_mass, w = own;
+        uint32_t before = bin_count;
+        const uint64_t own = sm.weight[i];
+        uint64_t m = bin_mass;
         for (uint32_t j = 0; j < n; ++j) {
           const uint32_t kj = sm.key[j];
-          if (kj > key || (kj == key && sm.index[j] < index)) {
-            if (kj != last_key) w = weight_of(scale.e(scale.z(logit_of(kj)))), last_key = kj;
-            ++before, m += w;
-          }
+          if (kj > key || (kj == key && sm.index[j] < index)) ++before, m += sm.weight[j];
         }
         if (count_open ? before + 1 == uint32_t(k) : m < limit && m + own >= limit) {
           sm.order.cut = {key, index};
@@ -563,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
       const uint32_t key = mine ? sm.key[tid] : 0, index = mine ? sm.index[tid] : 0;
       const float e = mine ? scale.e(scale.z(logit_of(key))) : 0.0f;
       const uint64_t own = weight_of(e);
-      sm.few_mass[tid] = own;
+      sm.weight[tid] = own;
       __syncthreads();
       uint32_t before = 0;
       uint64_t m = 0;
       for (uint32_t j = 0; mine && j < n; ++j) {
         const uint32_t kj = sm.key[j];
-        if (kj > key || (kj == key && sm.index[j] < index)) ++before, m += sm.few_mass[j];
+        if (kj > key || (kj == key && sm.index[j] < index)) ++before, m += sm.weight[j];
       }
       Cut last = {0, 0xffffffffu};
       if (count_open) {  // else top-k has been resolved, or keeps all that has a weight
@@ -587,11 +585,11 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
       }
       const bool kept = mine && !(e < floor_e) &&
                         (key > last.key || (key == last.key && index <= last.index));
-      sm.few_mass[tid] = kept ? own : 0;
+      sm.weight[tid] = kept ? own : 0;
       __syncthreads();
       uint64_t all = 0, upto = 0;
       for (uint32_t j = 0; j < n; ++j) {
-        const uint64_t w = sm.few_mass[j];
+        const uint64_t w = sm.weight[j];
         all += w;
         if (sm.index[j] <= index) upto += w;
       }
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
       fresh = order.step == kHistogram;
       const uint32_t lowest_bin = order.step == kListFew ? 0 : order.bin;
       if (fresh) {
-        for (int i = tid; i < kBins; i += kThreads) sm.mass[i] = 0, sm.counts[i] = 0;
+        for (int i = tid; i < kBins; i += kThreads) sm.mass[0][i] = sm.mass[1][i] = sm.mass[2][i] = 0, sm.counts[i] = 0;
         __syncthreads();
       }
       if (fresh) {
@@ -668,11 +666,11 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
     if (order.step == kCut) {
       cut = order.cut;
     } else {
-      // Too many tokens in one bin: the cut's key by bisection over its bits, then its
-      // index, every CTA over its slice.
-      uint64_t mass;   // of the tokens inside the cut that are not ranked behind
-      uint32_t count;  // (key, index)
-      auto sums_to = [&](uint32_t key, uint32_t index) {
+      // Too many tokens in one bin, as where logits are alike: the cut's key by bisection over
+      // its bits, every CTA over its slice, then its index by counting the tokens with it.
+      uint64_t mass;   // of the tokens inside the cut with at least
+      uint32_t count;  // this key
+      auto sums_to = [&](uint32_t key) {
         uint64_t m = 0;
         uint32_t c = 0;
 #pragma unroll 1
@@ -684,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
             const float l = clean(s.at(v, j));
             const uint32_t q = key_of(l);
             if (uint32_t(i) >= uint32_t(s.vocab) || !kept(q, i)) continue;
-            if (q < key || (q == key && uint32_t(i) > index)) continue;
+            if (q < key) continue;
             m += weight_of(scale.e(scale.z(l))), ++c;
           }
         }
@@ -693,28 +691,69 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
         mass = cluster_mass(), count = sm.count[slot];
       };
       constexpr uint32_t kAll = 0xffffffffu;
+      // bits of a key that are alike in all positive and in all negative logits of the type
+      constexpr int kLowBits = sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 13 : 16;
       bool open = by_count;
       uint64_t limit = by_count ? uint64_t(k) : threshold(double(p) * double(total), false);
 #pragma unroll 1
       for (;;) {
         uint32_t key = 0;  // the largest for which the sum reaches the limit
 #pragma unroll 1
-        for (int b = 31; b >= 0; --b) {
-          sums_to(key | 1u << b, kAll);
+        for (int b = 31; b >= kLowBits; --b) {
+          sums_to(key | 1u << b);
           if ((open ? uint64_t(count) : mass) >= limit) key |= 1u << b;
         }
-        uint32_t lo = 0, hi = uint32_t(s.vocab - 1);  // the first index for which it does
-        while (lo < hi) {
-          const uint32_t mid = (lo + hi) / 2;
-          sums_to(key, mid);
-          if ((open ? uint64_t(count) : mass) >= limit) hi = mid;
-          else lo = mid + 1;
+        if (!(key >> 31)) key |= (1u << kLowBits) - 1;
+        // the ties at this key that are kept, and the index of the last of them
+        const uint64_t w = weight_of(scale.e(scale.z(logit_of(key))));
+        if (key == kAll) mass = 0, count = 0;
+        else sums_to(key + 1);
+        const uint64_t ties = open ? limit - count : (limit - mass + w - 1) / w;
+        const uint64_t upto = mass + ties * w;
+        auto ties_of = [&](const uint4& v, int g) {
+          uint32_t n = 0;
+          for (int j = 0; j < kPer; ++j) {
+            const int i = s.first(g) + j;
+            n += key_of(clean(s.at(v, j))) == key && uint32_t(i) < uint32_t(s.vocab) && kept(key, i);
+          }
+          return n;
+        };
+        uint64_t mine = 0;
+        for (int g = s.w0 + lane; g < s.w1; g += 32) mine += ties_of(s.granule(g), g);
+        next_slot();
+        publish(mine, 0);
+        uint64_t run = 0;
+        for (uint32_t i = 0; i < rank; ++i) run += sm.cta_mass[slot][i];
+        for (int i = 0; i < warp; ++i) run += sm.warp_mass[i];
+        if (run < ties && run + sm.warp_mass[warp] >= ties) {
+          for (int g = s.w0 + lane;; g += 32) {  // ends: the warp has the last of them
+            uint4 v = make_uint4(0, 0, 0, 0);
+            uint64_t n = 0;
+            if (g < s.w1) {
+              v = s.granule(g);
+              n = ties_of(v, g);
+            }
+            const uint64_t through = run + warp_scan64(n, lane);
+            const uint32_t found = __ballot_sync(0xffffffffu, through >= ties);
+            if (found) {
+              if (lane == __ffs(int(found)) - 1) {
+                uint64_t left = ties - (through - n);
+                int i = s.first(g);
+                for (int j = 0; left > 0; ++j, ++i)
+                  if (key_of(clean(s.at(v, j))) == key && uint32_t(i) < uint32_t(s.vocab) && kept(key, i))
+                    if (--left == 0) break;
+                for (uint32_t c = 0; c < ctas; ++c) store_cluster(&sm.order.cut.index, c, uint32_t(i));
+              }
+              break;
+            }
+            run = __shfl_sync(0xffffffffu, through, 31);
+          }
         }
-        sums_to(key, lo);
-        cut = {key, lo};
+        cluster_sync();
+        cut = {key, sm.order.cut.index};
         if (!open || !by_mass) break;
         open = false;
-        limit = threshold(double(p) * double(mass), false);
+        limit = threshold(double(p) * double(upto), false);
       }
     }
   }
