@@ -261,17 +261,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t stage = buf, parity = 0, buf_parity = 1;
       bool ok = true;
       for (int i = buf; i < count; i += 2) {
-        if (!(ok = tc::warp_wait(&sm.sum_empty[buf], buf_parity))) break;
+        const uint32_t src = data + stage * kWideStageBytes;
+        const uint64_t dx = tc::tile_desc(src), dw = tc::tile_desc(src + kTileBytes);
+        // the accumulator last: it is what is waited for
         if (!(ok = tc::warp_wait(&sm.full[stage], parity))) break;
+        if (!(ok = tc::warp_wait(&sm.sum_empty[buf], buf_parity))) break;
         tc::fence_after_sync();
         if (lane == 0) {
-          const uint32_t src = data + stage * kWideStageBytes;
-          const uint64_t dx = tc::tile_desc(src), dw = tc::tile_desc(src + kTileBytes);
           for (int k = 0; k < 4; ++k)  // 32 bytes of k an instruction
             tc::mma_e4m3(tmem + buf * kWideCols, dx + 2 * k, dw + 2 * k, instruction, k > 0);
-          tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
           if (SPLIT) tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
           else tc::mma_commit_both(staging::smem_addr(&sm.empty[stage]));
+          tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
         }
         __syncwarp();
         stage += 2;
