@@ -365,8 +365,35 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
   finish(a, sum, w.inv_tokens);
 }
 
-// The pass for more experts than a warp's registers hold: a warp a token, the row read
-// again for each question.
+// A token's loss (before its sequence's share) and gradient by a warp, the row read again for
+// each question; f_of(e) is the weight f of expert e.
+template <typename T, int SCORE, typename F>
+__device__ __forceinline__ float token_by_warp(const T* l, T* d, int experts, float share, F&& f_of) {
+  const int lane = threadIdx.x & 31;
+  float top = 0.0f, total = 0.0f, dot = 0.0f;
+  if (SCORE == RESHARD_SCORE_SOFTMAX) {
+    top = -INFINITY;
+    for (int e = lane; e < experts; e += 32) top = fmaxf(top, to_float(l[e]));
+    top = warp_max(top);
+    if (top == -INFINITY) top = 0.0f;  // all scores 0
+  }
+  for (int e = lane; e < experts; e += 32) {
+    const float v = tc::unpack2(Score<SCORE>::of(to_float(l[e]), 0.0f, top)).x;
+    total += v;
+    dot = fmaf(v, f_of(e), dot);
+  }
+  total = warp_sum(total);
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  dot = warp_sum(dot) * inv;
+  if (d != nullptr)
+    for (int e = lane; e < experts; e += 32) {
+      const uint64_t v = Score<SCORE>::of(to_float(l[e]), 0.0f, top);
+      d[e] = from_float<T>(share * inv * tc::unpack2(Score<SCORE>::slope(v)).x * (f_of(e) - dot));
+    }
+  return dot;
+}
+
+// The pass for more experts than a warp's registers hold: a warp a token.
 template <typename T, int SCORE>
 __global__ void __launch_bounds__(256) balance_many_kernel(const __grid_constant__ BalanceArgs a) {
   extern __shared__ float f_smem[];
@@ -380,37 +407,75 @@ __global__ void __launch_bounds__(256) balance_many_kernel(const __grid_constant
   float sum = 0.0f;
   for (int i = first + warp; i < end; i += 8) {
     const int64_t t = int64_t(s) * a.seqlen + i;
-    const T* l = static_cast<const T*>(a.logits) + t * a.ld;
     T* d = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.ld : nullptr;
     if (a.mask && !a.mask[t]) {
       if (d)
         for (int e = lane; e < a.nexperts; e += 32) d[e] = from_float<T>(0.0f);
       continue;
     }
-    float top = 0.0f, total = 0.0f, dot = 0.0f;
-    if (SCORE == RESHARD_SCORE_SOFTMAX) {
-      top = -INFINITY;
-      for (int e = lane; e < a.nexperts; e += 32) top = fmaxf(top, to_float(l[e]));
-      top = warp_max(top);
-      if (top == -INFINITY) top = 0.0f;  // all scores 0
-    }
-    for (int e = lane; e < a.nexperts; e += 32) {
-      const float v = tc::unpack2(Score<SCORE>::of(to_float(l[e]), 0.0f, top)).x;
-      total += v;
-      dot = fmaf(v, f_smem[e], dot);
-    }
-    total = warp_sum(total);
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    dot = warp_sum(dot) * inv;
-    sum += dot;
-    if (!d) continue;
-    const float scale = w.share * inv;
-    for (int e = lane; e < a.nexperts; e += 32) {
-      const uint64_t v = Score<SCORE>::of(to_float(l[e]), 0.0f, top);
-      d[e] = from_float<T>(scale * tc::unpack2(Score<SCORE>::slope(v)).x * (f_smem[e] - dot));
-    }
+    sum += token_by_warp<T, SCORE>(static_cast<const T*>(a.logits) + t * a.ld, d, a.nexperts, w.share,
+                                   [&](int e) { return f_smem[e]; });
   }
   finish(a, lane == 0 ? sum : 0.0f, w.inv_tokens);
+}
+
+// Counts, loss and gradient of few tokens by one CTA, a warp a token: one launch instead of
+// two, the second of which waits for the first (61 tokens of 19 experts: 12.3 -> 6.3 us).
+constexpr int kSmallThreads = 1024;
+constexpr int64_t kSmallCounts = 4096, kSmallChoices = 8192;
+// The CTA's warps go through the tokens in rounds, each as long as 3 + experts / 32 steps:
+// 61 tokens of 19 experts (8 steps) take 6.3 us, 128 of 64 (20) 10.3 us, 128 of 256 (44) 12.4
+// us; the two kernels 10.3 us and more.
+inline bool small_enough(int64_t tokens, int64_t experts) {
+  return cdiv(tokens, kSmallThreads / 32) * (cdiv(experts, 32) + 3) <= 16;
+}
+
+template <typename T, int SCORE>
+__global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const __grid_constant__ BalanceArgs a) {
+  extern __shared__ int32_t counted[];  // [nseq][nexperts], then the tokens of each sequence
+  __shared__ float sums[kSmallThreads / 32];
+  __shared__ int live;
+  int32_t* tokens = counted + a.nseq * a.nexperts;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bins = a.nseq * a.nexperts, count = a.nseq * a.seqlen;
+  for (int i = threadIdx.x; i < bins + a.nseq; i += kSmallThreads) counted[i] = 0;
+  if (threadIdx.x == 0) live = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < count * a.topk; i += kSmallThreads) {
+    const int t = i / a.topk, s = t / a.seqlen;
+    if (a.mask && !a.mask[t]) continue;
+    const int e = a.experts[i];
+    if (uint32_t(e) < uint32_t(a.nexperts)) atomicAdd(&counted[s * a.nexperts + e], 1);
+    if (i == t * a.topk) atomicAdd(&tokens[s], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < bins; i += kSmallThreads) a.counts[i] = counted[i];
+  for (int i = threadIdx.x; i < a.nseq; i += kSmallThreads)
+    if (tokens[i] > 0) atomicAdd(&live, 1);
+  __syncthreads();
+  const float share = a.coef / float(max(live, 1)) * (a.grad ? *a.grad : 1.0f);
+  float sum = 0.0f;
+  for (int t = warp; t < count; t += kSmallThreads / 32) {
+    const int s = t / a.seqlen;
+    T* d = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.ld : nullptr;
+    if (a.mask && !a.mask[t]) {
+      if (d)
+        for (int e = lane; e < a.nexperts; e += 32) d[e] = from_float<T>(0.0f);
+      continue;
+    }
+    const float n = float(tokens[s]);
+    const float per_count = float(a.nexperts) / (float(a.topk) * n);
+    sum += token_by_warp<T, SCORE>(
+               static_cast<const T*>(a.logits) + t * a.ld, d, a.nexperts, share / n,
+               [&](int e) { return float(counted[s * a.nexperts + e]) * per_count; }) /
+           n;
+  }
+  if (lane == 0) sums[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0 && a.loss) {
+    for (int w = 1; w < kSmallThreads / 32; ++w) sum += sums[w];
+    *a.loss = sum * a.coef / float(max(live, 1));
+  }
 }
 
 int64_t header_bytes(int64_t nseq) { return cdiv(nseq * 4 + 4, 16) * 16; }  // tokens, done
@@ -446,12 +511,18 @@ const void* pass_kernel(int values) {
 }
 
 template <typename T, int SCORE>
+reshard_status_t launch_small(BalanceArgs& a, cudaStream_t stream) {
+  balance_small_kernel<T, SCORE>
+      <<<1, kSmallThreads, sizeof(int32_t) * size_t(a.nseq) * size_t(a.nexperts + 1), stream>>>(a);
+  return launched("reshard_balance_loss");
+}
+
+template <typename T, int SCORE>
 reshard_status_t launch_pass(BalanceArgs& a, int64_t sms, cudaStream_t stream) {
   constexpr int kPer = 16 / int(sizeof(T));
   const bool vec = a.nexperts % kPer == 0 && a.ld % kPer == 0 && aligned(a.logits, 16) &&
                    aligned(a.dlogits, 16);
-  // 16 logits a lane (fewer shuffles a logit than with 8: XXX) while a warp is enough,
-  // 8 where the row is short, up to 32
+  // 16 logits a lane while a warp is enough: half the shuffles a logit of 8 a lane; up to 32
   int lanes = 1;
   while (lanes < 32 && lanes * 16 < a.nexperts) lanes *= 2;
   const int values = int(cdiv(cdiv(a.nexperts, vec ? kPer : 1), lanes)) * (vec ? kPer : 1);
@@ -545,6 +616,13 @@ extern "C" reshard_status_t reshard_balance_loss(
   a.nexperts = int32_t(nexperts);
   a.score = score;
   a.coef = coef;
+  if (rs::small_enough(nseq * seqlen, nexperts) && nseq * (nexperts + 1) <= rs::kSmallCounts &&
+      nseq * seqlen * topk <= rs::kSmallChoices)
+    return rs::op::by_dtype(dtype, [&](auto t) {
+      using T = decltype(t);
+      return score == RESHARD_SCORE_SOFTMAX ? rs::launch_small<T, RESHARD_SCORE_SOFTMAX>(a, st)
+                                            : rs::launch_small<T, RESHARD_SCORE_SIGMOID>(a, st);
+    });
   // the counts: a cluster a sequence, more of them for choices beyond 4096 a CTA while there
   // are SMs for them; a short sequence takes one CTA
   const int64_t choices = seqlen * topk;
