@@ -29,8 +29,7 @@ using staging::smem_addr;
 using tc::cluster_sync;
 using tc::in_cta;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kFewThreads = 256, kManyThreads = 1024;  // of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;
 // Bins of 1/64 nat, a histogram of 8 nats at a time, for top-p alone; bins of 1/16 nat, all
@@ -38,7 +37,7 @@ constexpr int kBins = 512;
 constexpr int kBinsPerNat = 64, kWideBinsPerNat = 16;
 constexpr int kNats = 32;
 static_assert(kBins == kNats * kWideBinsPerNat, "one histogram for top-k");
-constexpr uint32_t kFew = kThreads;  // tokens with which the first CTA finishes a row on its own
+constexpr int kFew = 256;  // tokens with which the first CTA finishes a row on its own
 constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
 
 struct SampleArgs {
@@ -61,6 +60,10 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+__device__ __forceinline__ uint64_t pack(float2 v) {
+  return tc::pack2(__float_as_uint(v.x), __float_as_uint(v.y));
+}
+__device__ __forceinline__ uint64_t pack(float v) { return pack(make_float2(v, v)); }
 // Two float32 operations at once, each rounded on its own (and never contracted).
 __device__ __forceinline__ float2 add2(float2 a, float b) {
   uint64_t d, x = tc::pack2(__float_as_uint(a.x), __float_as_uint(a.y));
@@ -89,7 +92,22 @@ struct Scale {
   float top, inv;
   __device__ float2 z(float l0, float l1) const { return mul2(add2(make_float2(l0, l1), -top), inv); }
   __device__ float z(float l) const { return z(l, l).x; }
-  __device__ static float e(float z) { return fmaxf(expf(z), 0.0f); }
+  // e^z for z <= 0, and what has the weight 0 for what lies 40 below, -inf and NaN.  After
+  // Cody and Waite: z log2(e) = n + f with n whole (the sum with 1.5 * 2^23 rounds to it), f
+  // from log2(e) in two parts, and 2^n added to the exponent of 2^f.
+  __device__ static float2 e(float2 z) {
+    constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kWhole = 0x1.8p23f;
+    const uint64_t x = pack(make_float2(fmaxf(z.x, -40.0f), fmaxf(z.y, -40.0f)));
+    const uint64_t t = tc::fma2(x, pack(kLog2e), pack(kWhole));
+    const uint64_t n = pack(add2(tc::unpack2(t), -kWhole));
+    const float2 f = tc::unpack2(tc::fma2(x, pack(kRest), tc::fma2(x, pack(kLog2e), n ^ 0x8000000080000000ull)));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(f.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(f.y));
+    return make_float2(__uint_as_float(__float_as_uint(e.x) + (uint32_t(t) << 23)),
+                       __uint_as_float(__float_as_uint(e.y) + (uint32_t(t >> 32) << 23)));
+  }
+  __device__ static float e(float z) { return e(make_float2(z, z)).x; }
 };
 
 // round(2^40 e), e in [0, 1], as high * 2^22 + low: adding 48 = 1.5 * 2^5 leaves e's
@@ -127,6 +145,7 @@ __device__ __forceinline__ uint32_t bin_of(float z, float per_nat) {
 // The smallest whole number that is not below x as a float64 (above: that is above x).
 // Comparing sums with it replaces comparing their float64s with x.
 __device__ uint64_t threshold(double x, bool above) {
+  if (x < 0x1p53) return above ? __double2ull_rd(x) + 1 : __double2ull_ru(x);  // sums are exact
   if (!(x < 0x1p60)) return ~uint64_t(0);
   uint64_t s = __double2ull_ru(x) + 64;  // sums below 2^60 round by at most 64
   for (uint64_t o = 64; o; o >>= 1)
@@ -136,6 +155,13 @@ __device__ uint64_t threshold(double x, bool above) {
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint32_t warp_scan32(uint32_t v, int lane) {  // inclusive
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
   return v;
 }
 __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {  // inclusive
@@ -156,12 +182,9 @@ __device__ __forceinline__ void store_cluster(T* at, uint32_t rank, T value) {
   else
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(uint32_t(value)) : "memory");
 }
-__device__ __forceinline__ uint2 load_cluster8(const void* at, uint32_t rank) {
-  uint2 v;
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "r"(in_cta(smem_addr(at), rank))
-               : "memory");
+__device__ __forceinline__ uint32_t load_cluster(const uint32_t* at, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_cta(smem_addr(at), rank)) : "memory");
   return v;
 }
 __device__ __forceinline__ void sum_cluster(uint64_t* at, uint32_t rank, uint64_t v) {
@@ -194,39 +217,39 @@ struct Cut {
   uint32_t key, index;
 };
 
-enum Step : uint32_t { kList, kListFew, kHistogram, kBisect, kCut };
-// What every CTA does next, as the first one has decided.
-struct Order {
-  uint32_t step, bin;  // kList: that bin's tokens; kListFew: up to it; kHistogram: from it on
-  Cut cut;
+constexpr int kGroup = 32;  // bins of which a CTA sends the sums to the others
+constexpr int kGroups = kBins / kGroup;
+static_assert(kGroups <= 32, "a group a lane");
+constexpr int kListMost = 384;  // listed tokens: with slices of 32 KiB, five CTAs an SM
+
+struct Entry {  // a listed token as the first CTA compares it
+  uint64_t rank, weight;
 };
 
-constexpr int kListMost = 512;  // listed tokens, in the histogram's place
-
+template <int kWarps>
 struct SampleSmem {
   union {
     struct {
       alignas(16) uint32_t mass[3][kBins];  // 14 bits of the weights each
-      alignas(16) uint32_t counts[kBins];
+      uint32_t counts[kBins];
     };
-    struct {
-      uint32_t key[kListMost], index[kListMost];
-      uint64_t weight[kListMost];
-    };
+    uint64_t weight[kListMost];  // of the first CTA's list
+    alignas(16) Entry entry[kFew];
   };
+  uint32_t key[kListMost], index[kListMost];  // the list, in the first CTA
+  uint64_t group_mass[2][kGroups], bin_mass[kGroup];
   uint64_t warp_mass[kWarps];
   uint64_t cta_mass[2][kMaxCluster];  // added to by every warp of the cluster: each CTA's
-  uint32_t count[2];                  // sums of a pass, and the cluster's count
+  uint64_t limit, best_mass;          // sums of a pass, and the cluster's count
+  uint32_t group_count[2][kGroups], bin_count[kGroup];
+  uint32_t count[2];
   uint32_t top_key;                   // the largest logit
   uint32_t rising;                    // ~ the lowest index of the largest logit
   uint32_t below;                     // ~ the key below which no token is among the top k
-  uint64_t scan_mass[kWarps];
-  uint32_t scan_count[kWarps];
   uint32_t listed;
-  Order order;
-  uint64_t limit, best_mass;
+  Cut cut;
+  uint32_t bisect;                    // the bin held too many tokens to list
 };
-static_assert(16 * kListMost <= 16 * kBins, "the list lies in the histogram");
 
 // This CTA's slice of a row, in granules of 16 aligned bytes; what lies outside the row
 // in the first and last granule reads as -inf.
@@ -263,13 +286,23 @@ struct Slice {
     return infinite ? flattened(fetch(g)) : fetch(g);
   }
   __device__ static float largest(const uint4& v) { return op::largest_of(reinterpret_cast<const T(&)[kPer]>(v)); }
+  // element j of granule g, which v holds, j known at run time only
+  __device__ float element(const uint4& v, int g, int j) const {
+    if (RESIDENT) return to_float(reinterpret_cast<const T*>(place(g))[j]);
+    const uint32_t w = j * int(sizeof(T)) / 4;
+    uint32_t word = w < 2 ? (w < 1 ? v.x : v.y) : (w < 3 ? v.z : v.w);
+    if (sizeof(T) == 2 && (j & 1)) word >>= 16;
+    return to_float(reinterpret_cast<const T&>(word));
+  }
   __device__ static float at(const uint4& v, int j) { return to_float(reinterpret_cast<const T*>(&v)[j]); }
 };
 
-template <typename T, bool RESIDENT>
-__global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a) {
+template <typename T, bool RESIDENT, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kFewThreads ? 5 : 1) sample_kernel(const SampleArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  using Smem = SampleSmem<kWarps>;
   extern __shared__ __align__(16) unsigned char dynamic[];
-  SampleSmem& sm = *reinterpret_cast<SampleSmem*>(dynamic);
+  Smem& sm = *reinterpret_cast<Smem*>(dynamic);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -277,13 +310,14 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   const int64_t r = blockIdx.x / ctas;
   if (tid < 2 * kMaxCluster) sm.cta_mass[tid / kMaxCluster][tid % kMaxCluster] = 0;
   if (tid < 2) sm.count[tid] = 0;
-  if (tid == 0) sm.top_key = 0, sm.rising = 0, sm.below = 0;
+  if (tid < 2 * kGroups) sm.group_mass[0][tid] = 0, sm.group_count[0][tid] = 0;
+  if (tid == 0) sm.top_key = 0, sm.rising = 0, sm.below = 0, sm.listed = 0;
   tc::cluster_arrive();  // before another CTA adds to these
 
   Slice<T, RESIDENT> s;
   constexpr int kPer = s.kPer;
   s.row = static_cast<const T*>(a.logits) + r * a.ld;
-  s.smem = dynamic + (sizeof(SampleSmem) + 15) / 16 * 16;
+  s.smem = dynamic + sizeof(Smem);
   s.vocab = int(a.vocab);
   s.skew = int(reinterpret_cast<uintptr_t>(s.row) % 16 / sizeof(T));
   const int granules = (s.vocab + s.skew + kPer - 1) / kPer;
@@ -293,25 +327,43 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   s.w0 = min(s.g1, s.g0 + warp * per_warp);
   s.w1 = min(s.g1, s.w0 + per_warp);
 
-  // 1. the slice, and the largest logit
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int g = s.w0 + lane; g < s.w1; g += 32) {
-    const uint4 v = s.fetch(g);
-    if (RESIDENT) *s.place(g) = v;
-    top = fmaxf(top, s.largest(v));
-  }
   const float temperature = a.temperature ? a.temperature[r] : 1.0f;
-  const bool greedy = !(temperature > 0.0f);
   float p = a.top_p ? a.top_p[r] : 1.0f;
   int k = a.top_k ? a.top_k[r] : 0;
-  const float floor_e = fminf(a.min_p ? a.min_p[r] : 0.0f, 1.0f);
-  const float u = fmaxf(a.u[r], 0.0f);  // NaN: 0
-  if (!(p > 0.0f)) k = 1, p = 1.0f;     // only the first
+  const float min_p = a.min_p ? a.min_p[r] : 0.0f, given_u = a.u[r];
+  auto clear = [&] {  // the histogram
+    uint4* to = reinterpret_cast<uint4*>(sm.mass);
+    for (int i = tid; i < kBins; i += kThreads) to[i] = make_uint4(0, 0, 0, 0);
+  };
+  static_assert(offsetof(Smem, key) == 16 * kBins, "masses and counts in a row");
+  clear();
+
+  // 1. the slice, and the largest logit
+  float top = -INFINITY;
+  auto take = [&](int g, const uint4& v) {
+    if (RESIDENT) *s.place(g) = v;
+    top = fmaxf(top, s.largest(v));
+  };
+  // whole granules first, four loads in flight
+  const int whole0 = max(s.w0, int(s.skew > 0)), whole1 = min(s.w1, (s.vocab + s.skew) / kPer);
+  for (int g = s.w0 + lane; g < whole1; g += 4 * 32) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (g + 32 * i >= whole0 && g + 32 * i < whole1) v[i] = __ldg(reinterpret_cast<const uint4*>(s.row + s.first(g + 32 * i)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (g + 32 * i >= whole0 && g + 32 * i < whole1) take(g + 32 * i, v[i]);
+  }
+  // the row's ends
+  if (lane == 0 && s.w0 < min(s.w1, whole0)) take(s.w0, s.fetch(s.w0));
+  if (lane == ((s.w1 - 1 - s.w0) & 31) && max(s.w0, max(whole0, whole1)) < s.w1) take(s.w1 - 1, s.fetch(s.w1 - 1));
+  const bool greedy = !(temperature > 0.0f);
+  const float floor_e = fminf(min_p, 1.0f);
+  const float u = fmaxf(given_u, 0.0f);  // NaN: 0
+  if (!(p > 0.0f)) k = 1, p = 1.0f;      // only the first
   const bool by_count = !greedy && k > 0 && k < s.vocab;
   const bool by_mass = !greedy && p < 1.0f;
-  if (by_count || by_mass)
-    for (int i = tid; i < kBins; i += kThreads) sm.mass[0][i] = sm.mass[1][i] = sm.mass[2][i] = 0, sm.counts[i] = 0;
   const float mine_top = top;
   top = warp_max(top + 0.0f);
   tc::cluster_wait();  // the other CTAs have set their sums to 0
@@ -353,46 +405,64 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
   uint32_t bins = kBins;
   if (by_count && ~sm.below != 0 && !s.infinite)
     bins = min(bins, bin_of(scale.z(logit_of(~sm.below)), per_nat) + 1);
-  auto tally = [&](float z, float e, uint32_t begin) {
-    const uint32_t bin = bin_of(z, per_nat) - begin;
-    if (bin < bins) {
+  // The tokens of a granule in the histogram's bins, from the given one on: each lane takes
+  // its next one at a time, so that a warp makes as many rounds as its fullest lane needs.
+  float histogram_z;  // no token of these bins lies below (and few others lie above)
+  auto tally = [&](const uint4& v, int g, uint32_t begin) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) {
+      const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
+      hits |= uint32_t(z.x >= histogram_z) << j | uint32_t(z.y >= histogram_z) << (j + 1);
+    }
+    for (; hits; hits &= hits - 1) {
+      const float z = scale.z(s.element(v, g, __ffs(int(hits)) - 1));
+      const uint32_t bin = bin_of(z, per_nat) - begin;
+      if (bin >= bins) continue;
       atomicAdd(&sm.counts[bin], 1u);
-      const uint64_t w = weight_of(e);
+      const uint64_t w = weight_of(scale.e(z));
       atomicAdd(&sm.mass[0][bin], uint32_t(w) & 0x3fffu);
       atomicAdd(&sm.mass[1][bin], uint32_t(w >> 14) & 0x3fffu);
       atomicAdd(&sm.mass[2][bin], uint32_t(w >> 28));
     }
   };
+  uint32_t turn = 0;  // histograms take turns with the sums of their groups
+  auto send_groups = [&] {
+    __syncthreads();
+    // for the next one, before any CTA can be there
+    if (tid < kGroups) sm.group_mass[turn ^ 1][tid] = 0, sm.group_count[turn ^ 1][tid] = 0;
+    for (int i = warp; i < kGroups; i += kWarps) {
+      const int bin = i * kGroup + lane;
+      const uint32_t n = __reduce_add_sync(0xffffffffu, sm.counts[bin]);
+      const uint32_t m0 = __reduce_add_sync(0xffffffffu, sm.mass[0][bin]);
+      const uint32_t m1 = __reduce_add_sync(0xffffffffu, sm.mass[1][bin]);
+      const uint32_t m2 = __reduce_add_sync(0xffffffffu, sm.mass[2][bin]);
+      if (n && lane < int(ctas)) {
+        sum_cluster(&sm.group_count[turn][i], lane, n);
+        sum_cluster(&sm.group_mass[turn][i], lane, m0 + (uint64_t(m1) << 14) + (uint64_t(m2) << 28));
+      }
+    }
+  };
   Weights sums;
   uint32_t lowest = 0xffffffffu;
-  if (by_count || by_mass) {
-    for (int g = s.w0 + lane; g < s.w1; g += 32) {
-      const uint4 v = s.granule(g);
+  histogram_z = by_count || by_mass ? -float(bins) / per_nat : INFINITY;
+  for (int g = s.w0 + lane; g < s.w1; g += 32) {
+    const uint4 v = s.granule(g);
 #pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
-        const float e0 = scale.e(z.x), e1 = scale.e(z.y);
-        sums.add(e0, e1);
-        tally(z.x, e0, 0);
-        tally(z.y, e1, 0);
-      }
+    for (int j = 0; j < kPer; j += 2) {
+      const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
+      const float2 e = scale.e(z);
+      sums.add(e.x, e.y);
     }
-  } else {
-    for (int g = s.w0 + lane; g < s.w1; g += 32) {
-      const uint4 v = s.granule(g);
-#pragma unroll
-      for (int j = 0; j < kPer; j += 2) {
-        const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
-        sums.add(scale.e(z.x), scale.e(z.y));
-      }
-    }
-    if (greedy && holds_top)
-      for (int g = s.w0 + lane; g < s.w1 && lowest == 0xffffffffu; g += 32) {
-        const uint4 v = s.granule(g);
-        for (int j = kPer - 1; j >= 0; --j)
-          if (s.at(v, j) == scale.top) lowest = uint32_t(s.first(g) + j);
-      }
+    if (scale.z(s.largest(v)) >= histogram_z) tally(v, g, 0);
   }
+  if (by_count || by_mass) send_groups();
+  if (greedy && holds_top)
+    for (int g = s.w0 + lane; g < s.w1 && lowest == 0xffffffffu; g += 32) {
+      const uint4 v = s.granule(g);
+      for (int j = kPer - 1; j >= 0; --j)
+        if (s.at(v, j) == scale.top) lowest = uint32_t(s.first(g) + j);
+    }
   // Adds the threads' values to every CTA's sums (of the given slot, which are 0 before).
   uint32_t slot = 0;
   auto publish = [&](uint64_t mass, uint32_t count) {
@@ -440,88 +510,57 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
     return key > cut.key || (key == cut.key && uint32_t(i) <= cut.index);
   };
   if (by_count || by_mass) {
-    // The first CTA's view: the histograms' sums (two bins a thread) and what lies before.
-    static_assert(kBins == 2 * kThreads, "two bins a thread");
-    uint32_t counts[2] = {}, count_before = 0;
-    uint64_t masses[2] = {}, mass_before = 0;
+    // Every CTA decides, alike, from the sums of the cluster's histograms.
     uint32_t skipped_count = 0;   // tokens above the histogram's range
     uint64_t skipped_mass = 0;
     uint32_t begin = 0;           // the histogram's first bin
     bool count_open = by_count;   // top-k still to be resolved, else top-p
     uint64_t kept_mass = total;   // of the tokens that top-k keeps
-    uint32_t bin_count = 0;       // tokens and weights before the listed bin
-    uint64_t bin_mass = 0;
-    auto gather = [&] {
-      counts[0] = counts[1] = 0, masses[0] = masses[1] = 0;
-#pragma unroll 4
-      for (uint32_t c = 0; c < ctas; ++c) {
-        const uint2 n = load_cluster8(&sm.counts[2 * tid], c);
-        const uint2 m0 = load_cluster8(&sm.mass[0][2 * tid], c);
-        const uint2 m1 = load_cluster8(&sm.mass[1][2 * tid], c);
-        const uint2 m2 = load_cluster8(&sm.mass[2][2 * tid], c);
-        counts[0] += n.x, counts[1] += n.y;
-        masses[0] += m0.x + (uint64_t(m1.x) << 14) + (uint64_t(m2.x) << 28);
-        masses[1] += m0.y + (uint64_t(m1.y) << 14) + (uint64_t(m2.y) << 28);
-      }
-      const uint32_t cn = counts[0] + counts[1];
-      const uint64_t mn = masses[0] + masses[1];
-      uint64_t ci = warp_scan64(cn, lane), mi = warp_scan64(mn, lane);
-      __syncthreads();
-      if (lane == 31) sm.scan_count[warp] = uint32_t(ci), sm.scan_mass[warp] = mi;
-      __syncthreads();
-      count_before = skipped_count + uint32_t(ci) - cn;
-      mass_before = skipped_mass + mi - mn;
-      for (int i = 0; i < warp; ++i)
-        count_before += sm.scan_count[i], mass_before += sm.scan_mass[i];
-    };
-    // Orders the bin in which the last kept token lies to be listed; where it lies beyond
-    // the histogram, a histogram of the next nats.
+    uint32_t bin = 0;             // the bin in which the last kept token lies
+    uint32_t bin_count = 0, through = 0;  // tokens before it, and with it
+    uint64_t bin_mass = 0;                // weights before it
+    // Finds that bin; false where it lies beyond the histogram.
     auto decide = [&] {
-      if (tid == 0) {
-        sm.order.step = kHistogram;
-        sm.limit = threshold(double(p) * double(kept_mass), false);
-      }
+      if (tid == 0 && !count_open) sm.limit = threshold(double(p) * double(kept_mass), false);
+      if (tid < kGroup) sm.bin_mass[tid] = 0, sm.bin_count[tid] = 0;
       __syncthreads();
-      const uint64_t limit = sm.limit;
-      uint32_t c = count_before;
-      uint64_t m = mass_before;
-      for (int j = 0; j < 2; ++j) {
-        const bool inside = count_open ? c < uint32_t(k) && c + counts[j] >= uint32_t(k)
-                                       : m < limit && m + masses[j] >= limit;
-        if (inside) {
-          sm.order.step = c + counts[j] <= kFew ? kListFew : kList;
-          sm.order.bin = begin + 2 * tid + j;
-          sm.scan_count[0] = c;
-          sm.scan_mass[0] = m;
+      const uint64_t limit = count_open ? uint64_t(k) : sm.limit;
+      // the lane's share of a scan: whether the limit is reached in it, and what lies before
+      auto search = [&](uint32_t n, uint64_t m, uint32_t& count, uint64_t& mass) {
+        const uint32_t to_count = count + warp_scan32(n, lane);
+        const uint64_t to_mass = mass + warp_scan64(m, lane);
+        const uint64_t to = count_open ? to_count : to_mass;
+        const uint32_t found = __ballot_sync(0xffffffffu, to >= limit && to - (count_open ? n : m) < limit);
+        const int i = found ? __ffs(int(found)) - 1 : 31;
+        through = __shfl_sync(0xffffffffu, to_count, i);
+        count = found ? through - __shfl_sync(0xffffffffu, n, i) : through;
+        mass = __shfl_sync(0xffffffffu, found ? to_mass - m : to_mass, i);
+        return found ? i : -1;
+      };
+      const int group = search(lane < kGroups ? sm.group_count[turn][lane] : 0,
+                               lane < kGroups ? sm.group_mass[turn][lane] : 0, skipped_count, skipped_mass);
+      if (group < 0) return false;
+      if (warp < int(ctas)) {  // the group's bins from every CTA
+        const int i = group * kGroup + lane;
+        const uint32_t n = load_cluster(&sm.counts[i], warp);
+        const uint32_t m0 = load_cluster(&sm.mass[0][i], warp);
+        const uint32_t m1 = load_cluster(&sm.mass[1][i], warp);
+        const uint32_t m2 = load_cluster(&sm.mass[2][i], warp);
+        if (n) {
+          atomicAdd(&sm.bin_count[lane], n);
+          sum_cluster(&sm.bin_mass[lane], rank, m0 + (uint64_t(m1) << 14) + (uint64_t(m2) << 28));
         }
-        c += counts[j], m += masses[j];
       }
-      if (tid == kThreads - 1) sm.scan_count[1] = c, sm.scan_mass[1] = m;
       __syncthreads();
-      if (sm.order.step != kHistogram) {
-        bin_count = sm.scan_count[0], bin_mass = sm.scan_mass[0];
-        if (tid == 0) sm.listed = 0;
-        return;
-      }
-      skipped_count = sm.scan_count[1], skipped_mass = sm.scan_mass[1];
-      __syncthreads();
-      if (begin + kBins < uint32_t(kNats) * uint32_t(per_nat)) {
-        begin += kBins;
-      } else if (count_open && by_mass) {
-        count_open = false;
-        begin = 0, skipped_count = 0, skipped_mass = 0;
-      } else if (tid == 0) {
-        sm.order.step = kCut, sm.order.cut = {0, 0xffffffffu};
-      }
-      if (tid == 0) sm.order.bin = begin;
+      bin_count = skipped_count, bin_mass = skipped_mass;
+      bin = begin + group * kGroup + search(sm.bin_count[lane], sm.bin_mass[lane], bin_count, bin_mass);
+      return true;
     };
     // Ranks the listed tokens by (logit, index) and takes the last kept one.
     auto resolve = [&] {
       const uint32_t n = sm.listed;
-      if (n > uint32_t(kListMost)) {
-        if (tid == 0) sm.order.step = kBisect;
-        return;
-      }
+      if (tid == 0) sm.bisect = n > uint32_t(kListMost);
+      if (n > uint32_t(kListMost)) return;
       const uint64_t limit = sm.limit;
       for (uint32_t i = tid; i < n; i += kThreads)
         sm.weight[i] = weight_of(scale.e(scale.z(logit_of(sm.key[i]))));
@@ -536,136 +575,139 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
           if (kj > key || (kj == key && sm.index[j] < index)) ++before, m += sm.weight[j];
         }
         if (count_open ? before + 1 == uint32_t(k) : m < limit && m + own >= limit) {
-          sm.order.cut = {key, index};
+          sm.cut = {key, index};
           sm.best_mass = m + own;
         }
       }
-      __syncthreads();
-      if (!(count_open && by_mass)) {
-        if (tid == 0) sm.order.step = kCut;
-        return;
-      }
-      kept_mass = sm.best_mass;  // now top-p among what top-k keeps
-      count_open = false;
-      if (begin == 0) {          // its bin is in the histogram that the registers still hold
-        decide();
-      } else {
-        begin = 0, skipped_count = 0, skipped_mass = 0;
-        if (tid == 0) sm.order.step = kHistogram, sm.order.bin = 0;
-      }
     };
-    // The whole rest, with all tokens that may be kept in the list: a token a thread.
+    // The whole rest, with all tokens that may be kept in the list: `per` threads a token,
+    // which compare it with the others.
     auto finish_few = [&] {
-      const uint32_t n = sm.listed;
-      const bool mine = tid < int(n);
-      const uint32_t key = mine ? sm.key[tid] : 0, index = mine ? sm.index[tid] : 0;
+      const int n = int(sm.listed);
+      int per = 1;
+      while (per < 32 && 2 * per * n <= kThreads) per *= 2;
+      const int i = tid / per, part = tid % per;
+      const bool mine = i < n;
+      const uint32_t key = mine ? sm.key[i] : 0, index = mine ? sm.index[i] : 0;
       const float e = mine ? scale.e(scale.z(logit_of(key))) : 0.0f;
-      const uint64_t own = weight_of(e);
-      sm.weight[tid] = own;
+      const uint64_t own = weight_of(e), place = uint64_t(key) << 32 | uint32_t(~index);
+      if (mine && part == 0) sm.entry[i] = {place, own};
       __syncthreads();
       uint32_t before = 0;
       uint64_t m = 0;
-      for (uint32_t j = 0; mine && j < n; ++j) {
-        const uint32_t kj = sm.key[j];
-        if (kj > key || (kj == key && sm.index[j] < index)) ++before, m += sm.weight[j];
+#pragma unroll 4
+      for (int j = part; j < n; j += per) {
+        const ulonglong2 other = reinterpret_cast<const ulonglong2*>(sm.entry)[j];
+        if (other.x > place) ++before, m += other.y;
+      }
+      for (int o = 1; o < per; o *= 2) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        m += __shfl_xor_sync(0xffffffffu, m, o);
       }
       Cut last = {0, 0xffffffffu};
       if (count_open) {  // else top-k has been resolved, or keeps all that has a weight
-        if (mine && before + 1 == uint32_t(k)) sm.order.cut = {key, index}, sm.best_mass = m + own;
+        if (mine && before + 1 == uint32_t(k)) sm.cut = {key, index}, sm.best_mass = m + own;
         __syncthreads();
-        last = sm.order.cut, kept_mass = sm.best_mass;
-        __syncthreads();
+        last = sm.cut, kept_mass = sm.best_mass;
       }
       if (by_mass) {
+        __syncthreads();
         if (tid == 0) sm.limit = threshold(double(p) * double(kept_mass), false);
         __syncthreads();
-        if (mine && m < sm.limit && m + own >= sm.limit) sm.order.cut = {key, index};
+        if (mine && m < sm.limit && m + own >= sm.limit) sm.cut = {key, index};
         __syncthreads();
-        last = sm.order.cut;
+        last = sm.cut;
       }
       const bool kept = mine && !(e < floor_e) &&
                         (key > last.key || (key == last.key && index <= last.index));
-      sm.weight[tid] = kept ? own : 0;
+      __syncthreads();
+      if (mine && part == 0) sm.entry[i] = {index, kept ? own : 0};
       __syncthreads();
       uint64_t all = 0, upto = 0;
-      for (uint32_t j = 0; j < n; ++j) {
-        const uint64_t w = sm.weight[j];
-        all += w;
-        if (sm.index[j] <= index) upto += w;
+#pragma unroll 4
+      for (int j = part; j < n; j += per) {
+        const ulonglong2 other = reinterpret_cast<const ulonglong2*>(sm.entry)[j];
+        all += other.y;
+        if (other.x <= index) upto += other.y;
+      }
+      for (int o = 1; o < per; o *= 2) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        upto += __shfl_xor_sync(0xffffffffu, upto, o);
       }
       if (tid == 0) sm.limit = min(threshold(double(u) * double(all), true), all);
       __syncthreads();
-      if (kept && upto >= sm.limit && upto - own < sm.limit) answer(int(index), logit_of(key));
+      if (kept && part == 0 && upto >= sm.limit && upto - own < sm.limit) answer(int(index), logit_of(key));
     };
-    auto send = [&] {  // sm.order to every CTA
-      __syncthreads();
-      if (tid < int(ctas) && tid > 0) {
-        store_cluster(&sm.order.step, tid, sm.order.step);
-        store_cluster(&sm.order.bin, tid, sm.order.bin);
-        store_cluster(&sm.order.cut.key, tid, sm.order.cut.key);
-        store_cluster(&sm.order.cut.index, tid, sm.order.cut.index);
-      }
-    };
-
-    bool fresh = true;  // the histograms have just been made
-    Order order;
+    bool found;
     for (;;) {
-      if (rank == 0) {
-        if (fresh) {
-          gather();
-          decide();
-        } else {
-          resolve();
-        }
-        send();
-      }
-      cluster_sync();
-      order = sm.order;
-      if (order.step == kCut || order.step == kBisect) break;
-      fresh = order.step == kHistogram;
-      const uint32_t lowest_bin = order.step == kListFew ? 0 : order.bin;
-      if (fresh) {
-        for (int i = tid; i < kBins; i += kThreads) sm.mass[0][i] = sm.mass[1][i] = sm.mass[2][i] = 0, sm.counts[i] = 0;
-        __syncthreads();
-      }
-      if (fresh) {
-        for (int g = s.w0 + lane; g < s.w1; g += 32) {
-          const uint4 v = s.granule(g);
-#pragma unroll
-          for (int j = 0; j < kPer; j += 2) {
-            const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
-            tally(z.x, scale.e(z.x), order.bin);
-            tally(z.y, scale.e(z.y), order.bin);
-          }
+      found = decide();
+      if (!found) {
+        begin += kBins;
+        if (begin >= uint32_t(kNats) * uint32_t(per_nat)) {  // every token with a weight is kept
+          if (!(count_open && by_mass)) break;
+          count_open = false;  // (top-k's histogram is all there is: it serves top-p too)
+          begin = 0, skipped_count = 0, skipped_mass = 0;
+          continue;
         }
       } else {
         // no token of these bins lies below this (all rounding goes that way)
-        const float lowest_logit = __fsub_rd(
-            scale.top, __fdiv_ru(__fdiv_ru(float(order.bin + 1), per_nat), scale.inv));
+        const float lowest_logit =
+            __fsub_rd(scale.top, __fdiv_ru(__fdiv_ru(float(bin + 1), per_nat), scale.inv));
+        const bool few = through <= uint32_t(kFew);
+        const uint32_t lowest_bin = few ? 0 : bin;
         for (int g = s.w0 + lane; g < s.w1; g += 32) {
           const uint4 v = s.granule(g);
           if (!(s.largest(v) >= lowest_logit)) continue;
-#pragma unroll 1
-          for (int j = 0; j < kPer; ++j) {
-            const float l = clean(s.at(v, j));
-            const uint32_t bin = bin_of(scale.z(l), per_nat);
-            if (bin < lowest_bin || bin > order.bin) continue;
+          uint32_t hits = 0;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) hits |= uint32_t(s.at(v, j) >= lowest_logit) << j;
+          for (; hits; hits &= hits - 1) {
+            const int j = __ffs(int(hits)) - 1;
+            const float l = clean(s.element(v, g, j));
+            const uint32_t b = bin_of(scale.z(l), per_nat);
+            if (b < lowest_bin || b > bin) continue;
             const uint32_t to = add_cluster(&sm.listed, 0, 1);
             if (to >= uint32_t(kListMost)) continue;
             store_cluster(&sm.key[to], 0, key_of(l));
             store_cluster(&sm.index[to], 0, uint32_t(s.first(g) + j));
           }
         }
+        cluster_sync();
+        if (few) {
+          if (rank == 0) finish_few();
+          return;
+        }
+        if (rank == 0) {
+          resolve();
+          __syncthreads();
+          if (tid == 0) sm.listed = 0;
+          if (tid > 0 && tid < int(ctas)) {
+            store_cluster(&sm.bisect, tid, sm.bisect);
+            store_cluster(&sm.cut.key, tid, sm.cut.key);
+            store_cluster(&sm.cut.index, tid, sm.cut.index);
+            store_cluster(&sm.best_mass, tid, sm.best_mass);
+          }
+        }
+        cluster_sync();
+        if (sm.bisect || !(count_open && by_mass)) break;
+        kept_mass = sm.best_mass;  // now top-p among what top-k keeps, by a new histogram
+        count_open = false;
+        begin = 0, skipped_count = 0, skipped_mass = 0;
       }
+      clear();
+      __syncthreads();
+      histogram_z = -float(begin + bins) / per_nat;
+      for (int g = s.w0 + lane; g < s.w1; g += 32) {
+        const uint4 v = s.granule(g);
+        if (scale.z(s.largest(v)) >= histogram_z) tally(v, g, begin);
+      }
+      turn ^= 1;
+      send_groups();
       cluster_sync();
-      if (order.step == kListFew) {
-        if (rank == 0) finish_few();
-        return;
-      }
     }
-    if (order.step == kCut) {
-      cut = order.cut;
-    } else {
+    if (found && !sm.bisect) {
+      cut = sm.cut;
+    } else if (found) {
       // Too many tokens in one bin, as where logits are alike: the cut's key by bisection over
       // its bits, every CTA over its slice, then its index by counting the tokens with it.
       uint64_t mass;   // of the tokens inside the cut with at least
@@ -742,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
                 for (int j = 0; left > 0; ++j, ++i)
                   if (key_of(clean(s.at(v, j))) == key && uint32_t(i) < uint32_t(s.vocab) && kept(key, i))
                     if (--left == 0) break;
-                for (uint32_t c = 0; c < ctas; ++c) store_cluster(&sm.order.cut.index, c, uint32_t(i));
+                for (uint32_t c = 0; c < ctas; ++c) store_cluster(&sm.cut.index, c, uint32_t(i));
               }
               break;
             }
@@ -750,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
           }
         }
         cluster_sync();
-        cut = {key, sm.order.cut.index};
+        cut = {key, sm.cut.index};
         if (!open || !by_mass) break;
         open = false;
         limit = threshold(double(p) * double(upto), false);
@@ -760,8 +802,7 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
 
   // 4. the token
   const float cut_logit = cut.key == 0 ? -INFINITY : logit_of(cut.key);
-  auto chance = [&](float l, float z, int i) {  // 0 for a token that is not kept
-    const float e = scale.e(z);
+  auto chance = [&](float l, float e, int i) {  // 0 for a token that is not kept
     if (!(l >= cut_logit) || (l == cut_logit && uint32_t(i) > cut.index) || e < floor_e) return 0.0f;
     return e;
   };
@@ -770,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
 #pragma unroll
     for (int j = 0; j < kPer; j += 2) {
       const float l0 = s.at(v, j), l1 = s.at(v, j + 1);
-      const float2 z = scale.z(l0, l1);
-      w.add(chance(l0, z.x, s.first(g) + j), chance(l1, z.y, s.first(g) + j + 1));
+      const float2 e = scale.e(scale.z(l0, l1));
+      w.add(chance(l0, e.x, s.first(g) + j), chance(l1, e.y, s.first(g) + j + 1));
     }
     return w.sum();
   };
@@ -809,8 +850,8 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
         uint64_t sum = upto - mine;
         for (int j = 0; j < kPer; ++j) {
           const int i = s.first(g) + j;
-          const float l = s.at(v, j), z = scale.z(l);
-          sum += weight_of(chance(l, z, i));
+          const float l = s.at(v, j);
+          sum += weight_of(chance(l, scale.e(scale.z(l)), i));
           if (sum >= limit) {
             answer(i, l);
             break;
@@ -821,6 +862,12 @@ __global__ void __launch_bounds__(kThreads, 5) sample_kernel(const SampleArgs a)
     }
     run = __shfl_sync(0xffffffffu, upto, 31);
   }
+}
+
+template <typename T, int kThreads>
+const void* sample_pick(bool resident) {
+  return resident ? reinterpret_cast<const void*>(sample_kernel<T, true, kThreads>)
+                  : reinterpret_cast<const void*>(sample_kernel<T, false, kThreads>);
 }
 
 template <typename T>
@@ -836,16 +883,16 @@ reshard_status_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t s
   while (ctas < kMaxCluster && (bytes > ctas * 32768 || (rows * ctas < sms && bytes > ctas * 4096)))
     ctas *= 2;
   const int64_t slice = (cdiv(cdiv(bytes, 16) + 1, ctas) + 1) * 16;
-  const size_t fixed = (sizeof(SampleSmem) + 15) / 16 * 16;
+  const bool many = rows * ctas <= sms;
+  const size_t fixed = many ? sizeof(SampleSmem<kManyThreads / 32>) : sizeof(SampleSmem<kFewThreads / 32>);
   const bool resident = fixed + size_t(slice) <= 227 * 1024;
   const size_t smem = fixed + (resident ? size_t(slice) : 0);
-  const void* kernel = resident ? reinterpret_cast<const void*>(sample_kernel<T, true>)
-                                : reinterpret_cast<const void*>(sample_kernel<T, false>);
+  const void* kernel = many ? sample_pick<T, kManyThreads>(resident) : sample_pick<T, kFewThreads>(resident);
   ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (ce == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(rows * ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
