@@ -71,12 +71,9 @@ __device__ __forceinline__ float2 add2(float2 a, float b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
   return tc::unpack2(d);
 }
+// (a product with -1 is exact, and needs no change of signs beforehand)
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-  uint64_t d;
-  const uint64_t x = tc::pack2(__float_as_uint(a.x), __float_as_uint(a.y));
-  const uint64_t y = tc::pack2(__float_as_uint(-b.x), __float_as_uint(-b.y));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-  return tc::unpack2(d);
+  return tc::unpack2(tc::fma2(pack(b), pack(-1.0f), pack(a)));
 }
 __device__ __forceinline__ float2 mul2(float2 a, float b) {
   uint64_t d, x = tc::pack2(__float_as_uint(a.x), __float_as_uint(a.y));
@@ -99,8 +96,8 @@ struct Scale {
     constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kWhole = 0x1.8p23f;
     const uint64_t x = pack(make_float2(fmaxf(z.x, -40.0f), fmaxf(z.y, -40.0f)));
     const uint64_t t = tc::fma2(x, pack(kLog2e), pack(kWhole));
-    const uint64_t n = pack(add2(tc::unpack2(t), -kWhole));
-    const float2 f = tc::unpack2(tc::fma2(x, pack(kRest), tc::fma2(x, pack(kLog2e), n ^ 0x8000000080000000ull)));
+    const uint64_t minus_n = pack(sub2(make_float2(kWhole, kWhole), tc::unpack2(t)));
+    const float2 f = tc::unpack2(tc::fma2(x, pack(kRest), tc::fma2(x, pack(kLog2e), minus_n)));
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(f.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(f.y));
@@ -405,18 +402,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFewThreads ? 5 : 1) sam
   uint32_t bins = kBins;
   if (by_count && ~sm.below != 0 && !s.infinite)
     bins = min(bins, bin_of(scale.z(logit_of(~sm.below)), per_nat) + 1);
-  // The tokens of a granule in the histogram's bins, from the given one on: each lane takes
-  // its next one at a time, so that a warp makes as many rounds as its fullest lane needs.
-  float histogram_z;  // no token of these bins lies below (and few others lie above)
-  auto tally = [&](const uint4& v, int g, uint32_t begin) {
-    uint32_t hits = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; j += 2) {
-      const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
-      hits |= uint32_t(z.x >= histogram_z) << j | uint32_t(z.y >= histogram_z) << (j + 1);
-    }
-    for (; hits; hits &= hits - 1) {
-      const float z = scale.z(s.element(v, g, __ffs(int(hits)) - 1));
+  // The tokens of a granule in the histogram's bins, from the given one on.  Those that may be
+  // are marked first, z - histogram_z having no sign, the first element highest; then each
+  // lane takes its next one at a time, so that a warp makes as many rounds as its fullest
+  // lane needs.
+  float histogram_z = by_count || by_mass ? -float(bins) / per_nat : 0.0f;  // none lies below
+  auto mark = [&](uint32_t& below, float2 z) {
+    const float2 d = add2(z, -histogram_z);
+    below = __funnelshift_l(__float_as_uint(d.x), below, 1);
+    below = __funnelshift_l(__float_as_uint(d.y), below, 1);
+  };
+  auto tally = [&](uint32_t below, const uint4& v, int g, uint32_t begin) {
+    for (uint32_t hits = ~below << (32 - kPer); hits;) {
+      const int j = __clz(int(hits));
+      hits &= ~(0x80000000u >> j);
+      const float z = scale.z(s.element(v, g, j));
       const uint32_t bin = bin_of(z, per_nat) - begin;
       if (bin >= bins) continue;
       atomicAdd(&sm.counts[bin], 1u);
@@ -445,16 +445,28 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFewThreads ? 5 : 1) sam
   };
   Weights sums;
   uint32_t lowest = 0xffffffffu;
-  histogram_z = by_count || by_mass ? -float(bins) / per_nat : INFINITY;
-  for (int g = s.w0 + lane; g < s.w1; g += 32) {
-    const uint4 v = s.granule(g);
+  if (by_count || by_mass) {
+    for (int g = s.w0 + lane; g < s.w1; g += 32) {
+      const uint4 v = s.granule(g);
+      uint32_t below = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2) {
-      const float2 z = scale.z(s.at(v, j), s.at(v, j + 1));
-      const float2 e = scale.e(z);
-      sums.add(e.x, e.y);
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 z = scale.z(s.at(v, j), s.at(v, j + 1)), e = scale.e(z);
+        sums.add(e.x, e.y);
+        mark(below, z);
+      }
+      tally(below, v, g, 0);
     }
-    if (scale.z(s.largest(v)) >= histogram_z) tally(v, g, 0);
+  } else {
+#pragma unroll 2
+    for (int g = s.w0 + lane; g < s.w1; g += 32) {
+      const uint4 v = s.granule(g);
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        const float2 e = scale.e(scale.z(s.at(v, j), s.at(v, j + 1)));
+        sums.add(e.x, e.y);
+      }
+    }
   }
   if (by_count || by_mass) send_groups();
   if (greedy && holds_top)
@@ -699,7 +711,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFewThreads ? 5 : 1) sam
       histogram_z = -float(begin + bins) / per_nat;
       for (int g = s.w0 + lane; g < s.w1; g += 32) {
         const uint4 v = s.granule(g);
-        if (scale.z(s.largest(v)) >= histogram_z) tally(v, g, begin);
+        uint32_t below = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; j += 2) mark(below, scale.z(s.at(v, j), s.at(v, j + 1)));
+        tally(below, v, g, begin);
       }
       turn ^= 1;
       send_groups();
