@@ -36,6 +36,8 @@ constexpr int kBins = 512;
 // 32 nats beyond which every weight is 0, for top-k, whose histogram leaves out most tokens.
 constexpr int kBinsPerNat = 64, kWideBinsPerNat = 16;
 constexpr int kNats = 32;
+// Where top-p goes beyond 8 nats it seldom goes far, and ever more tokens lie there.
+constexpr int kNextBins = 128;
 static_assert(kBins == kNats * kWideBinsPerNat, "one histogram for top-k");
 constexpr int kFew = 256;  // tokens with which the first CTA finishes a row on its own
 constexpr uint64_t kOne = uint64_t(1) << 40;           // weight of the most likely token
@@ -654,11 +656,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFewThreads ? 5 : 1) sam
     for (;;) {
       found = decide();
       if (!found) {
-        begin += kBins;
-        if (begin >= uint32_t(kNats) * uint32_t(per_nat)) {  // every token with a weight is kept
+        begin += bins;
+        bins = kNextBins;
+        if (by_count || begin >= kNats * kBinsPerNat) {  // every token with a weight is kept
           if (!(count_open && by_mass)) break;
           count_open = false;  // (top-k's histogram is all there is: it serves top-p too)
-          begin = 0, skipped_count = 0, skipped_mass = 0;
+          bins = kBins, begin = 0, skipped_count = 0, skipped_mass = 0;
           continue;
         }
       } else {
