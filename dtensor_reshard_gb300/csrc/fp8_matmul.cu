@@ -132,8 +132,14 @@ __device__ __noinline__ void give_up(uint32_t* status, uint32_t code) {
 // loads its own 128 tokens and half of the features of every block (32 KiB of a 48 KiB
 // stage), the halves going to both CTAs, and multiplies and sums its own 128 tokens, two
 // warps a lane quarter, 128 columns each.  (One cta_group::2 instruction for both CTAs
-// loads as little but hands accumulators over between SMs: 416 us against XXX us for
+// loads as little but hands accumulators over between SMs: 416 us against 370 us for
 // 8192 x 14336 x 4096.)
+// What bounds it is the accumulators' way out of tensor memory, which the matrix instructions
+// need too: 8192 x 14336 x 4096 to bf16 takes 370 us (2.6 PFLOP/s), 340 us with the loads but
+// no sums, 301 us with one accumulator for all of k, which would be another product.  Two
+// accumulators of 256 columns fill the 512; 128 columns a half as four accumulators took 630
+// us, 16 summing warps 426 us and more, loads of 32 columns 484 us, scalar sums 384 us.
+// 16384 tokens over 16 experts of [2048, 7168]: 216 us (2.2 PFLOP/s).
 constexpr int kWideStages = 4;  // 2 where the expert table needs the room
 constexpr int kWideStageBytes = 3 * kTileBytes;
 constexpr int kWideCols = 256;
@@ -169,7 +175,8 @@ static_assert(wide_stages_at(kTableMost) + 2 * kWideStageBytes <= kSmemMost, "sh
 // SPLIT: for fewer tokens than fill the GPU that way, a tile of 128 tokens x 256 features a
 // cluster, of which each CTA takes a share of the blocks of k; the sums of 16 columns at a
 // time go to the CTA that adds them up, in rank order, through distributed shared memory
-// (in the place of the stages).
+// (in the place of the stages).  64 x 7168 x 7168 takes 16.5 us, 128 tokens 18.5 us, against
+// 25 us with 64-token tiles; 777 x 2867 x 819 to float32 10.3 us.
 constexpr int kSplitChunk = 16;  // columns
 constexpr int kSplitChunkBytes = kRows * kSplitChunk * 4;
 // Chunks that a CTA receives at most, from all CTAs of a split.
@@ -491,7 +498,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // One tile of 128 features x NT tokens a CTA: four summing warps, a loading warp and two
 // matrix warps.  `split` CTAs of a cluster take a share of the blocks of k each and send
 // their sums through distributed shared memory to the CTA that adds up the column, in rank
-// order.
+// order.  Bound by reading w where there is much of it (1024 tokens over 256 experts of [256,
+// 7168]: 67 us, 7.0 TB/s), by latencies where there is little (1 x 2688 x 7168: 7.6 us, of
+// which 3 us are the loads).  Four stages of loads and four accumulators keep both matrix
+// warps' instructions in flight: a group of four for so few tokens takes 560 clocks by
+// itself whatever their number.
 constexpr int kMatrixWarps = 2;
 constexpr int kNarrowThreads = 32 * (5 + kMatrixWarps);
 constexpr int kNarrowStages = 4, kNarrowBufs = 4;
