@@ -9,9 +9,9 @@
 // the row is read from HBM once however many questions are asked of it:
 //   1. the largest logit;
 //   2. the weights' sum, and for top-k and top-p a histogram of how far below the
-//      largest each token lies: counts and weights in 512 bins of ln p (for top-p of 1/64,
-//      8 nats at a time: few tokens lie so high, which keeps atomics rare; for top-k of 1/16,
-//      without the tokens that the lanes' largest logits rule out);
+//      largest each token lies: counts and weights in 512 bins of ln p (for top-p of 1/48,
+//      10.7 nats: few tokens lie so high, which keeps atomics rare; for top-k of 1/16, without
+//      the tokens that the lanes' largest logits rule out);
 //   3. the bin in which the last kept token lies: each CTA sends the sums of its groups of 32
 //      bins to the others, which then read that one group's bins, and all decide alike (one
 //      CTA that read all histograms and told the others took 11 000 clocks of a row's 37 000,
@@ -24,8 +24,8 @@
 // order of atomics nor the split over warps and CTAs can change a result.
 //
 // Bound by instructions (about 23 a token of a warp's 32) and by the cluster's meetings, not by
-// HBM: 256 rows of 131072 bf16 logits take 35 us greedy, 42 us whole, 83 us with top-p 0.9,
-// 71 us mixed (67 MB, 10 us of HBM); one row 11.6 us, 37 rows of 50021 float32 14.4 us.
+// HBM: 256 rows of 131072 bf16 logits take 35 us greedy, 42 us whole, 76 us with top-p 0.95,
+// 63 us mixed (67 MB, 10 us of HBM); one row 11.6 us, 37 rows of 50021 float32 14.4 us.
 // Rows of equal logits, which no histogram tells apart, are bisected: 256 of them 1.3 ms.
 #include <type_traits>
 
@@ -43,12 +43,13 @@ using tc::in_cta;
 constexpr int kFewThreads = 256, kManyThreads = 512;  // of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;
-// Bins of 1/64 nat, a histogram of 8 nats at a time, for top-p alone; bins of 1/16 nat, all
-// 32 nats beyond which every weight is 0, for top-k, whose histogram leaves out most tokens.
-constexpr int kBinsPerNat = 64, kWideBinsPerNat = 16;
+// Bins of 1/48 nat, 10.7 nats first, for top-p alone (256 rows of 131072 with top-p 0.95, ten
+// sets: 75.7 us on average; 1/64 79.6 us, 1/40 84.7 us); bins of 1/16 nat, all 32 nats beyond
+// which every weight is 0, for top-k, whose histogram leaves out most tokens.
+constexpr int kBinsPerNat = 48, kWideBinsPerNat = 16;
 constexpr int kNats = 32;
-// Where top-p goes beyond 8 nats it seldom goes far, and ever more tokens lie there (256 mixed
-// rows of 131072: 71 us with 2 nats, 74 with 1, 72 with 4, 77 with 8).
+// Where top-p goes beyond those it seldom goes far, and ever more tokens lie there (256 mixed
+// rows of 131072, one set: 71 us in steps of 2 nats, 74 of 1, 72 of 4, 77 of 8).
 constexpr int kNextBins = 128;
 static_assert(kBins == kNats * kWideBinsPerNat, "one histogram for top-k");
 constexpr int kFew = 256;  // tokens with which the first CTA finishes a row on its own
