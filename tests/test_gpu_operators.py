@@ -297,6 +297,28 @@ def test_sample_of_masked_rows_infinities_and_nan(vocab):
         assert int(tok[5]) % 2 == 1 or t == math.inf
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [15, 60])        # CTAs of 512 and of 256 threads
+def test_sample_wherever_the_cut_lies(dtype, rows):
+    """The last kept token at several depths below the largest, alone there, among a few hundred tokens that
+    are nearly alike, and among thousands; by top-p, by top-k, and by both."""
+    vocab = 20011
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    for depth in (0.5, 5.0, 10.6, 10.7, 13.25, 16.0):
+        for alike in (1, 100, 300, 390, 5000):
+            x = torch.full((rows, vocab), -60.0, device="cuda")
+            x[:, 7::97] = -depth - 3 - torch.rand(rows, len(range(7, vocab, 97)), generator=g, device="cuda")
+            x[:, 11:11 + 4 * alike:4] = -depth - 0.004 * torch.rand(rows, alike, generator=g, device="cuda")
+            x[:, 13000] = 0.0
+            # half of the mass of the alike tokens belongs to the nucleus
+            mass = alike * math.exp(-depth)
+            total = 1 + mass + (vocab // 97) * math.exp(-depth - 3.5)
+            p = [(1 + 0.5 * mass) / total, 1.0, 0.999 - 0.3 * mass / total] * (rows // 3)
+            k = [0, 1 + (alike + 1) // 2, 1 + alike - alike // 4] * (rows // 3)
+            _sample(x, dtype, [1.0] * rows, k, p, [0.0] * rows,
+                    torch.rand(rows, generator=g, device="cuda").tolist())
+
+
 def test_sample_odd_settings_and_defaults():
     g = torch.Generator("cuda").manual_seed(4)
     x = torch.randn(12, 700, device="cuda", generator=g) * 2
