@@ -10,7 +10,7 @@
 //
 // Bound by instructions (18 for the 32 logits of a warp, 70% of the issue slots) before
 // HBM: 64 sequences of 8192 tokens and 256 experts in bf16 take 110 us (4.9 TB/s, reads and
-// writes), 16 of them 38 us, 36 us with padding; of that the counts are 7 us.
+// writes), 16 of them 37 us, 35 us with padding; of that the counts are 7 us.
 #include "operators.cuh"
 #include "tensor_core.cuh"
 
@@ -72,11 +72,18 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
   int live = 0;
   for (int i = t0 + int(threadIdx.x); i < t1; i += kCountThreads) {
     const int64_t t = int64_t(s) * a.seqlen + i;
+    const int32_t* e = a.experts + t * a.topk;
+    int4 first = {}, second = {};  // on their way while the mask is
+    if (fours) {
+      first = __ldg(reinterpret_cast<const int4*>(e));
+      if (a.topk > 4) second = __ldg(reinterpret_cast<const int4*>(e + 4));
+    }
     if (a.mask && !a.mask[t]) continue;
     ++live;
-    const int32_t* e = a.experts + t * a.topk;
     if (fours) {
-      for (int j = 0; j < a.topk; j += 4) {
+      count(first.x), count(first.y), count(first.z), count(first.w);
+      if (a.topk > 4) count(second.x), count(second.y), count(second.z), count(second.w);
+      for (int j = 8; j < a.topk; j += 4) {
         const int4 v = __ldg(reinterpret_cast<const int4*>(e + j));
         count(v.x), count(v.y), count(v.z), count(v.w);
       }
@@ -159,15 +166,18 @@ struct Weighting {
   __device__ void make(const BalanceArgs& a, int s, float* f) {
     __shared__ int live;
     if (threadIdx.x == 0) live = 0;
+    const int n = max(a.tokens[s], 1);
+    const int32_t* counts = a.counts + int64_t(s) * a.nexperts;
+    const int first = int(threadIdx.x) < a.nexperts ? counts[threadIdx.x] : 0;
     __syncthreads();
     int mine = 0;
     for (int i = threadIdx.x; i < a.nseq; i += blockDim.x) mine += a.tokens[i] > 0;
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (threadIdx.x % 32 == 0 && mine) atomicAdd(&live, mine);
-    const int n = max(a.tokens[s], 1);
     const float per_count = float(a.nexperts) / (float(a.topk) * float(n));
-    for (int e = threadIdx.x; e < a.nexperts; e += blockDim.x)
-      f[e] = float(a.counts[int64_t(s) * a.nexperts + e]) * per_count;
+    if (int(threadIdx.x) < a.nexperts) f[threadIdx.x] = float(first) * per_count;
+    for (int e = threadIdx.x + blockDim.x; e < a.nexperts; e += blockDim.x)
+      f[e] = float(counts[e]) * per_count;
     __syncthreads();
     inv_tokens = 1.0f / float(n);
     share = a.coef / float(max(live, 1)) / float(n) * (a.grad ? *a.grad : 1.0f);
