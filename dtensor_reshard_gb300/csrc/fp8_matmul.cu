@@ -838,7 +838,7 @@ reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, in
 static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
 
 template <int NT, typename Y>
-reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int dev, int64_t sms,
+reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int64_t each, int dev, int64_t sms,
                                cudaStream_t stream) {
   CUtensorMap map_x, map_w;
   reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, NT);
@@ -847,19 +847,26 @@ reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int dev, int64_
   a.ntiles = int32_t(cdiv(a.n, kRows));
   int64_t tiles = a.ntiles * cdiv(a.tokens, NT);
   if (a.offsets) tiles = a.ntiles * (a.tokens / NT + (a.nexperts < a.tokens ? a.nexperts : a.tokens));
-  // As many CTAs a tile as keep to one wave, with two blocks each: a second wave would cost
-  // more than longer shares.
+  // CTAs a tile, within one wave (a second one would cost more than longer shares) and with two
+  // blocks each: the least of a share's blocks and, with several CTAs, the sums' way to the CTA
+  // that adds them up, in ns.  (32 x 2688: k = 512 takes 4.5 us undivided, 7.5 us by two CTAs,
+  // k = 4096 10.7 us and, by eight, 8.3 us; one token's k = 1024 5.0 us and, by four, 4.4 us;
+  // 64 tokens' k = 1024 6.9 us and, by four, 11.2 us.)
   const size_t table = ExpertTable::bytes(a.nexperts);
   auto smem_of = [&](int split) {
     return split > 1 ? NarrowSmem<NT>::sums_at(table) + sizeof(float) * kRows * size_t(cdiv(NT, split) * split)
                      : sizeof(NarrowSmem<NT>) + table;
   };
+  const int64_t block = NT == 64 ? 450 : 210, way = 600 + 100 * (each < NT ? each : NT);
+  int64_t best = a.blocks * block;
   int split = 1;
-  for (int s = kMostSplit; s > 1 && split == 1; --s)
-    if (a.blocks >= 2 * s && tiles * s <= 2 * sms &&
+  for (int s = 2; s <= kMostSplit; ++s) {
+    const int64_t cost = cdiv(a.blocks, s) * block + way;
+    if (cost < best && a.blocks >= 2 * s && tiles * s <= 2 * sms &&
         tiles <= resident_clusters(narrow_kernel<NT, Y>, dev, kNarrowThreads,
                                    NarrowSmem<NT>::sums_at(0) + sizeof(float) * kRows * (NT + kMostSplit), s))
-      split = s;
+      best = cost, split = s;
+  }
   if (tiles * split >= int64_t(1) << 31)
     return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
   void* args[] = {&map_x, &map_w, &a, &split};
@@ -882,8 +889,8 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
   if (st != RESHARD_OK) return st;
   // Few tokens (of an expert, on average; experts differ): reading w is all that counts.
   const int64_t each = cdiv(a.tokens, a.nexperts);
-  if (each <= (a.offsets ? 4 : 16)) return launch_narrow<16, Y>(a, o, dev, sms, stream);
-  if (each <= (a.offsets ? 8 : 32)) return launch_narrow<32, Y>(a, o, dev, sms, stream);
+  if (each <= (a.offsets ? 4 : 16)) return launch_narrow<16, Y>(a, o, each, dev, sms, stream);
+  if (each <= (a.offsets ? 8 : 32)) return launch_narrow<32, Y>(a, o, each, dev, sms, stream);
 
   // Otherwise the least of these estimates in ns, fitted to 20 sizes from 64 x 7168 x 7168 to
   // 4096 x 4096 x 4096 within 15%: a kernel's start and end, and a time for each block of k
@@ -911,7 +918,7 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
                                 : 10500 + cdiv(blocks, s) * 500;
     if (cost < best) best = cost, split = s;
   }
-  if (split == 0) return launch_narrow<64, Y>(a, o, dev, sms, stream);
+  if (split == 0) return launch_narrow<64, Y>(a, o, each, dev, sms, stream);
   auto most = [&](int64_t rows) {
     return cdiv(a.n, kWideCols) * (a.offsets ? a.tokens / rows + experts : cdiv(a.tokens, rows));
   };
