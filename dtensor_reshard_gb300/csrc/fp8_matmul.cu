@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // matrix warps.  `split` CTAs of a cluster take a share of the blocks of k each and send
 // their sums through distributed shared memory to the CTA that adds up the column, in rank
 // order.  Bound by reading w where there is much of it (1024 tokens over 256 experts of [256,
-// 7168]: 67 us, 7.0 TB/s), by latencies where there is little (1 x 2688 x 7168: 7.6 us, of
+// 7168]: 67 us, 7.0 TB/s), by latencies where there is little (1 x 2688 x 7168: 8.2 us, of
 // which 3 us are the loads).  Four stages of loads and four accumulators keep both matrix
 // warps' instructions in flight: a group of four for so few tokens takes 560 clocks by
 // itself whatever their number.
@@ -516,13 +516,17 @@ struct NarrowSmem {
   alignas(16) float scales[2][kScaleBlocks][NT + 4];  // no bank conflicts where they are written
   uint64_t full[kNarrowStages], empty[kNarrowStages], sum_full[kNarrowBufs], sum_empty[kNarrowBufs];
   uint32_t tmem;
-  // behind it: the expert table and, with several CTAs a tile, float sums[NT, rounded up to
-  // whole splits][kRows]
+  // behind it: the expert table and, with several CTAs a tile, the sums that this CTA adds up:
+  // float4 (4 tokens) [chunk of 4 tokens][CTA][kRows]
+  static constexpr int kChunks = NT / 4, kChunkBytes = 16 * kRows;
+  __host__ __device__ static constexpr size_t sum_bytes(int split) {
+    return size_t((kChunks + split - 1) / split * split) * kChunkBytes;
+  }
   __host__ __device__ static constexpr size_t sums_at(size_t table_bytes) {
     return (sizeof(NarrowSmem) + table_bytes + 15) / 16 * 16;
   }
 };
-static_assert(NarrowSmem<64>::sums_at(kTableMost) + (64 + kMostSplit) * kRows * 4 <= kSmemMost, "shared memory");
+static_assert(NarrowSmem<64>::sums_at(kTableMost) + NarrowSmem<64>::sum_bytes(7) <= kSmemMost, "7 needs the most");
 
 template <int NT, typename Y>
 __global__ void __launch_bounds__(kNarrowThreads, 2)
@@ -534,8 +538,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   NarrowSmem<NT>& sm = *reinterpret_cast<NarrowSmem<NT>*>(dynamic);
   ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(NarrowSmem<NT>)), a.nexperts);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float(*sums)[kRows] = reinterpret_cast<float(*)[kRows]>(
-      dynamic + NarrowSmem<NT>::sums_at(ExpertTable::bytes(a.nexperts)));
+  float4* sums = reinterpret_cast<float4*>(dynamic + NarrowSmem<NT>::sums_at(ExpertTable::bytes(a.nexperts)));
   const int rank = int(blockIdx.x) % split, index = int(blockIdx.x) / split;
 
   if (split > 1) tc::cluster_arrive();  // the others run before this CTA writes to them
@@ -683,19 +686,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         }
       }
     } else {
-      // column c to CTA c % split
-      const uint32_t at = staging::smem_addr(&sums[rank][feature]);
+      // chunk i to CTA i % split; 512 bytes a warp's store (a token at a time, 128 bytes: 32
+      // tokens x [2688, 4096] 8.3 us, so 6.2 us)
+      const uint32_t at = staging::smem_addr(sums + rank * kRows + feature);
 #pragma unroll
-      for (int i = 0; i < NT / 2; ++i) {
-        const float2 f = tc::unpack2(acc[i]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = 2 * i + h;
-          if (c < cols)
-            tc::store_cluster(tc::in_cta(at + c / split * split * int(sizeof(sums[0])), c % split),
-                              h ? f.y : f.x);
-        }
-      }
+      for (int i = 0; i < S::kChunks; ++i)
+        if (4 * i < cols)
+          tc::store_cluster16(tc::in_cta(at + i / split * split * S::kChunkBytes, i % split), acc[2 * i],
+                              acc[2 * i + 1]);
     }
   }
   __syncwarp();
@@ -703,13 +701,20 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     tc::cluster_sync();
     if (warp < 4 && tile.n0 + int(threadIdx.x) < a.n) {
       Y* y = static_cast<Y*>(a.y) + int64_t(tile.row) * a.ldy + tile.n0 + threadIdx.x;
-#pragma unroll 2
-      for (int c = rank; c < cols; c += split) {
-        float sum = 0.0f;
+      for (int i = rank; 4 * i < cols; i += split) {
+        const float4* from = sums + i / split * split * kRows + threadIdx.x;
+        float4 sum = {};
 #pragma unroll
-        for (int r = 0; r < kMostSplit; ++r)
-          if (r < split) sum += sums[c - rank + r][threadIdx.x];
-        y[int64_t(c) * a.ldy] = from_float<Y>(sum);
+        for (int r = 0; r < kMostSplit; ++r) {
+          if (r >= split) continue;
+          const float4 v = from[r * kRows];
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        Y* to = y + int64_t(4 * i) * a.ldy;
+        to[0] = from_float<Y>(sum.x);
+        if (4 * i + 1 < cols) to[a.ldy] = from_float<Y>(sum.y);
+        if (4 * i + 2 < cols) to[2 * a.ldy] = from_float<Y>(sum.z);
+        if (4 * i + 3 < cols) to[3 * a.ldy] = from_float<Y>(sum.w);
       }
     }
     __syncwarp();
@@ -837,6 +842,9 @@ reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, in
 }
 static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
 
+// ns that the sums of a tile's tokens take through a cluster.
+inline int64_t sums_way(int64_t tokens) { return 750 + 18 * tokens; }
+
 template <int NT, typename Y>
 reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int64_t each, int dev, int64_t sms,
                                cudaStream_t stream) {
@@ -849,22 +857,21 @@ reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int64_t each, i
   if (a.offsets) tiles = a.ntiles * (a.tokens / NT + (a.nexperts < a.tokens ? a.nexperts : a.tokens));
   // CTAs a tile, within one wave (a second one would cost more than longer shares) and with two
   // blocks each: the least of a share's blocks and, with several CTAs, the sums' way to the CTA
-  // that adds them up, in ns.  (32 x 2688: k = 512 takes 4.5 us undivided, 7.5 us by two CTAs,
-  // k = 4096 10.7 us and, by eight, 8.3 us; one token's k = 1024 5.0 us and, by four, 4.4 us;
-  // 64 tokens' k = 1024 6.9 us and, by four, 11.2 us.)
+  // that adds them up, in ns.  (32 tokens' k = 512 takes 4.5 us undivided, longer by two CTAs;
+  // k = 4096 10.7 us and, by eight, 6.2 us; one token's k = 1024 5.0 us and, by four, 4.2 us.)
   const size_t table = ExpertTable::bytes(a.nexperts);
   auto smem_of = [&](int split) {
-    return split > 1 ? NarrowSmem<NT>::sums_at(table) + sizeof(float) * kRows * size_t(cdiv(NT, split) * split)
+    return split > 1 ? NarrowSmem<NT>::sums_at(table) + NarrowSmem<NT>::sum_bytes(split)
                      : sizeof(NarrowSmem<NT>) + table;
   };
-  const int64_t block = NT == 64 ? 450 : 210, way = 600 + 100 * (each < NT ? each : NT);
+  const int64_t block = NT == 64 ? 450 : 210, way = sums_way(each < NT ? each : NT);
   int64_t best = a.blocks * block;
   int split = 1;
   for (int s = 2; s <= kMostSplit; ++s) {
     const int64_t cost = cdiv(a.blocks, s) * block + way;
     if (cost < best && a.blocks >= 2 * s && tiles * s <= 2 * sms &&
         tiles <= resident_clusters(narrow_kernel<NT, Y>, dev, kNarrowThreads,
-                                   NarrowSmem<NT>::sums_at(0) + sizeof(float) * kRows * (NT + kMostSplit), s))
+                                   NarrowSmem<NT>::sums_at(0) + NarrowSmem<NT>::sum_bytes(s), s))
       best = cost, split = s;
   }
   if (tiles * split >= int64_t(1) << 31)
@@ -904,6 +911,10 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
   const int64_t small = tiles(64, kRows), large = tiles(2 * kRows, kWideCols);
   const int64_t middle = tiles(kRows, kWideCols);
   int64_t best = 5500 + cdiv(small, 2 * sms) * blocks * (small > sms ? 650 : 450);
+  for (int s = 2; s <= kMostSplit; ++s) {
+    const int64_t cost = 5500 + cdiv(blocks, s) * 450 + sums_way(64);
+    if (cost < best && blocks >= 2 * s && small * s <= sms) best = cost;
+  }
   int split = 0;  // 0: narrow, -1: pairs, else CTAs a tile of 128 tokens
   const int64_t pairs = sms / 2;
   const int64_t pair_cost = 8000 + cdiv(large, pairs) * (blocks * 430 + 1500 + stray);
