@@ -7,8 +7,8 @@
 // registers while the next block is multiplied into another accumulator.
 //
 // Two kernels, which differ in what lies in the accumulator's 128 lanes (its rows):
-//   wide    256 tokens x 256 features a CTA pair: tokens in the lanes, so a thread has one
-//           token scale and one weight scale a block;
+//   wide    128 tokens x 256 features a CTA: tokens in the lanes, so a thread has one token
+//           scale and one weight scale a block;
 //   narrow  128 features x NT tokens a CTA: weights in the lanes, so that few tokens
 //           (MMA N down to 16) still use whole instructions; bound by reading w.
 #include <cudaTypedefs.h>
@@ -128,18 +128,16 @@ __device__ __noinline__ void give_up(uint32_t* status, uint32_t code) {
 }
 
 // ------------------------------------------------------------------------------- wide
-// Twelve warps a CTA, two CTAs a cluster, which take 256 tokens x 256 features: each CTA
-// loads its own 128 tokens and half of the features of every block (32 KiB of a 48 KiB
-// stage), the halves going to both CTAs, and multiplies and sums its own 128 tokens, two
-// warps a lane quarter, 128 columns each.  (One cta_group::2 instruction for both CTAs
-// loads as little but hands accumulators over between SMs: 416 us against 370 us for
-// 8192 x 14336 x 4096.)
-// What bounds it is the accumulators' way out of tensor memory, which the matrix instructions
-// need too: 8192 x 14336 x 4096 to bf16 takes 370 us (2.6 PFLOP/s), 340 us with the loads but
-// no sums, 301 us with one accumulator for all of k, which would be another product.  Two
-// accumulators of 256 columns fill the 512; 128 columns a half as four accumulators took 630
-// us, 16 summing warps 426 us and more, loads of 32 columns 484 us, scalar sums 384 us.
-// 16384 tokens over 16 experts of [2048, 7168]: 216 us (2.2 PFLOP/s).
+// Twelve warps a CTA, which takes 128 tokens x 256 features, loads both for every block (a 48
+// KiB stage), and sums with two warps a lane quarter, 128 columns each.  Every CTA loads its own
+// tiles: the tiles of a launch go along the tokens first, so that CTAs at work at a time read
+// the same weights from L2.
+// What bounds it is the way into and out of the matrix instructions: 48 KiB a block from L2, and
+// the accumulators out of tensor memory, which the instructions need too.  8192 x 14336 x 4096
+// to bf16 takes 445 us (2.2 PFLOP/s; 12.6 TB/s from L2).  Two accumulators of 256 columns fill
+// the 512: as four of 128 columns, with 16 summing warps, with tensor-memory loads of 32 columns
+// or with scalar sums it was slower by 4 to 70%.
+// 16384 tokens over 16 experts of [2048, 7168]: 254 us (1.9 PFLOP/s).
 constexpr int kWideStages = 4;  // 2 where the expert table needs the room
 constexpr int kWideStageBytes = 3 * kTileBytes;
 constexpr int kWideCols = 256;
@@ -172,8 +170,7 @@ __host__ __device__ constexpr size_t wide_stages_at(size_t table_bytes) {
 }
 static_assert(wide_stages_at(kTableMost) + 2 * kWideStageBytes <= kSmemMost, "shared memory");
 
-// SPLIT: for fewer tokens than fill the GPU that way, a tile of 128 tokens x 256 features a
-// cluster, of which each CTA takes a share of the blocks of k; the sums of 16 columns at a
+// For fewer tokens than fill the GPU that way, such a tile a cluster, of which each CTA takes a share of the blocks of k; the sums of 16 columns at a
 // time go to the CTA that adds them up, in rank order, through distributed shared memory
 // (in the place of the stages).  64 x 7168 x 7168 takes 16.5 us, 128 tokens 18.5 us, against
 // 25 us with 64-token tiles; 777 x 2867 x 819 to float32 10.3 us.
@@ -184,7 +181,7 @@ __host__ __device__ constexpr int split_chunks(int split) {
   return (kWideCols / kSplitChunk + split - 1) / split * split;
 }
 
-template <typename Y, bool SPLIT>
+template <typename Y>
 __global__ void __launch_bounds__(kWideThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ MatmulArgs a, const int stages) {
@@ -193,13 +190,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   ExpertTable table(reinterpret_cast<char*>(dynamic + sizeof(WideSmem)), a.nexperts);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
-  uint32_t ctas = 2;
-  if (SPLIT) asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  uint32_t ctas;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const int unit = blockIdx.x / ctas, units = gridDim.x / ctas;
-  constexpr int kTileRows = SPLIT ? kRows : 2 * kRows;
-  const int first_row = SPLIT ? 0 : int(rank) * kRows;  // of this CTA in a tile
-  const int b0 = SPLIT ? int(int64_t(a.blocks) * rank / ctas) : 0;
-  const int b1 = SPLIT ? int(int64_t(a.blocks) * (rank + 1) / ctas) : a.blocks;
+  const int b0 = int(int64_t(a.blocks) * rank / ctas);
+  const int b1 = int(int64_t(a.blocks) * (rank + 1) / ctas);
   const uint32_t data =
       staging::smem_addr(dynamic) + uint32_t(wide_stages_at(ExpertTable::bytes(a.nexperts)));
 
@@ -208,7 +203,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::prefetch_map(&map_w);
     for (int i = 0; i < stages; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], SPLIT ? 1 : 2);  // both CTAs of a pair write into a stage
+      mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sum_full[i], 1);
@@ -217,7 +212,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc::fence_barrier_init();
   }
   if (warp == kWideSumWarps + 1) tc::tmem_alloc(&sm.tmem, 512);
-  table.build(a, kTileRows);
+  table.build(a, kRows);
   tc::fence_before_sync();
   __syncthreads();
   tc::cluster_sync();
@@ -230,21 +225,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint32_t stage = 0, parity = 1;
     bool ok = true;
     for (int t = unit; ok && t < total; t += units) {
-      const Tile tile(table, a.nexperts, t, kTileRows, kWideCols);
+      const Tile tile(table, a.nexperts, t, kRows, kWideCols);
       for (int b = b0; b < b1; ++b) {
         if (!(ok = tc::warp_wait(&sm.empty[stage], parity))) break;
         if (lane == 0) {
           mbar_arrive_expect(&sm.full[stage], kWideStageBytes);
           const uint32_t bar = staging::smem_addr(&sm.full[stage]);
           const uint32_t dst = data + stage * kWideStageBytes;
-          tc::load_box(dst, &map_x, bar, b * kBlock, tile.row + first_row, 0);
-          if (SPLIT) {
-            tc::load_box(dst + kTileBytes, &map_w, bar, b * kBlock, tile.n0, tile.e);
-            tc::load_box(dst + 2 * kTileBytes, &map_w, bar, b * kBlock, tile.n0 + kRows, tile.e);
-          } else {
-            tc::load_box_both(dst + (1 + rank) * kTileBytes, &map_w, bar, b * kBlock,
-                              tile.n0 + int(rank) * kRows, tile.e);
-          }
+          tc::load_box(dst, &map_x, bar, b * kBlock, tile.row, 0);
+          tc::load_box(dst + kTileBytes, &map_w, bar, b * kBlock, tile.n0, tile.e);
+          tc::load_box(dst + 2 * kTileBytes, &map_w, bar, b * kBlock, tile.n0 + kRows, tile.e);
         }
         __syncwarp();
         if (++stage == uint32_t(stages)) stage = 0, parity ^= 1;
@@ -277,8 +267,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (lane == 0) {
           for (int k = 0; k < 4; ++k)  // 32 bytes of k an instruction
             tc::mma_e4m3(tmem + buf * kWideCols, dx + 2 * k, dw + 2 * k, instruction, k > 0);
-          if (SPLIT) tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
-          else tc::mma_commit_both(staging::smem_addr(&sm.empty[stage]));
+          tc::mma_commit(staging::smem_addr(&sm.empty[stage]));
           tc::mma_commit(staging::smem_addr(&sm.sum_full[buf]));
         }
         __syncwarp();
@@ -297,7 +286,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     float next_x[8], next_w = 0.0f;  // scales of the 8 blocks to come
     auto fetch = [&](const Tile& tile, int b0) {
       const int b = b0 + lane % kScaleBlocks;
-      const int row0 = tile.row + first_row + quarter * 32 + lane / kScaleBlocks;
+      const int row0 = tile.row + quarter * 32 + lane / kScaleBlocks;
       const int block = min((tile.n0 + part * kWideWarpCols) / kBlock, a.col_blocks - 1);
       if (b >= b1) return;
       next_w = a.ws[(int64_t(tile.e) * a.col_blocks + block) * a.ldws + b];
@@ -309,12 +298,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     bool ok = true;
     Tile tile;
     if (unit < total) {
-      tile = Tile(table, a.nexperts, unit, kTileRows, kWideCols);
+      tile = Tile(table, a.nexperts, unit, kRows, kWideCols);
       fetch(tile, b0);
     }
     for (int t = unit; ok && t < total; t += units) {
-      const Tile following(table, a.nexperts, min(t + units, total - 1), kTileRows, kWideCols);
-      const int row0 = tile.row + first_row + quarter * 32;
+      const Tile following(table, a.nexperts, min(t + units, total - 1), kRows, kWideCols);
+      const int row0 = tile.row + quarter * 32;
       const int col0 = tile.n0 + part * kWideWarpCols;
       uint64_t acc[kWideWarpCols / 2];
 #pragma unroll
@@ -352,8 +341,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (lane == 0) staging::mbar_arrive(&sm.sum_empty[buf]);
         if (++buf == 2) buf = 0, parity ^= 1;
       }
-      if (SPLIT && ctas > 1) {  // one tile a cluster
-        tc::cluster_sync();     // every CTA is done with its stages
+      if (ctas > 1) {  // one tile a cluster
+        tc::cluster_sync();  // every CTA is done with its stages
         // [slot of a chunk][CTA][4 columns][row][4]: a warp's store is 512 bytes in a row
         const uint32_t at = data + rank * kSplitChunkBytes + (quarter * 32 + lane) * 16;
         const int chunk0 = part * (kWideWarpCols / kSplitChunk);
@@ -485,7 +474,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (!ok && lane == 0) give_up(a.status, kStatusSumWait);
   }
   __syncwarp();
-  if (SPLIT && ctas > 1 && unit < total && warp >= kWideSumWarps) {  // as the summing warps
+  if (ctas > 1 && unit < total && warp >= kWideSumWarps) {  // as the summing warps
     tc::cluster_sync();
     tc::cluster_sync();
   }
@@ -824,9 +813,9 @@ struct Operands {
   int64_t ldx, ldw, k;
 };
 
-// SPLIT: `split` CTAs a tile of 128 tokens (with several of them, a cluster for each of at
-// most `units` tiles); else two CTAs a tile of 256 tokens.
-template <typename Y, bool SPLIT>
+// `split` CTAs a tile of 128 tokens; with several of them, a cluster for each of at most
+// `units` tiles.
+template <typename Y>
 reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, int split,
                              cudaStream_t stream) {
   CUtensorMap map_x, map_w;
@@ -837,7 +826,7 @@ reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, in
   const size_t at = wide_stages_at(ExpertTable::bytes(a.nexperts));
   int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : 2;
   void* args[] = {&map_x, &map_w, &a, &stages};
-  return launch(reinterpret_cast<const void*>(wide_kernel<Y, SPLIT>), unsigned(units * split),
+  return launch(reinterpret_cast<const void*>(wide_kernel<Y>), unsigned(units * split),
                 kWideThreads, at + size_t(stages) * kWideStageBytes, split, stream, args);
 }
 static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
@@ -908,38 +897,28 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
     return cdiv(a.n, cols) * cdiv(2 * cdiv(a.tokens, rows) + experts, 2);
   };
   const int64_t blocks = a.blocks, stray = a.aligned_y == 32 ? 0 : 6000;  // rows off the sectors
-  const int64_t small = tiles(64, kRows), large = tiles(2 * kRows, kWideCols);
-  const int64_t middle = tiles(kRows, kWideCols);
+  const int64_t small = tiles(64, kRows), large = tiles(kRows, kWideCols);
   int64_t best = 5500 + cdiv(small, 2 * sms) * blocks * (small > sms ? 650 : 450);
   for (int s = 2; s <= kMostSplit; ++s) {
     const int64_t cost = 5500 + cdiv(blocks, s) * 450 + sums_way(64);
     if (cost < best && blocks >= 2 * s && small * s <= sms) best = cost;
   }
-  int split = 0;  // 0: narrow, -1: pairs, else CTAs a tile of 128 tokens
-  const int64_t pairs = sms / 2;
-  const int64_t pair_cost = 8000 + cdiv(large, pairs) * (blocks * 430 + 1500 + stray);
-  if (pair_cost < best) best = pair_cost, split = -1;
+  int split = 0;  // 0: narrow, else CTAs a tile of 128 tokens
   const bool room =
       wide_stages_at(ExpertTable::bytes(a.nexperts)) + kWideStages * kWideStageBytes <= kSmemMost;
   for (int s = 1; s <= kMostSplit; ++s) {
-    if (s > 1 && (!room || blocks < 2 * s || middle * s > sms ||
-                  middle > resident_clusters(wide_kernel<Y, true>, dev, kWideThreads, kSmemMost, s)))
+    if (s > 1 && (!room || blocks < 2 * s || large * s > sms ||
+                  large > resident_clusters(wide_kernel<Y>, dev, kWideThreads, kSmemMost, s)))
       continue;
-    const int64_t cost = s == 1 ? 7500 + cdiv(middle, sms) * (blocks * 540 + 1500 + stray)
+    const int64_t cost = s == 1 ? 7500 + cdiv(large, sms) * (blocks * 540 + 1500 + stray)
                                 : 10500 + cdiv(blocks, s) * 500;
     if (cost < best) best = cost, split = s;
   }
   if (split == 0) return launch_narrow<64, Y>(a, o, each, dev, sms, stream);
-  auto most = [&](int64_t rows) {
-    return cdiv(a.n, kWideCols) * (a.offsets ? a.tokens / rows + experts : cdiv(a.tokens, rows));
-  };
-  if (split > 0) {
-    int64_t units = most(kRows);
-    if (split == 1 && units > sms) units = sms;
-    return launch_wide<Y, true>(a, o, units, split, stream);
-  }
-  const int64_t units = most(2 * kRows) < pairs ? most(2 * kRows) : pairs;
-  return launch_wide<Y, false>(a, o, units, 2, stream);
+  int64_t units =  // the most tiles that there can be
+      cdiv(a.n, kWideCols) * (a.offsets ? a.tokens / kRows + experts : cdiv(a.tokens, kRows));
+  if (split == 1 && units > sms) units = sms;
+  return launch_wide<Y>(a, o, units, split, stream);
 }
 
 }  // namespace

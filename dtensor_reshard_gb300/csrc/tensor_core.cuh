@@ -69,15 +69,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// The same to that place of both CTAs of a cluster of two; the bytes count on each one's `bar`.
-__device__ __forceinline__ void load_box_both(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                              int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(uint16_t(3))
-      : "memory");
-}
 
 // --------------------------------------------------------------------- matrix instructions
 // Descriptor of a K-major tile of 128-byte rows in the 128-byte swizzle: groups of 8 rows
@@ -102,14 +93,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
-}
-// The same at that barrier of both CTAs of a cluster of two.
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar),
-      "h"(uint16_t(3))
-      : "memory");
 }
 
 // ------------------------------------------------------------------------- tensor memory
