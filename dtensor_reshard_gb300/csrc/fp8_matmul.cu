@@ -756,10 +756,11 @@ reshard_status_t tile_map(CUtensorMap* map, const void* base, int64_t k, int64_t
 }
 
 // How many clusters of `split` CTAs are on the device at a time: fewer than its SMs divided
-// by the split, since a cluster lies in one part of the GPU (8 CTAs of an SM each: 16, not
-// 19).  Asked for once a device.
-template <typename Kernel>
-int resident_clusters(Kernel* kernel, int dev, unsigned threads, size_t smem, int split) {
+// by the split, since a cluster lies in one part of the GPU (8 CTAs of an SM each: 15, not
+// 19).  Asked for once a device and kernel: the record is the kernel's own (kernels differ in
+// what fits, though not in their type), so that no call changes what another one chooses.
+template <auto Kernel>
+int resident_clusters(int dev, unsigned threads, size_t smem, int split) {
   constexpr int kDevices = 16;
   static std::atomic<int> known[kDevices][kMostSplit + 1];
   if (dev < kDevices) {
@@ -776,9 +777,9 @@ int resident_clusters(Kernel* kernel, int dev, unsigned threads, size_t smem, in
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
           cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();  // an estimate is not worth an error: the launch reports its own
     return 1;
   }
@@ -859,7 +860,7 @@ reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int64_t each, i
   for (int s = 2; s <= kMostSplit; ++s) {
     const int64_t cost = cdiv(a.blocks, s) * block + way;
     if (cost < best && a.blocks >= 2 * s && tiles * s <= 2 * sms &&
-        tiles <= resident_clusters(narrow_kernel<NT, Y>, dev, kNarrowThreads,
+        tiles <= resident_clusters<narrow_kernel<NT, Y>>(dev, kNarrowThreads,
                                    NarrowSmem<NT>::sums_at(0) + NarrowSmem<NT>::sum_bytes(s), s))
       best = cost, split = s;
   }
@@ -908,7 +909,7 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
       wide_stages_at(ExpertTable::bytes(a.nexperts)) + kWideStages * kWideStageBytes <= kSmemMost;
   for (int s = 1; s <= kMostSplit; ++s) {
     if (s > 1 && (!room || blocks < 2 * s || large * s > sms ||
-                  large > resident_clusters(wide_kernel<Y>, dev, kWideThreads, kSmemMost, s)))
+                  large > resident_clusters<wide_kernel<Y>>(dev, kWideThreads, kSmemMost, s)))
       continue;
     const int64_t cost = s == 1 ? 7500 + cdiv(large, sms) * (blocks * 540 + 1500 + stray)
                                 : 10500 + cdiv(blocks, s) * 500;
