@@ -504,36 +504,6 @@ __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const __gr
 
 int64_t header_bytes(int64_t nseq) { return cdiv(nseq * 4 + 4, 16) * 16; }  // tokens, done
 
-reshard_status_t launch_in(const void* kernel, int64_t grid, int threads, size_t smem, int cluster,
-                           bool early, cudaStream_t stream, void** args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (early) {  // before the kernel in front of it has ended
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t ce = cudaLaunchKernelExC(&cfg, kernel, args);
-  if (ce != cudaSuccess)
-    return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
-  return RESHARD_OK;
-}
-
-template <typename T, int SCORE, bool VEC>
-const void* pass_kernel(int values) {
-  return values <= 8    ? reinterpret_cast<const void*>(balance_kernel<T, SCORE, VEC, 8>)
-         : values <= 16 ? reinterpret_cast<const void*>(balance_kernel<T, SCORE, VEC, 16>)
-                        : reinterpret_cast<const void*>(balance_kernel<T, SCORE, VEC, 32>);
-}
-
 template <typename T, int SCORE>
 reshard_status_t launch_small(BalanceArgs& a, cudaStream_t stream) {
   balance_small_kernel<T, SCORE>
@@ -541,8 +511,26 @@ reshard_status_t launch_small(BalanceArgs& a, cudaStream_t stream) {
   return launched("reshard_balance_loss");
 }
 
+constexpr const char* kWhat = "reshard_balance_loss";
+
+template <typename T, int SCORE, bool VEC, int N>
+reshard_status_t launch_values(BalanceArgs& a, int dev, int lanes, cudaStream_t stream) {
+  constexpr size_t kRing = VEC ? kAhead * sizeof(T) * 256 * N : 0;
+  void* args[] = {&a, &lanes};
+  return launch<balance_kernel<T, SCORE, VEC, N>, kRing + sizeof(float) * 32 * N>(
+      kWhat, dev, {int64_t(a.nseq) * a.chunks, 256, kRing + sizeof(float) * size_t(a.nexperts), 0, stream},
+      args);
+}
+
+template <typename T, int SCORE, bool VEC>
+reshard_status_t launch_lanes(BalanceArgs& a, int dev, int lanes, int values, cudaStream_t stream) {
+  return values <= 8    ? launch_values<T, SCORE, VEC, 8>(a, dev, lanes, stream)
+         : values <= 16 ? launch_values<T, SCORE, VEC, 16>(a, dev, lanes, stream)
+                        : launch_values<T, SCORE, VEC, 32>(a, dev, lanes, stream);
+}
+
 template <typename T, int SCORE>
-reshard_status_t launch_pass(BalanceArgs& a, int64_t sms, cudaStream_t stream) {
+reshard_status_t launch_pass(BalanceArgs& a, int dev, int64_t sms, cudaStream_t stream) {
   constexpr int kPer = 16 / int(sizeof(T));
   const bool vec = a.nexperts % kPer == 0 && a.ld % kPer == 0 && aligned(a.logits, 16) &&
                    aligned(a.dlogits, 16);
@@ -551,23 +539,16 @@ reshard_status_t launch_pass(BalanceArgs& a, int64_t sms, cudaStream_t stream) {
   while (lanes < 32 && lanes * 16 < a.nexperts) lanes *= 2;
   const int values = int(cdiv(cdiv(a.nexperts, vec ? kPer : 1), lanes)) * (vec ? kPer : 1);
   // as many CTAs as are on the GPU at a time
-  const void* kernel = values > 32 ? reinterpret_cast<const void*>(balance_many_kernel<T, SCORE>)
-                       : vec       ? pass_kernel<T, SCORE, true>(values)
-                                   : pass_kernel<T, SCORE, false>(values);
   const int64_t target = sms * (values > 32 ? 8 : values > 16 ? 2 : 3);
   const int64_t per_seq = target / a.nseq > 1 ? target / a.nseq : 1;
   a.chunk = int32_t(cdiv(cdiv(a.seqlen, per_seq), kChunk) * kChunk);
   a.chunks = int32_t(cdiv(a.seqlen, a.chunk));
-  void* args[] = {&a, &lanes};
-  size_t smem = sizeof(float) * size_t(a.nexperts);
-  if (vec && values <= 32) smem += kAhead * sizeof(T) * 256 * (values <= 8 ? 8 : values <= 16 ? 16 : 32);
-  if (smem > 48 * 1024) {
-    const cudaError_t ce =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (ce != cudaSuccess)
-      return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
-  }
-  return launch_in(kernel, int64_t(a.nseq) * a.chunks, 256, smem, 1, true, stream, args);
+  if (values <= 32)
+    return vec ? launch_lanes<T, SCORE, true>(a, dev, lanes, values, stream)
+               : launch_lanes<T, SCORE, false>(a, dev, lanes, values, stream);
+  void* args[] = {&a};
+  return launch<balance_many_kernel<T, SCORE>, sizeof(float) * RESHARD_MAX_EXPERTS>(
+      kWhat, dev, {int64_t(a.nseq) * a.chunks, 256, sizeof(float) * size_t(a.nexperts), 0, stream}, args);
 }
 
 }  // namespace
@@ -660,13 +641,15 @@ extern "C" reshard_status_t reshard_balance_loss(
       return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
   }
   void* args[] = {&a};
-  reshard_status_t status =
-      rs::launch_in(reinterpret_cast<const void*>(rs::count_kernel), nseq * a.clusters * cluster,
-                    rs::kCountThreads, sizeof(int32_t) * size_t(nexperts + 1), cluster, false, st, args);
+  const reshard_status_t status =
+      rs::op::launch<rs::count_kernel, sizeof(int32_t) * (RESHARD_MAX_EXPERTS + 1)>(
+          rs::kWhat, dev,
+          {nseq * a.clusters * cluster, rs::kCountThreads, sizeof(int32_t) * size_t(nexperts + 1), cluster, st},
+          args);
   if (status != RESHARD_OK || !(loss || dlogits)) return status;
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return score == RESHARD_SCORE_SOFTMAX ? rs::launch_pass<T, RESHARD_SCORE_SOFTMAX>(a, sms, st)
-                                          : rs::launch_pass<T, RESHARD_SCORE_SIGMOID>(a, sms, st);
+    return score == RESHARD_SCORE_SOFTMAX ? rs::launch_pass<T, RESHARD_SCORE_SOFTMAX>(a, dev, sms, st)
+                                          : rs::launch_pass<T, RESHARD_SCORE_SIGMOID>(a, dev, sms, st);
   });
 }

@@ -118,7 +118,6 @@ struct Tile {
 };
 
 constexpr size_t kTableMost = 8 * (RESHARD_MAX_EXPERTS + 1);  // ExpertTable::bytes
-constexpr size_t kSmemMost = 227 * 1024;                      // shared memory of a CTA
 
 // After a wait ran out: time for this thread's copies and matrix instructions to land
 // before shared and tensor memory are given back.
@@ -777,36 +776,13 @@ int resident_clusters(int dev, unsigned threads, size_t smem, int split) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
-          cudaSuccess ||
+  if (allow_smem<Kernel, kSmemMost>(dev) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();  // an estimate is not worth an error: the launch reports its own
     return 1;
   }
   if (dev < kDevices) known[dev][split].store(n, std::memory_order_relaxed);
   return n > 0 ? n : 1;
-}
-
-reshard_status_t launch(const void* kernel, unsigned grid, unsigned threads, size_t smem, int cluster,
-                        cudaStream_t stream, void** args) {
-  cudaError_t ce =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (ce == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    ce = cudaLaunchKernelExC(&cfg, kernel, args);
-  }
-  if (ce != cudaSuccess)
-    return fail(RESHARD_ERR_CUDA, std::string("reshard_fp8_matmul: ") + cudaGetErrorString(ce));
-  return RESHARD_OK;
 }
 
 struct Operands {
@@ -817,7 +793,7 @@ struct Operands {
 // `split` CTAs a tile of 128 tokens; with several of them, a cluster for each of at most
 // `units` tiles.
 template <typename Y>
-reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, int split,
+reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, int split, int dev,
                              cudaStream_t stream) {
   CUtensorMap map_x, map_w;
   reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, kRows);
@@ -827,8 +803,9 @@ reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, in
   const size_t at = wide_stages_at(ExpertTable::bytes(a.nexperts));
   int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : 2;
   void* args[] = {&map_x, &map_w, &a, &stages};
-  return launch(reinterpret_cast<const void*>(wide_kernel<Y>), unsigned(units * split),
-                kWideThreads, at + size_t(stages) * kWideStageBytes, split, stream, args);
+  return launch<wide_kernel<Y>, kSmemMost>(
+      "reshard_fp8_matmul", dev,
+      {units * split, kWideThreads, at + size_t(stages) * kWideStageBytes, split, stream}, args);
 }
 static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
 
@@ -867,8 +844,8 @@ reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int64_t each, i
   if (tiles * split >= int64_t(1) << 31)
     return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
   void* args[] = {&map_x, &map_w, &a, &split};
-  return launch(reinterpret_cast<const void*>(narrow_kernel<NT, Y>), unsigned(tiles * split),
-                kNarrowThreads, smem_of(split), split, stream, args);
+  return launch<narrow_kernel<NT, Y>, kSmemMost>(
+      "reshard_fp8_matmul", dev, {tiles * split, kNarrowThreads, smem_of(split), split, stream}, args);
 }
 
 template <typename Y>
@@ -919,7 +896,7 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
   int64_t units =  // the most tiles that there can be
       cdiv(a.n, kWideCols) * (a.offsets ? a.tokens / kRows + experts : cdiv(a.tokens, kRows));
   if (split == 1 && units > sms) units = sms;
-  return launch_wide<Y>(a, o, units, split, stream);
+  return launch_wide<Y>(a, o, units, split, dev, stream);
 }
 
 }  // namespace

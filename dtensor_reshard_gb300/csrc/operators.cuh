@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -72,6 +73,55 @@ inline int64_t dtype_size(int32_t d) { return d == RESHARD_FP32 ? 4 : 2; }
 // The status of the launch just made.
 inline reshard_status_t launched(const char* what) {
   const cudaError_t ce = cudaGetLastError();
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(ce));
+  return RESHARD_OK;
+}
+
+constexpr size_t kSmemMost = 227 * 1024;  // shared memory of a CTA
+
+// Lets Kernel have MOST bytes of dynamic shared memory, the most that any call needs: the
+// limit belongs to the kernel and the device, so no call may lower it under another thread's
+// launch.  Set once a device.
+template <auto Kernel, size_t MOST>
+cudaError_t allow_smem(int dev) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (MOST <= 48 * 1024 || (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t ce =
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(MOST));
+  if (ce == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return ce;
+}
+
+struct Launch {
+  int64_t grid;
+  int threads;
+  size_t smem;
+  int cluster;  // CTAs; 0: may start before the kernel in front of it has ended
+  cudaStream_t stream;
+};
+template <auto Kernel, size_t MOST>
+reshard_status_t launch(const char* what, int dev, const Launch& l, void** args) {
+  cudaError_t ce = allow_smem<Kernel, MOST>(dev);
+  if (ce == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(l.grid));
+    cfg.blockDim = dim3(unsigned(l.threads));
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.stream = l.stream;
+    cudaLaunchAttribute attr[1];
+    if (l.cluster == 0) {
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+    } else {
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {unsigned(l.cluster), 1, 1};
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    ce = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(Kernel), args);
+  }
   if (ce != cudaSuccess)
     return fail(RESHARD_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(ce));
   return RESHARD_OK;

@@ -895,12 +895,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == kFewThreads ? 5 : 1) sam
   }
 }
 
-template <typename T, int kThreads>
-const void* sample_pick(bool resident) {
-  return resident ? reinterpret_cast<const void*>(sample_kernel<T, true, kThreads>)
-                  : reinterpret_cast<const void*>(sample_kernel<T, false, kThreads>);
-}
-
 template <typename T>
 reshard_status_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t stream) {
   int dev = 0, sms = 0;
@@ -919,27 +913,16 @@ reshard_status_t launch_sample(const SampleArgs& a, int64_t rows, cudaStream_t s
   // float32: 14.4 us, with 512 threads 15.5 us)
   const bool many = rows * ctas <= sms;
   const size_t fixed = many ? sizeof(SampleSmem<kManyThreads / 32>) : sizeof(SampleSmem<kFewThreads / 32>);
-  const bool resident = fixed + size_t(slice) <= 227 * 1024;
+  const bool resident = fixed + size_t(slice) <= kSmemMost;
   const size_t smem = fixed + (resident ? size_t(slice) : 0);
-  const void* kernel = many ? sample_pick<T, kManyThreads>(resident) : sample_pick<T, kFewThreads>(resident);
-  ce = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (ce == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(rows * ctas));
-    cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(ctas), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void* args[] = {const_cast<SampleArgs*>(&a)};
-    ce = cudaLaunchKernelExC(&cfg, kernel, args);
-  }
-  if (ce != cudaSuccess)
-    return fail(RESHARD_ERR_CUDA, std::string("reshard_sample: ") + cudaGetErrorString(ce));
-  return RESHARD_OK;
+  const Launch l = {rows * ctas, many ? kManyThreads : kFewThreads, smem, ctas, stream};
+  void* args[] = {const_cast<SampleArgs*>(&a)};
+  const char* what = "reshard_sample";
+  if (many)
+    return resident ? launch<sample_kernel<T, true, kManyThreads>, kSmemMost>(what, dev, l, args)
+                    : launch<sample_kernel<T, false, kManyThreads>, kSmemMost>(what, dev, l, args);
+  return resident ? launch<sample_kernel<T, true, kFewThreads>, kSmemMost>(what, dev, l, args)
+                  : launch<sample_kernel<T, false, kFewThreads>, kSmemMost>(what, dev, l, args);
 }
 
 }  // namespace
