@@ -745,10 +745,18 @@ reshard_status_t tile_map(CUtensorMap* map, const void* base, int64_t k, int64_t
   const cuuint64_t dims[3] = {cuuint64_t(k), cuuint64_t(rows), cuuint64_t(planes)};
   const cuuint64_t strides[2] = {cuuint64_t(pitch), cuuint64_t(pitch) * cuuint64_t(rows)};
   const cuuint32_t box[3] = {kBlock, cuuint32_t(box_rows), 1}, steps[3] = {1, 1, 1};
-  const CUresult r =
-      encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, steps,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encoded = [&] {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                  steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encoded();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // a host thread's first call: the driver, unlike the runtime, does not make its device's
+    // context current
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encoded();
+  }
   if (r != CUDA_SUCCESS)
     return fail(RESHARD_ERR_CUDA, "cuTensorMapEncodeTiled: error " + std::to_string(int(r)));
   return RESHARD_OK;

@@ -85,3 +85,12 @@ def test_threads_with_sizes_of_their_own():
     jobs = [_product(e) for e in (2, 900, 3000)] + [_sample(v) for v in (300, 9000, 40000)]
     jobs += [_balance(e) for e in (544, 1024)]
     _run(jobs, 2000, lambda: torch.zeros(1, device="cuda"))
+
+
+def test_a_thread_that_has_not_used_the_gpu_yet():
+    """No context is current on a new host thread until a call makes it so."""
+    for make in (lambda: _product(2), lambda: _product(40), lambda: _sample(300), lambda: _balance(544)):
+        call, right = make()
+        call(None)                    # the library has met the device, the thread below has not
+        assert right()
+        _run([make()], 3, lambda: None)
