@@ -29,22 +29,26 @@ struct QuantizeArgs {
 // unit in the last place becomes the correctly rounded one by one more step of
 // q + (x - q * scale) * y, and the first such step brings x * y within that unit.  No
 // remainder underflows unless the quotient is below 2^-12, which e4m3 rounds to 0 anyway.
+//
+// The quotient is carried with its sign changed: a remainder of zero is +0, which must be taken
+// from, not added to, a quotient of -0 for that to stay -0.
 struct Divisor {
-  uint64_t minus, y;
+  uint64_t s2, minus_y;
   __device__ explicit Divisor(float s) {
-    const uint32_t m = __float_as_uint(-s), r = __float_as_uint(__frcp_rn(s));
-    minus = tc::pack2(m, m);
-    y = tc::pack2(r, r);
+    const uint32_t m = __float_as_uint(s), r = __float_as_uint(-__frcp_rn(s));
+    s2 = tc::pack2(m, m);
+    minus_y = tc::pack2(r, r);
   }
   // Blocks for which that holds; others (tiny or infinite scales) are divided one by one.
   __device__ static bool serves(float s) { return s >= 0x1p-90f && s < INFINITY; }
   __device__ float2 divide(float2 v) const {
     const uint64_t x = tc::pack2(__float_as_uint(v.x), __float_as_uint(v.y));
-    uint64_t q;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(y));
-    q = tc::fma2(tc::fma2(minus, q, x), y, q);
-    q = tc::fma2(tc::fma2(minus, q, x), y, q);
-    return tc::unpack2(q);
+    uint64_t q;  // -x / s
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(minus_y));
+    q = tc::fma2(tc::fma2(s2, q, x), minus_y, q);
+    q = tc::fma2(tc::fma2(s2, q, x), minus_y, q);
+    const float2 f = tc::unpack2(q);
+    return make_float2(-f.x, -f.y);
   }
 };
 
