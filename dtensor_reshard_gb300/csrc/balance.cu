@@ -64,13 +64,15 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const int part = blockIdx.x % (ctas * a.clusters), s = blockIdx.x / (ctas * a.clusters);
   const int parts = int(ctas) * a.clusters;
-  const int t0 = int(int64_t(a.seqlen) * part / parts), t1 = int(int64_t(a.seqlen) * (part + 1) / parts);
+  const uint32_t t0 = uint32_t(int64_t(a.seqlen) * part / parts);
+  const uint32_t t1 = uint32_t(int64_t(a.seqlen) * (part + 1) / parts);
   const bool fours = a.topk % 4 == 0 && reinterpret_cast<uintptr_t>(a.experts) % 16 == 0;
   auto count = [&](int e) {
     if (uint32_t(e) < uint32_t(a.nexperts)) atomicAdd(&counted[e], 1);
   };
   int live = 0;
-  for (int i = t0 + int(threadIdx.x); i < t1; i += kCountThreads) {
+  // (unsigned: a step beyond the last of nearly 2^31 tokens)
+  for (uint32_t i = t0 + threadIdx.x; i < t1; i += kCountThreads) {
     const int64_t t = int64_t(s) * a.seqlen + i;
     const int32_t* e = a.experts + t * a.topk;
     int4 first = {}, second = {};  // on their way while the mask is
@@ -270,21 +272,22 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
     balance_kernel(const __grid_constant__ BalanceArgs a, const int lanes) {
   using L = Logits<T, VEC, N>;
   const int s = blockIdx.x / a.chunks;
-  const int first = blockIdx.x % a.chunks * a.chunk;
-  const int end = min(a.seqlen, first + a.chunk);
+  // tokens are unsigned: the last chunk's end, and those fetched ahead, may lie beyond 2^31
+  const uint32_t first = blockIdx.x % a.chunks * a.chunk;
+  const uint32_t end = min(uint32_t(a.seqlen), first + a.chunk);
   const int lane = threadIdx.x & (lanes - 1), groups = 256 / lanes;
   const int64_t row0 = int64_t(s) * a.seqlen;
   const T* logits = static_cast<const T*>(a.logits) + row0 * a.ld;
   T* dlogits = a.dlogits ? static_cast<T*>(a.dlogits) + row0 * a.ld : nullptr;
-  auto live = [&](int t) { return t < end && (!a.mask || a.mask[row0 + t] != 0); };
-  int t = first + int(threadIdx.x) / lanes;
+  auto live = [&](uint32_t t) { return t < end && (!a.mask || a.mask[row0 + t] != 0); };
+  uint32_t t = first + threadIdx.x / lanes;
   // VEC: a ring of kAhead tokens' vectors in shared memory, each thread's own
   extern __shared__ __align__(16) float dynamic[];
   constexpr int kVectors = VEC ? N / L::kPer : 1;
   uint4* ring = reinterpret_cast<uint4*>(dynamic) + threadIdx.x;  // [kAhead][kVectors][256]
   float* f_smem = dynamic + (VEC ? kAhead * kVectors * 256 * 4 : 0);
   // (zeros for a token that does not count; what lies beyond the experts stays -inf)
-  auto fetch = [&](int t, bool on, int slot) {
+  auto fetch = [&](uint32_t t, bool on, int slot) {
     const T* row = logits + int64_t(on ? t : first) * a.ld;
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
   float sum = 0.0f;
   int slot = 0;
   // the groups of a warp walk together: the shuffles need all lanes
-  for (int base = first; base < end; base += groups, t += groups) {
+  for (uint32_t base = first; base < end; base += groups, t += groups) {
     L now;
     bool counts = on;
     if (VEC) {

@@ -45,3 +45,30 @@ def test_quantize_keeps_the_sign_of_zeros(cols, dtype, block_rows):
     want, _ = oo.quantize(_f64(x)[None], block_rows)
     negative = torch.signbit(x).cpu().numpy()
     assert np.array_equal(q.cpu().numpy(), _bytes(want[0], negative))
+
+
+# ---------------------------------------------------------------------------- balance
+@pytest.mark.parametrize("experts", [1, 8])       # rows off and on 16 bytes
+def test_balance_of_nearly_2_31_tokens(experts):
+    """Every token of the longest sequence is reached, and none beyond it."""
+    n, gone = 2 ** 31 - 8, 3
+    logits = torch.zeros(1, n, experts, dtype=torch.float16, device="cuda")
+    choices = torch.zeros(1, n, 1, dtype=torch.int32, device="cuda")
+    mask = torch.ones(1, n, dtype=torch.uint8, device="cuda")
+    mask[0, n - gone:] = 0
+    dlogits = torch.empty_like(logits)
+    ends = [slice(0, 10 ** 6), slice(n - 10 ** 8, n)]
+    for e in ends:
+        dlogits[:, e] = 7.0
+    counts = torch.empty(1, experts, dtype=torch.int32, device="cuda")
+    loss = torch.empty(1, device="cuda")
+    shape = (1, n, experts)
+    workspace = torch.empty(rs.reshard_balance_loss_workspace(shape), dtype=torch.uint8, device="cuda")
+    rs.reshard_balance_loss(logits, shape, "fp16", choices, 1, 1.0, workspace, counts, loss=loss,
+                            dlogits=dlogits, mask=mask)
+    assert counts[0].tolist() == [n - gone] + [0] * (experts - 1)
+    # f = E for the one expert, p = 1 / E: 1 a token; sums of at most 2^18 ones are exact,
+    # their shares of n and the loss round three times
+    assert abs(float(loss) - 1.0) <= 4 * 2.0 ** -24
+    for e in ends:                           # gradients of 2^-31 are 0 in float16
+        assert not bool(dlogits[:, e].any())
