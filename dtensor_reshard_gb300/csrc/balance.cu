@@ -35,6 +35,7 @@ struct BalanceArgs {
   int32_t* tokens;  // workspace: [nseq] tokens with mask
   float* parts;     // [nseq * chunks] the pass's sums over tokens
   uint32_t* done;   // CTAs of the pass that have written theirs
+  int32_t* live;    // sequences that have tokens, where there are many, else NULL
   int32_t nseq, seqlen, topk;
   int32_t chunk, chunks;            // tokens of a pass's CTA, CTAs of a sequence
   int32_t clusters;                 // of the counts of a sequence
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
     for (uint32_t r = 0; r < ctas; ++r)
       sum += __float_as_int(tc::load_cluster(tc::in_cta(at, r)));
     int32_t* to = i < a.nexperts ? &a.counts[int64_t(s) * a.nexperts + i] : &a.tokens[s];
+    if (a.live && i == a.nexperts && sum) atomicAdd(a.live, 1);
     if (a.clusters == 1) *to = sum;
     else if (sum) atomicAdd(to, sum);
   }
@@ -161,10 +163,16 @@ struct Score {
   }
 };
 
+// Sequences of which each CTA of the pass counts those with tokens by itself (up to four loads a
+// thread); for more the counting kernel does (262144 sequences of a token: 103 ms when each
+// CTA went through all of them).
+constexpr int kManySequences = 1024;
+
 // What a CTA of the pass needs of the counts: f[e] in shared memory, and the loss's share
 // of a token.
 struct Weighting {
   float share, inv_tokens;
+  int sequences;  // that have tokens
   __device__ void make(const BalanceArgs& a, int s, float* f) {
     __shared__ int live;
     if (threadIdx.x == 0) live = 0;
@@ -173,7 +181,10 @@ struct Weighting {
     const int first = int(threadIdx.x) < a.nexperts ? counts[threadIdx.x] : 0;
     __syncthreads();
     int mine = 0;
-    for (int i = threadIdx.x; i < a.nseq; i += blockDim.x) mine += a.tokens[i] > 0;
+    if (!a.live)
+      for (int i = threadIdx.x; i < a.nseq; i += blockDim.x) mine += a.tokens[i] > 0;
+    else if (threadIdx.x == 0)
+      mine = *a.live;
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (threadIdx.x % 32 == 0 && mine) atomicAdd(&live, mine);
     const float per_count = float(a.nexperts) / (float(a.topk) * float(n));
@@ -182,13 +193,14 @@ struct Weighting {
       f[e] = float(counts[e]) * per_count;
     __syncthreads();
     inv_tokens = 1.0f / float(n);
+    sequences = live;
     share = a.coef / float(max(live, 1)) / float(n) * (a.grad ? *a.grad : 1.0f);
   }
 };
 
 // The CTA's sum over its tokens, and in the last CTA of the launch the loss: all parts in
 // one fixed order.
-__device__ void finish(const BalanceArgs& a, float sum, float inv_tokens) {
+__device__ void finish(const BalanceArgs& a, float sum, float inv_tokens, int live) {
   __shared__ float sums[8];
   __shared__ double total[8];
   __shared__ bool last;
@@ -207,13 +219,10 @@ __device__ void finish(const BalanceArgs& a, float sum, float inv_tokens) {
   double mine = 0.0;
   for (uint32_t i = threadIdx.x; i < gridDim.x; i += 256) mine += double(__ldcg(a.parts + i));
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  int live = 0;
-  for (int i = threadIdx.x; i < a.nseq; i += 256) live += a.tokens[i] > 0;
-  live = __reduce_add_sync(0xffffffffu, live);
-  if (lane == 0) total[warp] = mine, sums[warp] = float(live);
+  if (lane == 0) total[warp] = mine;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) mine += total[w], live += int(sums[w]);
+    for (int w = 1; w < 8; ++w) mine += total[w];
     *a.loss = float(mine * double(a.coef) / double(max(live, 1)));
   }
 }
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
     if (dlogits && t < end) grad.store(dlogits + int64_t(t) * a.ld, lane, lanes, a.nexperts);
   }
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  finish(a, sum, w.inv_tokens);
+  finish(a, sum, w.inv_tokens, w.sequences);
 }
 
 // A token's loss (before its sequence's share) and gradient by a warp, the row read again for
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(256) balance_many_kernel(const __grid_constant
     sum += token_by_warp<T, SCORE>(static_cast<const T*>(a.logits) + t * a.ld, d, a.nexperts, w.share,
                                    [&](int e) { return f_smem[e]; });
   }
-  finish(a, lane == 0 ? sum : 0.0f, w.inv_tokens);
+  finish(a, lane == 0 ? sum : 0.0f, w.inv_tokens, w.sequences);
 }
 
 // Counts, loss and gradient of few tokens by one CTA, a warp a token: one launch instead of
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const __gr
   }
 }
 
-int64_t header_bytes(int64_t nseq) { return cdiv(nseq * 4 + 4, 16) * 16; }  // tokens, done
+int64_t header_bytes(int64_t nseq) { return cdiv(nseq * 4 + 8, 16) * 16; }  // tokens, done, live
 
 template <typename T, int SCORE>
 reshard_status_t launch_small(BalanceArgs& a, cudaStream_t stream) {
@@ -637,6 +646,12 @@ extern "C" reshard_status_t reshard_balance_loss(
   const int cluster = choices <= 2048 ? 1 : rs::kCountCluster;
   const int64_t useful = rs::op::cdiv(choices, 4096 * cluster), room = sms / (nseq * cluster);
   a.clusters = int32_t(useful < 1 || room < 1 ? 1 : useful < room ? useful : room);
+  if (nseq > rs::kManySequences) {  // (a cluster a sequence then)
+    a.live = static_cast<int32_t*>(workspace) + nseq + 1;
+    ce = cudaMemsetAsync(a.live, 0, 4, st);
+    if (ce != cudaSuccess)
+      return fail(RESHARD_ERR_CUDA, std::string("reshard_balance_loss: ") + cudaGetErrorString(ce));
+  }
   if (a.clusters > 1) {
     ce = cudaMemsetAsync(counts, 0, size_t(4 * nseq * nexperts), st);
     if (ce == cudaSuccess) ce = cudaMemsetAsync(a.tokens, 0, size_t(4 * nseq), st);

@@ -72,3 +72,60 @@ def test_balance_of_nearly_2_31_tokens(experts):
     assert abs(float(loss) - 1.0) <= 4 * 2.0 ** -24
     for e in ends:                           # gradients of 2^-31 are 0 in float16
         assert not bool(dlogits[:, e].any())
+
+
+def _many_sequences(n, experts=16, topk=2):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    logits = torch.randn(n, 1, experts, generator=g, device="cuda")
+    choices = logits.topk(topk, dim=2).indices.to(torch.int32)
+    mask = (torch.rand(n, 1, generator=g, device="cuda") < 0.7).to(torch.uint8)
+    shape = (n, 1, experts)
+    workspace = torch.empty(rs.reshard_balance_loss_workspace(shape), dtype=torch.uint8, device="cuda")
+    counts = torch.empty(n, experts, dtype=torch.int32, device="cuda")
+    loss, dlogits = torch.empty(1, device="cuda"), torch.full_like(logits, 7.0)
+
+    def call():
+        rs.reshard_balance_loss(logits, shape, "fp32", choices, topk, 1.0, workspace, counts, loss=loss,
+                                dlogits=dlogits, mask=mask)
+    return call, logits, choices, mask, counts, loss, dlogits
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 300000])
+def test_balance_of_many_sequences(n):
+    experts, topk = 16, 2
+    call, logits, choices, mask, counts, loss, dlogits = _many_sequences(n, experts, topk)
+    for _ in range(2):                       # the second call finds the first one's workspace
+        call()
+    on = mask[:, 0] != 0
+    want = torch.zeros(n, experts, dtype=torch.int32, device="cuda")
+    want.scatter_(1, choices[:, 0].long(), 1)
+    want[~on] = 0
+    assert torch.equal(counts, want)
+    live = int(on.sum())
+    p = torch.softmax(logits[:, 0].double(), dim=1)
+    f = want.double() * experts / topk
+    dot = (p * f).sum(1, keepdim=True)
+    grad = p * (f - dot) / live
+    # as for the smaller sizes: E / 32 + 53 roundings, of what is added up
+    rel = (experts / 32 + 53) * 2.0 ** -23
+    assert abs(float(loss) - float(dot[on].sum()) / live) <= 2 * rel * float(dot[on].sum()) / live
+    off = (dlogits[:, 0].double() - grad).abs()
+    assert bool((off <= 2 * rel * p * (f + dot) / live)[on].all())
+    assert not bool(dlogits[~on].any())
+
+
+def test_balance_takes_time_in_proportion_to_the_sequences():
+    """16 times the sequences take at most three times 16 times as long (256 times as long if
+    each sequence looked at all the others)."""
+    def us(n):
+        call = _many_sequences(n)[0]
+        times = []
+        for _ in range(7):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return sorted(times)[3]
+    assert us(16 * 32768) <= 48 * us(32768)
