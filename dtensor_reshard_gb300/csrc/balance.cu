@@ -11,6 +11,8 @@
 // Bound by instructions (18 for the 32 logits of a warp, 70% of the issue slots) before
 // HBM: 64 sequences of 8192 tokens and 256 experts in bf16 take 110 us (4.9 TB/s, reads and
 // writes), 16 of them 37 us, 35 us with padding; of that the counts are 7 us.
+#include <type_traits>
+
 #include "operators.cuh"
 #include "tensor_core.cuh"
 
@@ -114,10 +116,12 @@ __global__ void __launch_bounds__(kCountThreads) count_kernel(const __grid_const
 }
 
 // A token's scores before they are divided by their sum, two at a time: exp(l - top), or
-// 1 / (1 + exp(-l)).  Exponentials are 2^x, x rounded to float32: off by 2^-24 |x| and 2
-// units in the last place (expf spends five times the instructions on less); scores below
-// 2^-126 are 0.
-constexpr float kLog2E = 1.4426950408889634f;
+// 1 / (1 + exp(-l)).  Exponentials are 2^x, x = log2(e) z rounded to float32, which alone would put
+// them off by up to 2^-24 |z| beside the 2 units in the last place of 2^x.  For float32 logits 2^x is
+// multiplied by 1 + t, t = z - x ln 2 what the rounding left: then it is off by 5 units in the last
+// place at most.  For 16-bit logits it is not: their gradients are rounded to 2^-9 or 2^-12, and the
+// loss is a mean over tokens of errors of either sign.  Scores below 2^-126 are 0.
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -143,15 +147,34 @@ __device__ __forceinline__ float sum2(uint64_t v) {
   const float2 f = tc::unpack2(v);
   return f.x + f.y;
 }
-template <int SCORE>
+// z within bounds outside which e^z is 0, or 1 / (1 + e^z) below 2^-126 (a NaN stays one), so
+// that x and t are finite.
+__device__ __forceinline__ float at_least(float z, float low) {
+  float v;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(z), "f"(low));
+  return v;
+}
+__device__ __forceinline__ float at_most(float z, float high) {
+  float v;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(z), "f"(high));
+  return v;
+}
+template <int SCORE, bool FLOAT32>
 struct Score {
-  __device__ static uint64_t of(float l0, float l1, float top) {
-    if (SCORE == RESHARD_SCORE_SOFTMAX) {
-      const float2 x = tc::unpack2(mul2(add2(pair(l0, l1), both(-top)), both(kLog2E)));
-      return pair(exp2_of(x.x), exp2_of(x.y));
+  __device__ static uint64_t exp_of(uint64_t z) {
+    if (FLOAT32) {
+      float2 v = tc::unpack2(z);
+      if (SCORE == RESHARD_SCORE_SIGMOID) v = make_float2(at_most(v.x, 88.0f), at_most(v.y, 88.0f));
+      z = pair(at_least(v.x, -200.0f), at_least(v.y, -200.0f));
     }
-    const float2 x = tc::unpack2(mul2(pair(l0, l1), both(-kLog2E)));
-    const float2 d = tc::unpack2(add2(pair(exp2_of(x.x), exp2_of(x.y)), both(1.0f)));
+    const uint64_t x = mul2(z, both(kLog2E));
+    const float2 f = tc::unpack2(x);
+    const uint64_t e = pair(exp2_of(f.x), exp2_of(f.y));
+    return FLOAT32 ? tc::fma2(e, tc::fma2(x, both(-kLn2), z), e) : e;
+  }
+  __device__ static uint64_t of(float l0, float l1, float top) {
+    if (SCORE == RESHARD_SCORE_SOFTMAX) return exp_of(add2(pair(l0, l1), both(-top)));
+    const float2 d = tc::unpack2(add2(exp_of(pair(-l0, -l1)), both(1.0f)));
     float r0, r1;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
@@ -280,6 +303,7 @@ template <typename T, int SCORE, bool VEC, int N>
 __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
     balance_kernel(const __grid_constant__ BalanceArgs a, const int lanes) {
   using L = Logits<T, VEC, N>;
+  using S = Score<SCORE, std::is_same<T, float>::value>;
   const int s = blockIdx.x / a.chunks;
   // tokens are unsigned: the last chunk's end, and those fetched ahead, may lie beyond 2^31
   const uint32_t first = blockIdx.x % a.chunks * a.chunk;
@@ -374,7 +398,7 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
       }
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
-        p[i / 2] = Score<SCORE>::of(to_float(now.v[i]), to_float(now.v[i + 1]), top);
+        p[i / 2] = S::of(to_float(now.v[i]), to_float(now.v[i + 1]), top);
         total2 = add2(total2, p[i / 2]);
         dot2 = tc::fma2(p[i / 2], f[i / 2], dot2);
       }
@@ -390,7 +414,7 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
       const uint64_t scale = both(each), minus_dot = both(-each * dot);
 #pragma unroll
       for (int i = 0; i < N; i += 2)
-        grad.set(i, tc::unpack2(mul2(Score<SCORE>::slope(p[i / 2]), tc::fma2(f[i / 2], scale, minus_dot))));
+        grad.set(i, tc::unpack2(mul2(S::slope(p[i / 2]), tc::fma2(f[i / 2], scale, minus_dot))));
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) grad.v[i] = from_float<T>(0.0f);
@@ -405,6 +429,7 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
 // each question; f_of(e) is the weight f of expert e.
 template <typename T, int SCORE, typename F>
 __device__ __forceinline__ float token_by_warp(const T* l, T* d, int experts, float share, F&& f_of) {
+  using S = Score<SCORE, std::is_same<T, float>::value>;
   const int lane = threadIdx.x & 31;
   float top = 0.0f, total = 0.0f, dot = 0.0f;
   if (SCORE == RESHARD_SCORE_SOFTMAX) {
@@ -414,7 +439,7 @@ __device__ __forceinline__ float token_by_warp(const T* l, T* d, int experts, fl
     if (top == -INFINITY) top = 0.0f;  // all scores 0
   }
   for (int e = lane; e < experts; e += 32) {
-    const float v = tc::unpack2(Score<SCORE>::of(to_float(l[e]), 0.0f, top)).x;
+    const float v = tc::unpack2(S::of(to_float(l[e]), 0.0f, top)).x;
     total += v;
     dot = fmaf(v, f_of(e), dot);
   }
@@ -423,8 +448,8 @@ __device__ __forceinline__ float token_by_warp(const T* l, T* d, int experts, fl
   dot = warp_sum(dot) * inv;
   if (d != nullptr)
     for (int e = lane; e < experts; e += 32) {
-      const uint64_t v = Score<SCORE>::of(to_float(l[e]), 0.0f, top);
-      d[e] = from_float<T>(share * inv * tc::unpack2(Score<SCORE>::slope(v)).x * (f_of(e) - dot));
+      const uint64_t v = S::of(to_float(l[e]), 0.0f, top);
+      d[e] = from_float<T>(share * inv * tc::unpack2(S::slope(v)).x * (f_of(e) - dot));
     }
   return dot;
 }

@@ -875,8 +875,9 @@ int64_t reshard_balance_loss_workspace(int64_t nseq, int64_t seqlen, int64_t nex
  *   dlogits[t]   = grad * dloss / dlogits[t]   (f is constant; 0 where mask is 0)
  * For a loss over the whole batch pass it as one sequence.  f depends on the choices
  * alone, so loss and gradient come from one pass over the logits.  Choices outside
- * 0..E - 1 are dropped ones and count for no expert.  A token with no score above
- * 0 in float32 (all its logits -inf) has p = 0.  No token: loss 0.
+ * 0..E - 1 are dropped ones and count for no expert.  Scores below 2^-126 before
+ * they are divided by their sum count as 0; a token that has no others (all its logits
+ * -inf or, with sigmoid scores, below -87.3) has p = 0.  No token: loss 0.
  *
  * logits [nseq][seqlen][ld] of dtype BF16, FP16 or FP32; experts [nseq][seqlen][topk];
  * mask [nseq][seqlen] bytes or NULL; grad: device pointer to the gradient of the loss,

@@ -129,3 +129,78 @@ def test_balance_takes_time_in_proportion_to_the_sequences():
             times.append(a.elapsed_time(b))
         return sorted(times)[3]
     assert us(16 * 32768) <= 48 * us(32768)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens", [40, 3000])    # one launch, and two
+@pytest.mark.parametrize("experts", [8, 9, 1100])
+def test_balance_scores_far_from_zero(experts, tokens, score):
+    """Small scores are as exact, relative to themselves, as large ones."""
+    g = torch.Generator(device="cuda").manual_seed(experts)
+    if score == "softmax":                   # one likely expert, the others e^-20 to e^-85 of it
+        logits = -20 - 65 * torch.rand(1, tokens, experts, generator=g, device="cuda")
+        logits[:, :, 3] = 0.0
+    else:                                    # none likely
+        logits = -80 - 6 * torch.rand(1, tokens, experts, generator=g, device="cuda")
+    choices = (torch.arange(tokens, device="cuda") % experts).to(torch.int32).view(1, tokens, 1)
+    shape = (1, tokens, experts)
+    workspace = torch.empty(rs.reshard_balance_loss_workspace(shape), dtype=torch.uint8, device="cuda")
+    counts = torch.empty(1, experts, dtype=torch.int32, device="cuda")
+    dlogits = torch.empty_like(logits)
+    rs.reshard_balance_loss(logits, shape, "fp32", choices, 1, float(tokens), workspace, counts,
+                            dlogits=dlogits, score=score)
+    l = logits[0].double()
+    f = counts[0].double() * experts / tokens
+    if score == "softmax":
+        p = torch.softmax(l, dim=1)
+        slope = p
+    else:
+        p = torch.sigmoid(l) / torch.sigmoid(l).sum(1, keepdim=True)
+        slope = p * torch.sigmoid(-l)
+    dot = (p * f).sum(1, keepdim=True)
+    grad = slope * (f - dot)
+    # In units of 2^-24: an exponential 4 (2^x) + 4 (t's part of ln 2) + 2 (1 + t, the product), the
+    # difference l - top that it is taken of |z| / 2 at most where that is not exact (it is: top
+    # is 0); the sigmoid 1 + 2; the sum as much again and E / 32 + 5 additions; 9 for f, its mean
+    # (whose own terms are as far off), the quotient and the products.
+    each = 4 + 4 + 2 + 3
+    rel = (2 * each + 2 * (experts / 32 + 5) + 9) * 2.0 ** -24
+    off = (dlogits[0].double() - grad).abs()
+    assert bool((off <= rel * slope * (f + dot) + 2.0 ** -126).all()), float(
+        (off / (slope * (f + dot)).clamp_min(2.0 ** -100)).max() * 2 ** 24)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens", [200, 20000])  # one launch, and two
+def test_balance_of_a_score_next_to_one(tokens, score):
+    """The gradient of an expert whose score is e^-80 to e^-87 next to another one's 1, with all
+    choices: f = (0, 2), so that it is 2 p for the score p (in units of coef / n = 1)."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    z = -80 - 7 * torch.rand(tokens, generator=g, device="cuda")
+    logits = torch.stack([torch.full_like(z, 0.0 if score == "softmax" else 30.0), z], dim=1)[None]
+    choices = torch.ones(1, tokens, 1, dtype=torch.int32, device="cuda")
+    shape = (1, tokens, 2)
+    workspace = torch.empty(rs.reshard_balance_loss_workspace(shape), dtype=torch.uint8, device="cuda")
+    counts = torch.empty(1, 2, dtype=torch.int32, device="cuda")
+    dlogits = torch.empty_like(logits)
+    rs.reshard_balance_loss(logits, shape, "fp32", choices, 1, float(tokens), workspace, counts,
+                            dlogits=dlogits, score=score)
+    want = 2 * torch.exp(z.double())
+    # In units of 2^-24: 2^x 4, ln 2 in t 4 (|x| 1.9e-9 for |x| <= 126), the correction's product 1, the
+    # sigmoid's sum and reciprocal 3; coef / live / n 2, f 3, its product with the share 1, with the
+    # score 1, of the sum's reciprocal 2.
+    off = ((dlogits[0, :, 1].double() - want) / want).abs().max()
+    assert float(off) <= (4 + 4 + 1 + 3 + 2 + 3 + 1 + 1 + 2) * 2.0 ** -24
+
+
+def test_balance_of_scores_that_are_too_small():
+    """Sigmoid scores below 2^-126 are 0: the second token has none."""
+    logits = torch.tensor([[[-87.0, -88.0], [-88.0, -90.0]]], device="cuda")
+    choices = torch.zeros(1, 2, 1, dtype=torch.int32, device="cuda")
+    workspace = torch.empty(rs.reshard_balance_loss_workspace((1, 2, 2)), dtype=torch.uint8, device="cuda")
+    counts = torch.empty(1, 2, dtype=torch.int32, device="cuda")
+    loss, dlogits = torch.empty(1, device="cuda"), torch.full_like(logits, 7.0)
+    rs.reshard_balance_loss(logits, (1, 2, 2), "fp32", choices, 1, 1.0, workspace, counts, loss=loss,
+                            dlogits=dlogits, score="sigmoid")
+    assert float(loss) == 1.0                # f = (2, 0): 2 of the first token, over two tokens
+    assert not bool(dlogits[0, 1].any())
