@@ -594,7 +594,9 @@ reshard_status_t launch_pass(BalanceArgs& a, int dev, int64_t sms, cudaStream_t 
 using rs::fail;
 
 extern "C" int64_t reshard_balance_loss_workspace(int64_t nseq, int64_t seqlen, int64_t nexperts) {
-  if (nseq < 0 || seqlen < 0 || nexperts < 0) return 0;
+  constexpr int64_t kMost = int64_t(1) << 31;
+  if (nseq < 0 || seqlen < 0 || nexperts < 0 || nseq >= kMost || seqlen >= kMost || nseq * seqlen >= kMost)
+    return 0;
   return rs::header_bytes(nseq) + 4 * nseq * rs::op::cdiv(seqlen, rs::kChunk);
 }
 

@@ -308,10 +308,7 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const __grid_consta
 
 template <typename T>
 reshard_status_t launch_quantize(const QuantizeArgs& a, int block_rows, cudaStream_t stream) {
-  constexpr int64_t kMost = int64_t(1) << 31;
   const bool vec = aligned(a.x, 16) && a.ldx * sizeof(T) % 16 == 0 && aligned(a.q, 8) && a.ldq % 8 == 0;
-  if (a.col_blocks >= kMost || a.row_blocks >= kMost || a.col_blocks * a.row_blocks >= kMost)
-    return fail(RESHARD_ERR_UNSUPPORTED, "2^31 blocks or more");
   if (block_rows == 128) {
     const unsigned grid = unsigned(a.col_blocks * a.row_blocks);
     if (vec) quantize_tiles_kernel<T, true><<<grid, 256, 0, stream>>>(a);
@@ -344,7 +341,11 @@ extern "C" reshard_status_t reshard_fp8_quantize(const void* x, int32_t dtype, i
     return fail(RESHARD_ERR_INVALID_ARG, "block_rows must be 1 or 128");
   if (nmat < 0 || rows < 0 || cols < 0) return fail(RESHARD_ERR_INVALID_ARG, "negative size");
   if (nmat == 0 || rows == 0 || cols == 0) return RESHARD_OK;
-  const int64_t col_blocks = rs::op::cdiv(cols, 128);
+  const int64_t col_blocks = rs::op::cdiv(cols, 128), mat_blocks = rs::op::cdiv(rows, block_rows);
+  constexpr int64_t kMost = int64_t(1) << 31;  // of each first: the products fit 64 bits then
+  if (col_blocks >= kMost || nmat >= kMost || mat_blocks >= kMost || nmat * mat_blocks >= kMost ||
+      nmat * mat_blocks * col_blocks >= kMost)
+    return fail(RESHARD_ERR_UNSUPPORTED, "2^31 blocks or more");
   if (ldx < cols || ldq < cols || lds < col_blocks)
     return fail(RESHARD_ERR_INVALID_ARG, "row pitch smaller than a row");
   if (!x || !q || !scale) return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
@@ -352,7 +353,6 @@ extern "C" reshard_status_t reshard_fp8_quantize(const void* x, int32_t dtype, i
     using T = decltype(t);
     if (!rs::op::aligned(x, sizeof(T)) || !rs::op::aligned(scale, 4))
       return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
-    const int64_t mat_blocks = rs::op::cdiv(rows, block_rows);
     const rs::QuantizeArgs a = {x,   static_cast<uint8_t*>(q), scale,      rows,       cols,
                                 ldx, ldq,                      lds,        col_blocks, nmat * mat_blocks,
                                 mat_blocks};

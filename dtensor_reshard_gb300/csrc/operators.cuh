@@ -63,7 +63,7 @@ __device__ __forceinline__ float largest_of(const __half (&v)[N]) {
   return fmaxf(__low2float(m), __high2float(m));
 }
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t cdiv(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 inline bool float_dtype(int32_t d) {
   return d == RESHARD_BF16 || d == RESHARD_FP16 || d == RESHARD_FP32;
 }

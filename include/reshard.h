@@ -862,7 +862,7 @@ reshard_status_t reshard_sample(const void* logits, int32_t dtype, int64_t rows,
                                 const float* top_p, const float* min_p, const float* u,
                                 int32_t* token, float* logprob, void* stream);
 
-/* Workspace bytes of reshard_balance_loss for these sizes (0 for invalid ones). */
+/* Workspace bytes of reshard_balance_loss for these sizes (0 for those that it refuses). */
 int64_t reshard_balance_loss_workspace(int64_t nseq, int64_t seqlen, int64_t nexperts);
 
 /*
