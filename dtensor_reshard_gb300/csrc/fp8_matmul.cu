@@ -715,10 +715,16 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 // An inner size of zero: the rows of experts get zeros.
 template <typename Y>
 __global__ void zero_kernel(const MatmulArgs a) {
+  __shared__ int most;
+  if (threadIdx.x == 0) most = 0;
+  __syncthreads();
   int first = 0, end = a.tokens;
   if (a.offsets != nullptr) {
     first = min(max(a.offsets[0], 0), a.tokens);
-    end = min(a.offsets[a.nexperts], a.tokens);
+    for (int e = threadIdx.x; e <= a.nexperts; e += blockDim.x)  // one below an earlier one counts as that
+      atomicMax(&most, min(a.offsets[e], a.tokens));
+    __syncthreads();
+    end = most;
   }
   for (int r = first + int(blockIdx.x); r < end; r += int(gridDim.x))
     for (int c = threadIdx.x; c < a.n; c += blockDim.x)

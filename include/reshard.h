@@ -813,7 +813,8 @@ reshard_status_t reshard_fp8_quantize(const void* x, int32_t dtype, int64_t nmat
  * offsets == NULL: one weight matrix (nexperts 1) for all tokens.  Else rows are
  * sorted by expert and offsets[nexperts + 1] (device memory, not decreasing, within
  * 0..tokens) gives expert e the rows offsets[e] .. offsets[e + 1] - 1; rows of no
- * expert are not written.  Offsets outside 0..tokens are clamped to it.
+ * expert are not written.  Offsets outside 0..tokens are clamped to it, and one
+ * below an earlier one counts as that one.
  *
  * x [tokens][ldx] bytes, xs [tokens][ldxs]; w [nexperts][n][ldw] bytes, ws
  * [nexperts][ceil(n / 128)][ldws]; y [tokens][ldy] of ydtype BF16, FP16 or FP32.

@@ -204,3 +204,21 @@ def test_balance_of_scores_that_are_too_small():
                             dlogits=dlogits, score="sigmoid")
     assert float(loss) == 1.0                # f = (2, 0): 2 of the first token, over two tokens
     assert not bool(dlogits[0, 1].any())
+
+
+# ----------------------------------------------------------------------------- matmul
+@pytest.mark.parametrize("offsets", [[2, 9, 4, 6], [0, 0, 12, 3], [5, 5, 5, 5], [-4, 30, 1, 2], [7, 3, 9, 20]])
+def test_matmul_offsets_that_decrease(offsets):
+    """An offset below an earlier one counts as that one, with and without an inner size."""
+    first, most = min(max(offsets[0], 0), 20), min(max(offsets), 20)
+    for k in (0, 16):
+        x = torch.full((20, 16), 0x38, dtype=torch.uint8, device="cuda")        # 1.0
+        w = torch.full((3, 8, 16), 0x38, dtype=torch.uint8, device="cuda")
+        xs, ws = torch.ones(20, 1, device="cuda"), torch.ones(3, 1, 1, device="cuda")
+        y = torch.full((20, 8), 77.0, device="cuda")
+        rs.reshard_fp8_matmul(x, xs, w, ws, y, (20, 8, k), "fp32",
+                              offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                              nexperts=3, ldx=16, ldw=16)
+        want = torch.full((20, 8), 77.0)
+        want[first:most] = float(k)
+        assert torch.equal(y.cpu(), want), k
