@@ -226,6 +226,9 @@ def _load():
                                   vp, i64, vp], ctypes.c_int),
         "reshard_fp8_matmul": ([vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp,
                                 ctypes.c_int32, i64, vp], ctypes.c_int),
+        "reshard_fp8_matmul_path": ([vp, i64, i64, i64, i64, vp, ctypes.c_int32, i64,
+                                     ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
+                                    ctypes.c_int),
         "reshard_sample": ([vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp],
                            ctypes.c_int),
         "reshard_balance_loss_workspace": ([i64, i64, i64], i64),
@@ -845,6 +848,17 @@ def reshard_fp8_matmul(x, xs, w, ws, y, shape, dtype, offsets=None, nexperts: in
         k if ldw is None else ldw, _ptr(ws), blocks if ldws is None else ldws, _ptr(offsets),
         nexperts, tokens, n, k, _ptr(y), _dtype(dtype), n if ldy is None else ldy,
         _stream(stream)), "reshard_fp8_matmul")
+
+
+def reshard_fp8_matmul_path(y, shape, dtype, offsets=None, nexperts: int = 1, ldy=None):
+    """(tokens of a tile, CTAs that share a tile's values of k) that reshard_fp8_matmul would
+    take for these arguments; decided on the host, nothing is launched."""
+    tokens, n, k = shape
+    tile, split = ctypes.c_int32(), ctypes.c_int32()
+    _check(_lib.reshard_fp8_matmul_path(_ptr(offsets), nexperts, tokens, n, k, _ptr(y), _dtype(dtype),
+                                        n if ldy is None else ldy, ctypes.byref(tile),
+                                        ctypes.byref(split)), "reshard_fp8_matmul_path")
+    return int(tile.value), int(split.value)
 
 
 def reshard_sample(logits, shape, dtype, u, token, logprob=None, temperature=None, top_k=None,

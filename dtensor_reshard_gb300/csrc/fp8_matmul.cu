@@ -799,94 +799,64 @@ int resident_clusters(int dev, unsigned threads, size_t smem, int split) {
   return n > 0 ? n : 1;
 }
 
-struct Operands {
-  const void *x, *w;
-  int64_t ldx, ldw, k;
+// Which kernel a call takes: `tokens` of a tile (narrow with 16, 32 or 64, wide with 128),
+// `split` CTAs a tile, and `units` of them: tiles, or for wide undivided the CTAs that go
+// through the tiles.
+struct Path {
+  int tokens, split;
+  int64_t units;
 };
-
-// `split` CTAs a tile of 128 tokens; with several of them, a cluster for each of at most
-// `units` tiles.
-template <typename Y>
-reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, int64_t units, int split, int dev,
-                             cudaStream_t stream) {
-  CUtensorMap map_x, map_w;
-  reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, kRows);
-  if (st == RESHARD_OK) st = tile_map(&map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows);
-  if (st != RESHARD_OK) return st;
-  a.ntiles = int32_t(cdiv(a.n, kWideCols));
-  const size_t at = wide_stages_at(ExpertTable::bytes(a.nexperts));
-  int stages = at + kWideStages * kWideStageBytes <= kSmemMost ? kWideStages : 2;
-  void* args[] = {&map_x, &map_w, &a, &stages};
-  return launch<wide_kernel<Y>, kSmemMost>(
-      "reshard_fp8_matmul", dev,
-      {units * split, kWideThreads, at + size_t(stages) * kWideStageBytes, split, stream}, args);
-}
-static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
 
 // ns that the sums of a tile's tokens take through a cluster.
 inline int64_t sums_way(int64_t tokens) { return 750 + 18 * tokens; }
 
+// Experts that can have rows, where rows are sorted by expert.
+inline int64_t experts_with_rows(const MatmulArgs& a) {
+  return !a.offsets ? 0 : a.nexperts < a.tokens ? a.nexperts : a.tokens;
+}
+// The most tiles of rows x cols that there can be.
+inline int64_t most_tiles(const MatmulArgs& a, int64_t rows, int64_t cols) {
+  return cdiv(a.n, cols) * (a.offsets ? a.tokens / rows + experts_with_rows(a) : cdiv(a.tokens, rows));
+}
+
 template <int NT, typename Y>
-reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, int64_t each, int dev, int64_t sms,
-                               cudaStream_t stream) {
-  CUtensorMap map_x, map_w;
-  reshard_status_t st = tile_map(&map_x, o.x, o.k, a.tokens, 1, o.ldx, NT);
-  if (st == RESHARD_OK) st = tile_map(&map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows);
-  if (st != RESHARD_OK) return st;
-  a.ntiles = int32_t(cdiv(a.n, kRows));
-  int64_t tiles = a.ntiles * cdiv(a.tokens, NT);
-  if (a.offsets) tiles = a.ntiles * (a.tokens / NT + (a.nexperts < a.tokens ? a.nexperts : a.tokens));
+Path narrow_path(const MatmulArgs& a, int64_t each, int dev, int64_t sms) {
+  const int64_t tiles = most_tiles(a, NT, kRows);
   // CTAs a tile, within one wave (a second one would cost more than longer shares) and with two
   // blocks each: the least of a share's blocks and, with several CTAs, the sums' way to the CTA
   // that adds them up, in ns.  (32 tokens' k = 512 takes 4.5 us undivided, longer by two CTAs;
   // k = 4096 10.7 us and, by eight, 6.2 us; one token's k = 1024 5.0 us and, by four, 4.2 us.)
-  const size_t table = ExpertTable::bytes(a.nexperts);
-  auto smem_of = [&](int split) {
-    return split > 1 ? NarrowSmem<NT>::sums_at(table) + NarrowSmem<NT>::sum_bytes(split)
-                     : sizeof(NarrowSmem<NT>) + table;
-  };
   const int64_t block = NT == 64 ? 450 : 210, way = sums_way(each < NT ? each : NT);
   int64_t best = a.blocks * block;
   int split = 1;
   for (int s = 2; s <= kMostSplit; ++s) {
     const int64_t cost = cdiv(a.blocks, s) * block + way;
     if (cost < best && a.blocks >= 2 * s && tiles * s <= 2 * sms &&
-        tiles <= resident_clusters<narrow_kernel<NT, Y>>(dev, kNarrowThreads,
-                                   NarrowSmem<NT>::sums_at(0) + NarrowSmem<NT>::sum_bytes(s), s))
+        tiles <= resident_clusters<narrow_kernel<NT, Y>>(
+                     dev, kNarrowThreads, NarrowSmem<NT>::sums_at(0) + NarrowSmem<NT>::sum_bytes(s), s))
       best = cost, split = s;
   }
-  if (tiles * split >= int64_t(1) << 31)
-    return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
-  void* args[] = {&map_x, &map_w, &a, &split};
-  return launch<narrow_kernel<NT, Y>, kSmemMost>(
-      "reshard_fp8_matmul", dev, {tiles * split, kNarrowThreads, smem_of(split), split, stream}, args);
+  return {NT, split, tiles};
+}
+
+// Four stages of the wide kernel, which a split needs for its sums.
+inline bool wide_room(const MatmulArgs& a) {
+  return wide_stages_at(ExpertTable::bytes(a.nexperts)) + kWideStages * kWideStageBytes <= kSmemMost;
 }
 
 template <typename Y>
-reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t stream) {
-  if (a.blocks == 0) {
-    zero_kernel<Y><<<unsigned(a.tokens < 1024 ? a.tokens : 1024), 256, 0, stream>>>(a);
-    return launched("reshard_fp8_matmul");
-  }
-  int dev = 0, sms = 0;
-  cudaError_t ce = cudaGetDevice(&dev);
-  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (ce != cudaSuccess)
-    return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
-  reshard_status_t st = device_status_word(&a.status);
-  if (st != RESHARD_OK) return st;
+Path matmul_path(const MatmulArgs& a, int dev, int64_t sms) {
   // Few tokens (of an expert, on average; experts differ): reading w is all that counts.
   const int64_t each = cdiv(a.tokens, a.nexperts);
-  if (each <= (a.offsets ? 4 : 16)) return launch_narrow<16, Y>(a, o, each, dev, sms, stream);
-  if (each <= (a.offsets ? 8 : 32)) return launch_narrow<32, Y>(a, o, each, dev, sms, stream);
+  if (each <= (a.offsets ? 4 : 16)) return narrow_path<16, Y>(a, each, dev, sms);
+  if (each <= (a.offsets ? 8 : 32)) return narrow_path<32, Y>(a, each, dev, sms);
 
   // Otherwise the least of these estimates in ns, fitted to 20 sizes from 64 x 7168 x 7168 to
   // 4096 x 4096 x 4096 within 15%: a kernel's start and end, and a time for each block of k
   // that the CTAs of an SM go through one after the other (w from HBM costs all the same).
-  const int64_t experts = !a.offsets ? 0 : a.nexperts < a.tokens ? a.nexperts : a.tokens;
   // Tiles of `rows` tokens: an expert's last one may be short, half of one on average.
   auto tiles = [&](int64_t rows, int64_t cols) {
-    return cdiv(a.n, cols) * cdiv(2 * cdiv(a.tokens, rows) + experts, 2);
+    return cdiv(a.n, cols) * cdiv(2 * cdiv(a.tokens, rows) + experts_with_rows(a), 2);
   };
   const int64_t blocks = a.blocks, stray = a.aligned_y == 32 ? 0 : 6000;  // rows off the sectors
   const int64_t small = tiles(64, kRows), large = tiles(kRows, kWideCols);
@@ -896,8 +866,7 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
     if (cost < best && blocks >= 2 * s && small * s <= sms) best = cost;
   }
   int split = 0;  // 0: narrow, else CTAs a tile of 128 tokens
-  const bool room =
-      wide_stages_at(ExpertTable::bytes(a.nexperts)) + kWideStages * kWideStageBytes <= kSmemMost;
+  const bool room = wide_room(a);
   for (int s = 1; s <= kMostSplit; ++s) {
     if (s > 1 && (!room || blocks < 2 * s || large * s > sms ||
                   large > resident_clusters<wide_kernel<Y>>(dev, kWideThreads, kSmemMost, s)))
@@ -906,11 +875,111 @@ reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t st
                                 : 10500 + cdiv(blocks, s) * 500;
     if (cost < best) best = cost, split = s;
   }
-  if (split == 0) return launch_narrow<64, Y>(a, o, each, dev, sms, stream);
-  int64_t units =  // the most tiles that there can be
-      cdiv(a.n, kWideCols) * (a.offsets ? a.tokens / kRows + experts : cdiv(a.tokens, kRows));
-  if (split == 1 && units > sms) units = sms;
-  return launch_wide<Y>(a, o, units, split, dev, stream);
+  if (split == 0) return narrow_path<64, Y>(a, each, dev, sms);
+  const int64_t units = most_tiles(a, kRows, kWideCols);
+  return {kRows, split, split == 1 && units > sms ? sms : units};
+}
+
+struct Operands {
+  const void *x, *w;
+  int64_t ldx, ldw, k;
+};
+
+reshard_status_t tile_maps(CUtensorMap* map_x, CUtensorMap* map_w, const MatmulArgs& a, const Operands& o,
+                           int rows) {
+  const reshard_status_t st = tile_map(map_x, o.x, o.k, a.tokens, 1, o.ldx, rows);
+  return st == RESHARD_OK ? tile_map(map_w, o.w, o.k, a.n, a.nexperts, o.ldw, kRows) : st;
+}
+
+template <typename Y>
+reshard_status_t launch_wide(MatmulArgs& a, const Operands& o, const Path& p, int dev, cudaStream_t stream) {
+  CUtensorMap map_x, map_w;
+  const reshard_status_t st = tile_maps(&map_x, &map_w, a, o, kRows);
+  if (st != RESHARD_OK) return st;
+  a.ntiles = int32_t(cdiv(a.n, kWideCols));
+  int stages = wide_room(a) ? kWideStages : 2;
+  const size_t smem = wide_stages_at(ExpertTable::bytes(a.nexperts)) + size_t(stages) * kWideStageBytes;
+  void* args[] = {&map_x, &map_w, &a, &stages};
+  return launch<wide_kernel<Y>, kSmemMost>("reshard_fp8_matmul", dev,
+                                           {p.units * p.split, kWideThreads, smem, p.split, stream}, args);
+}
+static_assert(split_chunks(7) * kSplitChunkBytes <= kWideStages * kWideStageBytes, "7 needs the most");
+
+template <int NT, typename Y>
+reshard_status_t launch_narrow(MatmulArgs& a, const Operands& o, const Path& p, int dev, cudaStream_t stream) {
+  if (p.units * p.split >= int64_t(1) << 31)
+    return fail(RESHARD_ERR_UNSUPPORTED, "reshard_fp8_matmul: too many tiles");
+  CUtensorMap map_x, map_w;
+  const reshard_status_t st = tile_maps(&map_x, &map_w, a, o, NT);
+  if (st != RESHARD_OK) return st;
+  a.ntiles = int32_t(cdiv(a.n, kRows));
+  const size_t table = ExpertTable::bytes(a.nexperts);
+  const size_t smem = p.split > 1 ? NarrowSmem<NT>::sums_at(table) + NarrowSmem<NT>::sum_bytes(p.split)
+                                  : sizeof(NarrowSmem<NT>) + table;
+  int split = p.split;
+  void* args[] = {&map_x, &map_w, &a, &split};
+  return launch<narrow_kernel<NT, Y>, kSmemMost>("reshard_fp8_matmul", dev,
+                                                 {p.units * split, kNarrowThreads, smem, split, stream}, args);
+}
+
+// The current device's path for these sizes.
+template <typename Y>
+reshard_status_t path_here(const MatmulArgs& a, int* dev, Path* p) {
+  int sms = 0;
+  cudaError_t ce = cudaGetDevice(dev);
+  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, *dev);
+  if (ce != cudaSuccess)
+    return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
+  *p = matmul_path<Y>(a, *dev, sms);
+  return RESHARD_OK;
+}
+
+template <typename Y>
+reshard_status_t launch_matmul(MatmulArgs& a, const Operands& o, cudaStream_t stream) {
+  if (a.blocks == 0) {
+    zero_kernel<Y><<<unsigned(a.tokens < 1024 ? a.tokens : 1024), 256, 0, stream>>>(a);
+    return launched("reshard_fp8_matmul");
+  }
+  int dev = 0;
+  Path p;
+  reshard_status_t st = path_here<Y>(a, &dev, &p);
+  if (st == RESHARD_OK) st = device_status_word(&a.status);
+  if (st != RESHARD_OK) return st;
+  if (p.tokens == 16) return launch_narrow<16, Y>(a, o, p, dev, stream);
+  if (p.tokens == 32) return launch_narrow<32, Y>(a, o, p, dev, stream);
+  if (p.tokens == 64) return launch_narrow<64, Y>(a, o, p, dev, stream);
+  return launch_wide<Y>(a, o, p, dev, stream);
+}
+
+// The checks of sizes, offsets and y, and what of the arguments follows from them.
+reshard_status_t matmul_args(const int32_t* offsets, int64_t nexperts, int64_t tokens, int64_t n, int64_t k,
+                             void* y, int32_t ydtype, int64_t ldy, MatmulArgs* a) {
+  if (!float_dtype(ydtype)) return fail(RESHARD_ERR_INVALID_ARG, "ydtype must be BF16, FP16 or FP32");
+  if (tokens < 0 || n < 0 || k < 0 || nexperts < 1)
+    return fail(RESHARD_ERR_INVALID_ARG, "negative size");
+  if (!offsets && nexperts != 1)
+    return fail(RESHARD_ERR_INVALID_ARG, "several experts need offsets");
+  if (nexperts > RESHARD_MAX_EXPERTS) return fail(RESHARD_ERR_UNSUPPORTED, "too many experts");
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1024;  // rounding up to tiles stays in 32 bits
+  if (tokens >= kMost || n >= kMost || k >= kMost || nexperts * n >= kMost)
+    return fail(RESHARD_ERR_UNSUPPORTED, "size of nearly 2^31 or more");
+  if (tokens == 0 || n == 0) return RESHARD_OK;
+  if (ldy < n) return fail(RESHARD_ERR_INVALID_ARG, "row pitch smaller than a row");
+  if (!y) return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(offsets, 4) || !aligned(y, dtype_size(ydtype)))
+    return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
+  *a = {};
+  a->offsets = offsets;
+  a->nexperts = int32_t(nexperts);
+  a->tokens = int32_t(tokens);
+  a->n = int32_t(n);
+  a->blocks = int32_t(cdiv(k, 128));
+  a->col_blocks = int32_t(cdiv(n, 128));
+  a->y = y;
+  a->ldy = ldy;
+  const int64_t pitch = ldy * dtype_size(ydtype);
+  a->aligned_y = aligned(y, 32) && pitch % 32 == 0 ? 32 : aligned(y, 16) && pitch % 16 == 0 ? 16 : 0;
+  return RESHARD_OK;
 }
 
 }  // namespace
@@ -925,46 +994,39 @@ extern "C" reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const
                                                int64_t tokens, int64_t n, int64_t k, void* y,
                                                int32_t ydtype, int64_t ldy, void* stream) {
   rs::TraceRange trace("op.fp8_matmul");
-  if (!rs::op::float_dtype(ydtype))
-    return fail(RESHARD_ERR_INVALID_ARG, "ydtype must be BF16, FP16 or FP32");
-  if (tokens < 0 || n < 0 || k < 0 || nexperts < 1)
-    return fail(RESHARD_ERR_INVALID_ARG, "negative size");
-  if (!offsets && nexperts != 1)
-    return fail(RESHARD_ERR_INVALID_ARG, "several experts need offsets");
-  if (nexperts > RESHARD_MAX_EXPERTS) return fail(RESHARD_ERR_UNSUPPORTED, "too many experts");
-  constexpr int64_t kMost = (int64_t(1) << 31) - 1024;  // rounding up to tiles stays in 32 bits
-  if (tokens >= kMost || n >= kMost || k >= kMost || nexperts * n >= kMost)
-    return fail(RESHARD_ERR_UNSUPPORTED, "size of nearly 2^31 or more");
-  if (tokens == 0 || n == 0) return RESHARD_OK;
-  const int64_t blocks = rs::op::cdiv(k, 128);
-  if (ldx < k || ldw < k || ldxs < blocks || ldws < blocks || ldy < n)
+  rs::MatmulArgs a;
+  const reshard_status_t st = rs::matmul_args(offsets, nexperts, tokens, n, k, y, ydtype, ldy, &a);
+  if (st != RESHARD_OK || tokens == 0 || n == 0) return st;
+  if (ldx < k || ldw < k || ldxs < a.blocks || ldws < a.blocks)
     return fail(RESHARD_ERR_INVALID_ARG, "row pitch smaller than a row");
-  if (!y || (k > 0 && (!x || !xs || !w || !ws)))
-    return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
+  if (k > 0 && (!x || !xs || !w || !ws)) return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
   if (!rs::op::aligned(x, 16) || !rs::op::aligned(w, 16) || ldx % 16 != 0 || ldw % 16 != 0)
     return fail(RESHARD_ERR_INVALID_ARG, "x, w and their row pitches must be multiples of 16 bytes");
-  if (!rs::op::aligned(xs, 4) || !rs::op::aligned(ws, 4) || !rs::op::aligned(offsets, 4) ||
-      !rs::op::aligned(y, rs::op::dtype_size(ydtype)))
+  if (!rs::op::aligned(xs, 4) || !rs::op::aligned(ws, 4))
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
-  rs::MatmulArgs a = {};
   a.xs = xs;
   a.ws = ws;
   a.ldxs = ldxs;
   a.ldws = ldws;
-  a.offsets = offsets;
-  a.nexperts = int32_t(nexperts);
-  a.tokens = int32_t(tokens);
-  a.n = int32_t(n);
-  a.blocks = int32_t(blocks);
-  a.col_blocks = int32_t(rs::op::cdiv(n, 128));
-  a.y = y;
-  a.ldy = ldy;
-  const int64_t pitch = ldy * rs::op::dtype_size(ydtype);
-  a.aligned_y = rs::op::aligned(y, 32) && pitch % 32 == 0   ? 32
-                : rs::op::aligned(y, 16) && pitch % 16 == 0 ? 16
-                                                            : 0;
   const rs::Operands o = {x, w, ldx, ldw, k};
   return rs::op::by_dtype(ydtype, [&](auto t) {
     return rs::launch_matmul<decltype(t)>(a, o, static_cast<cudaStream_t>(stream));
   });
+}
+
+extern "C" reshard_status_t reshard_fp8_matmul_path(const int32_t* offsets, int64_t nexperts, int64_t tokens,
+                                                    int64_t n, int64_t k, const void* y, int32_t ydtype,
+                                                    int64_t ldy, int32_t* tile_tokens, int32_t* split) {
+  if (!tile_tokens || !split) return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
+  rs::MatmulArgs a;
+  rs::Path p = {0, 0, 0};
+  reshard_status_t st =
+      rs::matmul_args(offsets, nexperts, tokens, n, k, const_cast<void*>(y), ydtype, ldy, &a);
+  int dev = 0;
+  if (st == RESHARD_OK && tokens > 0 && n > 0 && k > 0)
+    st = rs::op::by_dtype(ydtype, [&](auto t) { return rs::path_here<decltype(t)>(a, &dev, &p); });
+  if (st != RESHARD_OK) return st;
+  *tile_tokens = p.tokens;
+  *split = p.split;
+  return RESHARD_OK;
 }

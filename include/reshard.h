@@ -830,6 +830,18 @@ reshard_status_t reshard_fp8_matmul(const void* x, int64_t ldx, const float* xs,
                                     int64_t n, int64_t k, void* y, int32_t ydtype, int64_t ldy,
                                     void* stream);
 
+/*
+ * The way reshard_fp8_matmul would take on the current device for these arguments, decided
+ * exactly as a call decides it; nothing is launched and no memory is touched, so any
+ * pointers that pass the call's checks may be given.  *tile_tokens: tokens of a tile, 16, 32
+ * or 64 (with 128 features) or 128 (with 256); *split: CTAs that share a tile's values of
+ * k.  Both are 0 where no product is computed (no tokens, features or inner size).
+ * Errors: as reshard_fp8_matmul.
+ */
+reshard_status_t reshard_fp8_matmul_path(const int32_t* offsets, int64_t nexperts, int64_t tokens,
+                                         int64_t n, int64_t k, const void* y, int32_t ydtype,
+                                         int64_t ldy, int32_t* tile_tokens, int32_t* split);
+
 /* Largest vocabulary reshard_sample accepts. */
 #define RESHARD_MAX_VOCAB (1 << 20)
 
