@@ -172,17 +172,28 @@ struct Score {
     const uint64_t e = pair(exp2_of(f.x), exp2_of(f.y));
     return FLOAT32 ? tc::fma2(e, tc::fma2(x, both(-kLn2), z), e) : e;
   }
-  __device__ static uint64_t of(float l0, float l1, float top) {
-    if (SCORE == RESHARD_SCORE_SOFTMAX) return exp_of(add2(pair(l0, l1), both(-top)));
-    const float2 d = tc::unpack2(add2(exp_of(pair(-l0, -l1)), both(1.0f)));
+  __device__ static uint64_t inverse(uint64_t v) {
+    const float2 d = tc::unpack2(v);
     float r0, r1;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
     return pair(r0, r1);
   }
+  // What is kept of two logits: their scores, or exp(-l), from which a score a = 1 / (1 + exp(-l))
+  // and 1 - a = exp(-l) a are made without the digits that 1 - a loses where a is nearly 1
+  // (16-bit gradients have not got them).
+  static constexpr bool kExp = SCORE == RESHARD_SCORE_SIGMOID && FLOAT32;
+  __device__ static uint64_t of(float l0, float l1, float top) {
+    if (SCORE == RESHARD_SCORE_SOFTMAX) return exp_of(add2(pair(l0, l1), both(-top)));
+    const uint64_t e = exp_of(pair(-l0, -l1));
+    return kExp ? e : inverse(add2(e, both(1.0f)));
+  }
+  __device__ static uint64_t score(uint64_t v) { return kExp ? inverse(add2(v, both(1.0f))) : v; }
   // the score's own slope: p (softmax) or p (1 - a)
   __device__ static uint64_t slope(uint64_t v) {
-    return SCORE == RESHARD_SCORE_SOFTMAX ? v : mul2(v, tc::fma2(v, both(-1.0f), both(1.0f)));
+    const uint64_t a = score(v);
+    if (SCORE == RESHARD_SCORE_SOFTMAX) return a;
+    return mul2(a, kExp ? mul2(v, a) : tc::fma2(a, both(-1.0f), both(1.0f)));
   }
 };
 
@@ -399,8 +410,9 @@ __global__ void __launch_bounds__(256, N <= 16 ? 3 : 2)
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         p[i / 2] = S::of(to_float(now.v[i]), to_float(now.v[i + 1]), top);
-        total2 = add2(total2, p[i / 2]);
-        dot2 = tc::fma2(p[i / 2], f[i / 2], dot2);
+        const uint64_t score = S::score(p[i / 2]);
+        total2 = add2(total2, score);
+        dot2 = tc::fma2(score, f[i / 2], dot2);
       }
       float total = sum2(total2), dot = sum2(dot2);
       for (int o = lanes / 2; o; o >>= 1) {
@@ -439,7 +451,7 @@ __device__ __forceinline__ float token_by_warp(const T* l, T* d, int experts, fl
     if (top == -INFINITY) top = 0.0f;  // all scores 0
   }
   for (int e = lane; e < experts; e += 32) {
-    const float v = tc::unpack2(S::of(to_float(l[e]), 0.0f, top)).x;
+    const float v = tc::unpack2(S::score(S::of(to_float(l[e]), 0.0f, top))).x;
     total += v;
     dot = fmaf(v, f_of(e), dot);
   }
