@@ -10,7 +10,8 @@
 //
 // Bound by instructions (18 for the 32 logits of a warp, 70% of the issue slots) before
 // HBM: 64 sequences of 8192 tokens and 256 experts in bf16 take 110 us (4.9 TB/s, reads and
-// writes), 16 of them 37 us, 35 us with padding; of that the counts are 7 us.
+// writes), 16 of them 37 us, 35 us with padding; of that the counts are 7 us.  In float32 16 of
+// them take 59 us (4.6 TB/s).
 #include <type_traits>
 
 #include "operators.cuh"
@@ -41,7 +42,7 @@ struct BalanceArgs {
   int32_t nseq, seqlen, topk;
   int32_t chunk, chunks;            // tokens of a pass's CTA, CTAs of a sequence
   int32_t clusters;                 // of the counts of a sequence
-  int32_t nexperts, score;
+  int32_t nexperts;
   float coef;
 };
 
@@ -670,7 +671,6 @@ extern "C" reshard_status_t reshard_balance_loss(
   a.seqlen = int32_t(seqlen);
   a.topk = int32_t(topk);
   a.nexperts = int32_t(nexperts);
-  a.score = score;
   a.coef = coef;
   if (rs::small_enough(nseq * seqlen, nexperts) && nseq * (nexperts + 1) <= rs::kSmallCounts &&
       nseq * seqlen * topk <= rs::kSmallChoices)

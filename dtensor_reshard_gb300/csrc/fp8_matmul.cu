@@ -131,12 +131,13 @@ __device__ __noinline__ void give_up(uint32_t* status, uint32_t code) {
 // KiB stage), and sums with two warps a lane quarter, 128 columns each.  Every CTA loads its own
 // tiles: the tiles of a launch go along the tokens first, so that CTAs at work at a time read
 // the same weights from L2.
-// What bounds it is the way into and out of the matrix instructions: 48 KiB a block from L2, and
-// the accumulators out of tensor memory, which the instructions need too.  8192 x 14336 x 4096
-// to bf16 takes 445 us (2.2 PFLOP/s; 12.6 TB/s from L2).  Two accumulators of 256 columns fill
-// the 512: as four of 128 columns, with 16 summing warps, with tensor-memory loads of 32 columns
-// or with scalar sums it was slower by 4 to 70%.
-// 16384 tokens over 16 experts of [2048, 7168]: 254 us (1.9 PFLOP/s).
+// What bounds it is the accumulators' way out of tensor memory, which the matrix instructions need
+// too, and into the sums: 8192 x 14336 x 4096 to bf16 takes 420 to 455 us, by the clock that the
+// power cap leaves (2.1 to 2.3 PFLOP/s), 307 us with all loads of accumulators but an eighth of the
+// additions; the tensor pipe is active 48% of the time, and L2 gives 12.6 TB/s.  Two accumulators of 256
+// columns fill the 512: as four of 128 columns, with 16 summing warps, with tensor-memory loads
+// of 32 columns or with scalar sums it was slower by 4 to 70%.
+// 16384 tokens over 16 experts of [2048, 7168]: 255 us (1.9 PFLOP/s).
 constexpr int kWideStages = 4;  // 2 where the expert table needs the room
 constexpr int kWideStageBytes = 3 * kTileBytes;
 constexpr int kWideCols = 256;
@@ -169,10 +170,11 @@ __host__ __device__ constexpr size_t wide_stages_at(size_t table_bytes) {
 }
 static_assert(wide_stages_at(kTableMost) + 2 * kWideStageBytes <= kSmemMost, "shared memory");
 
-// For fewer tokens than fill the GPU that way, such a tile a cluster, of which each CTA takes a share of the blocks of k; the sums of 16 columns at a
-// time go to the CTA that adds them up, in rank order, through distributed shared memory
-// (in the place of the stages).  64 x 7168 x 7168 takes 16.5 us, 128 tokens 18.5 us, against
-// 25 us with 64-token tiles; 777 x 2867 x 819 to float32 10.3 us.
+// For fewer tokens than fill the GPU that way, such a tile a cluster, of which each CTA
+// takes a share of the blocks of k; the sums of 16 columns at a time go to the CTA that
+// adds them up, in rank order, through distributed shared memory (in the place of the
+// stages).  64 x 7168 x 7168 takes 17.3 us, 128 tokens 20 us, by five CTAs a tile, against
+// 25 us with 64-token tiles; 513 x 2688 x 7168 by two 26 us.
 constexpr int kSplitChunk = 16;  // columns
 constexpr int kSplitChunkBytes = kRows * kSplitChunk * 4;
 // Chunks that a CTA receives at most, from all CTAs of a split.
@@ -486,11 +488,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // One tile of 128 features x NT tokens a CTA: four summing warps, a loading warp and two
 // matrix warps.  `split` CTAs of a cluster take a share of the blocks of k each and send
 // their sums through distributed shared memory to the CTA that adds up the column, in rank
-// order.  Bound by reading w where there is much of it (1024 tokens over 256 experts of [256,
-// 7168]: 67 us, 7.0 TB/s), by latencies where there is little (1 x 2688 x 7168: 8.2 us, of
-// which 3 us are the loads).  Four stages of loads and four accumulators keep both matrix
-// warps' instructions in flight: a group of four for so few tokens takes 560 clocks by
-// itself whatever their number.
+// order.  Bound by reading w where there is much of it (1024 tokens over 256 experts of
+// [256, 7168]: 68 us, 7.0 TB/s), by latencies where there is little (1 x 2688 x 7168: 8.2
+// us, of which 3 us are the loads; 777 x 2867 x 819 to float32 in 64-token tiles 8.3 to
+// 10.3 us).  Four stages of loads and four accumulators keep both matrix warps'
+// instructions in flight: a group of four for so few tokens takes 560 clocks by itself
+// whatever their number.
 constexpr int kMatrixWarps = 2;
 constexpr int kNarrowThreads = 32 * (5 + kMatrixWarps);
 constexpr int kNarrowStages = 4, kNarrowBufs = 4;

@@ -3,7 +3,7 @@
 //
 // scale = max(largest magnitude / 448, 2^-126), value = the nearest e4m3 to x / scale.  Read
 // once, 2 or 4 bytes a value, written once, 1 byte: bound by HBM for blocks of 128x128 (16
-// matrices of [2048, 7168] in bf16: 121 us, 5.8 TB/s) and nearly so for 1x128, where the
+// matrices of [2048, 7168] in bf16: 124 us, 5.7 TB/s) and nearly so for 1x128, where the
 // quotients' instructions fill 73% of the issue slots (8192 rows of 7168: 37 us, 4.8 TB/s).
 #include "operators.cuh"
 #include "tensor_core.cuh"

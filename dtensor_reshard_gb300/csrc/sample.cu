@@ -17,7 +17,8 @@
 //      CTA that read all histograms and told the others took 11 000 clocks of a row's 37 000,
 //      this 4 000).  Where no more than 256 tokens lie as high, these are listed and the
 //      first CTA finishes the row with them; else the tokens of that one bin are listed and
-//      ranked by (logit, index), which gives the last kept token exactly, and
+//      ranked by (logit, index), which gives the last kept token exactly (a bin of more than
+//      384 tokens is bisected over the logits' bits instead), and
 //   4. the kept weights' sums, and the token whose running sum passes the target, come from
 //      one more pass over the slices.
 // Weights are whole numbers (2^-40 of the largest), so sums are exact and neither the
@@ -25,8 +26,12 @@
 //
 // Bound by instructions (about 23 a token of a warp's 32) and by the cluster's meetings, not by
 // HBM: 256 rows of 131072 bf16 logits take 35 us greedy, 42 us whole, 76 us with top-p 0.95,
-// 63 us mixed (67 MB, 10 us of HBM); one row 11.6 us, 37 rows of 50021 float32 14.4 us.
-// Rows of equal logits, which no histogram tells apart, are bisected: 256 of them 1.3 ms.
+// 60 to 71 us mixed, by the set (67 MB, 10 us of HBM; all with a few likely tokens a row); one row
+// 12 to 15 us, 37 rows of 50021 float32 14.4 to 17 us.
+// Where a bin is bisected it takes 16 (16-bit logits) to 32 passes over the row.  That is where
+// logits are alike (256 equal rows of 131072: bf16 1.3 ms, float32 2.8 ms) and where top-p ends
+// among very many tokens: 256 rows of 131072 normal logits of deviation 0.5 to 2, top-p 0.95, take
+// 1.4 ms in bf16 and 3.5 ms in float32, of deviation 3 0.3 and 0.46 ms; of 32000 60 to 210 us.
 #include <type_traits>
 
 #include "operators.cuh"
@@ -124,8 +129,9 @@ struct Scale {
 
 // round(2^40 e), e in [0, 1], as high * 2^22 + low: adding 48 = 1.5 * 2^5 leaves e's
 // multiples of 2^-18 in the sum's low bits, adding 1.5 * 2^-17 to what is left those of
-// 2^-40.  The bits of both sums are added up as they are, in 32 bits (both halves of 256
-// weights fit), and their constant parts taken off at the end.
+// 2^-40.  The bits of both sums are added up as they are, in 32 bits (the low halves lie
+// within 2^21 either way, so that 1023 weights fit; a thread has 520 at most, of a row of
+// RESHARD_MAX_VOCAB by eight CTAs of 256 threads), and their constant parts taken off at the end.
 struct Weights {
   uint32_t high = 0, low = 0, n = 0;
   __device__ void add(float e0, float e1) {

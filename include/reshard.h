@@ -338,8 +338,9 @@ reshard_status_t gather_broadcast_execute(reshard_plan_t plan, const void* const
  * every wait on its shared-memory barriers; a wait that runs out (which a
  * correct run never does) records a nonzero code here instead of hanging or
  * trapping, and the kernel returns.  reshard_fp8_matmul's waits are bounded the same
- * way.  Codes: 0 none, 1 producer wait, 2 consumer wait, 3 self-test, 5, 6, 7
- * reshard_fp8_matmul's loading, matrix and summing warps.  Synchronous (reads device memory with cudaMemcpy);
+ * way.  Codes: 0 none, 1 producer wait, 2 consumer wait, 3 self-test, 4 a transpose
+ * block that its launch's element width does not allow, 5, 6, 7 reshard_fp8_matmul's
+ * loading, matrix and summing warps.  Synchronous (reads device memory with cudaMemcpy);
  * `clear` != 0 resets the word to 0 after reading.  Errors: INVALID_ARG, CUDA.
  */
 reshard_status_t reshard_device_status(int32_t clear, uint32_t* status);
