@@ -467,7 +467,9 @@ __device__ __forceinline__ float token_by_warp(const T* l, T* d, int experts, fl
   return dot;
 }
 
-// The pass for more experts than a warp's registers hold: a warp a token.
+// The pass for more experts than a warp's registers hold: a warp a token, which reads the row two
+// or three times (the later ones from L1) and waits for each: 16 x 8192 tokens of 1100 experts in bf16
+// take 292 us, of 1000 experts in registers 113 us.
 template <typename T, int SCORE>
 __global__ void __launch_bounds__(256) balance_many_kernel(const __grid_constant__ BalanceArgs a) {
   extern __shared__ float f_smem[];
