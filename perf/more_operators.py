@@ -247,8 +247,6 @@ def prepare(case, seed):
             state["scale"] = torch.zeros((t * k, cdiv(c, BLOCK)), device="cuda")
         else:
             state["rows"] = torch.zeros((t * k, c), dtype=dtype, device="cuda")
-        # scratch that a program keeps for the calls: ample for any of these sizes
-        state["workspace"] = torch.empty(4 << 20, dtype=torch.uint8, device="cuda")
         return state
     state["slot"] = _places(chosen, case["experts"])[0]
     state["rows"] = _normal((t * k, c), g).to(dtype)
@@ -430,7 +428,7 @@ def _own_distill(rs, state):
 def _own_dispatch(rs, state):
     case = state["case"]
     rs.reshard_expert_sort(state["experts"], (case["tokens"], case["topk"]), case["experts"],
-                           state["workspace"], state["slot"], state["offsets"])
+                           state["slot"], state["offsets"])
     shape = (case["tokens"], case["topk"], case["cols"])
     if not case["quantised"]:
         rs.reshard_expert_dispatch(state["x"], shape, case["dtype"], state["slot"], state["rows"])
