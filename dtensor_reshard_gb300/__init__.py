@@ -235,6 +235,13 @@ def _load():
         "reshard_balance_loss": ([vp, ctypes.c_int32, i64, i64, i64, i64, vp, i64, vp,
                                   ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, vp, i64, vp],
                                  ctypes.c_int),
+        "reshard_expert_sort": ([vp, i64, i64, i64, vp, vp, vp], ctypes.c_int),
+        "reshard_expert_dispatch": ([vp, ctypes.c_int32, i64, i64, i64, i64, vp, i64, vp, i64, vp, i64,
+                                     vp], ctypes.c_int),
+        "reshard_expert_combine": ([vp, ctypes.c_int32, i64, i64, i64, i64, i64, vp, vp, vp, i64, vp],
+                                   ctypes.c_int),
+        "reshard_expert_combine_grad": ([vp, ctypes.c_int32, i64, i64, i64, i64, vp, i64, vp, i64, vp,
+                                         vp, vp, vp], ctypes.c_int),
         "reshard_last_error": ([], ctypes.c_char_p),
         "reshard_version": ([], ctypes.c_char_p),
     }
@@ -893,3 +900,49 @@ def reshard_balance_loss(logits, shape, dtype, experts, topk: int, coef: float, 
         _ptr(experts), topk, _ptr(mask), SCORES[score] if isinstance(score, str) else int(score),
         coef, _ptr(grad), _ptr(loss), _ptr(counts), _ptr(dlogits), _ptr(workspace),
         workspace_bytes, _stream(stream)), "reshard_balance_loss")
+
+
+def reshard_expert_sort(experts, shape, nexperts: int, slot, offsets, stream=None):
+    """slot [tokens, topk] (int32): the place of each choice of experts [tokens, topk] (int32)
+    among all choices sorted by expert, -1 where it names none of 0..nexperts - 1; offsets
+    [nexperts + 1] (int32): each expert's first place.  ``shape`` = (tokens, topk)."""
+    tokens, topk = shape
+    _check(_lib.reshard_expert_sort(_ptr(experts), tokens, topk, nexperts, _ptr(slot), _ptr(offsets),
+                                    _stream(stream)), "reshard_expert_sort")
+
+
+def reshard_expert_dispatch(x, shape, dtype, slot, rows, scale=None, nrows=None, ldx=None, ldr=None,
+                            lds=None, stream=None):
+    """rows[slot[t, j]] = x[t] for x [tokens, cols] of ``dtype``; ``shape`` = (tokens, topk, cols).
+    With ``scale`` [nrows, ceil(cols / 128)] (float32) rows are e4m3 bytes.  rows has nrows rows,
+    by default tokens * topk; pitches default to dense rows."""
+    tokens, topk, cols = shape
+    _check(_lib.reshard_expert_dispatch(
+        _ptr(x), _dtype(dtype), tokens, topk, cols, cols if ldx is None else ldx, _ptr(slot),
+        tokens * topk if nrows is None else nrows, _ptr(rows), cols if ldr is None else ldr,
+        _ptr(scale), _cdiv(cols, 128) if lds is None else lds, _stream(stream)),
+        "reshard_expert_dispatch")
+
+
+def reshard_expert_combine(rows, shape, dtype, slot, out, weight=None, nrows=None, ldr=None,
+                           ldo=None, stream=None):
+    """out[t] = sum over j of weight[t, j] * rows[slot[t, j]]; ``shape`` = (tokens, topk, cols),
+    rows [nrows, cols] and out [tokens, cols] of ``dtype``, weight [tokens, topk] (float32) or
+    None for ones."""
+    tokens, topk, cols = shape
+    _check(_lib.reshard_expert_combine(
+        _ptr(rows), _dtype(dtype), tokens, topk, cols, tokens * topk if nrows is None else nrows,
+        cols if ldr is None else ldr, _ptr(slot), _ptr(weight), _ptr(out),
+        cols if ldo is None else ldo, _stream(stream)), "reshard_expert_combine")
+
+
+def reshard_expert_combine_grad(dout, shape, dtype, slot, rows=None, weight=None, drows=None,
+                                dweight=None, nrows=None, ldo=None, ldr=None, stream=None):
+    """Gradients of reshard_expert_combine: drows [nrows, cols] of ``dtype`` and dweight
+    [tokens, topk] (float32), each where given, from dout [tokens, cols]; rows is needed for
+    dweight."""
+    tokens, topk, cols = shape
+    _check(_lib.reshard_expert_combine_grad(
+        _ptr(dout), _dtype(dtype), tokens, topk, cols, cols if ldo is None else ldo, _ptr(slot),
+        tokens * topk if nrows is None else nrows, _ptr(rows), cols if ldr is None else ldr,
+        _ptr(weight), _ptr(drows), _ptr(dweight), _stream(stream)), "reshard_expert_combine_grad")

@@ -21,8 +21,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["planner.cpp", "batch.cpp", "kernels.cu", "bulk_fanout.cu", "transpose.cu",
            "static_scratch.cu", "realign_staged.cu", "refit.cpp", "partition.cpp",
-           "fp8_quantize.cu", "fp8_matmul.cu", "sample.cu", "balance.cu"]
-HEADERS = ["internal.h", "staging.cuh", "operators.cuh", "tensor_core.cuh"]
+           "fp8_quantize.cu", "fp8_matmul.cu", "sample.cu", "balance.cu",
+           "experts.cu"]
+HEADERS = ["internal.h", "staging.cuh", "operators.cuh", "tensor_core.cuh", "fp8_block.cuh"]
 
 
 def nvcc() -> str:

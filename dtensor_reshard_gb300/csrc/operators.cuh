@@ -1,5 +1,5 @@
 // operators.cuh -- pieces shared by the operators that run beside a refit
-// (fp8_quantize.cu, fp8_matmul.cu, sample.cu, balance.cu): element types,
+// (fp8_quantize.cu, fp8_matmul.cu, sample.cu, balance.cu, experts.cu): element types,
 // reductions and argument checks.
 #pragma once
 

@@ -765,7 +765,8 @@ reshard_status_t reshard_plan_destroy(reshard_plan_t plan);
  *   reshard_fp8_matmul     the product of such matrices, dense or per expert;
  *   reshard_sample         the next token of every request from its logits;
  *   reshard_balance_loss   the router's load-balance loss, the tokens each expert
- *                          got, and the gradient in the router's logits.
+ *                          got, and the gradient in the router's logits;
+ *   reshard_expert_*       the tokens' rows sorted by expert and back.
  * All matrices are row-major with a row pitch ("ld") in elements.  All of them follow
  * the conventions above: work is enqueued on `stream`, nothing is synchronised,
  * allocated or kept between calls, every call can be captured into a CUDA graph, and
@@ -908,6 +909,68 @@ reshard_status_t reshard_balance_loss(const void* logits, int32_t dtype, int64_t
                                       int32_t score, float coef, const float* grad, float* loss,
                                       int32_t* counts, void* dlogits, void* workspace,
                                       int64_t workspace_bytes, void* stream);
+
+/*
+ * Sort a router's choices by expert: experts[tokens][topk] names an expert of 0..nexperts - 1 for
+ * each choice; any other value is a dropped choice.  In the order of the experts, and for one
+ * expert in the order of the choices (token by token),
+ *   slot[t][j]  = the choice's place among all that are not dropped, -1 for a dropped one
+ *   offsets[e]  = the first place of expert e, offsets[nexperts] the number of places
+ * so that offsets serve reshard_fp8_matmul as they are.
+ *
+ * experts, slot [tokens][topk]; offsets [nexperts + 1].  Errors: INVALID_ARG (null pointer,
+ * negative size, misaligned pointer), UNSUPPORTED (nexperts > RESHARD_MAX_EXPERTS, tokens * topk
+ * of 2^31 or more), CUDA.
+ */
+reshard_status_t reshard_expert_sort(const int32_t* experts, int64_t tokens, int64_t topk,
+                                     int64_t nexperts, int32_t* slot, int32_t* offsets, void* stream);
+
+/*
+ * Rows of tokens to the places of their choices: rows[slot[t][j]] = x[t], and with `scale` in 8
+ * bits, exactly as reshard_fp8_quantize with blocks of 1 x 128 (scale[slot[t][j]] the row's
+ * scales).  Each row is read, and quantised, once.  A slot outside 0..nrows - 1 is skipped; rows
+ * of no choice are left as they are; the slots of different choices must differ.
+ * The gradient in x of the plain form is reshard_expert_combine of the rows' gradients without
+ * weights.
+ *
+ * x [tokens][ldx] of dtype BF16, FP16 or FP32; slot [tokens][topk]; rows [nrows][ldr] of dtype,
+ * or of bytes where scale is given; scale [nrows][lds] or NULL.  Any alignment to the type is
+ * accepted; rows that start on and have a multiple of 16 bytes are faster.  Errors: INVALID_ARG
+ * (null pointer, dtype, negative size, pitch too small, misaligned pointer), UNSUPPORTED (a size
+ * or tokens * topk of 2^31 or more, or a product of sizes that asks for 2^31 CTAs or more), CUDA.
+ */
+reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype, int64_t tokens, int64_t topk,
+                                         int64_t cols, int64_t ldx, const int32_t* slot, int64_t nrows,
+                                         void* rows, int64_t ldr, float* scale, int64_t lds,
+                                         void* stream);
+
+/*
+ * Back from the experts: out[t] = sum_j weight[t][j] * rows[slot[t][j]], in float32 in the order
+ * of j and rounded once.  Choices whose slot is outside 0..nrows - 1 count for nothing; a token
+ * without others gets 0.  weight NULL: all 1.
+ *
+ * rows [nrows][ldr] and out [tokens][ldo] of dtype BF16, FP16 or FP32; slot, weight
+ * [tokens][topk].  Errors: as reshard_expert_dispatch.
+ */
+reshard_status_t reshard_expert_combine(const void* rows, int32_t dtype, int64_t tokens, int64_t topk,
+                                        int64_t cols, int64_t nrows, int64_t ldr, const int32_t* slot,
+                                        const float* weight, void* out, int64_t ldo, void* stream);
+
+/*
+ * The gradients of reshard_expert_combine from that of its result:
+ *   drows[slot[t][j]] = weight[t][j] * dout[t]
+ *   dweight[t][j]     = sum_c dout[t][c] * rows[slot[t][j]][c]   (0 for a slot outside 0..nrows - 1)
+ * Rows of no choice are left as they are; the slots of different choices must differ.  drows and
+ * dweight may each be NULL; rows is read for dweight alone.
+ *
+ * dout [tokens][ldo], rows and drows [nrows][ldr] of dtype; slot, weight (or NULL: all 1),
+ * dweight [tokens][topk].  Errors: as reshard_expert_dispatch.
+ */
+reshard_status_t reshard_expert_combine_grad(const void* dout, int32_t dtype, int64_t tokens,
+                                             int64_t topk, int64_t cols, int64_t ldo,
+                                             const int32_t* slot, int64_t nrows, const void* rows,
+                                             int64_t ldr, const float* weight, void* drows,
+                                             float* dweight, void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* reshard_last_error(void);
