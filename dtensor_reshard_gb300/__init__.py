@@ -242,6 +242,10 @@ def _load():
                                    ctypes.c_int),
         "reshard_expert_combine_grad": ([vp, ctypes.c_int32, i64, i64, i64, i64, vp, i64, vp, i64, vp,
                                          vp, vp, vp], ctypes.c_int),
+        "reshard_logprob": ([vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp, ctypes.c_int32, vp, vp,
+                             i64, vp, vp], ctypes.c_int),
+        "reshard_logprob_grad": ([vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp],
+                                 ctypes.c_int),
         "reshard_last_error": ([], ctypes.c_char_p),
         "reshard_version": ([], ctypes.c_char_p),
     }
@@ -822,6 +826,7 @@ def nccl_exchange(gpu_rank, send_buf, recv_buf):
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_EXPERTS = _DEFINES["RESHARD_MAX_EXPERTS"]
 MAX_VOCAB = _DEFINES["RESHARD_MAX_VOCAB"]
+MAX_TOP = _DEFINES["RESHARD_MAX_TOP"]
 
 
 def _dtype(d) -> int:
@@ -946,3 +951,27 @@ def reshard_expert_combine_grad(dout, shape, dtype, slot, rows=None, weight=None
         _ptr(dout), _dtype(dtype), tokens, topk, cols, cols if ldo is None else ldo, _ptr(slot),
         tokens * topk if nrows is None else nrows, _ptr(rows), cols if ldr is None else ldr,
         _ptr(weight), _ptr(drows), _ptr(dweight), _stream(stream)), "reshard_expert_combine_grad")
+
+
+def reshard_logprob(logits, shape, dtype, target=None, logprob=None, entropy=None, top_token=None,
+                    top_logprob=None, ntop: int = 0, state=None, temperature=None, ld=None, ldtop=None,
+                    stream=None):
+    """Log-probability of target [rows] (int32), entropy, and the ntop most likely tokens with their
+    log-probabilities (top_token int32, top_logprob, both [rows, ntop]) of logits of ``shape``
+    (rows, vocab), each where given; state [rows, 4] (float32) is for reshard_logprob_grad."""
+    rows, vocab = shape
+    _check(_lib.reshard_logprob(
+        _ptr(logits), _dtype(dtype), rows, vocab, vocab if ld is None else ld, _ptr(temperature),
+        _ptr(target), _ptr(logprob), _ptr(entropy), ntop, _ptr(top_token), _ptr(top_logprob),
+        ntop if ldtop is None else ldtop, _ptr(state), _stream(stream)), "reshard_logprob")
+
+
+def reshard_logprob_grad(logits, shape, dtype, state, dlogits, target=None, dlogprob=None,
+                         dentropy=None, temperature=None, ld=None, stream=None):
+    """dlogits (which may be logits itself) from dlogprob and dentropy [rows], each where given;
+    state is what reshard_logprob wrote for the same logits, target and temperature."""
+    rows, vocab = shape
+    _check(_lib.reshard_logprob_grad(
+        _ptr(logits), _dtype(dtype), rows, vocab, vocab if ld is None else ld, _ptr(temperature),
+        _ptr(target), _ptr(state), _ptr(dlogprob), _ptr(dentropy), _ptr(dlogits), _stream(stream)),
+        "reshard_logprob_grad")

@@ -1,0 +1,160 @@
+// vocab_row.cuh -- a row of logits as logprob.cu and distill.cu take it: granules of 16 aligned
+// bytes at any alignment of the row, exponentials relative to a maximum two at a time, and a
+// gradient's granules on their way out.
+#pragma once
+
+#include "operators.cuh"
+#include "tensor_core.cuh"
+
+namespace rs {
+namespace vocab {
+
+using namespace op;
+
+template <typename T>
+__host__ __device__ constexpr float largest_finite() {
+  return sizeof(T) == 4 ? 3.402823466e38f : 3.389531390e38f;
+}
+template <>
+__host__ __device__ constexpr float largest_finite<__half>() { return 65504.0f; }
+
+// A logit as it counts: +inf as the type's largest finite value, so that differences of two
+// logits are never NaN; NaN as -inf; -0 as +0.
+template <typename T>
+__device__ __forceinline__ float clean(float l) {
+  return l == l ? fminf(l, largest_finite<T>()) + 0.0f : -INFINITY;
+}
+
+// Whole numbers in the order of the floats, and back.
+__device__ __forceinline__ uint32_t key_of(float l) {
+  const uint32_t b = __float_as_uint(l);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// 1 / T as a factor: 1 for T <= 0 and NaN, and never infinite.
+__device__ __forceinline__ float inverse_of(const float* temperature, int64_t r) {
+  const float t = temperature ? __ldg(temperature + r) : 1.0f;
+  return t > 0.0f ? fminf(1.0f / t, 3.402823466e38f) : 1.0f;
+}
+// The same for powers of 2.
+__device__ __forceinline__ float log2_scale(float inverse) {
+  return fminf(1.4426950408889634f * inverse, 3.402823466e38f);
+}
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint64_t both(float v) {
+  return tc::pack2(__float_as_uint(v), __float_as_uint(v));
+}
+__device__ __forceinline__ uint64_t pair(float2 v) {
+  return tc::pack2(__float_as_uint(v.x), __float_as_uint(v.y));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  const float2 f = tc::unpack2(v);
+  return f.x + f.y;
+}
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Exponents below this give 0 (and stay finite: 0 times one is 0).  The maximum also takes
+// the place of NaN, and of -inf.
+constexpr float kLeast = -200.0f;
+__device__ __forceinline__ float exponent(float x, float m, float c) { return fmaxf((x - m) * c, kLeast); }
+__device__ __forceinline__ uint64_t exponents(uint64_t x, uint64_t minus_m, uint64_t c) {
+  const float2 z = tc::unpack2(mul2(add2(x, minus_m), c));
+  return pair(make_float2(fmaxf(z.x, kLeast), fmaxf(z.y, kLeast)));
+}
+__device__ __forceinline__ uint64_t exp2_both(uint64_t z) {
+  const float2 f = tc::unpack2(z);
+  return pair(make_float2(exp2_of(f.x), exp2_of(f.y)));
+}
+
+__device__ __forceinline__ float2 pair_of(const float* e) { return make_float2(e[0], e[1]); }
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* e) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(e));
+}
+__device__ __forceinline__ float2 pair_of(const __half* e) {
+  return __half22float2(*reinterpret_cast<const __half2*>(e));
+}
+__device__ __forceinline__ void set_pair(float* to, float2 x) { to[0] = x.x, to[1] = x.y; }
+__device__ __forceinline__ void set_pair(__nv_bfloat16* to, float2 x) {
+  *reinterpret_cast<__nv_bfloat162*>(to) = __float22bfloat162_rn(x);
+}
+__device__ __forceinline__ void set_pair(__half* to, float2 x) {
+  *reinterpret_cast<__half2*>(to) = __float22half2_rn(x);
+}
+
+// A row in granules of 16 aligned bytes.  What lies outside the row in the first and the last
+// granule is neither read nor written; it reads as -inf.
+template <typename T>
+struct Row {
+  static constexpr int kPer = 16 / int(sizeof(T));
+  const T* row;
+  int vocab, skew;  // elements of the first granule that lie before the row
+
+  __device__ Row(const void* logits, int64_t r, int64_t ld, int64_t vocab_)
+      : row(static_cast<const T*>(logits) + r * ld), vocab(int(vocab_)) {
+    skew = int(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+  }
+  __device__ int granules() const { return (skew + vocab + kPer - 1) / kPer; }
+  __device__ int first(int g) const { return g * kPer - skew; }  // index of its first element
+  __device__ bool whole(int g) const { return first(g) >= 0 && first(g) + kPer <= vocab; }
+  __device__ uint4 fetch(int g) const {
+    const int i = first(g);
+    if (i >= 0 && i + kPer <= vocab) return __ldcs(reinterpret_cast<const uint4*>(row + i));
+    alignas(16) T v[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      v[j] = i + j >= 0 && i + j < vocab ? row[i + j] : from_float<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(v);
+  }
+  __device__ static uint4 nothing() {
+    alignas(16) T v[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] = from_float<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(v);
+  }
+  // Granule g of a row of the same pitch whose address is `to`; ALIKE: it lies alike on 16 bytes.
+  __device__ void store(T* to, int g, const uint4& v, bool alike) const {
+    const int i = first(g);
+    if (alike && i >= 0 && i + kPer <= vocab) {
+      __stcs(reinterpret_cast<uint4*>(to + i), v);
+      return;
+    }
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (i + j >= 0 && i + j < vocab) to[i + j] = e[j];
+  }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ float largest_in(const uint4 (&v)[N]) {
+  return largest_of(reinterpret_cast<const T(&)[N * Row<T>::kPer]>(v));
+}
+// +inf as the largest finite value, in place.
+template <typename T, int N>
+__device__ __forceinline__ void make_finite(uint4 (&v)[N]) {
+  T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+  for (int i = 0; i < N * Row<T>::kPer; ++i)
+    if (to_float(e[i]) == INFINITY) e[i] = from_float<T>(largest_finite<T>());
+}
+
+}  // namespace vocab
+}  // namespace rs

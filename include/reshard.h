@@ -766,11 +766,12 @@ reshard_status_t reshard_plan_destroy(reshard_plan_t plan);
  *   reshard_sample         the next token of every request from its logits;
  *   reshard_balance_loss   the router's load-balance loss, the tokens each expert
  *                          got, and the gradient in the router's logits;
- *   reshard_expert_*       the tokens' rows sorted by expert and back.
+ *   reshard_expert_*       the tokens' rows sorted by expert and back;
+ *   reshard_logprob        what logits say of given tokens, and its gradient.
  * All matrices are row-major with a row pitch ("ld") in elements.  All of them follow
  * the conventions above: work is enqueued on `stream`, nothing is synchronised,
  * allocated or kept between calls, every call can be captured into a CUDA graph, and
- * an output must not overlap an input.  A call without rows or columns launches nothing
+ * an output must not overlap an input unless its call says so.  A call without rows or columns launches nothing
  * (the loss of no token is written as 0).
  * Sums do not depend on the order in which the GPU runs: equal inputs give equal bits.
  */
@@ -971,6 +972,51 @@ reshard_status_t reshard_expert_combine_grad(const void* dout, int32_t dtype, in
                                              const int32_t* slot, int64_t nrows, const void* rows,
                                              int64_t ldr, const float* weight, void* drows,
                                              float* dweight, void* stream);
+
+/* Most alternatives of one reshard_logprob, and most teacher's tokens of one reshard_distill_loss. */
+#define RESHARD_MAX_TOP 256
+
+/*
+ * What a row of logits says of a given token.  With l = logits[r], T = temperature[r] (1 where it
+ * is <= 0 or NaN; 1 / T at most the largest float32), m = max l and z_i = (l_i - m) * (1 / T),
+ *   logprob[r]     = z_t - ln(sum_i exp(z_i)), t = target[r]
+ *   entropy[r]     = -sum_i p_i ln p_i, p = softmax(z)
+ *   top_token[r]   = the ntop tokens of the largest logits, the largest first and ties by the lowest
+ *                    index, and top_logprob[r] their log-probabilities.
+ * Logits of -inf, and NaN, have the probability 0 (log-probability -inf) and are no alternatives; +inf
+ * counts as the type's largest finite value.  Differences and results beyond float32's range are
+ * -inf.  Places of top_token without a token get -1, with
+ * log-probability -inf.  A row of -inf and NaN alone has logprob -inf and entropy 0.  A row whose
+ * target is outside 0..vocab - 1 does not count: logprob and entropy 0, no alternatives; with target
+ * NULL every row counts.  What is drawn by reshard_sample at the same temperature has the same
+ * log-probability here, to rounding.
+ *
+ * logits [rows][ld] of dtype BF16, FP16 or FP32 and any alignment; temperature, target [rows] in
+ * device memory, each may be NULL (logprob then is); logprob, entropy [rows], each may be NULL;
+ * top_token, top_logprob [rows][ldtop] where ntop > 0; state [rows][4], 16-byte aligned, or NULL:
+ * what reshard_logprob_grad takes.  Errors: INVALID_ARG (null pointer, dtype, negative size, pitch
+ * too small, misaligned pointer), UNSUPPORTED (vocab > RESHARD_MAX_VOCAB, ntop > RESHARD_MAX_TOP,
+ * 2^28 rows or more), CUDA.
+ */
+reshard_status_t reshard_logprob(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                 int64_t ld, const float* temperature, const int32_t* target,
+                                 float* logprob, float* entropy, int32_t ntop, int32_t* top_token,
+                                 float* top_logprob, int64_t ldtop, float* state, void* stream);
+
+/*
+ * The gradient in the logits from those of reshard_logprob's logprob and entropy (H):
+ *   dlogits[r][i] = (dlogprob[r] * ([i = target[r]] - p_i) - dentropy[r] * p_i * (ln p_i + H)) / T
+ * logits, temperature and target are those of the call that wrote state.  Rows that do not count and
+ * rows without a finite logit get 0, and rows whose gradients are both 0 get 0 without being read.
+ *
+ * dlogits [rows][ld] of dtype: it may be logits itself, else must not overlap it; one that lies
+ * alike on 16 bytes is faster.  dlogprob, dentropy [rows], each may be NULL (0).  Errors: as
+ * reshard_logprob, and UNSUPPORTED for sizes that ask for 2^31 CTAs or more.
+ */
+reshard_status_t reshard_logprob_grad(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                      int64_t ld, const float* temperature, const int32_t* target,
+                                      const float* state, const float* dlogprob, const float* dentropy,
+                                      void* dlogits, void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* reshard_last_error(void);
