@@ -246,6 +246,8 @@ def _load():
                              i64, vp, vp], ctypes.c_int),
         "reshard_logprob_grad": ([vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp],
                                  ctypes.c_int),
+        "reshard_distill_loss": ([vp, ctypes.c_int32, i64, i64, i64, vp, vp, vp, ctypes.c_int32, i64,
+                                  ctypes.c_int32, vp, vp, vp, vp], ctypes.c_int),
         "reshard_last_error": ([], ctypes.c_char_p),
         "reshard_version": ([], ctypes.c_char_p),
     }
@@ -975,3 +977,17 @@ def reshard_logprob_grad(logits, shape, dtype, state, dlogits, target=None, dlog
         _ptr(logits), _dtype(dtype), rows, vocab, vocab if ld is None else ld, _ptr(temperature),
         _ptr(target), _ptr(state), _ptr(dlogprob), _ptr(dentropy), _ptr(dlogits), _stream(stream)),
         "reshard_logprob_grad")
+
+
+def reshard_distill_loss(logits, shape, dtype, top_token, top_logprob, ntop: int, loss=None,
+                         dlogits=None, tail: bool = False, temperature=None, grad=None, ld=None,
+                         ldtop=None, stream=None):
+    """loss [rows] and dlogits (which may be logits itself), each where given: the divergence of
+    logits of ``shape`` (rows, vocab) from a teacher's ntop tokens a row (top_token int32,
+    top_logprob float32, both [rows, ntop]).  tail: the teacher's remaining probability counts as
+    one more outcome; else its list is scaled to 1."""
+    rows, vocab = shape
+    _check(_lib.reshard_distill_loss(
+        _ptr(logits), _dtype(dtype), rows, vocab, vocab if ld is None else ld, _ptr(temperature),
+        _ptr(top_token), _ptr(top_logprob), ntop, ntop if ldtop is None else ldtop, int(bool(tail)),
+        _ptr(grad), _ptr(loss), _ptr(dlogits), _stream(stream)), "reshard_distill_loss")

@@ -767,7 +767,8 @@ reshard_status_t reshard_plan_destroy(reshard_plan_t plan);
  *   reshard_balance_loss   the router's load-balance loss, the tokens each expert
  *                          got, and the gradient in the router's logits;
  *   reshard_expert_*       the tokens' rows sorted by expert and back;
- *   reshard_logprob        what logits say of given tokens, and its gradient.
+ *   reshard_logprob        what logits say of given tokens, and its gradient;
+ *   reshard_distill_loss   the divergence from a teacher's most likely tokens, and its gradient.
  * All matrices are row-major with a row pitch ("ld") in elements.  All of them follow
  * the conventions above: work is enqueued on `stream`, nothing is synchronised,
  * allocated or kept between calls, every call can be captured into a CUDA graph, and
@@ -1017,6 +1018,39 @@ reshard_status_t reshard_logprob_grad(const void* logits, int32_t dtype, int64_t
                                       int64_t ld, const float* temperature, const int32_t* target,
                                       const float* state, const float* dlogprob, const float* dentropy,
                                       void* dlogits, void* stream);
+
+/*
+ * The divergence of a student from a teacher of whom the ntop most likely tokens of each row are
+ * known (as reshard_logprob lists them), and its gradient in the student's logits, in one call.
+ * With p = softmax(logits[r] / T) (reshard_logprob's z and rules for temperature, NaN and infinite
+ * logits) and over the entries j of the row's list, token i_j = top_token[r][j] and y_j =
+ * top_logprob[r][j], already at the temperature wanted,
+ *   tail == 0:  q_j = exp(y_j) / sum_j exp(y_j),   q_R = 0   (y may be logits then)
+ *   tail != 0:  q_j = exp(y_j),   q_R = max(0, 1 - sum_j q_j), the probability of all other tokens,
+ *               p_R the student's (q_R counts as 0 where p_R is 0)
+ *   loss[r]       = sum_j q_j ln(q_j / p_{i_j}) + q_R ln(q_R / p_R)
+ *   dlogits[r][i] = grad[r] * dloss[r] / dlogits[r][i]
+ *                 = grad[r] / T * (p_i - sum_{j: i_j = i} q_j)       for a token of the list
+ *                   grad[r] / T * p_i * (1 - q_R / p_R)              for others
+ * One entry with y = 0 gives the negative log-likelihood of its token.  An entry whose token is
+ * outside 0..vocab - 1, or whose y is NaN, is none; a row without an entry above -inf does not
+ * count: loss and gradient 0.  A token may stand in a list twice: its probabilities add up in the
+ * gradient.  Where the student gives a token that has a teacher's probability none, the loss is
+ * +inf and the gradient is as above; a row of -inf and NaN alone has loss +inf and gradient 0.
+ * The teacher's sums and the loss are held in 64 bits.
+ *
+ * logits [rows][ld] of dtype BF16, FP16 or FP32 and any alignment; temperature [rows] or NULL (1);
+ * top_token, top_logprob [rows][ldtop]; grad [rows] or NULL (1); loss [rows] or NULL; dlogits
+ * [rows][ld] of dtype, or NULL: it may be logits itself, else must not overlap it, and one that
+ * lies alike on 16 bytes is faster.  Errors: INVALID_ARG (null pointer, dtype, negative size,
+ * ntop < 1, pitch too small, misaligned pointer), UNSUPPORTED (vocab > RESHARD_MAX_VOCAB, ntop >
+ * RESHARD_MAX_TOP, 2^28 rows or more), CUDA.
+ */
+reshard_status_t reshard_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                      int64_t ld, const float* temperature, const int32_t* top_token,
+                                      const float* top_logprob, int32_t ntop, int64_t ldtop,
+                                      int32_t tail, const float* grad, float* loss, void* dlogits,
+                                      void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* reshard_last_error(void);

@@ -86,3 +86,49 @@ def logprob_grad(x, t, target, g, h, eps):
                  + abs(h) * p * (np.abs(inner) * (each + 8 * U) + 8 * U * wide + off + Hoff + 6 * U * np.abs(mild)))
     err += 4 * U * inv * abs(g) * p   # A is one sum of both
     return v, err + eps[0] * (np.abs(v) + err) + eps[1]
+
+
+def distill(x, t, token, y, tail, g, eps):
+    """(loss, its bound, gradient, its bound) of one row; loss and gradient 0 for a row that does not
+    count.  The list's part is in 64 bits but for q (4 units where it is scaled to 1); ln S is off by
+    what S is."""
+    V = len(x)
+    ok = [(int(i), float(v)) for i, v in zip(token, y) if 0 <= i < V and not np.isnan(v)]
+    if not any(v > -np.inf for _, v in ok):
+        return 0.0, 0.0, np.zeros(V), np.zeros(V)
+    if x.max() == -np.inf:
+        return np.inf, 0.0, np.zeros(V), np.zeros(V)
+    z, p, normal, off, each = softmax(x, t)
+    ys = np.array([v for _, v in ok])
+    at = np.array([i for i, _ in ok])
+    inside = np.zeros(V, bool)
+    inside[at] = True
+    p_rest = p[~inside].sum()
+    if tail:
+        q, log_q, rest, q_off = np.exp(ys), ys, 0.0, 0.0
+        rest = max(0.0, 1.0 - q.sum()) if p_rest > 0 else 0.0
+    else:
+        log_q = ys - ys.max()
+        log_q = log_q - np.log(np.exp(log_q).sum())
+        # a float32 exponential of a float32 difference
+        q, rest, q_off = np.exp(log_q), 0.0, 8 * U * (2 + np.abs(np.where(ys > -np.inf, ys - ys.max(), 0)).max())
+    with np.errstate(all="ignore"):
+        terms = np.where(q > 0, q * (log_q - (z[at] - normal)), 0.0)
+    loss = terms.sum() + (rest * np.log(rest / p_rest) if rest > 0 else 0.0)
+    mass = q.sum() + rest
+    size = np.where(q > 0, q * (np.abs(np.where(q > 0, log_q, 0)) + np.abs(np.where(np.isfinite(z[at]), z[at], 0))
+                                + normal + 1), 0.0).sum()
+    loss_off = 3 * off * mass + (q * 4 * U * np.abs(np.where(np.isfinite(z[at]), z[at], 0))).sum() + 2 * q_off * size
+    share = rest / p_rest if rest > 0 else 0.0
+    grad = p * (1 - share)
+    grad_off = p * ((each + 8 * U) * abs(1 - share) + share * (2 * off + 8 * U) + 2 * U)
+    for i, v in zip(at, q):
+        if inside[i]:
+            grad[i] = p[i]
+            inside[i] = False
+            grad_off[i] = p[i] * (each[i] + 8 * U)
+        grad[i] -= v
+        grad_off[i] += v * (q_off + 4 * U)
+    f = g * inverse(t)
+    grad, grad_off = grad * f, grad_off * abs(f) + 4 * U * np.abs(grad * f)
+    return loss, loss_off + U * abs(loss), grad, grad_off + eps[0] * (np.abs(grad) + grad_off) + eps[1]
