@@ -4,8 +4,8 @@
 // With q the teacher's probabilities of its listed tokens, q_R what is left of 1 (or 0), p the
 // student's and p_R its probability of all other tokens: loss = sum q_j ln(q_j / p_j) + q_R ln(q_R /
 // p_R), dl = p - q for listed tokens and p (1 - q_R / p_R) for others.  A row needs the sum over its
-// logits before the first gradient, so a cluster of CTAs keeps it in registers between the two: it
-// is read once and written once.
+// logits before the first gradient, so a cluster of CTAs keeps it in shared memory between the two:
+// it is read once and written once.
 #include "vocab_row.cuh"
 
 namespace rs {
@@ -13,9 +13,11 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeld = 8;         // granules that a thread keeps; a slice's others are read again
+constexpr int kVecs = 4;
+constexpr int kRound = kVecs * kThreads;  // granules that a CTA works on at a time
+constexpr int kHeldRounds = 10;           // of a slice, kept in shared memory; others are read again
 constexpr int kMaxCluster = 8;
 constexpr int kListWarps = RESHARD_MAX_TOP / 32;
 
@@ -44,36 +46,52 @@ struct Shared {
   float top, other;                // of the row
   float outside;                   // 1 - q_R / p_R
   double rest, inv_q;              // q_R, 1 / sum of the list
+  uint32_t edges;                  // listed tokens among those at the row's ends, a bit a thread
 };
+
+__device__ __forceinline__ void copy_async(uint4* to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(staging::smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_but(std::integral_constant<int, N>) {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// f(0), f(1), ... f(N - 1), each number known when compiled
+template <int N, typename F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (N > 0) {
+    for_each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
+  }
+}
 
 __device__ __forceinline__ float load_far(const float* at, uint32_t rank) {
   return tc::load_cluster(tc::in_cta(staging::smem_addr(at), rank));
 }
-// (top, other) of two parts as one: a sum is relative to its part's largest logit.
-__device__ __forceinline__ void join(float& top, float& other, float c, int from) {
-  for (int o = from; o; o >>= 1) {
-    const float t = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, other, o);
-    const float both_top = fmaxf(top, t);
-    other = other * exp2_of(exponent(top, both_top, c)) + s * exp2_of(exponent(t, both_top, c));
-    top = both_top;
-  }
+// The largest of the warp's `top`, and the sum of its `other`, each relative to its lane's top.
+__device__ __forceinline__ void join(float& top, float& other, float c) {
+  const float own = top;
+  top = warp_max(top);
+  other = warp_sum(other * exp2_of(exponent(own, top, c)));
 }
 
+// Dynamic shared memory: the held granules, and a byte a granule whose bits say which of its elements
+// are listed.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
-  constexpr int kPer = Row<T>::kPer;
-  extern __shared__ uint32_t listed_bits[];  // of the slice's elements
+__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a, const int held_most) {
+  constexpr int kPer = Slice<T>::kPer;
+  extern __shared__ __align__(16) uint4 held[];
+  uint8_t* listed = reinterpret_cast<uint8_t*>(held + held_most);
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const uint32_t rank = tc::cluster_rank();
   const int64_t r = blockIdx.x / ctas;
-  const Row<T> row(a.logits, r, a.ld, a.vocab);
+  const Slice<T> row(a.logits, r, a.ld, a.vocab, int(rank), int(ctas));
   T* to = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ld : nullptr;
-  const int granules = row.granules();
-  const int g0 = int(int64_t(granules) * rank / ctas), g1 = int(int64_t(granules) * (rank + 1) / ctas);
-  const int elements = (g1 - g0) * kPer;
+  const int edge = rank == 0 ? row.edge() : -1;
   // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none
   const int k = a.ntop, list_warps = (k + 31) / 32;
   int mine = -1;
@@ -84,80 +102,134 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
       y = __ldg(a.top_logprob + r * a.ldtop + tid);
       if (uint32_t(mine) >= uint32_t(row.vocab) || !(y == y)) mine = -1, y = -INFINITY;
     }
-    if (tid < RESHARD_MAX_TOP) sh.token[tid] = mine;
+    sh.token[tid] = mine;
     const float most = warp_max(y);
     if (lane == 0) sh.list_top[warp] = most;
   }
-  for (int i = tid; i <= elements / 32; i += kThreads) listed_bits[i] = 0;
+  for (int i = tid; i < (row.n + 3) / 4; i += kThreads) reinterpret_cast<uint32_t*>(listed)[i] = 0;
+  if (tid == 0) sh.edges = 0;
   __syncthreads();
   float y_top = sh.list_top[0];
   for (int w = 1; w < list_warps; ++w) y_top = fmaxf(y_top, sh.list_top[w]);
+  auto put_zeros = [&] {
+    for (int g = tid; g < row.n; g += kThreads) store_granule(to + row.first + g * kPer, make_uint4(0, 0, 0, 0), a.alike);
+    if (edge >= 0) to[edge] = from_float<T>(0.0f);
+  };
   if (!(y_top > -INFINITY)) {  // a row that does not count
     if (rank == 0 && tid == 0 && a.loss) a.loss[r] = 0.0f;
-    if (to)
-      for (int g = g0 + tid; g < g1; g += kThreads) row.store(to, g, make_uint4(0, 0, 0, 0), a.alike);
+    if (to) put_zeros();
     return;
   }
-  // the slice, on its way while the list is worked on
-  uint4 v[kHeld];
+  // the slice, on its way while the list is worked on; each thread waits for its own granules only
+  const int in_smem = min(row.n, held_most);
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int g = g0 + i * kThreads + tid;
-    v[i] = g < g1 ? row.fetch(g) : Row<T>::nothing();
+  for (int i = 0; i < kHeldRounds; ++i) {
+    if ((i + 1) * kRound <= in_smem) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        const int g = i * kRound + j * kThreads + tid;
+        copy_async(held + g, row.granules() + g);
+      }
+    } else if (i * kRound < in_smem) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        const int g = i * kRound + j * kThreads + tid;
+        if (g < in_smem) copy_async(held + g, row.granules() + g);
+      }
+    }
+    copies_end_group();
   }
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   const uint64_t c2 = both(c);
   float x = -INFINITY;     // the student's logit of this thread's entry
   bool first = mine >= 0;  // of the entries with this token
-  const int place = mine + row.skew - g0 * kPer;
-  const bool here = mine >= 0 && place >= 0 && place < elements;
+  bool here = false;       // the token's gradient is this CTA's
   if (first) {
-    x = clean<T>(to_float(row.row[mine]));
+    x = row.at(mine);
+    const int place = mine - row.first;
+    here = place >= 0 && place < row.n * kPer;
+    const bool at_end = rank == 0 && (mine < row.head || mine >= row.last);
+    if (here) {
+      const int g = place / kPer;
+      atomicOr(reinterpret_cast<uint32_t*>(listed) + g / 4, 1u << (g % 4 * 8 + place % kPer));
+    } else if (at_end) {
+      atomicOr(&sh.edges, 1u << (mine < row.head ? mine : mine - row.last + row.head));
+      here = true;
+    }
     for (int j = 0; j < tid; ++j) first = first && sh.token[j] != mine;
-    if (here) atomicOr(&listed_bits[place / 32], 1u << (place % 32));
   }
+  const float at_edge = edge >= 0 ? row.at(edge) : -INFINITY;
   const bool again = __syncthreads_or(mine >= 0 && !first);  // some token stands there twice
   // the sum over tokens that are not listed, relative to each thread's own largest logit
-  float m = -INFINITY, other = 0.0f;
-  auto add = [&](uint4& granule, int g) {
-    uint4(&one)[1] = reinterpret_cast<uint4(&)[1]>(granule);
-    float largest = largest_in<T>(one);
-    if (largest == INFINITY) {
-      make_finite<T>(one);
-      largest = largest_finite<T>();
-    }
+  float m = at_edge, other = at_edge > -INFINITY && !(sh.edges >> (tid & 31) & 1) ? 1.0f : 0.0f;
+  auto add = [&](uint4(&v)[kVecs], float largest, int g0) {
     const float top = fmaxf(m, largest);
-    const uint64_t minus = both(-top);
-    const int at = (g - g0) * kPer;
-    const uint32_t bits = g < g1 ? listed_bits[at / 32] >> (at % 32) & ((1u << kPer) - 1) : 0;
-    const T* e = reinterpret_cast<const T*>(&granule);
+    const uint64_t minus = both(top > -INFINITY ? -top : 0.0f);
     uint64_t s2 = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      uint64_t w = exp2_both(exponents(pair(pair_of(e + i)), minus, c2));
+    for (int j = 0; j < kVecs; ++j) {
+      const T* e = reinterpret_cast<const T*>(&v[j]);
+      const int g = g0 + j * kThreads;
+      const uint32_t bits = g < row.n ? listed[g] : 0;
+      uint64_t w[kPer / 2];
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) w[i] = exp2_both(mul2(add2(pair(pair_of(e + 2 * i)), minus), c2));
       if (bits) {
-        float2 f = tc::unpack2(w);
-        if (bits >> i & 1) f.x = 0.0f;
-        if (bits >> (i + 1) & 1) f.y = 0.0f;
-        w = pair(f);
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) {
+          const float2 f = tc::unpack2(w[i]);
+          w[i] = pair(make_float2(bits >> (2 * i) & 1 ? 0.0f : f.x, bits >> (2 * i + 1) & 1 ? 0.0f : f.y));
+        }
       }
-      s2 = add2(s2, w);
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) s2 = add2(s2, w[i]);
     }
     other = fmaf(other, exp2_of(exponent(m, top, c)), sum2(s2));
     m = top;
   };
+  for_each<kHeldRounds>([&](auto i) {
+    constexpr int kFirst = decltype(i)::value * kRound;
+    const int g0 = kFirst + tid;
+    if (kFirst >= in_smem) return;
+    wait_but(std::integral_constant<int, kHeldRounds - 1 - decltype(i)::value>());
+    uint4 v[kVecs];
+    if (kFirst + kRound <= in_smem) {
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) add(v[i], g0 + i * kThreads + tid);
-  for (int g = g0 + kHeld * kThreads + tid; g < g1; g += kThreads) {
-    uint4 w = row.fetch(g);
-    add(w, g);
+      for (int j = 0; j < kVecs; ++j) v[j] = held[g0 + j * kThreads];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        v[j] = Slice<T>::nothing();
+        if (g0 + j * kThreads < in_smem) v[j] = held[g0 + j * kThreads];
+      }
+    }
+    float largest = largest_or_nan<T>(v);
+    if (!(largest < INFINITY)) {
+      make_clean<T>(v);
+      largest = largest_in<T>(v);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        if (g0 + j * kThreads < in_smem) held[g0 + j * kThreads] = v[j];
+    }
+    add(v, largest, g0);
+  });
+  auto read_again = [&](uint4(&v)[kVecs], int g0) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      v[j] = g0 + j * kThreads < row.n ? row.granules()[g0 + j * kThreads] : Slice<T>::nothing();
+    if (!(largest_or_nan<T>(v) < INFINITY)) make_clean<T>(v);
+  };
+  for (int g0 = in_smem + tid; g0 - tid < row.n; g0 += kRound) {
+    uint4 v[kVecs];
+    read_again(v, g0);
+    add(v, largest_in<T>(v), g0);
   }
-  join(m, other, c, 16);
+  join(m, other, c);
   if (lane == 0) sh.warp_top[warp] = m, sh.warp_other[warp] = other;
   __syncthreads();
   if (warp == 0) {
     float top = lane < kWarps ? sh.warp_top[lane] : -INFINITY, sum = lane < kWarps ? sh.warp_other[lane] : 0.0f;
-    join(top, sum, c, 16);
+    join(top, sum, c);
     if (lane == 0) sh.part_top = top, sh.part_other = sum;
   }
   if (ctas > 1) tc::cluster_sync();
@@ -169,10 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     float top = -INFINITY;
     other = 0.0f;
     if (lane < int(ctas)) top = load_far(&sh.part_top, lane), other = load_far(&sh.part_other, lane);
-    join(top, other, c, 4);
-    m = top;  // (lanes 0 to 7 have it)
-    m = __shfl_sync(0xffffffffu, m, 0);
-    other = __shfl_sync(0xffffffffu, other, 0);
+    join(top, other, c);
+    m = top;
     const float e = warp_sum(first ? exp2_of(exponent(x, m, c)) : 0.0f);
     if (mine >= 0) q = a.tail ? exp(double(y)) : double(expf(y - y_top));
     double all = q;
@@ -200,30 +270,44 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   }
   __syncthreads();
   if (to && empty) {
-    for (int g = g0 + tid; g < g1; g += kThreads) row.store(to, g, make_uint4(0, 0, 0, 0), a.alike);
+    put_zeros();
   } else if (to) {
     const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
     const float slope = fmaxf(fminf(g * inverse, 3.402823466e38f), -3.402823466e38f);
-    const uint64_t A = both(slope / sum * sh.outside), minus = both(-top);
-    auto put = [&](uint4& granule, int at) {
-      T* e = reinterpret_cast<T*>(&granule);
+    const float scale = fmaxf(fminf(slope / sum * sh.outside, 3.402823466e38f), -3.402823466e38f);
+    const uint64_t A = both(scale), minus = both(-top);
+    T* begin = to + row.first;
+    auto gradient = [&](uint4& v) {
+      T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
       for (int i = 0; i < kPer; i += 2)
-        set_pair(e + i, tc::unpack2(mul2(exp2_both(exponents(pair(pair_of(e + i)), minus, c2)), A)));
-      row.store(to, at, granule, a.alike);
+        set_pair(e + i, tc::unpack2(mul2(exp2_both(mul2(add2(pair(pair_of(e + i)), minus), c2)), A)));
     };
+    auto put = [&](uint4 v, int at) {
+      gradient(v);
+      store_granule(begin + at * kPer, v, a.alike);
+    };
+    int done = 0;
+    if (a.alike) {
+      for (; done + kRound <= in_smem; done += kRound) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int at = g0 + i * kThreads + tid;
-      if (at < g1) put(v[i], at);
+        for (int j = 0; j < kVecs; ++j) {
+          uint4 v = held[done + j * kThreads + tid];
+          gradient(v);
+          __stcs(reinterpret_cast<uint4*>(begin) + done + j * kThreads + tid, v);
+        }
+      }
     }
-    for (int at = g0 + kHeld * kThreads + tid; at < g1; at += kThreads) {
-      uint4 w = row.fetch(at);
-      uint4(&one)[1] = reinterpret_cast<uint4(&)[1]>(w);
-      if (largest_in<T>(one) == INFINITY) make_finite<T>(one);
-      put(w, at);
+    for (int at = done + tid; at < in_smem; at += kThreads) put(held[at], at);
+    for (int at = in_smem + tid; at - tid < row.n; at += kRound) {
+      uint4 v[kVecs];
+      read_again(v, at);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+        if (at + j * kThreads < row.n) put(v[j], at + j * kThreads);
     }
-    // the slice's listed tokens, behind what was just written for them as for others
+    if (edge >= 0) to[edge] = from_float<T>(exp2_of(exponent(at_edge, top, c)) * scale);
+    // the CTA's listed tokens, behind what was just written for them as for others
     __syncthreads();
     if (first && here) {
       double all = q;
@@ -256,17 +340,19 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
 
 template <typename T>
 reshard_status_t launch_distill(const DistillArgs& a, int64_t rows, int dev, int sms, cudaStream_t stream) {
-  // CTAs a row: so many that they hold it; more while SMs would stay without one, and a slice
-  // has 4 KiB or more
-  const int64_t bytes = a.vocab * int64_t(sizeof(T));
+  // CTAs a row: so many that three of them fit an SM; more while SMs would stay without one, and a
+  // slice has 8 KiB or more
+  const int64_t granules = a.vocab * int64_t(sizeof(T)) / 16;
   int ctas = 1;
-  while (ctas < kMaxCluster && (bytes > ctas * int64_t(kHeld * kThreads * 16) ||
-                                (rows * ctas < sms && bytes > ctas * 8192)))
+  while (ctas < kMaxCluster && (granules > ctas * int64_t(4 * kRound) || (rows * ctas < sms && granules > ctas * 512)))
     ctas *= 2;
-  const int64_t slice = cdiv(cdiv(bytes, 16) + 1, ctas) + 1;  // granules
-  const size_t smem = size_t(slice * (16 / int64_t(sizeof(T))) / 32 + 1) * 4;
-  constexpr size_t kMost = RESHARD_MAX_VOCAB / kMaxCluster / 8 + 64;
-  void* args[] = {const_cast<DistillArgs*>(&a)};
+  const int64_t slice = cdiv(granules, ctas);
+  constexpr int64_t kHeldMost = kHeldRounds * kRound;
+  int held = int(slice < kHeldMost ? slice : kHeldMost);
+  const size_t smem = size_t(16 * held) + size_t(cdiv(slice, 4) * 4);
+  constexpr size_t kMost = 16 * kHeldMost + RESHARD_MAX_VOCAB / kMaxCluster / (16 / sizeof(T)) + 16;
+  static_assert(kMost + sizeof(Shared) <= kSmemMost, "shared memory of a CTA");
+  void* args[] = {const_cast<DistillArgs*>(&a), &held};
   return launch<distill_kernel<T>, kMost>("reshard_distill_loss", dev, {rows * ctas, kThreads, smem, ctas, stream},
                                           args);
 }

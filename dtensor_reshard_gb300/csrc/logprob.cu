@@ -12,13 +12,13 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMany = 512, kSome = 256;  // threads of a CTA
 constexpr int kVecs = 4;          // granules that a thread has on their way
 constexpr int kMaxCluster = 8;
-constexpr int kCap = 4096;        // tokens that may be among the most likely, of a CTA
+constexpr int kCap = 1024;        // tokens that may be among the most likely, of a CTA
 constexpr int kFew = 256;         // of which so many are ranked at once
-static_assert(RESHARD_MAX_TOP <= kFew && kCap >= kFew, "lists");
+constexpr int kGroups = 32;       // groups of granules whose largest logits a thread notes
+static_assert(RESHARD_MAX_TOP <= kFew && kCap >= kFew && kCap % kMany == 0, "lists");
 
 struct LogprobArgs {
   const void* logits;
@@ -39,9 +39,10 @@ struct Part {
 };
 struct TopSmem {
   uint32_t key[kCap], index[kCap];
+  uint32_t hit[kCap];              // groups with such tokens
   uint64_t best[RESHARD_MAX_TOP];  // key, then ~index: the largest first
   uint32_t hist[256], count[32];
-  uint32_t n, n2, digit;
+  uint32_t n, n2, digit, hits;
 };
 
 __device__ __forceinline__ uint64_t place_of(uint32_t key, uint32_t index) {
@@ -66,18 +67,53 @@ __device__ __forceinline__ void append(TopSmem& sm, float l, int index) {
   if (at < uint32_t(kCap)) sm.key[at] = key_of(l), sm.index[at] = uint32_t(index);
 }
 
-// The lowest logit of a bucket (of the upper 16 bits of a key) that at least k threads' largest
-// logits reach, so that at least k tokens do; all finite logits reach the lowest.
-__device__ float first_threshold(float largest, int k) {
-  const uint32_t mine = largest > -INFINITY ? key_of(largest + 0.0f) >> 16 : 0;
+// A logit's bucket: the upper 16 bits of its key, 0 for -inf.
+__device__ __forceinline__ uint32_t bucket_of(float l) { return l > -INFINITY ? key_of(l + 0.0f) >> 16 : 0; }
+
+// The largest bucket that at least k threads' buckets reach, so that at least k tokens do; 1, which
+// all finite logits reach, where fewer have one.
+__device__ uint32_t shared_bucket(uint32_t mine, int k) {
   uint32_t bucket = 0;
-#pragma unroll 1
+#pragma unroll
   for (int b = 15; b >= 0; --b)
     if (__syncthreads_count(mine >= (bucket | 1u << b)) >= k) bucket |= 1u << b;
-  return logit_of(max(bucket, 0x80u) << 16);
+  return max(bucket, 1u);
+}
+
+// Lists the tokens that reach the bucket: of the groups that do, which are read again.  Groups are of
+// `per` rounds each.  Returns whether all are listed.
+template <typename T, int kThreads>
+__device__ bool list_reaching(TopSmem& sm, const uint16_t* noted, const Slice<T>& row, int rounds, int per,
+                              uint32_t bucket) {
+  constexpr int kPer = Slice<T>::kPer;
+  const int tid = threadIdx.x;
+  for (int i = 0; i * per < rounds; ++i)
+    if (noted[i * kThreads + tid] >= bucket) {
+      const uint32_t at = atomicAdd(&sm.hits, 1u);
+      if (at < uint32_t(kCap)) sm.hit[at] = uint32_t(i * kThreads + tid);
+    }
+  __syncthreads();
+  const uint32_t hits = sm.hits, granules = uint32_t(per * kVecs);
+  if (hits > uint32_t(kCap)) return false;
+  for (uint32_t w = tid; w < hits * granules; w += kThreads) {
+    const uint32_t h = sm.hit[w / granules], q = w % granules;
+    const int round = int(h / kThreads) * per + int(q / kVecs);
+    const int g = (round * kVecs + int(q % kVecs)) * kThreads + int(h % kThreads);
+    if (round >= rounds || g >= row.n) continue;
+    const uint4 v = __ldg(row.granules() + g);
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float l = clean<T>(to_float(e[j]));
+      if (bucket_of(l) >= bucket) append(sm, l, row.first + g * kPer + j);
+    }
+  }
+  __syncthreads();
+  return sm.n <= uint32_t(kCap);
 }
 
 // Puts the k largest of the n listed tokens (or all, if fewer) in order into sm.best.
+template <int kThreads>
 __device__ void rank_listed(TopSmem& sm, int n, int k) {
   const int tid = threadIdx.x;
   if (n > kFew) {
@@ -118,6 +154,7 @@ __device__ void rank_listed(TopSmem& sm, int n, int k) {
   while (per < 32 && 2 * per * n <= kThreads) per *= 2;
   for (int base = 0; base < n; base += kThreads / per) {
     const int i = base + tid / per;
+    if (base + (tid & ~31) / per >= n) break;  // a warp without any
     const uint64_t own = i < n ? place_of(sm.key[i], sm.index[i]) : 0;
     int before = 0;
     for (int j = tid % per; j < n; j += per) before += place_of(sm.key[j], sm.index[j]) > own;
@@ -127,29 +164,54 @@ __device__ void rank_listed(TopSmem& sm, int n, int k) {
   __syncthreads();
 }
 
-// More tokens reach the threshold than the list holds, as where a row's logits rise: the k-th
-// largest key eight bits at a time, by histograms of the CTA's granules g0 to g1, and then the
-// list anew, of tokens that share that key those of lowest index.
-template <typename T>
-__device__ void list_again(TopSmem& sm, const Row<T>& row, int g0, int g1, int k) {
-  constexpr int kPer = Row<T>::kPer;
+// More tokens reach the bucket than the list holds, as where logits are alike: the k-th largest key
+// eight bits at a time, by histograms of the CTA's tokens, and then the list anew, of tokens that
+// share that key those of lowest index.
+template <typename T, int kThreads>
+__device__ void list_again(TopSmem& sm, const Slice<T>& row, bool edges, int k) {
+  constexpr int kPer = Slice<T>::kPer, kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // The tokens in order, kThreads granules at a time: those before the first granule, the granules,
+  // those behind the last.  f(index of the first, how many, their logits)
+  const int steps = (row.n + kThreads - 1) / kThreads;
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int b = edges ? -1 : 0; b < (edges ? steps + 1 : steps); ++b) {
+      float l[kPer];
+      int index = 0, count = 0;
+      const int g = b * kThreads + tid;
+      if (b < 0 || b == steps) {
+        const int from = b < 0 ? 0 : row.last, to = b < 0 ? row.head : row.vocab;
+        index = from + tid;
+        count = index < to;
+        if (count) l[0] = row.at(index);
+      } else if (g < row.n) {
+        const uint4 v = __ldg(row.granules() + g);
+        const T* e = reinterpret_cast<const T*>(&v);
+        index = row.first + g * kPer;
+        count = kPer;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) l[j] = clean<T>(to_float(e[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j >= count) l[j] = -INFINITY;
+      f(index, l);
+    }
+  };
   uint32_t prefix = 0, need = uint32_t(k);
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
     if (tid < 256) sm.hist[tid] = 0;
     __syncthreads();
-    for (int g = g0 + tid; g < g1; g += kThreads) {
-      const uint4 v = row.fetch(g);
-      const T* e = reinterpret_cast<const T*>(&v);
+    each([&](int, const float(&l)[kPer]) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const float l = clean<T>(to_float(e[j]));
-        const uint32_t key = key_of(l);
-        if (l > -INFINITY && (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)))
+        const uint32_t key = key_of(l[j]);
+        if (l[j] > -INFINITY && (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)))
           atomicAdd(&sm.hist[key >> shift & 255], 1u);
       }
-    }
+    });
     __syncthreads();
     if (tid == 0) {
       uint32_t above = 0;
@@ -165,18 +227,14 @@ __device__ void list_again(TopSmem& sm, const Row<T>& row, int g0, int g1, int k
   }
   if (tid == 0) sm.n = 0;
   __syncthreads();
-  uint32_t ties = 0;  // of the granules before
-  for (int b = g0; b < g1; b += kThreads) {
-    const int g = b + tid;
-    const uint4 v = g < g1 ? row.fetch(g) : Row<T>::nothing();
-    const T* e = reinterpret_cast<const T*>(&v);
+  uint32_t ties = 0;  // of the tokens before
+  each([&](int index, const float(&l)[kPer]) {
     uint32_t mine = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const float l = clean<T>(to_float(e[j]));
-      const uint32_t key = key_of(l);
-      if (!(l > -INFINITY)) continue;
-      if (key > prefix) append(sm, l, row.first(g) + j);
+      const uint32_t key = key_of(l[j]);
+      if (!(l[j] > -INFINITY)) continue;
+      if (key > prefix) append(sm, l[j], index + j);
       mine += key == prefix;
     }
     uint32_t upto = mine;
@@ -193,18 +251,16 @@ __device__ void list_again(TopSmem& sm, const Row<T>& row, int g0, int g1, int k
     }
     if (mine && before < need) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float l = clean<T>(to_float(e[j]));
-        if (l > -INFINITY && key_of(l) == prefix && before++ < need) append(sm, l, row.first(g) + j);
-      }
+      for (int j = 0; j < kPer; ++j)
+        if (l[j] > -INFINITY && key_of(l[j]) == prefix && before++ < need) append(sm, l[j], index + j);
     }
     __syncthreads();
-  }
+  });
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const __grid_constant__ LogprobArgs a) {
-  constexpr int kPer = Row<T>::kPer;
+template <typename T, bool TOP, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+  constexpr int kPer = Slice<T>::kPer, kWarps = kThreads / 32;
   extern __shared__ __align__(16) unsigned char dynamic[];
   TopSmem& sm = *reinterpret_cast<TopSmem*>(dynamic);  // (TOP)
   __shared__ float warp_top[kWarps], warp_s[kWarps], warp_u[kWarps];
@@ -214,9 +270,33 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const __grid_const
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const uint32_t rank = tc::cluster_rank();
   const int64_t r = blockIdx.x / ctas;
-  const Row<T> row(a.logits, r, a.ld, a.vocab);
+  const Slice<T> row(a.logits, r, a.ld, a.vocab, int(rank), int(ctas));
   const int k = a.ntop;
+  // rounds of kVecs granules a thread, the next one's on their way while one is worked on; the first
+  // CTA also has what is left at the row's ends
+  constexpr int kRound = kVecs * kThreads;
+  const int rounds = (row.n + kRound - 1) / kRound;
+  const uint4* from = row.granules() + tid;
+  auto load = [&](uint4(&v)[kVecs], int i) {
+    if (i >= rounds) return;
+    const uint4* p = from + i * kRound;
+    if ((i + 1) * kRound <= row.n) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) v[j] = TOP ? __ldg(p + j * kThreads) : __ldcs(p + j * kThreads);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        v[j] = Slice<T>::nothing();
+        if (i * kRound + j * kThreads + tid < row.n) v[j] = __ldg(p + j * kThreads);
+      }
+    }
+  };
+  uint4 v[kVecs], w[kVecs];
+  load(v, 0);
   const int target = a.target ? __ldg(a.target + r) : 0;
+  const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
+  const int edge = rank == 0 ? row.edge() : -1;
+  const float at_edge = edge >= 0 ? row.at(edge) : -INFINITY;
   if (uint32_t(target) >= uint32_t(row.vocab)) {  // a row that does not count
     if (rank != 0) return;
     if (tid == 0) {
@@ -231,43 +311,26 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const __grid_const
       }
     return;
   }
-  const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   const uint64_t c2 = both(c);
   float chosen = 0.0f;
-  if (rank == 0 && tid == 0 && a.logprob) chosen = to_float(row.row[target]);
-  const int granules = row.granules();
-  const int g0 = int(int64_t(granules) * rank / ctas), g1 = int(int64_t(granules) * (rank + 1) / ctas);
-  // rounds of kVecs granules a thread, a round's spread evenly over the slice: the first tells
-  // what the most likely tokens reach wherever they are
-  const int blocks = (g1 - g0 + kThreads - 1) / kThreads, rounds = (blocks + kVecs - 1) / kVecs;
-  if (TOP && tid == 0) sm.n = 0;
-  float m = -INFINITY, s = 0.0f, u = 0.0f, threshold = 0.0f;
-  for (int i = 0; i < rounds; ++i) {
-    uint4 v[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int g = g0 + (j * rounds + i) * kThreads + tid;
-      v[j] = g < g1 ? row.fetch(g) : Row<T>::nothing();
-    }
-    float largest = largest_in<T>(v);
+  if (rank == 0 && tid == 0 && a.logprob) chosen = row.at(target);
+  uint16_t* noted = reinterpret_cast<uint16_t*>(dynamic + sizeof(TopSmem));  // [groups][kThreads]
+  const int per = (rounds + kGroups - 1) / kGroups;
+  uint32_t group = 0;
+  int in_group = 0;
+  uint16_t* note = noted + tid;
+  if (TOP && tid == 0) sm.n = sm.hits = 0;
+  float m = at_edge, s = at_edge > -INFINITY ? 1.0f : 0.0f, u = 0.0f;
+  auto work = [&](uint4(&g)[kVecs]) {
+    float largest = largest_in<T>(g);
     if (largest == INFINITY) {
-      make_finite<T>(v);
+      make_finite<T>(g);
       largest = largest_finite<T>();
     }
-    if (TOP) {
-      if (i == 0) threshold = first_threshold(largest, k);
-      if (largest >= threshold) {
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          const uint4(&one)[1] = reinterpret_cast<const uint4(&)[1]>(v[j]);
-          if (!(largest_in<T>(one) >= threshold)) continue;
-          const T* e = reinterpret_cast<const T*>(&v[j]);
-          const int at = row.first(g0 + (j * rounds + i) * kThreads + tid);
-#pragma unroll
-          for (int q = 0; q < kPer; ++q)
-            if (to_float(e[q]) >= threshold) append(sm, to_float(e[q]) + 0.0f, at + q);
-        }
-      }
+    if (TOP) {  // what the group has reached so far
+      group = max(group, bucket_of(largest));
+      *note = uint16_t(group);
+      if (++in_group == per) in_group = 0, group = 0, note += kThreads;
     }
     const float top = fmaxf(m, largest);
     const float shift = exponent(m, top, c), factor = exp2_of(shift);
@@ -275,24 +338,31 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const __grid_const
     const uint64_t minus = both(-top);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const T* e = reinterpret_cast<const T*>(&v[j]);
+      const T* e = reinterpret_cast<const T*>(&g[j]);
 #pragma unroll
       for (int q = 0; q < kPer; q += 2) {
-        const uint64_t z = exponents(pair(pair_of(e + q)), minus, c2), w = exp2_both(z);
-        s2 = add2(s2, w);
-        u2 = tc::fma2(w, z, u2);
+        const uint64_t z = exponents(pair(pair_of(e + q)), minus, c2), x = exp2_both(z);
+        s2 = add2(s2, x);
+        u2 = tc::fma2(x, z, u2);
       }
     }
     u = fmaf(fmaf(s, shift, u), factor, sum2(u2));
     s = fmaf(s, factor, sum2(s2));
     m = top;
+  };
+#pragma unroll 1
+  for (int i = 0; i < rounds; i += 2) {
+    load(w, i + 1);
+    work(v);
+    load(v, i + 2);
+    if (i + 1 < rounds) work(w);
   }
   // the CTA's sums
   float top = warp_max(m);
   if (lane == 0) warp_top[warp] = top;
   __syncthreads();
   top = warp_top[0];
-  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_top[w]);
+  for (int i = 1; i < kWarps; ++i) top = fmaxf(top, warp_top[i]);
   {
     const float shift = exponent(m, top, c), factor = exp2_of(shift);
     u = warp_sum(fmaf(s, shift, u) * factor);
@@ -300,15 +370,17 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const __grid_const
     if (lane == 0) warp_s[warp] = s, warp_u[warp] = u;
   }
   if (TOP) {
-    __syncthreads();
-    if (sm.n > uint32_t(kCap)) list_again(sm, row, g0, g1, k);
-    rank_listed(sm, int(sm.n), k);
+    const uint32_t bucket = shared_bucket(bucket_of(m), k);
+    if (bucket_of(at_edge) >= bucket) append(sm, at_edge, edge);
+    if (!list_reaching<T, kThreads>(sm, noted, row, rounds, per, bucket))
+      list_again<T, kThreads>(sm, row, rank == 0, k);
+    rank_listed<kThreads>(sm, int(sm.n), k);
   } else {
     __syncthreads();
   }
   if (tid == 0) {
     s = warp_s[0], u = warp_u[0];
-    for (int w = 1; w < kWarps; ++w) s += warp_s[w], u += warp_u[w];
+    for (int i = 1; i < kWarps; ++i) s += warp_s[i], u += warp_u[i];
     part = {top, s, u, TOP ? min(sm.n, uint32_t(k)) : 0};
   }
   __syncthreads();
@@ -331,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_kernel(const __grid_const
   if (rank == 0 && tid == 0) {
     const float entropy = empty ? 0.0f : fmaxf(normal - u / s * kLn2, 0.0f);
     if (a.logprob) {
-      const float l = clean<T>(chosen);
+      const float l = chosen;
       a.logprob[r] = empty || l == -INFINITY ? -INFINITY : (l == top ? 0.0f : (l - top) * inverse) - normal;
     }
     if (a.entropy) a.entropy[r] = entropy;
@@ -392,12 +464,15 @@ constexpr int kGradVecs = 4;
 // dl = g / T (1[target] - p) - h / T p (ln p + H), p = e^z / S: e^z times (A + B z).
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid_constant__ GradArgs a) {
-  constexpr int kPer = Row<T>::kPer;
+  constexpr int kPer = Slice<T>::kPer;
+  constexpr int kRound = kGradThreads * kGradVecs;
   const int64_t r = blockIdx.x / a.chunks;
-  const int chunk = int(blockIdx.x % a.chunks);
-  const Row<T> row(a.logits, r, a.ld, a.vocab);
+  const int chunk = int(blockIdx.x % a.chunks), tid = int(threadIdx.x);
+  const Slice<T> row(a.logits, r, a.ld, a.vocab, 0, 1);
   T* to = static_cast<T*>(a.dlogits) + r * a.ld;
-  const int first = chunk * kGradThreads * kGradVecs + int(threadIdx.x), granules = row.granules();
+  const int g0 = chunk * kRound + tid;
+  const bool full = (chunk + 1) * kRound <= row.n;
+  const int edge = chunk == 0 ? row.edge() : -1;
   const int target = a.target ? __ldg(a.target + r) : -1;
   const float4 state = __ldg(a.state + r);  // largest logit, 1 / S, ln S, entropy
   float g = a.dlogprob && a.target ? __ldg(a.dlogprob + r) : 0.0f, h = a.dentropy ? __ldg(a.dentropy + r) : 0.0f;
@@ -405,56 +480,74 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid
   if (g == 0.0f && h == 0.0f) {
 #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
-      const int at = first + i * kGradThreads;
-      if (at < granules) row.store(to, at, make_uint4(0, 0, 0, 0), a.alike);
+      const int at = g0 + i * kGradThreads;
+      if (at < row.n) store_granule(to + row.first + at * kPer, make_uint4(0, 0, 0, 0), a.alike);
     }
+    if (edge >= 0) to[edge] = from_float<T>(0.0f);
     return;
   }
   uint4 v[kGradVecs];
+  const uint4* from = row.granules() + g0;
 #pragma unroll
-  for (int i = 0; i < kGradVecs; ++i) {
-    const int at = first + i * kGradThreads;
-    v[i] = at < granules ? row.fetch(at) : Row<T>::nothing();
-  }
+  for (int i = 0; i < kGradVecs; ++i)
+    v[i] = full || g0 + i * kGradThreads < row.n ? __ldcs(from + i * kGradThreads) : Slice<T>::nothing();
+  const float at_edge = edge >= 0 ? row.at(edge) : 0.0f;
   if (largest_in<T>(v) == INFINITY) make_finite<T>(v);
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   // (finite, so that 0 times one is 0)
   auto finite = [](float x) { return fmaxf(fminf(x, 3.402823466e38f), -3.402823466e38f); };
   const float slope = finite(inverse * state.y), onehot = finite(g * inverse);
-  const uint64_t B = both(finite(-h * slope) * kLn2);
-  const uint64_t A = both(finite(-(g + h * (state.w - state.z)) * slope));
-  const uint64_t minus = both(-state.x), c2 = both(c);
+  const float a0 = finite(-(g + h * (state.w - state.z)) * slope), b0 = finite(-h * slope) * kLn2;
+  auto one = [&](float l) {
+    const float z = exponent(l, state.x, c);
+    return exp2_of(z) * fmaf(z, b0, a0);
+  };
+  const uint64_t A = both(a0), B = both(b0), minus = both(-state.x), c2 = both(c);
 #pragma unroll
   for (int i = 0; i < kGradVecs; ++i) {
-    const int at = first + i * kGradThreads;
-    if (at >= granules) break;
+    const int at = g0 + i * kGradThreads;
+    if (!full && at >= row.n) break;
     T* e = reinterpret_cast<T*>(&v[i]);
-    const int of_target = target - row.first(at);
+    const int index = row.first + at * kPer, of_target = target - index;
+    float chosen = 0.0f;
+    if (uint32_t(of_target) < uint32_t(kPer)) chosen = one(row.at(target)) + onehot;
 #pragma unroll
     for (int q = 0; q < kPer; q += 2) {
       const uint64_t z = exponents(pair(pair_of(e + q)), minus, c2), w = exp2_both(z);
-      float2 d = tc::unpack2(mul2(w, tc::fma2(z, B, A)));
-      if (of_target == q) d.x += onehot;
-      if (of_target == q + 1) d.y += onehot;
-      set_pair(e + q, d);
+      set_pair(e + q, tc::unpack2(mul2(w, tc::fma2(z, B, A))));
     }
-    row.store(to, at, v[i], a.alike);
+    if (uint32_t(of_target) < uint32_t(kPer)) {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q)
+        if (of_target == q) e[q] = from_float<T>(chosen);
+    }
+    store_granule(to + index, v[i], a.alike);
   }
+  if (edge >= 0) to[edge] = from_float<T>(one(at_edge) + (edge == target ? onehot : 0.0f));
 }
 
 // ---------------------------------------------------------------------------- launches
+template <typename T, bool TOP, int kThreads>
+reshard_status_t launch_threads(const LogprobArgs& a, int64_t rows, int ctas, int dev, cudaStream_t stream) {
+  const int64_t granules = a.vocab * int64_t(sizeof(T)) / 16;
+  const int64_t rounds = cdiv(cdiv(granules, ctas), kVecs * kThreads);
+  const size_t smem = sizeof(TopSmem) + size_t(2 * kThreads * (rounds < kGroups ? rounds : kGroups));
+  void* args[] = {const_cast<LogprobArgs*>(&a)};
+  return launch<logprob_kernel<T, TOP, kThreads>, TOP ? sizeof(TopSmem) + 2 * kThreads * kGroups : 0>(
+      "reshard_logprob", dev, {rows * ctas, kThreads, TOP ? smem : 0, ctas, stream}, args);
+}
+
 template <typename T>
 reshard_status_t launch_logprob(const LogprobArgs& a, int64_t rows, int dev, int sms, cudaStream_t stream) {
   // CTAs a row: more than one while SMs would stay without one, and a slice has 4 KiB or more
   const int64_t bytes = a.vocab * int64_t(sizeof(T));
   int ctas = 1;
   while (ctas < kMaxCluster && rows * ctas < sms && bytes > ctas * 8192) ctas *= 2;
-  void* args[] = {const_cast<LogprobArgs*>(&a)};
-  const char* what = "reshard_logprob";
-  if (a.ntop > 0)
-    return launch<logprob_kernel<T, true>, sizeof(TopSmem)>(
-        what, dev, {rows * ctas, kThreads, sizeof(TopSmem), ctas, stream}, args);
-  return launch<logprob_kernel<T, false>, 0>(what, dev, {rows * ctas, kThreads, 0, ctas, stream}, args);
+  if (a.ntop == 0) return launch_threads<T, false, kSome>(a, rows, ctas, dev, stream);
+  // the most likely tokens are told apart from the others by the threads' largest logits: with
+  // twice as many threads as tokens wanted, few others reach the last of those
+  return a.ntop <= kSome / 2 ? launch_threads<T, true, kSome>(a, rows, ctas, dev, stream)
+                             : launch_threads<T, true, kMany>(a, rows, ctas, dev, stream);
 }
 
 constexpr int64_t kMostRows = int64_t(1) << 28;
@@ -526,10 +619,9 @@ extern "C" reshard_status_t reshard_logprob_grad(const void* logits, int32_t dty
                     (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(dlogits)) % 16 == 0};
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    // (a row that starts inside a granule may end in one more)
-    const bool inside = !rs::op::aligned(logits, 16) || ld * size % 16 != 0;
-    a.chunks = int32_t(rs::op::cdiv(rs::op::cdiv(vocab, rs::vocab::Row<T>::kPer) + inside,
-                                    rs::kGradThreads * rs::kGradVecs));
+    // (one at least, which has what lies at the row's ends)
+    const int64_t chunks = rs::op::cdiv(vocab / rs::vocab::Slice<T>::kPer, rs::kGradThreads * rs::kGradVecs);
+    a.chunks = int32_t(chunks > 1 ? chunks : 1);
     const int64_t grid = rows * a.chunks;
     if (grid >= int64_t(1) << 31) return fail(RESHARD_ERR_UNSUPPORTED, "2^31 pieces of rows or more");
     rs::logprob_grad_kernel<T><<<unsigned(grid), rs::kGradThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);

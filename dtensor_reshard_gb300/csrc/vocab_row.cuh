@@ -1,7 +1,8 @@
 // vocab_row.cuh -- a row of logits as logprob.cu and distill.cu take it: granules of 16 aligned
-// bytes at any alignment of the row, exponentials relative to a maximum two at a time, and a
-// gradient's granules on their way out.
+// bytes at any alignment of the row, and exponentials relative to a maximum two at a time.
 #pragma once
+
+#include <type_traits>
 
 #include "operators.cuh"
 #include "tensor_core.cuh"
@@ -99,61 +100,92 @@ __device__ __forceinline__ void set_pair(__half* to, float2 x) {
   *reinterpret_cast<__half2*>(to) = __float22half2_rn(x);
 }
 
-// A row in granules of 16 aligned bytes.  What lies outside the row in the first and the last
-// granule is neither read nor written; it reads as -inf.
+// A CTA's slice of a row: granules of 16 aligned bytes, and what is left of the row at both ends,
+// fewer elements than a granule has, one a thread.
 template <typename T>
-struct Row {
+struct Slice {
   static constexpr int kPer = 16 / int(sizeof(T));
   const T* row;
-  int vocab, skew;  // elements of the first granule that lie before the row
+  int vocab;
+  int head, last;  // elements before the row's first granule; the first one behind its last
+  int first;       // index of the slice's first element
+  int n;           // granules of the slice
 
-  __device__ Row(const void* logits, int64_t r, int64_t ld, int64_t vocab_)
+  __device__ Slice(const void* logits, int64_t r, int64_t ld, int64_t vocab_, int part, int parts)
       : row(static_cast<const T*>(logits) + r * ld), vocab(int(vocab_)) {
-    skew = int(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+    head = min(vocab, int((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(T)));
+    const int granules = (vocab - head) / kPer;
+    last = head + granules * kPer;
+    const int a = int(int64_t(granules) * part / parts);
+    first = head + a * kPer;
+    n = int(int64_t(granules) * (part + 1) / parts) - a;
   }
-  __device__ int granules() const { return (skew + vocab + kPer - 1) / kPer; }
-  __device__ int first(int g) const { return g * kPer - skew; }  // index of its first element
-  __device__ bool whole(int g) const { return first(g) >= 0 && first(g) + kPer <= vocab; }
-  __device__ uint4 fetch(int g) const {
-    const int i = first(g);
-    if (i >= 0 && i + kPer <= vocab) return __ldcs(reinterpret_cast<const uint4*>(row + i));
-    alignas(16) T v[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      v[j] = i + j >= 0 && i + j < vocab ? row[i + j] : from_float<T>(-INFINITY);
-    return *reinterpret_cast<const uint4*>(v);
+  __device__ const uint4* granules() const { return reinterpret_cast<const uint4*>(row + first); }
+  // The element at the row's ends that is this thread's, or -1.
+  __device__ int edge() const {
+    const int i = int(threadIdx.x) < head ? int(threadIdx.x) : int(threadIdx.x) - head + last;
+    return i < vocab ? i : -1;
   }
+  __device__ float at(int i) const { return clean<T>(to_float(row[i])); }
   __device__ static uint4 nothing() {
     alignas(16) T v[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) v[j] = from_float<T>(-INFINITY);
     return *reinterpret_cast<const uint4*>(v);
   }
-  // Granule g of a row of the same pitch whose address is `to`; ALIKE: it lies alike on 16 bytes.
-  __device__ void store(T* to, int g, const uint4& v, bool alike) const {
-    const int i = first(g);
-    if (alike && i >= 0 && i + kPer <= vocab) {
-      __stcs(reinterpret_cast<uint4*>(to + i), v);
-      return;
-    }
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (i + j >= 0 && i + j < vocab) to[i + j] = e[j];
-  }
 };
 
+// A granule to a row whose elements lie at `to`; ALIKE: on 16 bytes as those it was made of.
+template <typename T>
+__device__ __forceinline__ void store_granule(T* to, const uint4& v, bool alike) {
+  if (alike) {
+    __stcs(reinterpret_cast<uint4*>(to), v);
+    return;
+  }
+  const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+  for (int j = 0; j < Slice<T>::kPer; ++j) to[j] = e[j];
+}
+
+// The largest value of some granules: a NaN loses against any number, or (_or_nan) wins.
 template <typename T, int N>
 __device__ __forceinline__ float largest_in(const uint4 (&v)[N]) {
-  return largest_of(reinterpret_cast<const T(&)[N * Row<T>::kPer]>(v));
+  return largest_of(reinterpret_cast<const T(&)[N * Slice<T>::kPer]>(v));
 }
 // +inf as the largest finite value, in place.
 template <typename T, int N>
 __device__ __forceinline__ void make_finite(uint4 (&v)[N]) {
   T* e = reinterpret_cast<T*>(v);
 #pragma unroll
-  for (int i = 0; i < N * Row<T>::kPer; ++i)
+  for (int i = 0; i < N * Slice<T>::kPer; ++i)
     if (to_float(e[i]) == INFINITY) e[i] = from_float<T>(largest_finite<T>());
+}
+
+template <typename T, int N>
+__device__ __forceinline__ float largest_or_nan(const uint4 (&v)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    const float* e = reinterpret_cast<const float*>(v);
+    float m = e[0];
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(e[i]));
+    return m;
+  } else {
+    using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const P* e = reinterpret_cast<const P*>(v);
+    P m = e[0];
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i) m = __hmax2_nan(m, e[i]);
+    float f = to_float(m.x);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(f) : "f"(to_float(m.y)));
+    return f;
+  }
+}
+// NaN as -inf and +inf as the largest finite value, in place.
+template <typename T, int N>
+__device__ __forceinline__ void make_clean(uint4 (&v)[N]) {
+  T* e = reinterpret_cast<T*>(v);
+#pragma unroll
+  for (int i = 0; i < N * Slice<T>::kPer; ++i) e[i] = from_float<T>(clean<T>(to_float(e[i])));
 }
 
 }  // namespace vocab
