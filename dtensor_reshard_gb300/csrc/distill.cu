@@ -4,8 +4,8 @@
 // With q the teacher's probabilities of its listed tokens, q_R what is left of 1 (or 0), p the
 // student's and p_R its probability of all other tokens: loss = sum q_j ln(q_j / p_j) + q_R ln(q_R /
 // p_R), dl = p - q for listed tokens and p (1 - q_R / p_R) for others.  A row needs the sum over its
-// logits before the first gradient, so a cluster of CTAs keeps it in shared memory between the two:
-// it is read once and written once.
+// logits before the first gradient: it is read twice, the second time from the L2 cache, which holds
+// the rows that are on the SMs.
 #include "vocab_row.cuh"
 
 namespace rs {
@@ -13,11 +13,11 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;
-constexpr int kRound = kVecs * kThreads;  // granules that a CTA works on at a time
-constexpr int kHeldRounds = 10;           // of a slice, kept in shared memory; others are read again
+constexpr int kVecs = 4;                  // granules that a thread has on their way
+constexpr int kRound = kVecs * kThreads;
+constexpr int kMarked = 64 * 1024;        // granules of a slice whose listed elements can be marked
 constexpr int kMaxCluster = 8;
 constexpr int kListWarps = RESHARD_MAX_TOP / 32;
 
@@ -49,23 +49,6 @@ struct Shared {
   uint32_t edges;                  // listed tokens among those at the row's ends, a bit a thread
 };
 
-__device__ __forceinline__ void copy_async(uint4* to, const uint4* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(staging::smem_addr(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_but(std::integral_constant<int, N>) {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// f(0), f(1), ... f(N - 1), each number known when compiled
-template <int N, typename F>
-__device__ __forceinline__ void for_each(F&& f) {
-  if constexpr (N > 0) {
-    for_each<N - 1>(f);
-    f(std::integral_constant<int, N - 1>());
-  }
-}
-
 __device__ __forceinline__ float load_far(const float* at, uint32_t rank) {
   return tc::load_cluster(tc::in_cta(staging::smem_addr(at), rank));
 }
@@ -76,13 +59,12 @@ __device__ __forceinline__ void join(float& top, float& other, float c) {
   other = warp_sum(other * exp2_of(exponent(own, top, c)));
 }
 
-// Dynamic shared memory: the held granules, and a byte a granule whose bits say which of its elements
-// are listed.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a, const int held_most) {
+// Dynamic shared memory (TAIL): a byte a granule whose bits say which of its elements are listed.
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kPer = Slice<T>::kPer;
-  extern __shared__ __align__(16) uint4 held[];
-  uint8_t* listed = reinterpret_cast<uint8_t*>(held + held_most);
+  extern __shared__ uint32_t marks[];
+  const uint8_t* listed = reinterpret_cast<const uint8_t*>(marks);
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t ctas;
@@ -92,6 +74,34 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
   const Slice<T> row(a.logits, r, a.ld, a.vocab, int(rank), int(ctas));
   T* to = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ld : nullptr;
   const int edge = rank == 0 ? row.edge() : -1;
+  // rounds of kVecs granules a thread, the next one's on their way while one is worked on
+  const int rounds = (row.n + kRound - 1) / kRound;
+  const uint4* from = row.granules() + tid;
+  auto load = [&](uint4(&v)[kVecs], int i) {
+    if (i >= rounds) return;
+    const uint4* p = from + i * kRound;
+    if ((i + 1) * kRound <= row.n) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) v[j] = p[j * kThreads];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        v[j] = Slice<T>::nothing();
+        if (i * kRound + j * kThreads + tid < row.n) v[j] = p[j * kThreads];
+      }
+    }
+  };
+  auto each_round = [&](auto&& work) {
+    uint4 v[kVecs], w[kVecs];
+    load(v, 0);
+#pragma unroll 1
+    for (int i = 0; i < rounds; i += 2) {
+      load(w, i + 1);
+      work(v, i);
+      load(v, i + 2);
+      if (i + 1 < rounds) work(w, i + 1);
+    }
+  };
   // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none
   const int k = a.ntop, list_warps = (k + 31) / 32;
   int mine = -1;
@@ -106,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     const float most = warp_max(y);
     if (lane == 0) sh.list_top[warp] = most;
   }
-  for (int i = tid; i < (row.n + 3) / 4; i += kThreads) reinterpret_cast<uint32_t*>(listed)[i] = 0;
+  if (TAIL)
+    for (int i = tid; i < (row.n + 3) / 4; i += kThreads) marks[i] = 0;
   if (tid == 0) sh.edges = 0;
   __syncthreads();
   float y_top = sh.list_top[0];
@@ -120,25 +131,6 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     if (to) put_zeros();
     return;
   }
-  // the slice, on its way while the list is worked on; each thread waits for its own granules only
-  const int in_smem = min(row.n, held_most);
-#pragma unroll
-  for (int i = 0; i < kHeldRounds; ++i) {
-    if ((i + 1) * kRound <= in_smem) {
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const int g = i * kRound + j * kThreads + tid;
-        copy_async(held + g, row.granules() + g);
-      }
-    } else if (i * kRound < in_smem) {
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const int g = i * kRound + j * kThreads + tid;
-        if (g < in_smem) copy_async(held + g, row.granules() + g);
-      }
-    }
-    copies_end_group();
-  }
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   const uint64_t c2 = both(c);
   float x = -INFINITY;     // the student's logit of this thread's entry
@@ -149,36 +141,47 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     const int place = mine - row.first;
     here = place >= 0 && place < row.n * kPer;
     const bool at_end = rank == 0 && (mine < row.head || mine >= row.last);
-    if (here) {
+    if (TAIL && here) {
       const int g = place / kPer;
-      atomicOr(reinterpret_cast<uint32_t*>(listed) + g / 4, 1u << (g % 4 * 8 + place % kPer));
-    } else if (at_end) {
-      atomicOr(&sh.edges, 1u << (mine < row.head ? mine : mine - row.last + row.head));
+      atomicOr(&marks[g / 4], 1u << (g % 4 * 8 + place % kPer));
+    }
+    if (at_end) {
+      if (TAIL) atomicOr(&sh.edges, 1u << (mine < row.head ? mine : mine - row.last + row.head));
       here = true;
     }
     for (int j = 0; j < tid; ++j) first = first && sh.token[j] != mine;
   }
   const float at_edge = edge >= 0 ? row.at(edge) : -INFINITY;
   const bool again = __syncthreads_or(mine >= 0 && !first);  // some token stands there twice
-  // the sum over tokens that are not listed, relative to each thread's own largest logit
-  float m = at_edge, other = at_edge > -INFINITY && !(sh.edges >> (tid & 31) & 1) ? 1.0f : 0.0f;
-  auto add = [&](uint4(&v)[kVecs], float largest, int g0) {
+  // the sum over all tokens, or (TAIL) those that are not listed, relative to each thread's own
+  // largest logit
+  float m = at_edge, other = at_edge > -INFINITY && !(TAIL && sh.edges >> (tid & 31) & 1) ? 1.0f : 0.0f;
+  bool unclean = false;
+  each_round([&](uint4(&v)[kVecs], int round) {
+    float largest = largest_or_nan<T>(v);
+    if (!(largest < INFINITY)) {
+      unclean = true;
+      make_clean<T>(v);
+      largest = largest_in<T>(v);
+    }
     const float top = fmaxf(m, largest);
     const uint64_t minus = both(top > -INFINITY ? -top : 0.0f);
     uint64_t s2 = 0;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const T* e = reinterpret_cast<const T*>(&v[j]);
-      const int g = g0 + j * kThreads;
-      const uint32_t bits = g < row.n ? listed[g] : 0;
       uint64_t w[kPer / 2];
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) w[i] = exp2_both(mul2(add2(pair(pair_of(e + 2 * i)), minus), c2));
-      if (bits) {
+      if (TAIL) {
+        const int g = round * kRound + j * kThreads + tid;
+        const uint32_t bits = g < row.n ? listed[g] : 0;
+        if (bits) {
 #pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) {
-          const float2 f = tc::unpack2(w[i]);
-          w[i] = pair(make_float2(bits >> (2 * i) & 1 ? 0.0f : f.x, bits >> (2 * i + 1) & 1 ? 0.0f : f.y));
+          for (int i = 0; i < kPer / 2; ++i) {
+            const float2 f = tc::unpack2(w[i]);
+            w[i] = pair(make_float2(bits >> (2 * i) & 1 ? 0.0f : f.x, bits >> (2 * i + 1) & 1 ? 0.0f : f.y));
+          }
         }
       }
 #pragma unroll
@@ -186,44 +189,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     }
     other = fmaf(other, exp2_of(exponent(m, top, c)), sum2(s2));
     m = top;
-  };
-  for_each<kHeldRounds>([&](auto i) {
-    constexpr int kFirst = decltype(i)::value * kRound;
-    const int g0 = kFirst + tid;
-    if (kFirst >= in_smem) return;
-    wait_but(std::integral_constant<int, kHeldRounds - 1 - decltype(i)::value>());
-    uint4 v[kVecs];
-    if (kFirst + kRound <= in_smem) {
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) v[j] = held[g0 + j * kThreads];
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        v[j] = Slice<T>::nothing();
-        if (g0 + j * kThreads < in_smem) v[j] = held[g0 + j * kThreads];
-      }
-    }
-    float largest = largest_or_nan<T>(v);
-    if (!(largest < INFINITY)) {
-      make_clean<T>(v);
-      largest = largest_in<T>(v);
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j)
-        if (g0 + j * kThreads < in_smem) held[g0 + j * kThreads] = v[j];
-    }
-    add(v, largest, g0);
   });
-  auto read_again = [&](uint4(&v)[kVecs], int g0) {
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-      v[j] = g0 + j * kThreads < row.n ? row.granules()[g0 + j * kThreads] : Slice<T>::nothing();
-    if (!(largest_or_nan<T>(v) < INFINITY)) make_clean<T>(v);
-  };
-  for (int g0 = in_smem + tid; g0 - tid < row.n; g0 += kRound) {
-    uint4 v[kVecs];
-    read_again(v, g0);
-    add(v, largest_in<T>(v), g0);
-  }
   join(m, other, c);
   if (lane == 0) sh.warp_top[warp] = m, sh.warp_other[warp] = other;
   __syncthreads();
@@ -243,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     if (lane < int(ctas)) top = load_far(&sh.part_top, lane), other = load_far(&sh.part_other, lane);
     join(top, other, c);
     m = top;
-    const float e = warp_sum(first ? exp2_of(exponent(x, m, c)) : 0.0f);
-    if (mine >= 0) q = a.tail ? exp(double(y)) : double(expf(y - y_top));
+    const float e = TAIL ? warp_sum(first ? exp2_of(exponent(x, m, c)) : 0.0f) : 0.0f;
+    if (mine >= 0) q = TAIL ? exp(double(y)) : double(expf(y - y_top));
     double all = q;
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     sh.q[tid] = q;
@@ -262,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
   if (tid == 0) {
     double all = sh.list_q[0];
     for (int w = 1; w < list_warps; ++w) all += sh.list_q[w];
-    sh.rest = 0.0, sh.outside = 1.0f, sh.inv_q = a.tail ? 1.0 : 1.0 / all;
-    if (a.tail && all < 1.0 && sh.other > 0.0f) {  // (else it has nowhere to be)
+    sh.rest = 0.0, sh.outside = 1.0f, sh.inv_q = TAIL ? 1.0 : 1.0 / all;
+    if (TAIL && all < 1.0 && sh.other > 0.0f) {  // (else it has nowhere to be)
       sh.rest = 1.0 - all;
       sh.outside = float(1.0 - sh.rest * (double(sum) / double(sh.other)));
     }
@@ -277,35 +243,25 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     const float scale = fmaxf(fminf(slope / sum * sh.outside, 3.402823466e38f), -3.402823466e38f);
     const uint64_t A = both(scale), minus = both(-top);
     T* begin = to + row.first;
-    auto gradient = [&](uint4& v) {
-      T* e = reinterpret_cast<T*>(&v);
+    each_round([&](uint4(&v)[kVecs], int round) {
+      if (unclean) make_clean<T>(v);
+      T* e = reinterpret_cast<T*>(v);
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2)
+      for (int i = 0; i < kVecs * kPer; i += 2)
         set_pair(e + i, tc::unpack2(mul2(exp2_both(mul2(add2(pair(pair_of(e + i)), minus), c2)), A)));
-    };
-    auto put = [&](uint4 v, int at) {
-      gradient(v);
-      store_granule(begin + at * kPer, v, a.alike);
-    };
-    int done = 0;
-    if (a.alike) {
-      for (; done + kRound <= in_smem; done += kRound) {
+      const int g0 = round * kRound + tid;
+      if (a.alike && (round + 1) * kRound <= row.n) {
+        uint4* p = reinterpret_cast<uint4*>(begin) + g0;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) __stcs(p + j * kThreads, v[j]);
+      } else {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-          uint4 v = held[done + j * kThreads + tid];
-          gradient(v);
-          __stcs(reinterpret_cast<uint4*>(begin) + done + j * kThreads + tid, v);
+          const int g = g0 + j * kThreads;
+          if (g < row.n) store_granule(begin + g * kPer, v[j], a.alike);
         }
       }
-    }
-    for (int at = done + tid; at < in_smem; at += kThreads) put(held[at], at);
-    for (int at = in_smem + tid; at - tid < row.n; at += kRound) {
-      uint4 v[kVecs];
-      read_again(v, at);
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j)
-        if (at + j * kThreads < row.n) put(v[j], at + j * kThreads);
-    }
+    });
     if (edge >= 0) to[edge] = from_float<T>(exp2_of(exponent(at_edge, top, c)) * scale);
     // the CTA's listed tokens, behind what was just written for them as for others
     __syncthreads();
@@ -323,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     q *= sh.inv_q;
     if (!(q <= 0.0)) {
       const double z = x == top ? 0.0 : double(x - top) * double(inverse);
-      term = q * ((double(y) - z) + (a.tail ? 0.0 : log(sh.inv_q) - double(y_top)) + log(double(sum)));
+      term = q * ((double(y) - z) + (TAIL ? 0.0 : log(sh.inv_q) - double(y_top)) + log(double(sum)));
     }
     for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
     if (lane == 0) sh.list_q[warp] = term;
@@ -340,21 +296,18 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
 
 template <typename T>
 reshard_status_t launch_distill(const DistillArgs& a, int64_t rows, int dev, int sms, cudaStream_t stream) {
-  // CTAs a row: so many that three of them fit an SM; more while SMs would stay without one, and a
-  // slice has 8 KiB or more
+  // CTAs a row: more than one while SMs would stay without one, and a slice has 8 KiB or more; or
+  // where one could not mark its elements
   const int64_t granules = a.vocab * int64_t(sizeof(T)) / 16;
   int ctas = 1;
-  while (ctas < kMaxCluster && (granules > ctas * int64_t(4 * kRound) || (rows * ctas < sms && granules > ctas * 512)))
+  while (ctas < kMaxCluster && (granules > ctas * int64_t(kMarked) || (rows * ctas < sms && granules > ctas * 512)))
     ctas *= 2;
-  const int64_t slice = cdiv(granules, ctas);
-  constexpr int64_t kHeldMost = kHeldRounds * kRound;
-  int held = int(slice < kHeldMost ? slice : kHeldMost);
-  const size_t smem = size_t(16 * held) + size_t(cdiv(slice, 4) * 4);
-  constexpr size_t kMost = 16 * kHeldMost + RESHARD_MAX_VOCAB / kMaxCluster / (16 / sizeof(T)) + 16;
-  static_assert(kMost + sizeof(Shared) <= kSmemMost, "shared memory of a CTA");
-  void* args[] = {const_cast<DistillArgs*>(&a), &held};
-  return launch<distill_kernel<T>, kMost>("reshard_distill_loss", dev, {rows * ctas, kThreads, smem, ctas, stream},
-                                          args);
+  static_assert(RESHARD_MAX_VOCAB / 4 <= kMaxCluster * kMarked, "marks of a slice");
+  void* args[] = {const_cast<DistillArgs*>(&a)};
+  const char* what = "reshard_distill_loss";
+  if (!a.tail) return launch<distill_kernel<T, false>, 0>(what, dev, {rows * ctas, kThreads, 0, ctas, stream}, args);
+  const size_t smem = size_t(cdiv(cdiv(granules, ctas), 4) * 4);
+  return launch<distill_kernel<T, true>, kMarked>(what, dev, {rows * ctas, kThreads, smem, ctas, stream}, args);
 }
 
 }  // namespace
