@@ -38,14 +38,13 @@ struct DistillArgs {
 // What the threads of a CTA, and the CTAs of a cluster, tell each other.
 struct Shared {
   int32_t token[RESHARD_MAX_TOP];  // the teacher's list, -1 for what is no entry
-  double q[RESHARD_MAX_TOP];       // its probabilities
-  double list_q[kListWarps];       // sums of the list's warps
-  float list_e[kListWarps], list_top[kListWarps];
+  double q[RESHARD_MAX_TOP];       // its probabilities, not yet scaled to 1
+  int32_t table[kThreads];         // its tokens, by a hash: a token that stands there twice meets itself
+  double list_q[kListWarps], list_term[kListWarps];  // sums of the list's warps
+  float list_e[kListWarps];
   float warp_top[kWarps], warp_other[kWarps];
-  float part_top, part_other;      // of the CTA: its largest logit, its sum over other tokens
-  float top, other;                // of the row
-  float outside;                   // 1 - q_R / p_R
-  double rest, inv_q;              // q_R, 1 / sum of the list
+  float part_top, part_other;      // of the CTA: its largest logit, its sum (over other tokens)
+  uint32_t again;                  // whether one does
   uint32_t edges;                  // listed tokens among those at the row's ends, a bit a thread
 };
 
@@ -60,6 +59,34 @@ __device__ __forceinline__ void join(float& top, float& other, float c) {
 }
 
 // Dynamic shared memory (TAIL): a byte a granule whose bits say which of its elements are listed.
+__device__ __forceinline__ uint64_t keep_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t drop_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint4 load_with(const uint4* at, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at), "l"(policy) : "memory");
+  return v;
+}
+
+// ln x for a positive finite x, within 2^-24 where x is near 1 and 2^-24 |ln x| elsewhere: of x = m 2^n, m next
+// to 1, by float32 and n ln 2 by float64, whose own logarithm takes 1.5 us on these SMs.
+__device__ double log_of(float x) {
+  int n = 0;
+  if (x < 0x1p-126f) x *= 0x1p32f, n = -32;
+  const uint32_t b = __float_as_uint(x) - 0x3f3504f3u;  // (sqrt(1/2))
+  n += int(b) >> 23;
+  const float m = __uint_as_float((b & 0x7fffffu) + 0x3f3504f3u);
+  return fma(double(n), 0.69314718055994530942, double(logf(m)));
+}
+
 template <typename T, bool TAIL>
 __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kPer = Slice<T>::kPer;
@@ -77,51 +104,45 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   // rounds of kVecs granules a thread, the next one's on their way while one is worked on
   const int rounds = (row.n + kRound - 1) / kRound;
   const uint4* from = row.granules() + tid;
+  uint64_t policy;
   auto load = [&](uint4(&v)[kVecs], int i) {
-    if (i >= rounds) return;
+    if (uint32_t(i) >= uint32_t(rounds)) return;
     const uint4* p = from + i * kRound;
     if ((i + 1) * kRound <= row.n) {
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) v[j] = p[j * kThreads];
+      for (int j = 0; j < kVecs; ++j) v[j] = load_with(p + j * kThreads, policy);
     } else {
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         v[j] = Slice<T>::nothing();
-        if (i * kRound + j * kThreads + tid < row.n) v[j] = p[j * kThreads];
+        if (i * kRound + j * kThreads + tid < row.n) v[j] = load_with(p + j * kThreads, policy);
       }
     }
   };
-  auto each_round = [&](auto&& work) {
-    uint4 v[kVecs], w[kVecs];
-    load(v, 0);
-#pragma unroll 1
-    for (int i = 0; i < rounds; i += 2) {
-      load(w, i + 1);
-      work(v, i);
-      load(v, i + 2);
-      if (i + 1 < rounds) work(w, i + 1);
-    }
-  };
-  // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none
+  uint4 v[kVecs], w[kVecs];
+  policy = keep_policy();
+  load(v, 0);
+  sh.table[tid] = -1;
+  if (tid == 0) sh.again = sh.edges = 0;
+  __syncthreads();
+  // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none.  Every
+  // warp looks for an entry by itself, so that none waits for another.
   const int k = a.ntop, list_warps = (k + 31) / 32;
   int mine = -1;
-  float y = -INFINITY;
-  if (warp < list_warps) {
-    if (tid < k) {
-      mine = __ldg(a.top_token + r * a.ldtop + tid);
-      y = __ldg(a.top_logprob + r * a.ldtop + tid);
-      if (uint32_t(mine) >= uint32_t(row.vocab) || !(y == y)) mine = -1, y = -INFINITY;
+  float y = -INFINITY, y_top = -INFINITY;
+  for (int i = 0; i < list_warps; ++i) {
+    const int at = i * 32 + lane;
+    int token = -1;
+    float value = -INFINITY;
+    if (at < k) {
+      token = __ldg(a.top_token + r * a.ldtop + at);
+      value = __ldg(a.top_logprob + r * a.ldtop + at);
+      if (uint32_t(token) >= uint32_t(row.vocab) || !(value == value)) token = -1, value = -INFINITY;
     }
-    sh.token[tid] = mine;
-    const float most = warp_max(y);
-    if (lane == 0) sh.list_top[warp] = most;
+    if (i == warp) mine = token, y = value;
+    y_top = fmaxf(y_top, value);
   }
-  if (TAIL)
-    for (int i = tid; i < (row.n + 3) / 4; i += kThreads) marks[i] = 0;
-  if (tid == 0) sh.edges = 0;
-  __syncthreads();
-  float y_top = sh.list_top[0];
-  for (int w = 1; w < list_warps; ++w) y_top = fmaxf(y_top, sh.list_top[w]);
+  y_top = warp_max(y_top);
   auto put_zeros = [&] {
     for (int g = tid; g < row.n; g += kThreads) store_granule(to + row.first + g * kPer, make_uint4(0, 0, 0, 0), a.alike);
     if (edge >= 0) to[edge] = from_float<T>(0.0f);
@@ -133,31 +154,43 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   }
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   const uint64_t c2 = both(c);
-  float x = -INFINITY;     // the student's logit of this thread's entry
-  bool first = mine >= 0;  // of the entries with this token
-  bool here = false;       // the token's gradient is this CTA's
-  if (first) {
-    x = row.at(mine);
-    const int place = mine - row.first;
-    here = place >= 0 && place < row.n * kPer;
-    const bool at_end = rank == 0 && (mine < row.head || mine >= row.last);
-    if (TAIL && here) {
-      const int g = place / kPer;
-      atomicOr(&marks[g / 4], 1u << (g % 4 * 8 + place % kPer));
+  const int place = mine - row.first;
+  const bool at_end = rank == 0 && mine >= 0 && (mine < row.head || mine >= row.last);
+  const bool inside = mine >= 0 && place >= 0 && place < row.n * kPer;
+  T student = from_float<T>(-INFINITY);  // its logit of this thread's entry, on its way until it is used
+  double q = 0.0;
+  if (warp < list_warps) {
+    sh.token[tid] = mine;
+    if (mine >= 0) {
+      for (uint32_t at = uint32_t(mine) * 2654435761u >> 23;; at = (at + 1) % kThreads) {  // half full at most
+        const int other = atomicCAS(&sh.table[at], -1, mine);
+        if (other == mine) sh.again = 1;
+        if (other == mine || other == -1) break;
+      }
+      student = row.row[mine];
+      // in 64 bits where what is left of 1 counts, which can be small
+      q = TAIL ? exp(double(y)) : double(expf(y - y_top));
     }
-    if (at_end) {
-      if (TAIL) atomicOr(&sh.edges, 1u << (mine < row.head ? mine : mine - row.last + row.head));
-      here = true;
-    }
-    for (int j = 0; j < tid; ++j) first = first && sh.token[j] != mine;
+    sh.q[tid] = q;
+    double all = q;
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) sh.list_q[warp] = all;
   }
   const float at_edge = edge >= 0 ? row.at(edge) : -INFINITY;
-  const bool again = __syncthreads_or(mine >= 0 && !first);  // some token stands there twice
+  bool edge_counts = at_edge > -INFINITY;
+  if (TAIL) {
+    for (int i = tid; i < (row.n + 3) / 4; i += kThreads) marks[i] = 0;
+    __syncthreads();
+    if (inside) atomicOr(&marks[place / kPer / 4], 1u << (place / kPer % 4 * 8 + place % kPer));
+    if (at_end) atomicOr(&sh.edges, 1u << (mine < row.head ? mine : mine - row.last + row.head));
+    __syncthreads();
+    edge_counts = edge_counts && !(sh.edges >> (tid & 31) & 1);
+  }
   // the sum over all tokens, or (TAIL) those that are not listed, relative to each thread's own
   // largest logit
-  float m = at_edge, other = at_edge > -INFINITY && !(TAIL && sh.edges >> (tid & 31) & 1) ? 1.0f : 0.0f;
+  float m = at_edge, other = edge_counts ? 1.0f : 0.0f;
   bool unclean = false;
-  each_round([&](uint4(&v)[kVecs], int round) {
+  auto add = [&](uint4(&v)[kVecs], int round) {
     float largest = largest_or_nan<T>(v);
     if (!(largest < INFINITY)) {
       unclean = true;
@@ -189,61 +222,61 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     }
     other = fmaf(other, exp2_of(exponent(m, top, c)), sum2(s2));
     m = top;
-  });
+  };
+#pragma unroll 1
+  for (int i = 0; i < rounds; i += 2) {
+    load(w, i + 1);
+    add(v, i);
+    load(v, i + 2);
+    if (i + 1 < rounds) add(w, i + 1);
+  }
+  // the gradient goes through the row backwards: what was read last is the likeliest to be in the L2
+  policy = drop_policy();
+  if (to) load(v, rounds - 1);
   join(m, other, c);
   if (lane == 0) sh.warp_top[warp] = m, sh.warp_other[warp] = other;
   __syncthreads();
-  if (warp == 0) {
-    float top = lane < kWarps ? sh.warp_top[lane] : -INFINITY, sum = lane < kWarps ? sh.warp_other[lane] : 0.0f;
-    join(top, sum, c);
-    if (lane == 0) sh.part_top = top, sh.part_other = sum;
-  }
-  if (ctas > 1) tc::cluster_sync();
-  else __syncthreads();
-  // the row's sums, and the list's: of the student over its different tokens, of the teacher over
-  // its entries.  The teacher's are in 64 bits: what is left of 1 can be small.
-  double q = 0.0;
-  if (warp < list_warps) {
-    float top = -INFINITY;
-    other = 0.0f;
+  const bool again = sh.again != 0;  // tokens stand there twice: what to do once, the first of them does
+  bool first = mine >= 0;
+  if (again)
+    for (int j = 0; first && j < tid; ++j) first = sh.token[j] != mine;
+  float top = lane < kWarps ? sh.warp_top[lane] : -INFINITY;
+  other = lane < kWarps ? sh.warp_other[lane] : 0.0f;
+  join(top, other, c);
+  if (ctas > 1) {
+    if (tid == 0) sh.part_top = top, sh.part_other = other;
+    tc::cluster_sync();
+    top = -INFINITY, other = 0.0f;
     if (lane < int(ctas)) top = load_far(&sh.part_top, lane), other = load_far(&sh.part_other, lane);
     join(top, other, c);
-    m = top;
-    const float e = TAIL ? warp_sum(first ? exp2_of(exponent(x, m, c)) : 0.0f) : 0.0f;
-    if (mine >= 0) q = TAIL ? exp(double(y)) : double(expf(y - y_top));
-    double all = q;
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    sh.q[tid] = q;
-    if (lane == 0) {
-      sh.list_e[warp] = e, sh.list_q[warp] = all;
-      if (warp == 0) sh.top = m, sh.other = other;
-    }
+    tc::cluster_arrive();  // this CTA has read the others' parts
   }
-  if (ctas > 1) tc::cluster_arrive();  // this CTA has read the others' parts
-  __syncthreads();
-  const float top = sh.top;
   const bool empty = !(top > -INFINITY);
-  float sum = sh.other;
-  for (int w = 0; w < list_warps; ++w) sum += sh.list_e[w];
-  if (tid == 0) {
-    double all = sh.list_q[0];
-    for (int w = 1; w < list_warps; ++w) all += sh.list_q[w];
-    sh.rest = 0.0, sh.outside = 1.0f, sh.inv_q = TAIL ? 1.0 : 1.0 / all;
-    if (TAIL && all < 1.0 && sh.other > 0.0f) {  // (else it has nowhere to be)
-      sh.rest = 1.0 - all;
-      sh.outside = float(1.0 - sh.rest * (double(sum) / double(sh.other)));
+  const float x = clean<T>(to_float(student));
+  float sum = other, outside = 1.0f;  // S; 1 - q_R / p_R
+  double rest = 0.0;                  // q_R
+  if (TAIL) {
+    if (warp < list_warps) {
+      const float e = warp_sum(first ? exp2_of(exponent(x, top, c)) : 0.0f);
+      if (lane == 0) sh.list_e[warp] = e;
+    }
+    __syncthreads();
+    double all = 0.0;
+    for (int i = 0; i < list_warps; ++i) sum += sh.list_e[i], all += sh.list_q[i];
+    if (all < 1.0 && other > 0.0f) {  // (else it has nowhere to be)
+      rest = 1.0 - all;
+      outside = 1.0f - float(rest) * (sum / other);
     }
   }
-  __syncthreads();
   if (to && empty) {
     put_zeros();
   } else if (to) {
     const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
     const float slope = fmaxf(fminf(g * inverse, 3.402823466e38f), -3.402823466e38f);
-    const float scale = fmaxf(fminf(slope / sum * sh.outside, 3.402823466e38f), -3.402823466e38f);
+    const float scale = fmaxf(fminf(slope / sum * outside, 3.402823466e38f), -3.402823466e38f);
     const uint64_t A = both(scale), minus = both(-top);
     T* begin = to + row.first;
-    each_round([&](uint4(&v)[kVecs], int round) {
+    auto put = [&](uint4(&v)[kVecs], int round) {
       if (unclean) make_clean<T>(v);
       T* e = reinterpret_cast<T*>(v);
 #pragma unroll
@@ -261,35 +294,54 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
           if (g < row.n) store_granule(begin + g * kPer, v[j], a.alike);
         }
       }
-    });
+    };
+#pragma unroll 1
+    for (int i = rounds - 1; i >= 0; i -= 2) {
+      load(w, i - 1);
+      put(v, i);
+      load(v, i - 2);
+      if (i > 0) put(w, i - 1);
+    }
     if (edge >= 0) to[edge] = from_float<T>(exp2_of(exponent(at_edge, top, c)) * scale);
-    // the CTA's listed tokens, behind what was just written for them as for others
     __syncthreads();
-    if (first && here) {
-      double all = q;
+  }
+  if (warp < list_warps) {
+    double all = 1.0, inv_q = 1.0;  // the list's sum where it is scaled to 1
+    if (!TAIL) {
+      all = sh.list_q[0];
+      for (int i = 1; i < list_warps; ++i) all += sh.list_q[i];
+      inv_q = double(1.0f / float(all));
+      inv_q = fma(inv_q, fma(-all, inv_q, 1.0), inv_q);
+    }
+    // the CTA's listed tokens, behind what was just written for them as for others
+    if (to && !empty && first && (inside || at_end)) {
+      const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
+      const float slope = fmaxf(fminf(g * inverse, 3.402823466e38f), -3.402823466e38f);
+      double mass = q;
       if (again)
         for (int j = tid + 1; j < k; ++j)
-          if (sh.token[j] == mine) all += sh.q[j];
+          if (sh.token[j] == mine) mass += sh.q[j];
       const float p = exp2_of(exponent(x, top, c)) / sum;
-      to[mine] = from_float<T>(slope * (p - float(all * sh.inv_q)));
+      to[mine] = from_float<T>(slope * (p - float(mass * inv_q)));
     }
-  }
-  if (rank == 0 && a.loss && warp < list_warps) {
-    double term = 0.0;
-    q *= sh.inv_q;
-    if (!(q <= 0.0)) {
-      const double z = x == top ? 0.0 : double(x - top) * double(inverse);
-      term = q * ((double(y) - z) + (TAIL ? 0.0 : log(sh.inv_q) - double(y_top)) + log(double(sum)));
+    if (rank == 0 && a.loss) {
+      double term = 0.0;
+      q *= inv_q;
+      if (!(q <= 0.0)) {
+        const double z = x == top ? 0.0 : double(x - top) * double(inverse);
+        term = q * ((double(y) - (TAIL ? 0.0 : double(y_top)) - z) + (log_of(sum) - (TAIL ? 0.0 : log_of(float(all)))));
+      }
+      for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+      if (lane == 0) sh.list_term[warp] = term;
     }
-    for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-    if (lane == 0) sh.list_q[warp] = term;
   }
   if (ctas > 1) tc::cluster_wait();
+  if (rank != 0 || !a.loss) return;
   __syncthreads();
-  if (rank == 0 && a.loss && tid == 0) {
-    double loss = sh.list_q[0];
-    for (int w = 1; w < list_warps; ++w) loss += sh.list_q[w];
-    if (sh.rest > 0.0) loss += sh.rest * log(sh.rest * (double(sum) / double(sh.other)));
+  if (tid == 0) {
+    double loss = sh.list_term[0];
+    for (int i = 1; i < list_warps; ++i) loss += sh.list_term[i];
+    if (rest > 0.0) loss += rest * (log_of(float(rest)) + log_of(sum) - log_of(other));
     a.loss[r] = empty ? INFINITY : float(loss);
   }
 }
