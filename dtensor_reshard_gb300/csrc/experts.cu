@@ -1,6 +1,8 @@
 // experts.cu -- a router's choices sorted by expert (reshard_expert_sort), the rows of tokens
 // at the places of their experts, as they are or in 8 bits (reshard_expert_dispatch), and back
 // with weights (reshard_expert_combine, reshard_expert_combine_grad).
+#include <type_traits>
+
 #include "fp8_block.cuh"
 
 namespace rs {
@@ -11,6 +13,7 @@ using namespace op;
 // ------------------------------------------------------------------------------- sort
 constexpr int kSortCluster = 8;
 constexpr size_t kSortSmem = 200 * 1024;
+constexpr int kKept = 8;
 
 struct SortArgs {
   const int32_t* experts;
@@ -38,19 +41,28 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   const uint32_t part = rank * warps + warp, parts = ctas * warps;
   const uint32_t b0 = uint32_t(batches * part / parts), b1 = uint32_t(batches * (part + 1) / parts);
   int32_t* mine = counted + warp * E;
+  // 32 choices of the warp, the first kKept of them kept; others are read again
   auto choice = [&](uint32_t b) {
     const uint64_t i = uint64_t(b) * 32 + lane;
     const int e = b < b1 && i < a.n ? __ldg(a.experts + i) : -1;
     return uint32_t(e) < uint32_t(E) ? e : -1;
   };
+  int kept[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) kept[i] = choice(b0 + i);
   __syncthreads();
-  for (uint32_t b = b0; b < b1; ++b) {
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (kept[i] >= 0) atomicAdd(&mine[kept[i]], 1);
+#pragma unroll 4
+  for (uint32_t b = b0 + kKept; b < b1; ++b) {
     const int e = choice(b);
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
   for (int e = tid; e < E; e += threads) {
     int sum = 0;
+#pragma unroll 8
     for (int w = 0; w < warps; ++w) {
       const int c = counted[w * E + e];
       counted[w * E + e] = sum;
@@ -92,8 +104,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   }
   if (rank == 0 && tid == 0) a.offsets[E] = carry;
   tc::cluster_arrive();  // this CTA has read the others' totals
-  for (uint32_t b = b0; b < b1; ++b) {
-    const int e = choice(b);
+  auto give = [&](uint32_t b, int e) {
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     const int before = __popc(same & ((1u << lane) - 1));
     int place = -1;
@@ -102,7 +113,19 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     if (e >= 0 && before == 0) mine[e] += __popc(same);
     __syncwarp();
     const uint64_t i = uint64_t(b) * 32 + lane;
-    if (i < a.n) a.slot[i] = place;
+    if (b < b1 && i < a.n) a.slot[i] = place;
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (b0 + i < b1) give(b0 + i, kept[i]);
+#pragma unroll 1
+  for (uint32_t b = b0 + kKept; b < b1; b += 4) {
+    int e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = choice(b + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i < b1) give(b + i, e[i]);
   }
   tc::cluster_wait();
 }
@@ -114,201 +137,301 @@ struct DispatchArgs {
   float* scale;
   const int32_t* slot;
   int64_t ldx, ldr, lds;  // bytes; floats
-  int64_t tokens, cols;
-  int64_t vecs, chunks;   // accesses of a row; CTAs that share one
+  uint32_t tokens, cols;
+  uint32_t vecs, chunks;  // accesses of a row; CTAs that share one
   uint32_t nrows;
-  int32_t topk, lanes;    // lanes of a token
+  uint32_t topk, lanes;    // lanes (in 8 bits: sixteens of lanes) of a token
 };
 
 // Each row is read once and written to all of its places.
-constexpr int kDispatchVecs = 4;  // of a thread
+constexpr int kDispatchVecs = 4;    // of a thread
+constexpr int kDispatchBlocks = 4;  // of a lane, in 8 bits, for many tokens
 template <typename V>
 __global__ void __launch_bounds__(256) dispatch_kernel(const __grid_constant__ DispatchArgs a) {
-  const int lane = threadIdx.x & (a.lanes - 1);
-  const int64_t group = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
-  const int64_t t = group * (256 / a.lanes) + threadIdx.x / a.lanes;
+  const uint32_t lane = threadIdx.x & (a.lanes - 1);
+  const uint32_t t = blockIdx.x / a.chunks * (256 / a.lanes) + threadIdx.x / a.lanes;
   if (t >= a.tokens) return;
-  const int64_t c0 = chunk * kDispatchVecs * a.lanes + lane;
-  const V* x = reinterpret_cast<const V*>(a.x + t * a.ldx);
+  const uint32_t c0 = blockIdx.x % a.chunks * (kDispatchVecs * a.lanes) + lane;
+  const V* x = reinterpret_cast<const V*>(a.x + t * a.ldx) + c0;
   V v[kDispatchVecs];
 #pragma unroll
-  for (int i = 0; i < kDispatchVecs; ++i)
-    if (c0 + i * a.lanes < a.vecs) v[i] = __ldcs(x + c0 + i * a.lanes);
-  const int32_t* slot = a.slot + t * a.topk;
+  for (uint32_t i = 0; i < kDispatchVecs; ++i)
+    if (c0 + i * a.lanes < a.vecs) v[i] = __ldcs(x + i * a.lanes);
+  const int32_t* slot = a.slot + int64_t(t) * a.topk;
 #pragma unroll 4
-  for (int j = 0; j < a.topk; ++j) {
+  for (uint32_t j = 0; j < a.topk; ++j) {
     const uint32_t s = uint32_t(__ldg(slot + j));
     if (s >= a.nrows) continue;
-    V* to = reinterpret_cast<V*>(a.rows + int64_t(s) * a.ldr);
+    V* to = reinterpret_cast<V*>(a.rows + s * a.ldr) + c0;
 #pragma unroll
-    for (int i = 0; i < kDispatchVecs; ++i)
-      if (c0 + i * a.lanes < a.vecs) to[c0 + i * a.lanes] = v[i];
+    for (uint32_t i = 0; i < kDispatchVecs; ++i)
+      if (c0 + i * a.lanes < a.vecs) to[i * a.lanes] = v[i];
   }
 }
 
-// The same in 8 bits: sixteen lanes a block of 128 values, quantised once.  VEC: every row of x
-// starts on 16 bytes, of the 8-bit rows on 8.
-template <typename T, bool VEC>
+// The same in 8 bits: sixteen lanes a block of 128 values, which is quantised once; a lane has B
+// blocks of its token, so that a place's address is made once for all of them.  Lane i stores the
+// scale of the i-th.  VEC: every row of x starts on 16 bytes, of the 8-bit rows on 8.
+template <typename T, bool VEC, int B>
 __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant__ DispatchArgs a) {
-  const uint64_t group = uint64_t(blockIdx.x) * 16 + threadIdx.x / 16;
-  const int64_t blocks = a.chunks, tt = int64_t(group / uint64_t(blocks));
-  const int64_t block = int64_t(group % uint64_t(blocks)), t = tt < a.tokens ? tt : a.tokens - 1;
-  const int c = threadIdx.x % 16 * 8;
-  const int64_t col = block * 128 + c;
-  const int inside = int(min(max(a.cols - col, int64_t(0)), int64_t(8)));
-  const int left = tt < a.tokens ? inside : 0;
-  const T* x = reinterpret_cast<const T*>(a.x + t * a.ldx) + col;
-  Eight<T> e;
-  const bool whole = __all_sync(0xffffffffu, VEC && left == 8);
-  if (whole) {
-    e.load(x);
-  } else if (VEC) {
-    e.load(x, left);
-  } else {
-    const T* begin = reinterpret_cast<const T*>(a.x);
-    const T* end = reinterpret_cast<const T*>(a.x + (a.tokens - 1) * a.ldx) + a.cols;
-    e.template load_granules<false>(x, begin, end);
-    e.align(x, left);
-  }
-  float m = e.largest();
-  for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float s = scale_of(m);
-  const uint2 q = e.quotients(s);
-  const int count = tt < a.tokens ? int(min(a.cols - (col - c), int64_t(128))) : 0;
-  const int32_t* slot = a.slot + t * a.topk;
-#pragma unroll 4
-  for (int j = 0; j < a.topk; ++j) {
-    const uint32_t to = uint32_t(__ldg(slot + j));
-    const bool on = to < a.nrows && tt < a.tokens;
-    uint8_t* row = a.rows + (on ? int64_t(to) * a.ldr + (col - c) : 0);
-    if (on && c == 0) a.scale[int64_t(to) * a.lds + block] = s;
-    if (whole) {
-      if (on) *reinterpret_cast<uint2*>(row + c) = q;
-    } else {
-      store_row(row, q, on ? count : 0);
+  const uint32_t sixteenth = threadIdx.x / 16, l = threadIdx.x % 16;
+  const uint32_t tt = blockIdx.x / a.chunks * (16 / a.lanes) + sixteenth / a.lanes;
+  const bool there = tt < a.tokens;
+  const uint32_t t = there ? tt : a.tokens - 1;
+  const uint32_t block0 = blockIdx.x % a.chunks * (B * a.lanes) + sixteenth % a.lanes;
+  const uint32_t step = a.lanes * 128, col0 = block0 * 128;
+  const T* x = reinterpret_cast<const T*>(a.x + t * a.ldx) + col0 + 8 * l;
+  const int32_t* slot = a.slot + int64_t(t) * a.topk;
+  const uint32_t my_block = block0 + l * a.lanes;
+  const bool scales = l < B && there && my_block * 128 < a.cols;
+  Eight<T> e[B];
+  uint2 q[B];
+  float scale = 0.0f;
+  auto quantise = [&] {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      float m = e[i].largest();
+      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float s = scale_of(m);
+      if (l == i) scale = s;
+      q[i] = e[i].quotients(s);
     }
+  };
+  // blocks that lie inside the row
+  const uint32_t blocks = there && col0 < a.cols ? (a.cols - col0 + step - 1) / step : 0;
+  const bool whole = __all_sync(0xffffffffu, VEC && a.cols % 128 == 0);
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (i < blocks) e[i].load(x + i * step);
+    quantise();
+    const uint32_t to0 = col0 + 8 * l;
+#pragma unroll 4
+    for (uint32_t j = 0; j < a.topk; ++j) {
+      const uint32_t to = uint32_t(__ldg(slot + j));
+      if (to >= a.nrows) continue;
+      uint8_t* row = a.rows + to * a.ldr + to0;
+      if (scales) a.scale[to * a.lds + my_block] = scale;
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        if (i < blocks) *reinterpret_cast<uint2*>(row + i * step) = q[i];
+    }
+    return;
+  }
+  int count[B];  // values of the block that lie inside the row
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    count[i] = i < blocks ? int(min(a.cols - (col0 + i * step), 128u)) : 0;
+    const int left = min(max(count[i] - int(8 * l), 0), 8);
+    if (VEC) {
+      e[i].load(x + i * step, left);
+    } else {
+      const T* begin = reinterpret_cast<const T*>(a.x);
+      const T* end = reinterpret_cast<const T*>(a.x + (a.tokens - 1) * a.ldx) + a.cols;
+      e[i].template load_granules<false>(x + i * step, begin, end);
+      e[i].align(x + i * step, left);
+    }
+  }
+  quantise();
+#pragma unroll 1
+  for (uint32_t j = 0; j < a.topk; ++j) {
+    const uint32_t to = uint32_t(__ldg(slot + j));
+    const bool on = to < a.nrows && there;
+    uint8_t* row = a.rows + (on ? to * a.ldr + col0 : 0);
+    if (on && scales) a.scale[to * a.lds + my_block] = scale;
+#pragma unroll
+    for (int i = 0; i < B; ++i) store_row(row + i * step, q[i], on ? count[i] : 0);
   }
 }
 
 // ---------------------------------------------------------------------------- combine
 struct CombineArgs {
-  const void *rows, *dout;
-  void *out, *drows;
+  const unsigned char *rows, *dout;
+  unsigned char *out, *drows;
   const int32_t* slot;
   const float* weight;
   float* dweight;
-  int64_t ldr, ldo;     // elements
-  int64_t tokens, vecs, chunks;
-  uint32_t nrows;
-  int32_t topk, lanes;
+  int64_t ldr, ldo;        // bytes
+  uint32_t tokens, vecs;   // accesses of a row
+  uint32_t chunks, span;   // CTAs that share a row, and their accesses
+  uint32_t nrows, topk, lanes;
 };
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Values {
-  T v[N];
+// Elements of one access of W bytes as they lie in memory: whole words, which the compiler would
+// take apart into a register an element, and their values.
+template <typename T, int W>
+struct Access {
+  static constexpr int kWords = W < 4 ? 1 : W / 4, kElements = W / int(sizeof(T)) > 0 ? W / int(sizeof(T)) : 1;
+  uint32_t word[kWords];
+
+  __device__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) word[i] = 0;
+  }
+  __device__ void load(const unsigned char* at) {
+    if constexpr (W == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at);
+      word[0] = v.x, word[1] = v.y, word[2] = v.z, word[3] = v.w;
+    } else if constexpr (W == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(at);
+      word[0] = v.x, word[1] = v.y;
+    } else if constexpr (W == 4) {
+      word[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else {
+      word[0] = *reinterpret_cast<const uint16_t*>(at);
+    }
+  }
+  __device__ void store(unsigned char* at) const {
+    if constexpr (W == 16) *reinterpret_cast<uint4*>(at) = make_uint4(word[0], word[1], word[2], word[3]);
+    else if constexpr (W == 8) *reinterpret_cast<uint2*>(at) = make_uint2(word[0], word[1]);
+    else if constexpr (W == 4) *reinterpret_cast<uint32_t*>(at) = word[0];
+    else *reinterpret_cast<uint16_t*>(at) = uint16_t(word[0]);
+  }
+  __device__ float value(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(word[i]);
+    const uint32_t w = word[i / 2];
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+    else
+      return __half2float(__ushort_as_half(uint16_t(i % 2 ? w >> 16 : w)));
+  }
+  __device__ void set(const float (&f)[kElements]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kElements; ++i) word[i] = __float_as_uint(f[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kElements; i += 2) {
+        const float2 v = make_float2(f[i], i + 1 < kElements ? f[i + 1] : 0.0f);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          const __nv_bfloat162 h = __float22bfloat162_rn(v);
+          word[i / 2] = reinterpret_cast<const uint32_t&>(h);
+        } else {
+          const __half2 h = __float22half2_rn(v);
+          word[i / 2] = reinterpret_cast<const uint32_t&>(h);
+        }
+      }
+    }
+  }
 };
 
 constexpr int kTogether = 8;  // choices whose rows are on their way at a time
 
-// out = sum of weight x row over a token's choices, in float32 in the order of the choices.
-template <typename T, int N>
+// out = sum of weight x row over a token's choices, in float32 in the order of the choices.  A CTA
+// has `span` accesses of its tokens' rows.
+template <typename T, int W>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineArgs a) {
-  using V = Values<T, N>;
-  const int lane = threadIdx.x & (a.lanes - 1);
-  const int64_t group = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
-  const int64_t t = group * (256 / a.lanes) + threadIdx.x / a.lanes;
-  const int64_t c = chunk * a.lanes + lane;
-  if (t >= a.tokens || c >= a.vecs) return;
-  float sum[N];
+  using A = Access<T, W>;
+  constexpr int N = A::kElements;
+  const uint32_t lane = threadIdx.x & (a.lanes - 1);
+  const uint32_t t = blockIdx.x / a.chunks * (256 / a.lanes) + threadIdx.x / a.lanes;
+  if (t >= a.tokens) return;
+  const uint32_t c0 = blockIdx.x % a.chunks * a.span + lane, c1 = min(c0 - lane + a.span, a.vecs);
+  const int64_t first = int64_t(t) * a.topk;
+  unsigned char* out = a.out + t * a.ldo;
+  const unsigned char* row[kTogether];
+  float w[kTogether];
+  auto places = [&](uint32_t j0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum[i] = 0.0f;
-  for (int j0 = 0; j0 < a.topk; j0 += kTogether) {
-    V v[kTogether];
-    float w[kTogether];
-    bool on[kTogether];
+    for (uint32_t j = 0; j < kTogether; ++j) {
+      const uint32_t s = j0 + j < a.topk ? uint32_t(__ldg(a.slot + first + j0 + j)) : 0xffffffffu;
+      w[j] = s < a.nrows && a.weight ? __ldg(a.weight + first + j0 + j) : 1.0f;
+      row[j] = s < a.nrows ? a.rows + s * a.ldr : nullptr;
+    }
+  };
+  auto add = [&](float(&sum)[N], uint32_t c) {
+    A v[kTogether];
 #pragma unroll
     for (int j = 0; j < kTogether; ++j) {
-      const int64_t at = t * a.topk + j0 + j;
-      const uint32_t s = j0 + j < a.topk ? uint32_t(__ldg(a.slot + at)) : 0xffffffffu;
-      on[j] = s < a.nrows;
-      w[j] = on[j] && a.weight ? __ldg(a.weight + at) : 1.0f;
-      if (on[j]) v[j] = *(reinterpret_cast<const V*>(static_cast<const T*>(a.rows) + int64_t(s) * a.ldr) + c);
+      v[j].clear();
+      if (row[j]) v[j].load(row[j] + c * uint64_t(W));
     }
 #pragma unroll
-    for (int j = 0; j < kTogether; ++j) {
-      if (!on[j]) continue;
+    for (int j = 0; j < kTogether; ++j)
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum[i] = fmaf(w[j], to_float(v[j].v[i]), sum[i]);
+      for (int i = 0; i < N; ++i) sum[i] = fmaf(w[j], v[j].value(i), sum[i]);
+  };
+  places(0);
+  for (uint32_t c = c0; c < c1; c += a.lanes) {
+    float sum[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+    add(sum, c);
+    if (a.topk > kTogether) {
+      for (uint32_t j0 = kTogether; j0 < a.topk; j0 += kTogether) places(j0), add(sum, c);
+      places(0);
     }
+    A v;
+    v.set(sum);
+    v.store(out + c * uint64_t(W));
   }
-  V out;
-#pragma unroll
-  for (int i = 0; i < N; ++i) out.v[i] = from_float<T>(sum[i]);
-  *(reinterpret_cast<V*>(static_cast<T*>(a.out) + t * a.ldo) + c) = out;
 }
 
 // drows = weight x dout at the places of a token's choices; dweight = the products of dout with
 // its rows.  LANES: of a token, a warp or a CTA.
-template <typename T, int N, int LANES, bool DOT>
+template <typename T, int W, int LANES, bool DOT>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const __grid_constant__ CombineArgs a) {
-  using V = Values<T, N>;
+  using A = Access<T, W>;
+  constexpr int N = A::kElements;
   __shared__ float part[8][kTogether];
-  const int lane = threadIdx.x % LANES, warp = threadIdx.x / 32;
-  const int64_t t = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const uint32_t lane = threadIdx.x % LANES, warp = threadIdx.x / 32;
+  const uint32_t t = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   if (t >= a.tokens) return;  // (whole warps, and with a CTA a token none)
-  const V* dout = reinterpret_cast<const V*>(static_cast<const T*>(a.dout) + t * a.ldo);
-  for (int j0 = 0; j0 < a.topk; j0 += kTogether) {
-    const int together = min(kTogether, a.topk - j0);
+  const int64_t first = int64_t(t) * a.topk;
+  const unsigned char* dout = a.dout + t * a.ldo;
+  for (uint32_t j0 = 0; j0 < a.topk; j0 += kTogether) {
+    const uint32_t together = min(uint32_t(kTogether), a.topk - j0);
     uint32_t s[kTogether];
     float w[kTogether], dot[kTogether];
 #pragma unroll
-    for (int j = 0; j < kTogether; ++j) {
-      const int64_t at = t * a.topk + j0 + j;
-      s[j] = j < together ? uint32_t(__ldg(a.slot + at)) : 0xffffffffu;
-      w[j] = j < together && a.weight ? __ldg(a.weight + at) : 1.0f;
+    for (uint32_t j = 0; j < kTogether; ++j) {
+      s[j] = j < together ? uint32_t(__ldg(a.slot + first + j0 + j)) : 0xffffffffu;
+      w[j] = j < together && a.weight ? __ldg(a.weight + first + j0 + j) : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int64_t c = lane; c < a.vecs; c += LANES) {
-      const V d = dout[c];
-      V r[kTogether];
-      if (DOT) {
+    for (uint32_t c = lane; c < a.vecs; c += LANES) {
+      A d, r[kTogether];
+      d.load(dout + c * uint64_t(W));
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j)
-          if (s[j] < a.nrows)
-            r[j] = *(reinterpret_cast<const V*>(static_cast<const T*>(a.rows) + int64_t(s[j]) * a.ldr) + c);
+      for (int j = 0; j < kTogether; ++j) {
+        r[j].clear();
+        if (DOT && s[j] < a.nrows) r[j].load(a.rows + s[j] * a.ldr + c * uint64_t(W));
       }
 #pragma unroll
       for (int j = 0; j < kTogether; ++j) {
         if (s[j] >= a.nrows) continue;
         if (DOT) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) dot[j] = fmaf(to_float(d.v[i]), to_float(r[j].v[i]), dot[j]);
+          for (int i = 0; i < N; ++i) dot[j] = fmaf(d.value(i), r[j].value(i), dot[j]);
         }
         if (!a.drows) continue;
-        V g;
+        float f[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) g.v[i] = from_float<T>(w[j] * to_float(d.v[i]));
-        *(reinterpret_cast<V*>(static_cast<T*>(a.drows) + int64_t(s[j]) * a.ldr) + c) = g;
+        for (int i = 0; i < N; ++i) f[i] = w[j] * d.value(i);
+        A g;
+        g.set(f);
+        g.store(a.drows + s[j] * a.ldr + c * uint64_t(W));
       }
     }
-    if (!DOT) continue;
+    if constexpr (DOT) {
 #pragma unroll
-    for (int j = 0; j < kTogether; ++j) dot[j] = warp_sum(dot[j]);
-    float* to = a.dweight + t * a.topk + j0;
-    if (LANES == 32) {
-      if (lane == 0)
-        for (int j = 0; j < kTogether; ++j)
-          if (j < together) to[j] = dot[j];
-    } else {
-      if (threadIdx.x % 32 == 0)
-        for (int j = 0; j < kTogether; ++j) part[warp][j] = dot[j];
-      __syncthreads();
-      if (int(threadIdx.x) < together) {
-        float sum = 0.0f;
-        for (int i = 0; i < 8; ++i) sum += part[i][threadIdx.x];
-        to[threadIdx.x] = sum;
+      for (int j = 0; j < kTogether; ++j) dot[j] = warp_sum(dot[j]);
+      float* to = a.dweight + first + j0;
+      if (LANES == 32) {
+        if (lane == 0)
+          for (uint32_t j = 0; j < kTogether; ++j)
+            if (j < together) to[j] = dot[j];
+      } else {
+        if (threadIdx.x % 32 == 0)
+          for (int j = 0; j < kTogether; ++j) part[warp][j] = dot[j];
+        __syncthreads();
+        if (threadIdx.x < together) {
+          float sum = 0.0f;
+          for (int i = 0; i < 8; ++i) sum += part[i][threadIdx.x];
+          to[threadIdx.x] = sum;
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 }
@@ -386,9 +509,12 @@ extern "C" reshard_status_t reshard_expert_sort(const int32_t* experts, int64_t 
     return fail(RESHARD_ERR_CUDA, std::string("reshard_expert_sort: ") + cudaGetErrorString(ce));
   if (n == 0) return RESHARD_OK;
   rs::SortArgs a = {experts, slot, offsets, uint32_t(n), int32_t(nexperts)};
-  int64_t warps = 32;
+  // one CTA up to kKept times 32 choices for each of its warps; a warp for each 32 choices while
+  // there are few, and no more than the counts of shared memory
+  int64_t warps = 8;
+  while (warps < 32 && warps * 32 < n) warps *= 2;
   while ((warps + 2) * nexperts * 4 > int64_t(rs::kSortSmem)) warps /= 2;
-  const int ctas = n <= 8192 ? 1 : rs::kSortCluster;
+  const int ctas = n <= warps * 32 * rs::kKept ? 1 : rs::kSortCluster;
   void* args[] = {&a};
   return rs::op::launch<rs::sort_kernel, rs::kSortSmem>(
       "reshard_expert_sort", dev,
@@ -420,27 +546,37 @@ extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype
   a.ldx = ldx * size;
   a.ldr = scale ? ldr : ldr * size;
   a.lds = lds;
-  a.tokens = tokens;
-  a.cols = cols;
+  a.tokens = uint32_t(tokens);
+  a.cols = uint32_t(cols);
   a.nrows = uint32_t(nrows);
-  a.topk = int32_t(topk);
+  a.topk = uint32_t(topk);
   if (scale) {
-    a.chunks = blocks;
-    const int64_t grid = rs::op::cdiv(tokens * blocks, 16);
+    // sixteen lanes a block: as many of a CTA's sixteen on one token as it has blocks for
+    a.lanes = 1;
+    while (a.lanes < 16 && a.lanes < blocks) a.lanes *= 2;
+    const bool many = tokens * blocks >= 64 * 1024;  // every SM has a few CTAs all the same
+    const int64_t chunks = rs::op::cdiv(blocks, (many ? rs::kDispatchBlocks : 1) * int64_t(a.lanes));
+    const int64_t grid = rs::op::cdiv(tokens, 16 / a.lanes) * chunks;
+    a.chunks = uint32_t(chunks);
     if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
     const bool vec = rs::all_aligned(16, {x}, {a.ldx}) && rs::all_aligned(8, {rows}, {a.ldr});
     return rs::op::by_dtype(dtype, [&](auto t) {
       using T = decltype(t);
-      if (vec) rs::dispatch_fp8_kernel<T, true><<<unsigned(grid), 256, 0, st>>>(a);
-      else rs::dispatch_fp8_kernel<T, false><<<unsigned(grid), 256, 0, st>>>(a);
+      constexpr int B = rs::kDispatchBlocks;
+      if (vec && many) rs::dispatch_fp8_kernel<T, true, B><<<unsigned(grid), 256, 0, st>>>(a);
+      else if (vec) rs::dispatch_fp8_kernel<T, true, 1><<<unsigned(grid), 256, 0, st>>>(a);
+      else if (many) rs::dispatch_fp8_kernel<T, false, B><<<unsigned(grid), 256, 0, st>>>(a);
+      else rs::dispatch_fp8_kernel<T, false, 1><<<unsigned(grid), 256, 0, st>>>(a);
       return rs::op::launched("reshard_expert_dispatch");
     });
   }
   return rs::by_width(size, {x, rows}, {a.ldx, a.ldr, cols * size}, [&](auto w) {
-    a.vecs = cols * size / w;
-    a.lanes = rs::lanes_of(a.vecs);
-    a.chunks = rs::op::cdiv(a.vecs, rs::kDispatchVecs * a.lanes);
-    const int64_t grid = rs::op::cdiv(tokens, 256 / a.lanes) * a.chunks;
+    const int64_t vecs = cols * size / w;
+    a.lanes = uint32_t(rs::lanes_of(vecs));
+    const int64_t chunks = rs::op::cdiv(vecs, rs::kDispatchVecs * int64_t(a.lanes));
+    const int64_t grid = rs::op::cdiv(tokens, 256 / a.lanes) * chunks;
+    a.vecs = uint32_t(vecs);
+    a.chunks = uint32_t(chunks);
     if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
     rs::dispatch_kernel<typename rs::Word<w>::type><<<unsigned(grid), 256, 0, st>>>(a);
     return rs::op::launched("reshard_expert_dispatch");
@@ -464,25 +600,30 @@ extern "C" reshard_status_t reshard_expert_combine(const void* rows, int32_t dty
       !rs::op::aligned(weight, 4))
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
   rs::CombineArgs a = {};
-  a.rows = rows;
-  a.out = out;
+  a.rows = static_cast<const unsigned char*>(rows);
+  a.out = static_cast<unsigned char*>(out);
   a.slot = slot;
   a.weight = weight;
-  a.ldr = ldr;
-  a.ldo = ldo;
-  a.tokens = tokens;
+  a.ldr = ldr * size;
+  a.ldo = ldo * size;
+  a.tokens = uint32_t(tokens);
   a.nrows = uint32_t(nrows);
-  a.topk = int32_t(topk);
+  a.topk = uint32_t(topk);
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     return rs::by_width(size, {rows, out}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
-      constexpr int N = w / int(sizeof(T)) > 0 ? w / int(sizeof(T)) : 1;
-      a.vecs = cols / N;
-      a.lanes = rs::lanes_of(a.vecs);
-      a.chunks = rs::op::cdiv(a.vecs, a.lanes);
-      const int64_t grid = rs::op::cdiv(tokens, 256 / a.lanes) * a.chunks;
+      const int64_t vecs = cols * size / w, lanes = rs::lanes_of(vecs), groups = rs::op::cdiv(tokens, 256 / lanes);
+      // a CTA a whole row, or so much of it that there are some 2048 of them
+      int64_t rounds = rs::op::cdiv(vecs, lanes);
+      if (groups * rounds > 2048) rounds = rs::op::cdiv(groups * rounds, 2048) < rounds ? rs::op::cdiv(groups * rounds, 2048) : rounds;
+      else rounds = 1;
+      const int64_t chunks = rs::op::cdiv(vecs, lanes * rounds), grid = groups * chunks;
+      a.vecs = uint32_t(vecs);
+      a.lanes = uint32_t(lanes);
+      a.span = uint32_t(lanes * rounds);
+      a.chunks = uint32_t(chunks);
       if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
-      rs::combine_kernel<T, N><<<unsigned(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      rs::combine_kernel<T, w><<<unsigned(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
       return rs::op::launched("reshard_expert_combine");
     });
   });
@@ -506,32 +647,31 @@ extern "C" reshard_status_t reshard_expert_combine_grad(const void* dout, int32_
       !rs::op::aligned(slot, 4) || !rs::op::aligned(weight, 4) || !rs::op::aligned(dweight, 4))
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type");
   rs::CombineArgs a = {};
-  a.rows = rows;
-  a.dout = dout;
-  a.drows = drows;
+  a.rows = static_cast<const unsigned char*>(rows);
+  a.dout = static_cast<const unsigned char*>(dout);
+  a.drows = static_cast<unsigned char*>(drows);
   a.slot = slot;
   a.weight = weight;
   a.dweight = dweight;
-  a.ldr = ldr;
-  a.ldo = ldo;
-  a.tokens = tokens;
+  a.ldr = ldr * size;
+  a.ldo = ldo * size;
+  a.tokens = uint32_t(tokens);
   a.nrows = uint32_t(nrows);
-  a.topk = int32_t(topk);
+  a.topk = uint32_t(topk);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const void* read = dweight ? rows : nullptr;
     return rs::by_width(size, {dout, read, drows}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
-      constexpr int N = w / int(sizeof(T)) > 0 ? w / int(sizeof(T)) : 1;
-      a.vecs = cols / N;
+      a.vecs = uint32_t(cols * size / w);
       const bool cta = a.vecs > 128;  // a CTA a token, else a warp
       const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
       if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
       const unsigned g = unsigned(grid);
-      if (dweight && cta) rs::combine_grad_kernel<T, N, 256, true><<<g, 256, 0, st>>>(a);
-      else if (dweight) rs::combine_grad_kernel<T, N, 32, true><<<g, 256, 0, st>>>(a);
-      else if (cta) rs::combine_grad_kernel<T, N, 256, false><<<g, 256, 0, st>>>(a);
-      else rs::combine_grad_kernel<T, N, 32, false><<<g, 256, 0, st>>>(a);
+      if (dweight && cta) rs::combine_grad_kernel<T, w, 256, true><<<g, 256, 0, st>>>(a);
+      else if (dweight) rs::combine_grad_kernel<T, w, 32, true><<<g, 256, 0, st>>>(a);
+      else if (cta) rs::combine_grad_kernel<T, w, 256, false><<<g, 256, 0, st>>>(a);
+      else rs::combine_grad_kernel<T, w, 32, false><<<g, 256, 0, st>>>(a);
       return rs::op::launched("reshard_expert_combine_grad");
     });
   });

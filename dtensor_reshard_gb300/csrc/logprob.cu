@@ -38,9 +38,15 @@ struct Part {
   uint32_t listed;         // its most likely tokens, in order in TopSmem::best
 };
 struct TopSmem {
-  uint32_t key[kCap], index[kCap];
-  uint32_t hit[kCap];              // groups with such tokens
+  union {
+    struct {
+      uint32_t key[kCap], index[kCap];
+      uint32_t hit[kCap];  // groups with such tokens
+    };
+    uint64_t other[kMaxCluster][RESHARD_MAX_TOP];  // in the end: the lists of the cluster's CTAs
+  };
   uint64_t best[RESHARD_MAX_TOP];  // key, then ~index: the largest first
+  uint32_t rank[RESHARD_MAX_TOP];  // how many tokens of other CTAs come before each
   uint32_t hist[256], count[32];
   uint32_t n, n2, digit, hits;
 };
@@ -312,14 +318,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     return;
   }
   const uint64_t c2 = both(c);
-  float chosen = 0.0f;
-  if (rank == 0 && tid == 0 && a.logprob) chosen = row.at(target);
+  T chosen = from_float<T>(0.0f);  // on its way until it is used
+  if (rank == 0 && tid == 0 && a.logprob) chosen = row.row[target];
   uint16_t* noted = reinterpret_cast<uint16_t*>(dynamic + sizeof(TopSmem));  // [groups][kThreads]
   const int per = (rounds + kGroups - 1) / kGroups;
   uint32_t group = 0;
   int in_group = 0;
   uint16_t* note = noted + tid;
-  if (TOP && tid == 0) sm.n = sm.hits = 0;
+  if (TOP) {
+    if (tid == 0) sm.n = sm.hits = 0;
+    if (tid < RESHARD_MAX_TOP) sm.rank[tid] = 0;
+  }
   float m = at_edge, s = at_edge > -INFINITY ? 1.0f : 0.0f, u = 0.0f;
   auto work = [&](uint4(&g)[kVecs]) {
     float largest = largest_in<T>(g);
@@ -389,21 +398,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     s = part.sum, u = part.moment;
   } else {
     tc::cluster_sync();
-    for (uint32_t o = 0; o < ctas; ++o) top = fmaxf(top, load_far(&part.top, o));
-    s = u = 0.0f;
-    for (uint32_t o = 0; o < ctas; ++o) {
-      const float shift = exponent(load_far(&part.top, o), top, c), factor = exp2_of(shift);
-      const float so = load_far(&part.sum, o);
-      u = fmaf(fmaf(so, shift, load_far(&part.moment, o)), factor, u);
-      s = fmaf(so, factor, s);
+    m = -INFINITY, s = u = 0.0f;
+    if (lane < int(ctas)) {
+      m = load_far(&part.top, lane);
+      s = load_far(&part.sum, lane);
+      u = load_far(&part.moment, lane);
     }
+    top = warp_max(m);
+    const float shift = exponent(m, top, c), factor = exp2_of(shift);
+    u = warp_sum(fmaf(s, shift, u) * factor);
+    s = warp_sum(s * factor);
   }
   const bool empty = !(top > -INFINITY);
   const float normal = empty ? 0.0f : logf(s);
   if (rank == 0 && tid == 0) {
     const float entropy = empty ? 0.0f : fmaxf(normal - u / s * kLn2, 0.0f);
     if (a.logprob) {
-      const float l = chosen;
+      const float l = clean<T>(to_float(chosen));
       a.logprob[r] = empty || l == -INFINITY ? -INFINITY : (l == top ? 0.0f : (l - top) * inverse) - normal;
     }
     if (a.entropy) a.entropy[r] = entropy;
@@ -413,24 +424,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     const int listed = int(part.listed);
     int all = listed;
     if (ctas > 1) {
-      all = 0;
-      for (uint32_t o = 0; o < ctas; ++o) all += int(load_far(&part.listed, o));
+      // a warp a list of another CTA: it is fetched, and counted before each token of this one
+      const int theirs = lane < int(ctas) ? int(load_far(&part.listed, lane)) : 0;
+      all = __reduce_add_sync(0xffffffffu, theirs);
+      for (int o = warp; o < int(ctas); o += kWarps) {
+        const int n = __shfl_sync(0xffffffffu, theirs, o);
+        if (o == int(rank)) continue;
+        for (int i = lane; i < n; i += 32) sm.other[o][i] = load_far(&sm.best[i], o);
+        __syncwarp();
+        for (int i = lane; i < listed; i += 32) {
+          const uint64_t own = sm.best[i];
+          int lo = 0, hi = n;
+          while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (sm.other[o][mid] > own) lo = mid + 1;
+            else hi = mid;
+          }
+          if (lo) atomicAdd(&sm.rank[i], uint32_t(lo));
+        }
+      }
+      __syncthreads();
     }
     for (int i = tid; i < listed; i += kThreads) {
       const uint64_t own = sm.best[i];
-      int at = i;
-      if (ctas > 1) {
-        for (uint32_t o = 0; o < ctas; ++o) {
-          if (o == rank) continue;
-          int lo = 0, hi = int(load_far(&part.listed, o));  // tokens of that CTA before this one
-          while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (load_far(&sm.best[mid], o) > own) lo = mid + 1;
-            else hi = mid;
-          }
-          at += lo;
-        }
-      }
+      const int at = i + int(sm.rank[i]);
       if (at >= k) continue;
       const float l = logit_of(uint32_t(own >> 32));
       a.top_token[r * a.ldtop + at] = int32_t(~uint32_t(own));
