@@ -46,14 +46,6 @@ struct BalanceArgs {
   float coef;
 };
 
-// The next kernel of the stream may start as far as it does not need this one.
-__device__ __forceinline__ void let_next_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Counts a sequence's choices: every CTA of a cluster counts its share of the tokens in
 // shared memory, then adds up the cluster's counts of its share of the experts.  With one
 // cluster a sequence the sums are the result; several add theirs to zeros.

@@ -120,9 +120,11 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     }
   };
   uint4 v[kVecs], w[kVecs];
+  sh.table[tid] = -1;
+  let_next_start();
+  wait_for_previous();
   policy = keep_policy();
   load(v, 0);
-  sh.table[tid] = -1;
   if (tid == 0) sh.again = sh.edges = 0;
   __syncthreads();
   // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none.  Every
@@ -357,9 +359,9 @@ reshard_status_t launch_distill(const DistillArgs& a, int64_t rows, int dev, int
   static_assert(RESHARD_MAX_VOCAB / 4 <= kMaxCluster * kMarked, "marks of a slice");
   void* args[] = {const_cast<DistillArgs*>(&a)};
   const char* what = "reshard_distill_loss";
-  if (!a.tail) return launch<distill_kernel<T, false>, 0>(what, dev, {rows * ctas, kThreads, 0, ctas, stream}, args);
+  if (!a.tail) return launch<distill_kernel<T, false>, 0>(what, dev, {rows * ctas, kThreads, 0, ctas, stream, true}, args);
   const size_t smem = size_t(cdiv(cdiv(granules, ctas), 4) * 4);
-  return launch<distill_kernel<T, true>, kMarked>(what, dev, {rows * ctas, kThreads, smem, ctas, stream}, args);
+  return launch<distill_kernel<T, true>, kMarked>(what, dev, {rows * ctas, kThreads, smem, ctas, stream, true}, args);
 }
 
 }  // namespace

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const uint32_t rank = tc::cluster_rank();
+  let_next_start();
   for (int i = tid; i < warps * E; i += threads) counted[i] = 0;
   const uint64_t batches = (uint64_t(a.n) + 31) / 32;
   const uint32_t part = rank * warps + warp, parts = ctas * warps;
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     const int e = b < b1 && i < a.n ? __ldg(a.experts + i) : -1;
     return uint32_t(e) < uint32_t(E) ? e : -1;
   };
+  wait_for_previous();
   int kept[kKept];
 #pragma unroll
   for (int i = 0; i < kKept; ++i) kept[i] = choice(b0 + i);
@@ -60,15 +62,29 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
-  for (int e = tid; e < E; e += threads) {
+  // each warp's first place of an expert among the CTA's: four lanes an expert, a quarter of the warps
+  // each (8 warps at least)
+  const int quarter = warps / 4, part_of = lane % 4;
+  for (int base = 0; base < E; base += threads / 4) {
+    const int e = base + tid / 4;
+    int32_t* column = counted + part_of * quarter * E + min(e, E - 1);
     int sum = 0;
 #pragma unroll 8
-    for (int w = 0; w < warps; ++w) {
-      const int c = counted[w * E + e];
-      counted[w * E + e] = sum;
-      sum += c;
+    for (int w = 0; w < quarter; ++w) sum += column[w * E];
+    int to = sum;  // and of the quarters before
+    for (int o = 1; o < 4; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, to, o, 4);
+      if (part_of >= o) to += v;
     }
-    total[e] = sum;
+    if (e >= E) continue;
+    if (part_of == 3) total[e] = to;
+    to -= sum;
+#pragma unroll 8
+    for (int w = 0; w < quarter; ++w) {
+      const int c = column[w * E];
+      column[w * E] = to;
+      to += c;
+    }
   }
   tc::cluster_sync();
   int carry = 0;  // choices of the experts before
@@ -77,10 +93,14 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     int before = 0, all = 0;
     if (e < E) {
       const uint32_t at = staging::smem_addr(&total[e]);
-      for (uint32_t r = 0; r < ctas; ++r) {
-        const int c = __float_as_int(tc::load_cluster(tc::in_cta(at, r)));
-        before += r < rank ? c : 0;
-        all += c;
+      int c[kSortCluster];
+#pragma unroll
+      for (uint32_t r = 0; r < kSortCluster; ++r)
+        c[r] = r < ctas ? __float_as_int(tc::load_cluster(tc::in_cta(at, r))) : 0;
+#pragma unroll
+      for (uint32_t r = 0; r < kSortCluster; ++r) {
+        before += r < rank ? c[r] : 0;
+        all += c[r];
       }
     }
     int to = all;  // inclusive scan over the CTA
@@ -90,11 +110,9 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     }
     if (lane == 31) warp_sum[warp] = to;
     __syncthreads();
-    int chunk = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) to += warp_sum[w];
-      chunk += warp_sum[w];
-    }
+    const int of_warp = lane < warps ? warp_sum[lane] : 0;
+    to += __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
+    const int chunk = __reduce_add_sync(0xffffffffu, of_warp);
     if (e < E) {
       first[e] = carry + to - all + before;
       if (rank == 0) a.offsets[e] = carry + to - all;
@@ -152,6 +170,8 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const __grid_constant__ D
   const uint32_t t = blockIdx.x / a.chunks * (256 / a.lanes) + threadIdx.x / a.lanes;
   if (t >= a.tokens) return;
   const uint32_t c0 = blockIdx.x % a.chunks * (kDispatchVecs * a.lanes) + lane;
+  let_next_start();
+  wait_for_previous();
   const V* x = reinterpret_cast<const V*>(a.x + t * a.ldx) + c0;
   V v[kDispatchVecs];
 #pragma unroll
@@ -184,6 +204,8 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
   const int32_t* slot = a.slot + int64_t(t) * a.topk;
   const uint32_t my_block = block0 + l * a.lanes;
   const bool scales = l < B && there && my_block * 128 < a.cols;
+  let_next_start();
+  wait_for_previous();
   Eight<T> e[B];
   uint2 q[B];
   float scale = 0.0f;
@@ -264,9 +286,29 @@ struct Access {
   static constexpr int kWords = W < 4 ? 1 : W / 4, kElements = W / int(sizeof(T)) > 0 ? W / int(sizeof(T)) : 1;
   uint32_t word[kWords];
 
-  __device__ void clear() {
+  // Zeros, or what lies at `at` where `on`: one predicated instruction, behind which the next load
+  // follows at once (as a branch the compiler draws what is done with the values into it, so that
+  // one load waits for another: 158 us for 4096 x 8 rows of 7168 instead of 85).
+  __device__ void load_if(bool on, const unsigned char* at) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) word[i] = 0;
+    if constexpr (W == 16) {
+      asm volatile("{.reg .pred p; setp.ne.u32 p, %5, 0; @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];}"
+                   : "+r"(word[0]), "+r"(word[1]), "+r"(word[2]), "+r"(word[3])
+                   : "l"(at), "r"(uint32_t(on)));
+    } else if constexpr (W == 8) {
+      asm volatile("{.reg .pred p; setp.ne.u32 p, %3, 0; @p ld.global.v2.u32 {%0, %1}, [%2];}"
+                   : "+r"(word[0]), "+r"(word[1])
+                   : "l"(at), "r"(uint32_t(on)));
+    } else if constexpr (W == 4) {
+      asm volatile("{.reg .pred p; setp.ne.u32 p, %2, 0; @p ld.global.u32 %0, [%1];}"
+                   : "+r"(word[0])
+                   : "l"(at), "r"(uint32_t(on)));
+    } else {
+      asm volatile("{.reg .pred p; setp.ne.u32 p, %2, 0; @p ld.global.u16 %0, [%1];}"
+                   : "+r"(word[0])
+                   : "l"(at), "r"(uint32_t(on)));
+    }
   }
   __device__ void load(const unsigned char* at) {
     if constexpr (W == 16) {
@@ -320,7 +362,7 @@ constexpr int kTogether = 8;  // choices whose rows are on their way at a time
 // out = sum of weight x row over a token's choices, in float32 in the order of the choices.  A CTA
 // has `span` accesses of its tokens' rows.
 template <typename T, int W>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineArgs a) {
+__global__ void __launch_bounds__(256, 3) combine_kernel(const __grid_constant__ CombineArgs a) {
   using A = Access<T, W>;
   constexpr int N = A::kElements;
   const uint32_t lane = threadIdx.x & (a.lanes - 1);
@@ -343,14 +385,15 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Co
     A v[kTogether];
 #pragma unroll
     for (int j = 0; j < kTogether; ++j) {
-      v[j].clear();
-      if (row[j]) v[j].load(row[j] + c * uint64_t(W));
+      v[j].load_if(row[j] != nullptr, row[j] + c * uint64_t(W));
     }
 #pragma unroll
     for (int j = 0; j < kTogether; ++j)
 #pragma unroll
       for (int i = 0; i < N; ++i) sum[i] = fmaf(w[j], v[j].value(i), sum[i]);
   };
+  let_next_start();
+  wait_for_previous();
   places(0);
   for (uint32_t c = c0; c < c1; c += a.lanes) {
     float sum[N];
@@ -370,7 +413,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Co
 // drows = weight x dout at the places of a token's choices; dweight = the products of dout with
 // its rows.  LANES: of a token, a warp or a CTA.
 template <typename T, int W, int LANES, bool DOT>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const __grid_constant__ CombineArgs a) {
+__global__ void __launch_bounds__(256, 3) combine_grad_kernel(const __grid_constant__ CombineArgs a) {
   using A = Access<T, W>;
   constexpr int N = A::kElements;
   __shared__ float part[8][kTogether];
@@ -379,6 +422,8 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const __grid_constant
   if (t >= a.tokens) return;  // (whole warps, and with a CTA a token none)
   const int64_t first = int64_t(t) * a.topk;
   const unsigned char* dout = a.dout + t * a.ldo;
+  let_next_start();
+  wait_for_previous();
   for (uint32_t j0 = 0; j0 < a.topk; j0 += kTogether) {
     const uint32_t together = min(uint32_t(kTogether), a.topk - j0);
     uint32_t s[kTogether];
@@ -394,8 +439,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const __grid_constant
       d.load(dout + c * uint64_t(W));
 #pragma unroll
       for (int j = 0; j < kTogether; ++j) {
-        r[j].clear();
-        if (DOT && s[j] < a.nrows) r[j].load(a.rows + s[j] * a.ldr + c * uint64_t(W));
+        if (DOT) r[j].load_if(s[j] < a.nrows, a.rows + s[j] * a.ldr + c * uint64_t(W));
       }
 #pragma unroll
       for (int j = 0; j < kTogether; ++j) {
@@ -475,6 +519,13 @@ reshard_status_t too_many(int64_t grid) {
   return grid < kMost ? RESHARD_OK : fail(RESHARD_ERR_UNSUPPORTED, "2^31 pieces of rows or more");
 }
 
+// Launches `grid` CTAs of 256 threads, which may start before the kernel in front of them has ended.
+template <auto Kernel, typename Args>
+reshard_status_t start(const char* what, int64_t grid, cudaStream_t stream, const Args& a) {
+  void* args[] = {const_cast<Args*>(&a)};
+  return launch<Kernel, 0>(what, 0, {grid, 256, 0, 0, stream}, args);
+}
+
 // What the calls on rows have in common.
 reshard_status_t check(int32_t dtype, int64_t tokens, int64_t topk, int64_t cols, int64_t nrows) {
   if (!float_dtype(dtype)) return fail(RESHARD_ERR_INVALID_ARG, "dtype must be BF16, FP16 or FP32");
@@ -518,7 +569,7 @@ extern "C" reshard_status_t reshard_expert_sort(const int32_t* experts, int64_t 
   void* args[] = {&a};
   return rs::op::launch<rs::sort_kernel, rs::kSortSmem>(
       "reshard_expert_sort", dev,
-      {ctas, int(32 * warps), size_t((warps + 2) * nexperts * 4), ctas, st}, args);
+      {ctas, int(32 * warps), size_t((warps + 2) * nexperts * 4), ctas, st, true}, args);
 }
 
 extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype, int64_t tokens,
@@ -563,11 +614,10 @@ extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype
     return rs::op::by_dtype(dtype, [&](auto t) {
       using T = decltype(t);
       constexpr int B = rs::kDispatchBlocks;
-      if (vec && many) rs::dispatch_fp8_kernel<T, true, B><<<unsigned(grid), 256, 0, st>>>(a);
-      else if (vec) rs::dispatch_fp8_kernel<T, true, 1><<<unsigned(grid), 256, 0, st>>>(a);
-      else if (many) rs::dispatch_fp8_kernel<T, false, B><<<unsigned(grid), 256, 0, st>>>(a);
-      else rs::dispatch_fp8_kernel<T, false, 1><<<unsigned(grid), 256, 0, st>>>(a);
-      return rs::op::launched("reshard_expert_dispatch");
+      if (vec && many) return rs::start<rs::dispatch_fp8_kernel<T, true, B>>("reshard_expert_dispatch", grid, st, a);
+      if (vec) return rs::start<rs::dispatch_fp8_kernel<T, true, 1>>("reshard_expert_dispatch", grid, st, a);
+      if (many) return rs::start<rs::dispatch_fp8_kernel<T, false, B>>("reshard_expert_dispatch", grid, st, a);
+      return rs::start<rs::dispatch_fp8_kernel<T, false, 1>>("reshard_expert_dispatch", grid, st, a);
     });
   }
   return rs::by_width(size, {x, rows}, {a.ldx, a.ldr, cols * size}, [&](auto w) {
@@ -578,8 +628,7 @@ extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype
     a.vecs = uint32_t(vecs);
     a.chunks = uint32_t(chunks);
     if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
-    rs::dispatch_kernel<typename rs::Word<w>::type><<<unsigned(grid), 256, 0, st>>>(a);
-    return rs::op::launched("reshard_expert_dispatch");
+    return rs::start<rs::dispatch_kernel<typename rs::Word<w>::type>>("reshard_expert_dispatch", grid, st, a);
   });
 }
 
@@ -623,8 +672,7 @@ extern "C" reshard_status_t reshard_expert_combine(const void* rows, int32_t dty
       a.span = uint32_t(lanes * rounds);
       a.chunks = uint32_t(chunks);
       if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
-      rs::combine_kernel<T, w><<<unsigned(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-      return rs::op::launched("reshard_expert_combine");
+      return rs::start<rs::combine_kernel<T, w>>("reshard_expert_combine", grid, static_cast<cudaStream_t>(stream), a);
     });
   });
 }
@@ -667,12 +715,11 @@ extern "C" reshard_status_t reshard_expert_combine_grad(const void* dout, int32_
       const bool cta = a.vecs > 128;  // a CTA a token, else a warp
       const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
       if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
-      const unsigned g = unsigned(grid);
-      if (dweight && cta) rs::combine_grad_kernel<T, w, 256, true><<<g, 256, 0, st>>>(a);
-      else if (dweight) rs::combine_grad_kernel<T, w, 32, true><<<g, 256, 0, st>>>(a);
-      else if (cta) rs::combine_grad_kernel<T, w, 256, false><<<g, 256, 0, st>>>(a);
-      else rs::combine_grad_kernel<T, w, 32, false><<<g, 256, 0, st>>>(a);
-      return rs::op::launched("reshard_expert_combine_grad");
+      const char* what = "reshard_expert_combine_grad";
+      if (dweight && cta) return rs::start<rs::combine_grad_kernel<T, w, 256, true>>(what, grid, st, a);
+      if (dweight) return rs::start<rs::combine_grad_kernel<T, w, 32, true>>(what, grid, st, a);
+      if (cta) return rs::start<rs::combine_grad_kernel<T, w, 256, false>>(what, grid, st, a);
+      return rs::start<rs::combine_grad_kernel<T, w, 32, false>>(what, grid, st, a);
     });
   });
 }

@@ -297,6 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
       }
     }
   };
+  let_next_start();
+  wait_for_previous();
   uint4 v[kVecs], w[kVecs];
   load(v, 0);
   const int target = a.target ? __ldg(a.target + r) : 0;
@@ -490,6 +492,8 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid
   const int g0 = chunk * kRound + tid;
   const bool full = (chunk + 1) * kRound <= row.n;
   const int edge = chunk == 0 ? row.edge() : -1;
+  let_next_start();
+  wait_for_previous();
   const int target = a.target ? __ldg(a.target + r) : -1;
   const float4 state = __ldg(a.state + r);  // largest logit, 1 / S, ln S, entropy
   float g = a.dlogprob && a.target ? __ldg(a.dlogprob + r) : 0.0f, h = a.dentropy ? __ldg(a.dentropy + r) : 0.0f;
@@ -551,7 +555,7 @@ reshard_status_t launch_threads(const LogprobArgs& a, int64_t rows, int ctas, in
   const size_t smem = sizeof(TopSmem) + size_t(2 * kThreads * (rounds < kGroups ? rounds : kGroups));
   void* args[] = {const_cast<LogprobArgs*>(&a)};
   return launch<logprob_kernel<T, TOP, kThreads>, TOP ? sizeof(TopSmem) + 2 * kThreads * kGroups : 0>(
-      "reshard_logprob", dev, {rows * ctas, kThreads, TOP ? smem : 0, ctas, stream}, args);
+      "reshard_logprob", dev, {rows * ctas, kThreads, TOP ? smem : 0, ctas, stream, true}, args);
 }
 
 template <typename T>
@@ -641,7 +645,8 @@ extern "C" reshard_status_t reshard_logprob_grad(const void* logits, int32_t dty
     a.chunks = int32_t(chunks > 1 ? chunks : 1);
     const int64_t grid = rows * a.chunks;
     if (grid >= int64_t(1) << 31) return fail(RESHARD_ERR_UNSUPPORTED, "2^31 pieces of rows or more");
-    rs::logprob_grad_kernel<T><<<unsigned(grid), rs::kGradThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return rs::op::launched("reshard_logprob_grad");
+    void* args[] = {&a};
+    return rs::op::launch<rs::logprob_grad_kernel<T>, 0>(
+        "reshard_logprob_grad", 0, {grid, rs::kGradThreads, 0, 0, static_cast<cudaStream_t>(stream)}, args);
   });
 }

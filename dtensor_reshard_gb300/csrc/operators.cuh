@@ -94,12 +94,21 @@ cudaError_t allow_smem(int dev) {
   return ce;
 }
 
+// The next kernel of the stream may start as far as it does not need this one.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 struct Launch {
   int64_t grid;
   int threads;
   size_t smem;
-  int cluster;  // CTAs; 0: may start before the kernel in front of it has ended
+  int cluster;  // CTAs; 0: none, and may start before the kernel in front of it has ended
   cudaStream_t stream;
+  bool early = false;  // a cluster too may: the kernel waits for the one in front before it reads or writes
 };
 template <auto Kernel, size_t MOST>
 reshard_status_t launch(const char* what, int dev, const Launch& l, void** args) {
@@ -110,16 +119,18 @@ reshard_status_t launch(const char* what, int dev, const Launch& l, void** args)
     cfg.blockDim = dim3(unsigned(l.threads));
     cfg.dynamicSmemBytes = l.smem;
     cfg.stream = l.stream;
-    cudaLaunchAttribute attr[1];
-    if (l.cluster == 0) {
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-    } else {
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim = {unsigned(l.cluster), 1, 1};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (l.cluster == 0 || l.early) {
+      attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (l.cluster != 0) {
+      attr[n].id = cudaLaunchAttributeClusterDimension;
+      attr[n++].val.clusterDim = {unsigned(l.cluster), 1, 1};
     }
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = unsigned(n);
     ce = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(Kernel), args);
   }
   if (ce != cudaSuccess)
