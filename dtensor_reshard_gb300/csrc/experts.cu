@@ -25,7 +25,9 @@ struct SortArgs {
 // A stable counting sort.  The choices go in order to the warps of a cluster (CTA by CTA); each
 // warp counts its own for every expert, the counts become each warp's first place of every
 // expert, and each warp goes through its choices again, 32 at a time, and gives them their
-// places: the expert's next one, and within the 32 by the lanes before with the same expert.
+// places: the expert's next one, and within the 32 by the lanes before with the same expert.  That takes
+// 180 instructions for 32 choices, which fill one cluster's SMs: several clusters count all of them,
+// and each gives some warps' choices their places (65536 choices: one cluster 13.9 us, eight 9.4).
 __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t counted[];  // [warps][nexperts], total [nexperts], first [nexperts]
   __shared__ int32_t warp_sum[32];
@@ -36,6 +38,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   const uint32_t rank = tc::cluster_rank();
+  const int copy = blockIdx.x / ctas, copies = gridDim.x / ctas;
   let_next_start();
   for (int i = tid; i < warps * E; i += threads) counted[i] = 0;
   const uint64_t batches = (uint64_t(a.n) + 31) / 32;
@@ -62,31 +65,23 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
-  // each warp's first place of an expert among the CTA's: four lanes an expert, a quarter of the warps
-  // each (8 warps at least)
-  const int quarter = warps / 4, part_of = lane % 4;
-  for (int base = 0; base < E; base += threads / 4) {
-    const int e = base + tid / 4;
-    int32_t* column = counted + part_of * quarter * E + min(e, E - 1);
+  // each warp's first place of an expert among the CTA's
+  for (int e = tid; e < E; e += threads) {
     int sum = 0;
-#pragma unroll 8
-    for (int w = 0; w < quarter; ++w) sum += column[w * E];
-    int to = sum;  // and of the quarters before
-    for (int o = 1; o < 4; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, to, o, 4);
-      if (part_of >= o) to += v;
+    for (int w = 0; w < warps; w += 8) {  // (eight warps at least)
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = counted[(w + i) * E + e];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        counted[(w + i) * E + e] = sum;
+        sum += c[i];
+      }
     }
-    if (e >= E) continue;
-    if (part_of == 3) total[e] = to;
-    to -= sum;
-#pragma unroll 8
-    for (int w = 0; w < quarter; ++w) {
-      const int c = column[w * E];
-      column[w * E] = to;
-      to += c;
-    }
+    total[e] = sum;
   }
-  tc::cluster_sync();
+  if (ctas > 1) tc::cluster_sync();
+  else __syncthreads();
   int carry = 0;  // choices of the experts before
   for (int base = 0; base < E; base += threads) {
     const int e = base + tid;
@@ -115,13 +110,13 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     const int chunk = __reduce_add_sync(0xffffffffu, of_warp);
     if (e < E) {
       first[e] = carry + to - all + before;
-      if (rank == 0) a.offsets[e] = carry + to - all;
+      if (rank == 0 && copy == 0) a.offsets[e] = carry + to - all;
     }
     carry += chunk;
     __syncthreads();
   }
-  if (rank == 0 && tid == 0) a.offsets[E] = carry;
-  tc::cluster_arrive();  // this CTA has read the others' totals
+  if (rank == 0 && copy == 0 && tid == 0) a.offsets[E] = carry;
+  if (ctas > 1) tc::cluster_arrive();  // this CTA has read the others' totals
   auto give = [&](uint32_t b, int e) {
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     const int before = __popc(same & ((1u << lane) - 1));
@@ -133,19 +128,21 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
     const uint64_t i = uint64_t(b) * 32 + lane;
     if (b < b1 && i < a.n) a.slot[i] = place;
   };
-#pragma unroll
-  for (int i = 0; i < kKept; ++i)
-    if (b0 + i < b1) give(b0 + i, kept[i]);
+  // (in a loop of few instructions: unrolled, fetching them costs more than running them)
+  const bool ours = warp * copies / warps == copy;
 #pragma unroll 1
-  for (uint32_t b = b0 + kKept; b < b1; b += 4) {
-    int e[4];
+  for (uint32_t b = b0; ours && b < b1; b += kKept) {
+    if (b != b0)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = choice(b + i);
+      for (int i = 0; i < kKept; ++i) kept[i] = choice(b + i);
+#pragma unroll 1
+    for (uint32_t i = 0; i < kKept && b + i < b1; ++i) {
+      give(b + i, kept[0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (b + i < b1) give(b + i, e[i]);
+      for (int j = 1; j < kKept; ++j) kept[j - 1] = kept[j];
+    }
   }
-  tc::cluster_wait();
+  if (ctas > 1) tc::cluster_wait();
 }
 
 // --------------------------------------------------------------------------- dispatch
@@ -567,9 +564,11 @@ extern "C" reshard_status_t reshard_expert_sort(const int32_t* experts, int64_t 
   while ((warps + 2) * nexperts * 4 > int64_t(rs::kSortSmem)) warps /= 2;
   const int ctas = n <= warps * 32 * rs::kKept ? 1 : rs::kSortCluster;
   void* args[] = {&a};
+  // clusters that share the places: a warp of each scheduler has some in all of them
+  const int64_t copies = n <= ctas * warps * 32 || warps < 8 ? 1 : warps / 4;
   return rs::op::launch<rs::sort_kernel, rs::kSortSmem>(
       "reshard_expert_sort", dev,
-      {ctas, int(32 * warps), size_t((warps + 2) * nexperts * 4), ctas, st, true}, args);
+      {copies * ctas, int(32 * warps), size_t((warps + 2) * nexperts * 4), ctas, st, true}, args);
 }
 
 extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype, int64_t tokens,

@@ -40,15 +40,16 @@ struct Part {
 struct TopSmem {
   union {
     struct {
-      uint32_t key[kCap], index[kCap];
-      uint32_t hit[kCap];  // groups with such tokens
+      uint64_t listed[kCap];  // key, then ~index: the largest first
+      uint32_t hit[kCap];     // groups with such tokens
     };
     uint64_t other[kMaxCluster][RESHARD_MAX_TOP];  // in the end: the lists of the cluster's CTAs
   };
-  uint64_t best[RESHARD_MAX_TOP];  // key, then ~index: the largest first
+  uint64_t best[RESHARD_MAX_TOP];  // the most likely of them in order
   uint32_t rank[RESHARD_MAX_TOP];  // how many tokens of other CTAs come before each
   uint32_t hist[256], count[32];
   uint32_t n, n2, digit, hits;
+  uint32_t either[kMany / 32], common[kMany / 32];
 };
 
 __device__ __forceinline__ uint64_t place_of(uint32_t key, uint32_t index) {
@@ -70,7 +71,7 @@ __device__ __forceinline__ T load_far(const T* at, uint32_t rank) {
 // Adds a token to the list; beyond its end it is only counted.
 __device__ __forceinline__ void append(TopSmem& sm, float l, int index) {
   const uint32_t at = atomicAdd(&sm.n, 1u);
-  if (at < uint32_t(kCap)) sm.key[at] = key_of(l), sm.index[at] = uint32_t(index);
+  if (at < uint32_t(kCap)) sm.listed[at] = place_of(key_of(l), uint32_t(index));
 }
 
 // A logit's bucket: the upper 16 bits of its key, 0 for -inf.
@@ -78,32 +79,43 @@ __device__ __forceinline__ uint32_t bucket_of(float l) { return l > -INFINITY ? 
 
 // The largest bucket that at least k threads' buckets reach, so that at least k tokens do; 1, which
 // all finite logits reach, where fewer have one.
-__device__ uint32_t shared_bucket(uint32_t mine, int k) {
-  uint32_t bucket = 0;
-#pragma unroll
-  for (int b = 15; b >= 0; --b)
+// Bits that all have alike take no step.
+template <int kThreads>
+__device__ uint32_t shared_bucket(uint32_t mine, int k, uint32_t* either, uint32_t* common) {
+  const uint32_t any = __reduce_or_sync(0xffffffffu, mine), all = __reduce_and_sync(0xffffffffu, mine);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) either[warp] = any, common[warp] = all;
+  __syncthreads();
+  const uint32_t some = __reduce_or_sync(0xffffffffu, lane < kThreads / 32 ? either[lane] : 0);
+  uint32_t bucket = __reduce_and_sync(0xffffffffu, lane < kThreads / 32 ? common[lane] : 0xffffu);
+  const uint32_t open = some & ~bucket;
+  bucket &= ~((2u << (31 - __clz(int(open | 1)))) - 1);  // of the bits above the highest open one
+#pragma unroll 1
+  for (int b = 31 - __clz(int(open | 1)); b >= 0; --b)
     if (__syncthreads_count(mine >= (bucket | 1u << b)) >= k) bucket |= 1u << b;
   return max(bucket, 1u);
 }
 
 // Lists the tokens that reach the bucket: of the groups that do, which are read again.  Groups are of
-// `per` rounds each.  Returns whether all are listed.
+// 2^log2_per rounds each.  Returns whether all are listed.
 template <typename T, int kThreads>
-__device__ bool list_reaching(TopSmem& sm, const uint16_t* noted, const Slice<T>& row, int rounds, int per,
+__device__ bool list_reaching(TopSmem& sm, const uint16_t* noted, const Slice<T>& row, int rounds, int log2_per,
                               uint32_t bucket) {
   constexpr int kPer = Slice<T>::kPer;
   const int tid = threadIdx.x;
-  for (int i = 0; i * per < rounds; ++i)
+  for (int i = 0; i << log2_per < rounds; ++i)
     if (noted[i * kThreads + tid] >= bucket) {
       const uint32_t at = atomicAdd(&sm.hits, 1u);
       if (at < uint32_t(kCap)) sm.hit[at] = uint32_t(i * kThreads + tid);
     }
   __syncthreads();
-  const uint32_t hits = sm.hits, granules = uint32_t(per * kVecs);
+  const uint32_t hits = sm.hits;
+  static_assert(kVecs == 4, "of a round");
+  const int log2_granules = log2_per + 2;  // of a group
   if (hits > uint32_t(kCap)) return false;
-  for (uint32_t w = tid; w < hits * granules; w += kThreads) {
-    const uint32_t h = sm.hit[w / granules], q = w % granules;
-    const int round = int(h / kThreads) * per + int(q / kVecs);
+  for (uint32_t w = tid; w < hits << log2_granules; w += kThreads) {
+    const uint32_t h = sm.hit[w >> log2_granules], q = w & ((1u << log2_granules) - 1);
+    const int round = (int(h / kThreads) << log2_per) + int(q / kVecs);
     const int g = (round * kVecs + int(q % kVecs)) * kThreads + int(h % kThreads);
     if (round >= rounds || g >= row.n) continue;
     const uint4 v = __ldg(row.granules() + g);
@@ -124,13 +136,9 @@ __device__ void rank_listed(TopSmem& sm, int n, int k) {
   const int tid = threadIdx.x;
   if (n > kFew) {
     // the k-th largest key, by its bits; what reaches it goes to the front of the list
-    uint32_t key[kCap / kThreads], index[kCap / kThreads];
+    uint64_t mine[kCap / kThreads];
 #pragma unroll
-    for (int i = 0; i < kCap / kThreads; ++i) {
-      const int at = i * kThreads + tid;
-      key[i] = at < n ? sm.key[at] : 0;
-      index[i] = at < n ? sm.index[at] : 0;
-    }
+    for (int i = 0; i < kCap / kThreads; ++i) mine[i] = i * kThreads + tid < n ? sm.listed[i * kThreads + tid] : 0;
     if (tid < 32) sm.count[tid] = 0;
     if (tid == 0) sm.n2 = 0;
     __syncthreads();
@@ -140,18 +148,15 @@ __device__ void rank_listed(TopSmem& sm, int n, int k) {
       const uint32_t at_least = cut | 1u << b;
       int c = 0;
 #pragma unroll
-      for (int i = 0; i < kCap / kThreads; ++i) c += key[i] >= at_least;
+      for (int i = 0; i < kCap / kThreads; ++i) c += uint32_t(mine[i] >> 32) >= at_least;
       c = __reduce_add_sync(0xffffffffu, c);
       if (tid % 32 == 0 && c) atomicAdd(&sm.count[b], uint32_t(c));
       __syncthreads();
       if (sm.count[b] >= uint32_t(k)) cut = at_least;
     }
 #pragma unroll
-    for (int i = 0; i < kCap / kThreads; ++i) {
-      if (key[i] < cut || i * kThreads + tid >= n) continue;
-      const uint32_t at = atomicAdd(&sm.n2, 1u);
-      sm.key[at] = key[i], sm.index[at] = index[i];
-    }
+    for (int i = 0; i < kCap / kThreads; ++i)
+      if (uint32_t(mine[i] >> 32) >= cut) sm.listed[atomicAdd(&sm.n2, 1u)] = mine[i];
     __syncthreads();
     n = int(sm.n2);
   }
@@ -161,9 +166,10 @@ __device__ void rank_listed(TopSmem& sm, int n, int k) {
   for (int base = 0; base < n; base += kThreads / per) {
     const int i = base + tid / per;
     if (base + (tid & ~31) / per >= n) break;  // a warp without any
-    const uint64_t own = i < n ? place_of(sm.key[i], sm.index[i]) : 0;
+    const uint64_t own = i < n ? sm.listed[i] : ~uint64_t(0);
     int before = 0;
-    for (int j = tid % per; j < n; j += per) before += place_of(sm.key[j], sm.index[j]) > own;
+#pragma unroll 4
+    for (int j = tid % per; j < n; j += per) before += sm.listed[j] > own;
     for (int o = 1; o < per; o *= 2) before += __shfl_xor_sync(0xffffffffu, before, o);
     if (i < n && tid % per == 0 && before < k) sm.best[before] = own;
   }
@@ -323,7 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
   T chosen = from_float<T>(0.0f);  // on its way until it is used
   if (rank == 0 && tid == 0 && a.logprob) chosen = row.row[target];
   uint16_t* noted = reinterpret_cast<uint16_t*>(dynamic + sizeof(TopSmem));  // [groups][kThreads]
-  const int per = (rounds + kGroups - 1) / kGroups;
+  int log2_per = 0;
+  while (kGroups << log2_per < rounds) ++log2_per;
   uint32_t group = 0;
   int in_group = 0;
   uint16_t* note = noted + tid;
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     if (TOP) {  // what the group has reached so far
       group = max(group, bucket_of(largest));
       *note = uint16_t(group);
-      if (++in_group == per) in_group = 0, group = 0, note += kThreads;
+      if (++in_group == 1 << log2_per) in_group = 0, group = 0, note += kThreads;
     }
     const float top = fmaxf(m, largest);
     const float shift = exponent(m, top, c), factor = exp2_of(shift);
@@ -381,9 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     if (lane == 0) warp_s[warp] = s, warp_u[warp] = u;
   }
   if (TOP) {
-    const uint32_t bucket = shared_bucket(bucket_of(m), k);
+    const uint32_t bucket = shared_bucket<kThreads>(bucket_of(m), k, sm.either, sm.common);
     if (bucket_of(at_edge) >= bucket) append(sm, at_edge, edge);
-    if (!list_reaching<T, kThreads>(sm, noted, row, rounds, per, bucket))
+    if (!list_reaching<T, kThreads>(sm, noted, row, rounds, log2_per, bucket))
       list_again<T, kThreads>(sm, row, rank == 0, k);
     rank_listed<kThreads>(sm, int(sm.n), k);
   } else {
