@@ -31,8 +31,6 @@ struct DistillArgs {
   float* loss;
   void* dlogits;
   int32_t ntop;
-  bool tail;   // the teacher's remaining probability is one more outcome
-  bool alike;  // logits and gradients lie alike on 16 bytes
 };
 
 // What the threads of a CTA, and the CTAs of a cluster, tell each other.
@@ -87,7 +85,7 @@ __device__ double log_of(float x) {
   return fma(double(n), 0.69314718055994530942, double(logf(m)));
 }
 
-template <typename T, bool TAIL>
+template <typename T, bool TAIL, bool ALIKE>
 __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kPer = Slice<T>::kPer;
   extern __shared__ uint32_t marks[];
@@ -123,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   sh.table[tid] = -1;
   let_next_start();
   wait_for_previous();
-  policy = keep_policy();
+  policy = to ? keep_policy() : drop_policy();
   load(v, 0);
   if (tid == 0) sh.again = sh.edges = 0;
   __syncthreads();
@@ -146,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   }
   y_top = warp_max(y_top);
   auto put_zeros = [&] {
-    for (int g = tid; g < row.n; g += kThreads) store_granule(to + row.first + g * kPer, make_uint4(0, 0, 0, 0), a.alike);
+    for (int g = tid; g < row.n; g += kThreads) store_granule<ALIKE>(to + row.first + g * kPer, make_uint4(0, 0, 0, 0));
     if (edge >= 0) to[edge] = from_float<T>(0.0f);
   };
   if (!(y_top > -INFINITY)) {  // a row that does not count
@@ -285,15 +283,14 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
       for (int i = 0; i < kVecs * kPer; i += 2)
         set_pair(e + i, tc::unpack2(mul2(exp2_both(mul2(add2(pair(pair_of(e + i)), minus), c2)), A)));
       const int g0 = round * kRound + tid;
-      if (a.alike && (round + 1) * kRound <= row.n) {
-        uint4* p = reinterpret_cast<uint4*>(begin) + g0;
+      if ((round + 1) * kRound <= row.n) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) __stcs(p + j * kThreads, v[j]);
+        for (int j = 0; j < kVecs; ++j) store_granules<ALIKE>(begin + (g0 + j * kThreads) * kPer, v[j]);
       } else {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           const int g = g0 + j * kThreads;
-          if (g < row.n) store_granule(begin + g * kPer, v[j], a.alike);
+          if (g < row.n) store_granule<ALIKE>(begin + g * kPer, v[j]);
         }
       }
     };
@@ -349,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
 }
 
 template <typename T>
-reshard_status_t launch_distill(const DistillArgs& a, int64_t rows, int dev, int sms, cudaStream_t stream) {
+reshard_status_t launch_distill(const DistillArgs& a, bool tail, int64_t rows, int dev, int sms,
+                                cudaStream_t stream) {
   // CTAs a row: more than one while SMs would stay without one, and a slice has 8 KiB or more; or
   // where one could not mark its elements
   const int64_t granules = a.vocab * int64_t(sizeof(T)) / 16;
@@ -359,9 +357,14 @@ reshard_status_t launch_distill(const DistillArgs& a, int64_t rows, int dev, int
   static_assert(RESHARD_MAX_VOCAB / 4 <= kMaxCluster * kMarked, "marks of a slice");
   void* args[] = {const_cast<DistillArgs*>(&a)};
   const char* what = "reshard_distill_loss";
-  if (!a.tail) return launch<distill_kernel<T, false>, 0>(what, dev, {rows * ctas, kThreads, 0, ctas, stream, true}, args);
-  const size_t smem = size_t(cdiv(cdiv(granules, ctas), 4) * 4);
-  return launch<distill_kernel<T, true>, kMarked>(what, dev, {rows * ctas, kThreads, smem, ctas, stream, true}, args);
+  const size_t smem = tail ? size_t(cdiv(cdiv(granules, ctas), 4) * 4) : 0;
+  const Launch l = {rows * ctas, kThreads, smem, ctas, stream, true};
+  // whether logits and gradients lie alike on 16 bytes
+  if ((reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.dlogits)) % 16 == 0 || !a.dlogits)
+    return tail ? launch<distill_kernel<T, true, true>, kMarked>(what, dev, l, args)
+                : launch<distill_kernel<T, false, true>, 0>(what, dev, l, args);
+  return tail ? launch<distill_kernel<T, true, false>, kMarked>(what, dev, l, args)
+              : launch<distill_kernel<T, false, false>, 0>(what, dev, l, args);
 }
 
 }  // namespace
@@ -405,9 +408,8 @@ extern "C" reshard_status_t reshard_distill_loss(const void* logits, int32_t dty
   if (ce != cudaSuccess)
     return fail(RESHARD_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(ce));
   const rs::DistillArgs a = {
-      logits, vocab, ld, ldtop, temperature, top_token, top_logprob, grad, loss, dlogits, ntop, tail != 0,
-      (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(dlogits)) % 16 == 0};
+      logits, vocab, ld, ldtop, temperature, top_token, top_logprob, grad, loss, dlogits, ntop};
   return rs::op::by_dtype(dtype, [&](auto t) {
-    return rs::launch_distill<decltype(t)>(a, rows, dev, sms, static_cast<cudaStream_t>(stream));
+    return rs::launch_distill<decltype(t)>(a, tail != 0, rows, dev, sms, static_cast<cudaStream_t>(stream));
   });
 }

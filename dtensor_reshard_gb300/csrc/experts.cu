@@ -218,13 +218,15 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
   };
   // blocks that lie inside the row
   const uint32_t blocks = there && col0 < a.cols ? (a.cols - col0 + step - 1) / step : 0;
-  const bool whole = __all_sync(0xffffffffu, VEC && a.cols % 128 == 0);
-  if (whole) {
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-      if (i < blocks) e[i].load(x + i * step);
-    quantise();
+  if (VEC && a.cols % 8 == 0) {  // each lane has eight values of a block, or none of the last
     const uint32_t to0 = col0 + 8 * l;
+    const uint32_t mine = there && to0 < a.cols ? (a.cols - to0 + step - 1) / step : 0;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (i < mine) e[i].load(x + i * step);
+      else if (a.cols % 128 != 0) e[i].load(x, 0);  // zeros beside values
+    }
+    quantise();
 #pragma unroll 4
     for (uint32_t j = 0; j < a.topk; ++j) {
       const uint32_t to = uint32_t(__ldg(slot + j));
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
       if (scales) a.scale[to * a.lds + my_block] = scale;
 #pragma unroll
       for (int i = 0; i < B; ++i)
-        if (i < blocks) *reinterpret_cast<uint2*>(row + i * step) = q[i];
+        if (i < mine) *reinterpret_cast<uint2*>(row + i * step) = q[i];
     }
     return;
   }

@@ -136,15 +136,38 @@ struct Slice {
 };
 
 // A granule to a row whose elements lie at `to`; ALIKE: on 16 bytes as those it was made of.
-template <typename T>
-__device__ __forceinline__ void store_granule(T* to, const uint4& v, bool alike) {
-  if (alike) {
+template <bool ALIKE, typename T>
+__device__ __forceinline__ void store_granule(T* to, const uint4& v) {
+  if (ALIKE) {
     __stcs(reinterpret_cast<uint4*>(to), v);
     return;
   }
   const T* e = reinterpret_cast<const T*>(&v);
 #pragma unroll
   for (int j = 0; j < Slice<T>::kPer; ++j) to[j] = e[j];
+}
+// The same of a whole warp whose lanes have granules next to each other: each lane stores the 16 aligned bytes that end in its own granule, the first
+// and the last the elements that are left at both ends (2048 x 131072 bf16: 225 us, element by
+// element 483; in float32, whose elements are twice as wide, 349 against 309).
+template <bool ALIKE, typename T>
+__device__ __forceinline__ void store_granules(T* to, const uint4& v) {
+  if (ALIKE || sizeof(T) == 4) return store_granule<ALIKE>(to, v);
+  constexpr int kPer = Slice<T>::kPer;
+  const int lane = threadIdx.x % 32;
+  const uint32_t skew = uint32_t(reinterpret_cast<uintptr_t>(to) % 16);  // bytes, alike in all lanes
+  uint4 before;
+  before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
+  before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
+  before.z = __shfl_up_sync(0xffffffffu, v.z, 1);
+  before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
+  const uint32_t shift = 16 - skew;  // of the two granules' bytes, those from here on
+  const uint4 out = staging::funnel16(before, v, shift / 4, 0x3210u + 0x1111u * (shift % 4));
+  if (lane > 0) __stcs(reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(to) - skew), out);
+  const int in_front = kPer - int(skew / sizeof(T));  // elements up to the next 16 bytes
+  const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if ((lane == 0 && j < in_front) || (lane == 31 && j >= in_front)) to[j] = e[j];
 }
 
 // The largest value of some granules: a NaN loses against any number, or (_or_nan) wins.
