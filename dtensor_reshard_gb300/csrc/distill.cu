@@ -272,8 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     put_zeros();
   } else if (to) {
     const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
-    const float slope = fmaxf(fminf(g * inverse, 3.402823466e38f), -3.402823466e38f);
-    const float scale = fmaxf(fminf(slope / sum * outside, 3.402823466e38f), -3.402823466e38f);
+    const float slope = factor_of(g * inverse, g), scale = factor_of(slope / sum * outside, g);
     const uint64_t A = both(scale), minus = both(-top);
     T* begin = to + row.first;
     auto put = [&](uint4(&v)[kVecs], int round) {
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     // the CTA's listed tokens, behind what was just written for them as for others
     if (to && !empty && first && (inside || at_end)) {
       const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
-      const float slope = fmaxf(fminf(g * inverse, 3.402823466e38f), -3.402823466e38f);
+      const float slope = factor_of(g * inverse, g);
       double mass = q;
       if (again)
         for (int j = tid + 1; j < k; ++j)

@@ -535,10 +535,10 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid
   const float at_edge = edge >= 0 ? row.at(edge) : 0.0f;
   if (largest_in<T>(v) == INFINITY) make_finite<T>(v);
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
-  // (finite, so that 0 times one is 0)
-  auto finite = [](float x) { return fmaxf(fminf(x, 3.402823466e38f), -3.402823466e38f); };
-  const float slope = finite(inverse * state.y), onehot = finite(g * inverse);
-  const float a0 = finite(-(g + h * (state.w - state.z)) * slope), b0 = finite(-h * slope) * kLn2;
+  const float both_of = g + h;  // (NaN or infinite where one of them is)
+  const float slope = inverse * state.y, onehot = factor_of(g * inverse, g);
+  const float a0 = factor_of(-(g + h * (state.w - state.z)) * slope, both_of);
+  const float b0 = factor_of(-h * slope, h) * kLn2;
   auto one = [&](float l) {
     const float z = exponent(l, state.x, c);
     return exp2_of(z) * fmaf(z, b0, a0);
@@ -619,15 +619,16 @@ extern "C" reshard_status_t reshard_logprob(const void* logits, int32_t dtype, i
   if (ok != RESHARD_OK) return ok;
   if (ntop < 0) return fail(RESHARD_ERR_INVALID_ARG, "negative size");
   if (ntop > RESHARD_MAX_TOP) return fail(RESHARD_ERR_UNSUPPORTED, "more alternatives than RESHARD_MAX_TOP");
-  if (rows == 0 || vocab == 0) return RESHARD_OK;
+  if (rows == 0) return RESHARD_OK;
   if (ntop > 0 && ldtop < ntop) return fail(RESHARD_ERR_INVALID_ARG, "row pitch smaller than a row");
-  if (!logits || (logprob && !target) || (ntop > 0 && (!top_token || !top_logprob)))
+  if (!logprob && !entropy && ntop == 0 && !state) return RESHARD_OK;
+  // (without a vocabulary no row counts, and none is read)
+  if ((!logits && vocab > 0) || (logprob && !target) || (ntop > 0 && (!top_token || !top_logprob)))
     return fail(RESHARD_ERR_INVALID_ARG, "null pointer");
   if (!rs::op::aligned(logits, rs::op::dtype_size(dtype)) || !rs::op::aligned(temperature, 4) ||
       !rs::op::aligned(target, 4) || !rs::op::aligned(logprob, 4) || !rs::op::aligned(entropy, 4) ||
       !rs::op::aligned(top_token, 4) || !rs::op::aligned(top_logprob, 4) || !rs::op::aligned(state, 16))
     return fail(RESHARD_ERR_INVALID_ARG, "pointer not aligned to its element type, or state to 16 bytes");
-  if (!logprob && !entropy && ntop == 0 && !state) return RESHARD_OK;
   int dev = 0, sms = 0;
   cudaError_t ce = cudaGetDevice(&dev);
   if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -35,14 +35,20 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// 1 / T as a factor: 1 for T <= 0 and NaN, and never infinite.
+constexpr float kLargest = 3.402823466e38f;
+// 1 / T as a factor: 1 for T <= 0 and NaN; never infinite, and never 0 (a logit of -inf has the
+// exponent -inf at any temperature).
 __device__ __forceinline__ float inverse_of(const float* temperature, int64_t r) {
   const float t = temperature ? __ldg(temperature + r) : 1.0f;
-  return t > 0.0f ? fminf(1.0f / t, 3.402823466e38f) : 1.0f;
+  return t > 0.0f ? fminf(fmaxf(1.0f / t, 0x1p-126f), kLargest) : 1.0f;
+}
+// A gradient's factor, finite where its gradient g is: 0 times it is 0.
+__device__ __forceinline__ float factor_of(float x, float g) {
+  return fabsf(g) < INFINITY ? fminf(fmaxf(x, -kLargest), kLargest) : x;
 }
 // The same for powers of 2.
 __device__ __forceinline__ float log2_scale(float inverse) {
-  return fminf(1.4426950408889634f * inverse, 3.402823466e38f);
+  return fminf(1.4426950408889634f * inverse, kLargest);
 }
 constexpr float kLn2 = 0.6931471805599453f;
 

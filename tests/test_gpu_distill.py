@@ -237,3 +237,33 @@ def test_a_teachers_list_of_its_own_logits():
     _, got = _check(x.cpu(), "bf16", token.cpu(), y.cpu(), True, temperature.cpu())
     assert np.max(np.abs(got)) < 1e-4
     _check(x.cpu(), "bf16", token.cpu(), y.cpu(), False, temperature.cpu())
+
+
+def test_an_infinite_temperature_and_gradients_that_are_not_finite():
+    rows, vocab, k = 4, 700, 9
+    x, token, y, _, _ = _case(rows, vocab, k, 23)
+    x[0, ::2] = -math.inf
+    token[0] = torch.arange(k) * 2 + 1
+    token[3] = -1
+    temperature = torch.tensor([math.inf, math.inf, 1.0, 1.0])
+    grad = torch.tensor([1.0, math.nan, math.inf, math.nan])
+    loss, dl = torch.empty(rows, device="cuda"), torch.empty(rows, vocab, device="cuda")
+    for tail in (False, True):
+        rs.reshard_distill_loss(x.cuda(), (rows, vocab), "fp32", token.cuda(), y.cuda(), k, loss=loss, dlogits=dl,
+                                tail=tail, temperature=temperature.cuda(), grad=grad.cuda())
+        torch.cuda.synchronize()
+        flat = x.clone()
+        flat[0] = torch.where(flat[0] > -math.inf, 0.0, flat[0])
+        want, bound, _, _ = lo.distill(_f64(flat[0]), 1.0, token[0].numpy(), _f64(y[0]), tail, 1.0, EPS["fp32"])
+        assert abs(float(loss[0]) - want) <= bound
+        assert bool(dl[0].isfinite().all()) and float(dl[0].abs().max()) <= 2.0 ** -120   # 1 / T
+        assert bool(dl[1].isnan().all()) and not bool(dl[2].isfinite().any()) and bool((dl[3] == 0).all())
+
+
+def test_a_value_that_is_infinite_is_not_taken_for_a_loss():
+    x, token, y, _, _ = _case(2, 300, 5, 29)
+    y[0, 1] = math.inf
+    loss = torch.empty(2, device="cuda")
+    rs.reshard_distill_loss(x.cuda(), (2, 300), "fp32", token.cuda(), y.cuda(), 5, loss=loss)
+    torch.cuda.synchronize()
+    assert math.isnan(float(loss[0])) and math.isfinite(float(loss[1]))

@@ -336,3 +336,38 @@ def test_rows_far_apart():
         assert np.array_equal(token[r].cpu().numpy(), lo.most_likely(y, 3))
         want, bound = lo.logprob_grad(y, 1.0, int(target[r]), 1.0, 0.0, EPS["bf16"])
         assert np.all(np.abs(_f64(view[r]) - want) <= bound)
+
+
+def test_an_infinite_temperature_and_no_vocabulary():
+    x = torch.randn(3, 500, generator=torch.Generator().manual_seed(3))
+    x[1, ::3] = -math.inf
+    x[2, 7] = math.nan
+    target = torch.tensor([4, 1, 9], dtype=torch.int32)
+    logprob, entropy, _, _, _ = _score(x, "fp32", target, torch.full((3,), math.inf), 0)
+    counts = [500, 500 - 167, 499]        # all that count are as likely as each other
+    for r in range(3):
+        want = math.log(counts[r])
+        # ln S of S equal ones, S exact: two roundings of the logarithm, and one of the result
+        assert abs(float(logprob[r]) + want) <= 4 * 2.0 ** -24 * want
+        assert abs(float(entropy[r]) - want) <= 4 * 2.0 ** -24 * want
+    lp, token = torch.full((2,), 5.0, device="cuda"), torch.full((2, 3), 5, dtype=torch.int32, device="cuda")
+    top = torch.full((2, 3), 5.0, device="cuda")
+    rs.reshard_logprob(None, (2, 0), "bf16", target=torch.zeros(2, dtype=torch.int32, device="cuda"), logprob=lp,
+                       top_token=token, top_logprob=top, ntop=3)
+    torch.cuda.synchronize()
+    assert bool((lp == 0).all()) and bool((token == -1).all()) and bool((top == -math.inf).all())
+
+
+def test_gradients_that_are_not_finite_stay_so():
+    x = torch.randn(5, 300, generator=torch.Generator().manual_seed(5))
+    x[4] = -math.inf
+    target = torch.tensor([1, 2, 3, -1, 5], dtype=torch.int32)
+    dl = torch.tensor([math.nan, math.inf, 1.0, math.nan, math.nan])
+    state, grad = torch.empty(5, 4, device="cuda"), torch.empty(5, 300, device="cuda")
+    rs.reshard_logprob(x.cuda(), (5, 300), "fp32", target=target.cuda(), state=state)
+    rs.reshard_logprob_grad(x.cuda(), (5, 300), "fp32", state, grad, target=target.cuda(), dlogprob=dl.cuda())
+    torch.cuda.synchronize()
+    assert bool(grad[0].isnan().all())
+    assert not bool(grad[1].isfinite().any())
+    assert bool(grad[2].isfinite().all())
+    assert bool((grad[3:] == 0).all())       # rows that do not count, or have no finite logit
