@@ -68,9 +68,27 @@ __device__ __forceinline__ T load_far(const T* at, uint32_t rank) {
   return reinterpret_cast<const T&>(v);
 }
 
+// An arrival at the cluster's barrier that orders nothing: what was read is in registers.
+__device__ __forceinline__ void arrive_read() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 // Brings `bytes` (a multiple of 16) at `at`, 16-byte aligned, to the L2 cache.
 __device__ __forceinline__ void prefetch(const void* at, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
+
+// Places for `count` entries of each lane of a warp behind the `taken` ones: one atomic a warp.
+__device__ __forceinline__ uint32_t claim(uint32_t count, uint32_t* taken) {
+  const int lane = threadIdx.x & 31;
+  uint32_t upto = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  uint32_t base = 0;
+  if (lane == 31 && upto) base = atomicAdd(taken, upto);
+  return __shfl_sync(0xffffffffu, base, 31) + upto - count;
 }
 
 // Adds a token to the list; beyond its end it is only counted.
@@ -78,15 +96,32 @@ __device__ __forceinline__ void append(TopSmem& sm, float l, int index) {
   const uint32_t at = atomicAdd(&sm.n, 1u);
   if (at < uint32_t(kCap)) sm.listed[at] = place_of(key_of(l), uint32_t(index));
 }
+// The same for a granule of each lane of a warp (or none): its tokens that reach the threshold.
+template <typename T>
+__device__ __forceinline__ void append_reaching(TopSmem& sm, const uint4& v, bool there, int first, float threshold) {
+  const T* e = reinterpret_cast<const T*>(&v);
+  uint32_t reaching = 0;
+#pragma unroll
+  for (int j = 0; j < Slice<T>::kPer; ++j) reaching |= uint32_t(to_float(e[j]) >= threshold) << j;
+  if (!there) reaching = 0;
+  uint32_t at = claim(__popc(reaching), &sm.n);
+  for (; reaching; reaching &= reaching - 1, ++at) {
+    const uint32_t j = __ffs(int(reaching)) - 1, w = j * sizeof(T) / 4;
+    uint32_t word = w < 2 ? (w < 1 ? v.x : v.y) : (w < 3 ? v.z : v.w);
+    if (sizeof(T) == 2 && (j & 1)) word >>= 16;
+    const float l = clean<T>(to_float(reinterpret_cast<const T&>(word)));
+    if (at < uint32_t(kCap)) sm.listed[at] = place_of(key_of(l), uint32_t(first) + j);
+  }
+}
 
 // A logit's bucket: the upper 16 bits of its key, 0 for -inf.
 __device__ __forceinline__ uint32_t bucket_of(float l) { return l > -INFINITY ? key_of(l + 0.0f) >> 16 : 0; }
 
-// The largest bucket that at least k threads' buckets reach, so that at least k tokens do; 1, which
-// all finite logits reach, where fewer have one.
-// Bits that all have alike take no step.
+// A logit that at least k threads' largest reach, so that at least k tokens do: the lowest one whose
+// key has the upper 16 bits that k threads' have at least, which are found bit by bit (none that all
+// have alike); the lowest finite one where fewer threads have any.
 template <int kThreads>
-__device__ uint32_t shared_bucket(uint32_t mine, int k, uint32_t* either, uint32_t* common) {
+__device__ float shared_threshold(uint32_t mine, int k, uint32_t* either, uint32_t* common) {
   const uint32_t any = __reduce_or_sync(0xffffffffu, mine), all = __reduce_and_sync(0xffffffffu, mine);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) either[warp] = any, common[warp] = all;
@@ -98,38 +133,37 @@ __device__ uint32_t shared_bucket(uint32_t mine, int k, uint32_t* either, uint32
 #pragma unroll 1
   for (int b = 31 - __clz(int(open | 1)); b >= 0; --b)
     if (__syncthreads_count(mine >= (bucket | 1u << b)) >= k) bucket |= 1u << b;
-  return max(bucket, 1u);
+  return bucket < 0x80 ? -kLargest : logit_of(bucket << 16);
 }
 
-// Lists the tokens that reach the bucket: of the groups that do, which are read again.  Groups are of
-// 2^log2_per rounds each.  Returns whether all are listed.
+// Lists the tokens that reach the threshold: of the groups that do, which are read again.  Groups are
+// of 2^log2_per rounds each.  Returns whether all are listed.
 template <typename T, int kThreads>
 __device__ bool list_reaching(TopSmem& sm, const uint16_t* noted, const Slice<T>& row, int rounds, int log2_per,
-                              uint32_t bucket) {
-  constexpr int kPer = Slice<T>::kPer;
-  const int tid = threadIdx.x;
-  for (int i = 0; i << log2_per < rounds; ++i)
-    if (noted[i * kThreads + tid] >= bucket) {
-      const uint32_t at = atomicAdd(&sm.hits, 1u);
-      if (at < uint32_t(kCap)) sm.hit[at] = uint32_t(i * kThreads + tid);
-    }
+                              float threshold) {
+  const int tid = threadIdx.x, groups = rounds > 0 ? ((rounds - 1) >> log2_per) + 1 : 0;
+  const uint32_t bucket = bucket_of(threshold);
+  uint32_t reaching = 0;  // a bit a group
+#pragma unroll 4
+  for (int i = 0; i < groups; ++i) reaching |= uint32_t(noted[i * kThreads + tid] >= bucket) << i;
+  uint32_t at = claim(__popc(reaching), &sm.hits);
+  for (; reaching; reaching &= reaching - 1, ++at)
+    if (at < uint32_t(kCap)) sm.hit[at] = uint32_t((__ffs(int(reaching)) - 1) * kThreads + tid);
   __syncthreads();
   const uint32_t hits = sm.hits;
-  static_assert(kVecs == 4, "of a round");
+  static_assert(kVecs == 4 && kGroups <= 32, "of a round; bits");
   const int log2_granules = log2_per + 2;  // of a group
   if (hits > uint32_t(kCap)) return false;
-  for (uint32_t w = tid; w < hits << log2_granules; w += kThreads) {
-    const uint32_t h = sm.hit[w >> log2_granules], q = w & ((1u << log2_granules) - 1);
+  const uint32_t all = hits << log2_granules;
+#pragma unroll 1
+  for (uint32_t w = tid; (w & ~31) < all; w += kThreads) {  // (a warp at a time)
+    const uint32_t h = w < all ? sm.hit[w >> log2_granules] : 0, q = w & ((1u << log2_granules) - 1);
     const int round = (int(h / kThreads) << log2_per) + int(q / kVecs);
     const int g = (round * kVecs + int(q % kVecs)) * kThreads + int(h % kThreads);
-    if (round >= rounds || g >= row.n) continue;
-    const uint4 v = __ldg(row.granules() + g);
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float l = clean<T>(to_float(e[j]));
-      if (bucket_of(l) >= bucket) append(sm, l, row.first + g * kPer + j);
-    }
+    const bool there = w < all && round < rounds && g < row.n;
+    uint4 v = Slice<T>::nothing();
+    if (there) v = __ldg(row.granules() + g);
+    append_reaching<T>(sm, v, there, row.first + g * Slice<T>::kPer, threshold);
   }
   __syncthreads();
   return sm.n <= uint32_t(kCap);
@@ -181,7 +215,7 @@ __device__ void rank_listed(TopSmem& sm, int n, int k) {
   __syncthreads();
 }
 
-// More tokens reach the bucket than the list holds, as where logits are alike: the k-th largest key
+// More tokens reach the threshold than the list holds, as where logits are alike: the k-th largest key
 // eight bits at a time, by histograms of the CTA's tokens, and then the list anew, of tokens that
 // share that key those of lowest index.
 template <typename T, int kThreads>
@@ -402,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     if (lane == 0) warp_s[warp] = s, warp_u[warp] = u;
   }
   if (TOP) {
-    const uint32_t bucket = shared_bucket<kThreads>(bucket_of(m), k, sm.either, sm.common);
-    if (bucket_of(at_edge) >= bucket) append(sm, at_edge, edge);
-    if (!list_reaching<T, kThreads>(sm, noted, row, rounds, log2_per, bucket))
+    const float threshold = shared_threshold<kThreads>(bucket_of(m), k, sm.either, sm.common);
+    if (at_edge >= threshold) append(sm, at_edge, edge);
+    if (!list_reaching<T, kThreads>(sm, noted, row, rounds, log2_per, threshold))
       list_again<T, kThreads>(sm, row, rank == 0, k);
     rank_listed<kThreads>(sm, int(sm.n), k);
   } else {
@@ -417,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
   }
   __syncthreads();
   // the row's
+  int theirs = 0;  // the most likely tokens of CTA `lane`
   if (ctas == 1) {
     s = part.sum, u = part.moment;
   } else {
@@ -426,11 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
       m = load_far(&part.top, lane);
       s = load_far(&part.sum, lane);
       u = load_far(&part.moment, lane);
+      if (TOP) theirs = int(load_far(&part.listed, lane));
     }
     top = warp_max(m);
     const float shift = exponent(m, top, c), factor = exp2_of(shift);
     u = warp_sum(fmaf(s, shift, u) * factor);
     s = warp_sum(s * factor);
+    if (!TOP) arrive_read();
   }
   const bool empty = !(top > -INFINITY);
   const float normal = empty ? 0.0f : logf(s);
@@ -448,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     int all = listed;
     if (ctas > 1) {
       // a warp a list of another CTA: it is fetched, and counted before each token of this one
-      const int theirs = lane < int(ctas) ? int(load_far(&part.listed, lane)) : 0;
       all = __reduce_add_sync(0xffffffffu, theirs);
       for (int o = warp; o < int(ctas); o += kWarps) {
         const int n = __shfl_sync(0xffffffffu, theirs, o);
@@ -466,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
           if (lo) atomicAdd(&sm.rank[i], uint32_t(lo));
         }
       }
+      arrive_read();  // this CTA has read what it needs of the others
       __syncthreads();
     }
     for (int i = tid; i < listed; i += kThreads) {
@@ -482,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         a.top_logprob[r * a.ldtop + i] = -INFINITY;
       }
   }
-  if (ctas > 1) tc::cluster_sync();  // no CTA's shared memory goes away under a reader
+  if (ctas > 1) tc::cluster_wait();  // no CTA's shared memory goes away under a reader
 }
 
 // --------------------------------------------------------------------------- gradient
