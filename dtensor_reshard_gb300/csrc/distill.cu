@@ -33,16 +33,56 @@ struct DistillArgs {
   int32_t ntop;
 };
 
-// What the threads of a CTA, and the CTAs of a cluster, tell each other.
+// A number as the sum of two float32, the second what the first's rounding left: 48 bits or so in
+// operations that these SMs have many of, where those on float64 take 16 clocks a warp each.
+struct Two {
+  float high, low;
+};
+__device__ __forceinline__ Two sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two s = sum_of(a.high, b.high);
+  return sum_of(s.high, __fadd_rn(s.low, __fadd_rn(a.low, b.low)));
+}
+__device__ __forceinline__ Two operator-(Two a) { return {-a.high, -a.low}; }
+__device__ __forceinline__ Two operator*(Two a, float b) {
+  const float p = __fmul_rn(a.high, b);
+  return sum_of(p, fmaf(a.low, b, fmaf(a.high, b, -p)));
+}
+// The warp's sum.
+__device__ __forceinline__ Two sum_of_warp(Two v) {
+  for (int o = 16; o; o >>= 1)
+    v = v + Two{__shfl_xor_sync(0xffffffffu, v.high, o), __shfl_xor_sync(0xffffffffu, v.low, o)};
+  return v;
+}
+// ln x for a positive finite x: of x = m 2^n, m next to 1, by float32 and n ln 2, so that it is off by
+// 2^-24 of ln m and not of ln x.
+__device__ __forceinline__ Two log_of(float x) {
+  int n = 0;
+  if (x < 0x1p-126f) x *= 0x1p32f, n = -32;
+  const uint32_t b = __float_as_uint(x) - 0x3f3504f3u;  // (sqrt(1/2))
+  n += int(b) >> 23;
+  const float m = __uint_as_float((b & 0x7fffffu) + 0x3f3504f3u);
+  return Two{0x1.62e430p-1f, -0x1.05c610p-29f} * float(n) + Two{logf(m), 0.0f};  // ln 2
+}
+
+// What the threads of a CTA, and the CTAs of a cluster, tell each other.  The teacher's probabilities
+// are in 64 bits (Q) where what is left of 1 counts, which can be small.
+template <typename Q>
 struct Shared {
   int32_t token[RESHARD_MAX_TOP];  // the teacher's list, -1 for what is no entry
-  double q[RESHARD_MAX_TOP];       // its probabilities, not yet scaled to 1
+  Q q[RESHARD_MAX_TOP];            // its probabilities, not yet scaled to 1
+  Q list_q[kListWarps];            // sums of the list's warps
+  Two list_term[kListWarps];
   int32_t table[kThreads];         // its tokens, by a hash: a token that stands there twice meets itself
-  double list_q[kListWarps], list_term[kListWarps];  // sums of the list's warps
   float list_e[kListWarps];
   float warp_top[kWarps], warp_other[kWarps];
   float part_top, part_other;      // of the CTA: its largest logit, its sum (over other tokens)
+  float rest;                      // q_R
   uint32_t again;                  // whether one does
+  uint32_t endless;                // whether the loss is infinite
   uint32_t edges;                  // listed tokens among those at the row's ends, a bit a thread
 };
 
@@ -74,23 +114,13 @@ __device__ __forceinline__ uint4 load_with(const uint4* at, uint64_t policy) {
   return v;
 }
 
-// ln x for a positive finite x, within 2^-24 where x is near 1 and 2^-24 |ln x| elsewhere: of x = m 2^n, m next
-// to 1, by float32 and n ln 2 by float64, whose own logarithm takes 1.5 us on these SMs.
-__device__ double log_of(float x) {
-  int n = 0;
-  if (x < 0x1p-126f) x *= 0x1p32f, n = -32;
-  const uint32_t b = __float_as_uint(x) - 0x3f3504f3u;  // (sqrt(1/2))
-  n += int(b) >> 23;
-  const float m = __uint_as_float((b & 0x7fffffu) + 0x3f3504f3u);
-  return fma(double(n), 0.69314718055994530942, double(logf(m)));
-}
-
 template <typename T, bool TAIL, bool ALIKE>
 __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kPer = Slice<T>::kPer;
   extern __shared__ uint32_t marks[];
   const uint8_t* listed = reinterpret_cast<const uint8_t*>(marks);
-  __shared__ Shared sh;
+  using Q = typename std::conditional<TAIL, double, float>::type;
+  __shared__ Shared<Q> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -123,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   wait_for_previous();
   policy = to ? keep_policy() : drop_policy();
   load(v, 0);
-  if (tid == 0) sh.again = sh.edges = 0;
+  if (tid == 0) sh.again = sh.edges = sh.endless = 0;
   __syncthreads();
   // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none.  Every
   // warp looks for an entry by itself, so that none waits for another.
@@ -158,24 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   const bool at_end = rank == 0 && mine >= 0 && (mine < row.head || mine >= row.last);
   const bool inside = mine >= 0 && place >= 0 && place < row.n * kPer;
   T student = from_float<T>(-INFINITY);  // its logit of this thread's entry, on its way until it is used
-  double q = 0.0;
-  if (warp < list_warps) {
-    sh.token[tid] = mine;
-    if (mine >= 0) {
-      for (uint32_t at = uint32_t(mine) * 2654435761u >> 23;; at = (at + 1) % kThreads) {  // half full at most
-        const int other = atomicCAS(&sh.table[at], -1, mine);
-        if (other == mine) sh.again = 1;
-        if (other == mine || other == -1) break;
-      }
-      student = row.row[mine];
-      // in 64 bits where what is left of 1 counts, which can be small
-      q = TAIL ? exp(double(y)) : double(expf(y - y_top));
-    }
-    sh.q[tid] = q;
-    double all = q;
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (lane == 0) sh.list_q[warp] = all;
-  }
+  if (mine >= 0) student = row.row[mine];
   const float at_edge = edge >= 0 ? row.at(edge) : -INFINITY;
   bool edge_counts = at_edge > -INFINITY;
   if (TAIL) {
@@ -185,6 +198,23 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     if (at_end) atomicOr(&sh.edges, 1u << (mine < row.head ? mine : mine - row.last + row.head));
     __syncthreads();
     edge_counts = edge_counts && !(sh.edges >> (tid & 31) & 1);
+  }
+  Q q = 0;
+  if (warp < list_warps) {
+    sh.token[tid] = mine;
+    if (mine >= 0) {
+      for (uint32_t at = uint32_t(mine) * 2654435761u >> 23;; at = (at + 1) % kThreads) {  // half full at most
+        const int other = atomicCAS(&sh.table[at], -1, mine);
+        if (other == mine) sh.again = 1;
+        if (other == mine || other == -1) break;
+      }
+      if constexpr (TAIL) q = exp(double(y));
+      else q = expf(y - y_top);
+    }
+    sh.q[tid] = q;
+    Q all = q;
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) sh.list_q[warp] = all;
   }
   // the sum over all tokens, or (TAIL) those that are not listed, relative to each thread's own
   // largest logit
@@ -253,20 +283,21 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   }
   const bool empty = !(top > -INFINITY);
   const float x = clean<T>(to_float(student));
-  float sum = other, outside = 1.0f;  // S; 1 - q_R / p_R
-  double rest = 0.0;                  // q_R
+  float sum = other, outside = 1.0f, rest = 0.0f;  // S; 1 - q_R / p_R; q_R
   if (TAIL) {
     if (warp < list_warps) {
       const float e = warp_sum(first ? exp2_of(exponent(x, top, c)) : 0.0f);
       if (lane == 0) sh.list_e[warp] = e;
     }
-    __syncthreads();
-    double all = 0.0;
-    for (int i = 0; i < list_warps; ++i) sum += sh.list_e[i], all += sh.list_q[i];
-    if (all < 1.0 && other > 0.0f) {  // (else it has nowhere to be)
-      rest = 1.0 - all;
-      outside = 1.0f - float(rest) * (sum / other);
+    if (tid == 0) {
+      Q left = 1;
+      for (int i = 0; i < list_warps; ++i) left -= sh.list_q[i];
+      sh.rest = left > 0 && other > 0.0f ? float(left) : 0.0f;  // (without other tokens it has nowhere to be)
     }
+    __syncthreads();
+    for (int i = 0; i < list_warps; ++i) sum += sh.list_e[i];
+    rest = sh.rest;
+    if (rest > 0.0f) outside = 1.0f - rest * (sum / other);
   }
   if (to && empty) {
     put_zeros();
@@ -304,32 +335,33 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     __syncthreads();
   }
   if (warp < list_warps) {
-    double all = 1.0, inv_q = 1.0;  // the list's sum where it is scaled to 1
+    float all = 1.0f;  // the list's sum where it is scaled to 1
     if (!TAIL) {
-      all = sh.list_q[0];
-      for (int i = 1; i < list_warps; ++i) all += sh.list_q[i];
-      inv_q = double(1.0f / float(all));
-      inv_q = fma(inv_q, fma(-all, inv_q, 1.0), inv_q);
+      all = float(sh.list_q[0]);
+      for (int i = 1; i < list_warps; ++i) all += float(sh.list_q[i]);
     }
+    const float inv_q = 1.0f / all;
     // the CTA's listed tokens, behind what was just written for them as for others
     if (to && !empty && first && (inside || at_end)) {
       const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
       const float slope = factor_of(g * inverse, g);
-      double mass = q;
+      Q mass = q;
       if (again)
         for (int j = tid + 1; j < k; ++j)
           if (sh.token[j] == mine) mass += sh.q[j];
       const float p = exp2_of(exponent(x, top, c)) / sum;
-      to[mine] = from_float<T>(slope * (p - float(mass * inv_q)));
+      to[mine] = from_float<T>(slope * (p - float(mass) * inv_q));
     }
     if (rank == 0 && a.loss) {
-      double term = 0.0;
-      q *= inv_q;
-      if (!(q <= 0.0)) {
-        const double z = x == top ? 0.0 : double(x - top) * double(inverse);
-        term = q * ((double(y) - (TAIL ? 0.0 : double(y_top)) - z) + (log_of(sum) - (TAIL ? 0.0 : log_of(float(all)))));
+      // q (ln q - ln p) = q ((y - ln of the list's sum) - (z - ln S))
+      Two term = {0.0f, 0.0f};
+      const float scaled = float(q) * inv_q;
+      if (mine >= 0 && !(scaled <= 0.0f)) {
+        const Two z = sum_of(x, -top) * inverse, ln_q = sum_of(y, TAIL ? 0.0f : -y_top);
+        if (z.high > -INFINITY) term = ((ln_q + -z) + (log_of(sum) + -log_of(all))) * scaled;
+        else sh.endless = 1;
       }
-      for (int o = 16; o; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+      term = sum_of_warp(term);
       if (lane == 0) sh.list_term[warp] = term;
     }
   }
@@ -337,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   if (rank != 0 || !a.loss) return;
   __syncthreads();
   if (tid == 0) {
-    double loss = sh.list_term[0];
-    for (int i = 1; i < list_warps; ++i) loss += sh.list_term[i];
-    if (rest > 0.0) loss += rest * (log_of(float(rest)) + log_of(sum) - log_of(other));
-    a.loss[r] = empty ? INFINITY : float(loss);
+    Two loss = sh.list_term[0];
+    for (int i = 1; i < list_warps; ++i) loss = loss + sh.list_term[i];
+    if (rest > 0.0f) loss = loss + (log_of(rest) + (log_of(sum) + -log_of(other))) * rest;
+    a.loss[r] = empty || sh.endless ? INFINITY : loss.high + loss.low;
   }
 }
 

@@ -618,10 +618,12 @@ reshard_status_t launch_threads(const LogprobArgs& a, int64_t rows, int ctas, in
 
 template <typename T>
 reshard_status_t launch_logprob(const LogprobArgs& a, int64_t rows, int dev, int sms, cudaStream_t stream) {
-  // CTAs a row: more than one while SMs would stay without one, and a slice has 4 KiB or more
+  // CTAs a row: more than one while an eighth of the SMs would stay without one (61 rows of 50021
+  // float32, with the gradient: two CTAs a row 12.3 us, four 10.2; 37 rows with alternatives: four, for
+  // 148 SMs, 9.6, eight 10.7), and a slice has 8 KiB or more
   const int64_t bytes = a.vocab * int64_t(sizeof(T));
   int ctas = 1;
-  while (ctas < kMaxCluster && rows * ctas < sms && bytes > ctas * 8192) ctas *= 2;
+  while (ctas < kMaxCluster && rows * ctas * 8 < int64_t(sms) * 7 && bytes > ctas * 8192) ctas *= 2;
   if (a.ntop == 0) return launch_threads<T, false, kSome>(a, rows, ctas, dev, stream);
   // the most likely tokens are told apart from the others by the threads' largest logits: with
   // twice as many threads as tokens wanted, few others reach the last of those
