@@ -13,13 +13,14 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMany = 512, kFew = 128;     // threads of a CTA: for long rows, and for short ones
+constexpr int kWarpsMost = kMany / 32;
 constexpr int kVecs = 4;                  // granules that a thread has on their way
-constexpr int kRound = kVecs * kThreads;
+constexpr int kTable = 512;               // of the list's tokens, half full at most
 constexpr int kMarked = 64 * 1024;        // granules of a slice whose listed elements can be marked
 constexpr int kMaxCluster = 8;
 constexpr int kListWarps = RESHARD_MAX_TOP / 32;
+static_assert(RESHARD_MAX_TOP <= kMany && 2 * RESHARD_MAX_TOP <= kTable, "an entry a thread");
 
 struct DistillArgs {
   const void* logits;
@@ -76,9 +77,9 @@ struct Shared {
   Q q[RESHARD_MAX_TOP];            // its probabilities, not yet scaled to 1
   Q list_q[kListWarps];            // sums of the list's warps
   Two list_term[kListWarps];
-  int32_t table[kThreads];         // its tokens, by a hash: a token that stands there twice meets itself
+  int32_t table[kTable];           // its tokens, by a hash: a token that stands there twice meets itself
   float list_e[kListWarps];
-  float warp_top[kWarps], warp_other[kWarps];
+  float warp_top[kWarpsMost], warp_other[kWarpsMost];
   float part_top, part_other;      // of the CTA: its largest logit, its sum (over other tokens)
   float rest;                      // q_R
   uint32_t again;                  // whether one does
@@ -114,9 +115,9 @@ __device__ __forceinline__ uint4 load_with(const uint4* at, uint64_t policy) {
   return v;
 }
 
-template <typename T, bool TAIL, bool ALIKE>
-__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
-  constexpr int kPer = Slice<T>::kPer;
+template <typename T, bool TAIL, bool ALIKE, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
+  constexpr int kPer = Slice<T>::kPer, kWarps = kThreads / 32, kRound = kVecs * kThreads;
   extern __shared__ uint32_t marks[];
   const uint8_t* listed = reinterpret_cast<const uint8_t*>(marks);
   using Q = typename std::conditional<TAIL, double, float>::type;
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
     }
   };
   uint4 v[kVecs], w[kVecs];
-  sh.table[tid] = -1;
+  for (int i = tid; i < kTable; i += kThreads) sh.table[i] = -1;
   let_next_start();
   wait_for_previous();
   policy = to ? keep_policy() : drop_policy();
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   if (warp < list_warps) {
     sh.token[tid] = mine;
     if (mine >= 0) {
-      for (uint32_t at = uint32_t(mine) * 2654435761u >> 23;; at = (at + 1) % kThreads) {  // half full at most
+      for (uint32_t at = uint32_t(mine) * 2654435761u >> 23;; at = (at + 1) % kTable) {  // half full at most
         const int other = atomicCAS(&sh.table[at], -1, mine);
         if (other == mine) sh.again = 1;
         if (other == mine || other == -1) break;
@@ -376,26 +377,38 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
   }
 }
 
-template <typename T>
-reshard_status_t launch_distill(const DistillArgs& a, bool tail, int64_t rows, int dev, int sms,
-                                cudaStream_t stream) {
-  // CTAs a row: more than one while SMs would stay without one, and a slice has 8 KiB or more; or
-  // where one could not mark its elements
+template <typename T, int kThreads>
+reshard_status_t launch_threads(const DistillArgs& a, bool tail, int64_t rows, int ctas, int dev, cudaStream_t stream) {
   const int64_t granules = a.vocab * int64_t(sizeof(T)) / 16;
-  int ctas = 1;
-  while (ctas < kMaxCluster && (granules > ctas * int64_t(kMarked) || (rows * ctas < sms && granules > ctas * 512)))
-    ctas *= 2;
-  static_assert(RESHARD_MAX_VOCAB / 4 <= kMaxCluster * kMarked, "marks of a slice");
   void* args[] = {const_cast<DistillArgs*>(&a)};
   const char* what = "reshard_distill_loss";
   const size_t smem = tail ? size_t(cdiv(cdiv(granules, ctas), 4) * 4) : 0;
   const Launch l = {rows * ctas, kThreads, smem, ctas, stream, true};
   // whether logits and gradients lie alike on 16 bytes
   if ((reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.dlogits)) % 16 == 0 || !a.dlogits)
-    return tail ? launch<distill_kernel<T, true, true>, kMarked>(what, dev, l, args)
-                : launch<distill_kernel<T, false, true>, 0>(what, dev, l, args);
-  return tail ? launch<distill_kernel<T, true, false>, kMarked>(what, dev, l, args)
-              : launch<distill_kernel<T, false, false>, 0>(what, dev, l, args);
+    return tail ? launch<distill_kernel<T, true, true, kThreads>, kMarked>(what, dev, l, args)
+                : launch<distill_kernel<T, false, true, kThreads>, 0>(what, dev, l, args);
+  return tail ? launch<distill_kernel<T, true, false, kThreads>, kMarked>(what, dev, l, args)
+              : launch<distill_kernel<T, false, false, kThreads>, 0>(what, dev, l, args);
+}
+
+template <typename T>
+reshard_status_t launch_distill(const DistillArgs& a, bool tail, int64_t rows, int dev, int sms,
+                                cudaStream_t stream) {
+  // CTAs a row: more than one while an eighth of the SMs would stay without one, and a slice has 32 KiB
+  // or more (64 rows of 9000 bf16: 4.9 us, with slices of 8 KiB 6.8); or where one could not mark its
+  // elements
+  const int64_t granules = a.vocab * int64_t(sizeof(T)) / 16;
+  int ctas = 1;
+  while (ctas < kMaxCluster && (granules > ctas * int64_t(kMarked) ||
+                                (rows * ctas * 8 < int64_t(sms) * 7 && granules > ctas * 2048)))
+    ctas *= 2;
+  static_assert(RESHARD_MAX_VOCAB / 4 <= kMaxCluster * kMarked, "marks of a slice");
+  // short rows in small CTAs, of which an SM has more (4000 rows of 300 bf16: 20 us, in CTAs of 512
+  // threads 70)
+  return granules <= kVecs * kFew * 2 && a.ntop <= kFew
+             ? launch_threads<T, kFew>(a, tail, rows, ctas, dev, stream)
+             : launch_threads<T, kMany>(a, tail, rows, ctas, dev, stream);
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kMany = 512, kSome = 256;  // threads of a CTA
+constexpr int kMany = 512, kSome = 256, kFewest = 128;  // threads of a CTA
 constexpr int kVecs = 4;          // granules that a thread has on their way
 constexpr int kMaxCluster = 8;
 constexpr int kCap = 1024;        // tokens that may be among the most likely, of a CTA
@@ -253,7 +253,7 @@ __device__ void list_again(TopSmem& sm, const Slice<T>& row, bool edges, int k) 
   uint32_t prefix = 0, need = uint32_t(k);
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) sm.hist[tid] = 0;
+    for (int i = tid; i < 256; i += kThreads) sm.hist[i] = 0;
     __syncthreads();
     each([&](int, const float(&l)[kPer]) {
 #pragma unroll
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
   uint16_t* note = noted + tid;
   if (TOP) {
     if (tid == 0) sm.n = sm.hits = 0;
-    if (tid < RESHARD_MAX_TOP) sm.rank[tid] = 0;
+    for (int i = tid; i < k; i += kThreads) sm.rank[i] = 0;
   }
   float m = at_edge, s = at_edge > -INFINITY ? 1.0f : 0.0f, u = 0.0f;
   auto work = [&](uint4(&g)[kVecs]) {
@@ -620,13 +620,20 @@ template <typename T>
 reshard_status_t launch_logprob(const LogprobArgs& a, int64_t rows, int dev, int sms, cudaStream_t stream) {
   // CTAs a row: more than one while an eighth of the SMs would stay without one (61 rows of 50021
   // float32, with the gradient: two CTAs a row 12.3 us, four 10.2; 37 rows with alternatives: four, for
-  // 148 SMs, 9.6, eight 10.7), and a slice has 8 KiB or more
+  // 148 SMs, 9.6, eight 10.7), and a slice has 32 KiB or more (16 rows of 9000 float32: 2.9 us, with slices
+  // of 8 KiB 4.1)
   const int64_t bytes = a.vocab * int64_t(sizeof(T));
   int ctas = 1;
-  while (ctas < kMaxCluster && rows * ctas * 8 < int64_t(sms) * 7 && bytes > ctas * 8192) ctas *= 2;
-  if (a.ntop == 0) return launch_threads<T, false, kSome>(a, rows, ctas, dev, stream);
+  while (ctas < kMaxCluster && rows * ctas * 8 < int64_t(sms) * 7 && bytes > ctas * 32768) ctas *= 2;
+  // short rows in small CTAs, of which an SM has more (4000 rows of 300 bf16: 10.2 us, with 20
+  // alternatives 24.7; in CTAs of 256 threads 18.1 and 43.4)
+  const bool is_short = bytes <= 16 * kVecs * kFewest * 2;
+  if (a.ntop == 0)
+    return is_short ? launch_threads<T, false, kFewest>(a, rows, ctas, dev, stream)
+                    : launch_threads<T, false, kSome>(a, rows, ctas, dev, stream);
   // the most likely tokens are told apart from the others by the threads' largest logits: with
   // twice as many threads as tokens wanted, few others reach the last of those
+  if (is_short && a.ntop <= kFewest / 2) return launch_threads<T, true, kFewest>(a, rows, ctas, dev, stream);
   return a.ntop <= kSome / 2 ? launch_threads<T, true, kSome>(a, rows, ctas, dev, stream)
                              : launch_threads<T, true, kMany>(a, rows, ctas, dev, stream);
 }
