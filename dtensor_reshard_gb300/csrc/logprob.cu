@@ -2,7 +2,20 @@
 // likely tokens of each row of logits; reshard_logprob_grad: the gradient in the logits.
 //
 // With z = (l - m) / T, S = sum e^z and U = sum e^z z: logprob = z_t - ln S, entropy =
-// ln S - U / S.  One pass: a thread carries its own largest logit with S and U relative to it.
+// ln S - U / S.  One pass: a thread carries its own largest logit with S and U relative to it, in
+// float32; differences of logits and 1 / T are rounded once each, exponentials are powers of 2.
+//
+// The pass is bound by HBM: 4096 rows of 131072 bf16 take 144 us (6.7 TB/s; 30000 instructions a row,
+// 62% of the issue slots), and so is the gradient, 152 us for 2048 rows read and written (7.0 TB/s).
+//
+// The most likely tokens: with the pass done, the k-th largest of the threads' own largest logits is
+// reached by k tokens, and by few others (77 of 131072 for k = 64); the groups of granules that reach it,
+// which each thread noted, are read again, their tokens listed, and the list is ranked exactly by
+// comparing all with all.  Nothing of the row's size is sorted or kept.  2048 rows of 131072 bf16 with 64
+// tokens: 95 us (71 of HBM alone: 70% of the issue slots, and a fifth of a row's time at barriers and the list),
+// with 1 token 97, with 128 131, with 256 219 us.  (A threshold from the first granules alone listed 512
+// tokens: 245 us.)  A row whose list overflows, as one of equal logits, goes through the histograms of
+// list_again: 2048 such rows 1.5 ms.
 #include <type_traits>
 
 #include "vocab_row.cuh"

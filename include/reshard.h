@@ -772,9 +772,9 @@ reshard_status_t reshard_plan_destroy(reshard_plan_t plan);
  * All matrices are row-major with a row pitch ("ld") in elements.  All of them follow
  * the conventions above: work is enqueued on `stream`, nothing is synchronised,
  * allocated or kept between calls, every call can be captured into a CUDA graph, and
- * an output must not overlap an input unless its call says so.  A call without rows or columns launches nothing
- * (the loss of no token is written as 0).
- * Sums do not depend on the order in which the GPU runs: equal inputs give equal bits.
+ * an output must not overlap an input unless its call says so.  A call without rows or columns
+ * launches nothing (but the loss of no token is written as 0, and so is what a row says without a
+ * vocabulary).  Sums do not depend on the order in which the GPU runs: equal calls give equal bits.
  */
 
 /* Scores of reshard_balance_loss. */
@@ -990,7 +990,8 @@ reshard_status_t reshard_expert_combine_grad(const void* dout, int32_t dtype, in
  * log-probability -inf.  A row of -inf and NaN alone has logprob -inf and entropy 0.  A row whose
  * target is outside 0..vocab - 1 does not count: logprob and entropy 0, no alternatives; with target
  * NULL every row counts.  What is drawn by reshard_sample at the same temperature has the same
- * log-probability here, to rounding.
+ * log-probability here, to rounding.  A row's sums are split by where it lies on 16 bytes and by how
+ * many rows there are: the same logits elsewhere, or among others, may differ by roundings.
  *
  * logits [rows][ld] of dtype BF16, FP16 or FP32 and any alignment; temperature, target [rows] in
  * device memory, each may be NULL (logprob then is); logprob, entropy [rows], each may be NULL;
