@@ -24,7 +24,7 @@ SOURCES = ["planner.cpp", "batch.cpp", "kernels.cu", "bulk_fanout.cu", "transpos
            "fp8_quantize.cu", "fp8_matmul.cu", "sample.cu", "balance.cu",
            "experts.cu", "logprob.cu", "distill.cu"]
 HEADERS = ["internal.h", "staging.cuh", "operators.cuh", "tensor_core.cuh", "fp8_block.cuh",
-           "vocab_row.cuh"]
+           "vocab_row.cuh", "shifted_rows.cuh"]
 
 
 def nvcc() -> str:

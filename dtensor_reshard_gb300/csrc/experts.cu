@@ -5,11 +5,13 @@
 // Beside the sort all of them move rows, each once, and are bound by HBM: 4096 tokens of 7168 bf16 with
 // 8 choices take 81 us to their places (6.4 TB/s), 49 us in 8 bits, 80 us back (6.7 TB/s), and 152 us
 // for both gradients (6.6 TB/s).  Rows that do not start on 16 bytes go in accesses of 8, 4 or 2 bytes:
-// 7170 columns back in 105 us, 7169 in 154 us, to their places in 122 and 128 us; in 8 bits rows of other than
-// eight columns each take 110 us.
+// 7170 columns back in 105 us; rows of 16-bit elements that no such access fits in shifted granules
+// (shifted_rows.cuh): 7169 columns back in 121 us, to their places in 113; in 8 bits, rows of columns
+// that are no multiple of 8 take 108 us.
 #include <type_traits>
 
 #include "fp8_block.cuh"
+#include "shifted_rows.cuh"
 
 namespace rs {
 namespace {
@@ -168,7 +170,7 @@ struct DispatchArgs {
 // Each row is read once and written to all of its places.  A thread has four accesses of its row on
 // their way, and makes a place's address once for them.
 constexpr int kDispatchVecs = 4;    // of a thread
-constexpr int kDispatchBlocks = 4;  // of a lane, in 8 bits, for many tokens
+constexpr int kDispatchBlocks = 4;  // of a lane, in 8 bits
 template <typename V>
 __global__ void __launch_bounds__(256) dispatch_kernel(const __grid_constant__ DispatchArgs a) {
   const uint32_t lane = threadIdx.x & (a.lanes - 1);
@@ -249,9 +251,12 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
     return;
   }
   int count[B];  // values of the block that lie inside the row
+  bool some[B];  // whether either half of the warp has any
 #pragma unroll
   for (int i = 0; i < B; ++i) {
     count[i] = i < blocks ? int(min(a.cols - (col0 + i * step), 128u)) : 0;
+    some[i] = __any_sync(0xffffffffu, count[i] > 0);
+    if (!some[i]) continue;
     const int left = min(max(count[i] - int(8 * l), 0), 8);
     if (VEC) {
       e[i].load(x + i * step, left);
@@ -270,7 +275,8 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
     uint8_t* row = a.rows + (on ? to * a.ldr + col0 : 0);
     if (on && scales) a.scale[to * a.lds + my_block] = scale;
 #pragma unroll
-    for (int i = 0; i < B; ++i) store_row(row + i * step, q[i], on ? count[i] : 0);
+    for (int i = 0; i < B; ++i)
+      if (some[i]) store_row(row + i * step, q[i], on ? count[i] : 0);
   }
 }
 
@@ -282,7 +288,7 @@ struct CombineArgs {
   const float* weight;
   float* dweight;
   int64_t ldr, ldo;        // bytes
-  uint32_t tokens, vecs;   // accesses of a row
+  uint32_t tokens, cols, vecs;  // accesses of a row
   uint32_t chunks, span;   // CTAs that share a row, and their accesses
   uint32_t nrows, topk, lanes;
 };
@@ -537,6 +543,16 @@ reshard_status_t start(const char* what, int64_t grid, cudaStream_t stream, cons
   return launch<Kernel, 0>(what, 0, {grid, 256, 0, 0, stream}, args);
 }
 
+// Whether rows go in shifted granules: of 16-bit elements, long enough for a warp's worth, and not
+// aligned to `least` bytes.  4096 x 8 rows of 7169 bf16, in accesses of an element and shifted: to their
+// places 128 and 112 us, back 154 and 121, gradients 278 and 230; of 7170, in accesses of two elements
+// and shifted: 124 and 108, 105 and 120, 201 and 225.  So least is 8 to their places, else 4.
+bool goes_shifted(int64_t size, int64_t cols, int64_t least, std::initializer_list<const void*> pointers,
+                  std::initializer_list<int64_t> bytes) {
+  return size == 2 && cols >= 256 && !all_aligned(least, pointers, bytes);
+}
+constexpr int64_t kLongRow = 1024;  // columns from which a CTA has a token, else a warp
+
 // What the calls on rows have in common.
 reshard_status_t check(int32_t dtype, int64_t tokens, int64_t topk, int64_t cols, int64_t nrows) {
   if (!float_dtype(dtype)) return fail(RESHARD_ERR_INVALID_ARG, "dtype must be BF16, FP16 or FP32");
@@ -618,12 +634,15 @@ extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype
     // sixteen lanes a block: as many of a CTA's sixteen on one token as it has blocks for
     a.lanes = 1;
     while (a.lanes < 16 && a.lanes < blocks) a.lanes *= 2;
-    const bool many = tokens * blocks >= 64 * 1024;  // every SM has a few CTAs all the same
-    const int64_t chunks = rs::op::cdiv(blocks, (many ? rs::kDispatchBlocks : 1) * int64_t(a.lanes));
+    const bool vec = rs::all_aligned(16, {x}, {a.ldx}) && rs::all_aligned(8, {rows}, {a.ldr});
+    // four blocks a lane where every SM has a few CTAs all the same, and five eighths of them are blocks of
+    // the row (4096 tokens to 8 places: 5120 columns 39.7 us, with one block 42.3; 4096 columns 36.6 and 31.6)
+    const int64_t four = rs::kDispatchBlocks * int64_t(a.lanes), fours = rs::op::cdiv(blocks, four);
+    const bool many = tokens * blocks >= 64 * 1024 && blocks * 8 >= fours * four * 5;
+    const int64_t chunks = many ? fours : rs::op::cdiv(blocks, int64_t(a.lanes));
     const int64_t grid = rs::op::cdiv(tokens, 16 / a.lanes) * chunks;
     a.chunks = uint32_t(chunks);
     if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
-    const bool vec = rs::all_aligned(16, {x}, {a.ldx}) && rs::all_aligned(8, {rows}, {a.ldr});
     return rs::op::by_dtype(dtype, [&](auto t) {
       using T = decltype(t);
       constexpr int B = rs::kDispatchBlocks;
@@ -632,6 +651,12 @@ extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype
       if (many) return rs::start<rs::dispatch_fp8_kernel<T, false, B>>("reshard_expert_dispatch", grid, st, a);
       return rs::start<rs::dispatch_fp8_kernel<T, false, 1>>("reshard_expert_dispatch", grid, st, a);
     });
+  }
+  if (rs::goes_shifted(size, cols, 8, {x, rows}, {a.ldx, a.ldr, cols * size})) {
+    const bool cta = cols >= rs::kLongRow;  // (elements are moved as they are: one type does)
+    const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
+    return cta ? rs::start<rs::shifted::dispatch_kernel<__half, 256, rs::DispatchArgs>>("reshard_expert_dispatch", grid, st, a)
+               : rs::start<rs::shifted::dispatch_kernel<__half, 32, rs::DispatchArgs>>("reshard_expert_dispatch", grid, st, a);
   }
   return rs::by_width(size, {x, rows}, {a.ldx, a.ldr, cols * size}, [&](auto w) {
     const int64_t vecs = cols * size / w;
@@ -671,8 +696,18 @@ extern "C" reshard_status_t reshard_expert_combine(const void* rows, int32_t dty
   a.tokens = uint32_t(tokens);
   a.nrows = uint32_t(nrows);
   a.topk = uint32_t(topk);
+  a.cols = uint32_t(cols);
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
+    if constexpr (sizeof(T) == 2) {
+      if (rs::goes_shifted(size, cols, 4, {rows, out}, {a.ldr, a.ldo, cols * size})) {
+        const bool cta = cols >= rs::kLongRow;
+        const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        return cta ? rs::start<rs::shifted::combine_kernel<T, 256, rs::CombineArgs>>("reshard_expert_combine", grid, st, a)
+                   : rs::start<rs::shifted::combine_kernel<T, 32, rs::CombineArgs>>("reshard_expert_combine", grid, st, a);
+      }
+    }
     return rs::by_width(size, {rows, out}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
       const int64_t vecs = cols * size / w, lanes = rs::lanes_of(vecs), groups = rs::op::cdiv(tokens, 256 / lanes);
       // a CTA a whole row, or so much of it that there are some 2048 of them
@@ -719,16 +754,29 @@ extern "C" reshard_status_t reshard_expert_combine_grad(const void* dout, int32_
   a.tokens = uint32_t(tokens);
   a.nrows = uint32_t(nrows);
   a.topk = uint32_t(topk);
+  a.cols = uint32_t(cols);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return rs::op::by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const void* read = dweight ? rows : nullptr;
+    const char* what = "reshard_expert_combine_grad";
+    if constexpr (sizeof(T) == 2) {
+      if (rs::goes_shifted(size, cols, 4, {dout, read, drows}, {a.ldr, a.ldo, cols * size})) {
+        const bool cta = cols >= rs::kLongRow;
+        const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
+        using rs::CombineArgs;
+        using namespace rs::shifted;
+        if (dweight && cta) return rs::start<combine_grad_kernel<T, 256, true, CombineArgs>>(what, grid, st, a);
+        if (dweight) return rs::start<combine_grad_kernel<T, 32, true, CombineArgs>>(what, grid, st, a);
+        if (cta) return rs::start<combine_grad_kernel<T, 256, false, CombineArgs>>(what, grid, st, a);
+        return rs::start<combine_grad_kernel<T, 32, false, CombineArgs>>(what, grid, st, a);
+      }
+    }
     return rs::by_width(size, {dout, read, drows}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
       a.vecs = uint32_t(cols * size / w);
       const bool cta = a.vecs > 128;  // a CTA a token, else a warp
       const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
       if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
-      const char* what = "reshard_expert_combine_grad";
       if (dweight && cta) return rs::start<rs::combine_grad_kernel<T, w, 256, true>>(what, grid, st, a);
       if (dweight) return rs::start<rs::combine_grad_kernel<T, w, 32, true>>(what, grid, st, a);
       if (cta) return rs::start<rs::combine_grad_kernel<T, w, 256, false>>(what, grid, st, a);

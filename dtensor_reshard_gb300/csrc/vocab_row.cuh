@@ -161,6 +161,10 @@ __device__ __forceinline__ void store_granules(T* to, const uint4& v) {
   constexpr int kPer = Slice<T>::kPer;
   const int lane = threadIdx.x % 32;
   const uint32_t skew = uint32_t(reinterpret_cast<uintptr_t>(to) % 16);  // bytes, alike in all lanes
+  if (skew == 0) {
+    __stcs(reinterpret_cast<uint4*>(to), v);
+    return;
+  }
   uint4 before;
   before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
   before.y = __shfl_up_sync(0xffffffffu, v.y, 1);

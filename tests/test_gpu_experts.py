@@ -258,3 +258,58 @@ def test_dispatch_gradient_is_a_combination_without_weights():
     a, b = (rows.double() * drows.double()).sum(), (x.double() * dx.double()).sum()
     assert abs(float(a - b)) <= k * 2.0 ** -24 * float((rows.double() * drows.double()).abs().sum())
     assert bool((dx[3] == 0).all()) and int(offsets[-1]) == (t - 1) * k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cols,pad", [(7168, 0), (7176, 0), (7172, 1), (5100, 3), (9216, 0), (2049, 0)])
+def test_many_tokens(cols, pad, dtype):
+    """Tokens enough for the kernels that take several blocks of a row a lane, or a whole row a CTA."""
+    tokens, topk = 2100, 3
+    nrows = tokens * topk
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = (torch.randn(tokens, cols, generator=g, device="cuda") * 3).to(DT[dtype])
+    slot = torch.randperm(nrows, generator=g, device="cuda").to(torch.int32).view(tokens, topk)
+    slot[5, 1] = -1
+    shape, kw = (tokens, topk, cols), dict(ldr=cols + pad)
+    xin, _ = _placed(x, cols + pad, pad, 9.0)
+    at = slot.long().flatten()
+    ok = at >= 0
+    token = torch.arange(tokens, device="cuda").repeat_interleave(topk)
+    # as they are
+    rows, view = _placed(torch.full((nrows, cols), 5.0, dtype=DT[dtype], device="cuda"), cols + pad, pad, 7.0)
+    rs.reshard_expert_dispatch(xin, shape, dtype, slot, rows, ldx=cols + pad, **kw)
+    want = torch.full((nrows, cols), 5.0, dtype=DT[dtype], device="cuda")
+    want[at[ok]] = x[token[ok]]
+    assert torch.equal(view[:, :cols], want) and bool((view[:, cols:] == 7.0).all())
+    # in 8 bits
+    B = -(-cols // 128)
+    q, s = torch.empty(tokens, cols, dtype=torch.uint8, device="cuda"), torch.empty(tokens, B, device="cuda")
+    rs.reshard_fp8_quantize(x, q, s, (tokens, cols), dtype)
+    rows8, view8 = _placed(torch.full((nrows, cols), 0xA5, dtype=torch.uint8, device="cuda"), cols + pad, pad, 0x5A)
+    scale = torch.full((nrows, B), -5.0, device="cuda")
+    rs.reshard_expert_dispatch(xin, shape, dtype, slot, rows8, scale=scale, ldx=cols + pad, **kw)
+    want8, wants = torch.full_like(view8[:, :cols], 0xA5), torch.full_like(scale, -5.0)
+    want8[at[ok]], wants[at[ok]] = q[token[ok]], s[token[ok]]
+    assert torch.equal(view8[:, :cols], want8) and bool((view8[:, cols:] == 0x5A).all()) and torch.equal(scale, wants)
+    # and back, with gradients: the bounds of expert_oracles
+    w = torch.randn(tokens, topk, generator=g, device="cuda")
+    out, oview = _placed(torch.full((tokens, cols), 5.0, dtype=DT[dtype], device="cuda"), cols + pad, pad, 7.0)
+    rs.reshard_expert_combine(rows, shape, dtype, slot, out, weight=w, ldo=cols + pad, **kw)
+    terms = torch.where(ok.view(tokens, topk, 1), x.double()[:, None] * w.double()[..., None], 0.0)
+    total, size = terms.sum(1), terms.abs().sum(1)
+    err = topk * 2.0 ** -24 * size
+    assert bool(((oview[:, :cols].double() - total).abs() <= err + EPS[dtype][0] * (total.abs() + err)
+                 + EPS[dtype][1]).all())
+    assert bool((oview[:, cols:] == 7.0).all())
+    drows, dview = _placed(torch.full((nrows, cols), 5.0, dtype=DT[dtype], device="cuda"), cols + pad, pad, 7.0)
+    dw = torch.empty(tokens, topk, device="cuda")
+    rs.reshard_expert_combine_grad(xin, shape, dtype, slot, rows=rows, weight=w, drows=drows, dweight=dw,
+                                   ldo=cols + pad, **kw)
+    # (exact products of the type's values by w, rounded to float32 and to the type)
+    grad = torch.full((nrows, cols), 5.0, dtype=torch.float64, device="cuda")
+    grad[at[ok]] = (x.double()[token] * w.double().flatten()[:, None])[ok]
+    assert bool(((dview[:, :cols].double() - grad).abs() <= (EPS[dtype][0] + 2.0 ** -23) * grad.abs()
+                 + EPS[dtype][1]).all())
+    dots = torch.where(ok.view(tokens, topk), (x.double() ** 2).sum(1)[:, None], 0.0)
+    assert bool(((dw.double() - dots).abs() <= (cols / 32 + 24) * 2.0 ** -24 * dots).all())
+    assert bool((dview[:, cols:] == 7.0).all())
