@@ -267,3 +267,21 @@ def test_a_value_that_is_infinite_is_not_taken_for_a_loss():
     rs.reshard_distill_loss(x.cuda(), (2, 300), "fp32", token.cuda(), y.cuda(), 5, loss=loss)
     torch.cuda.synchronize()
     assert math.isnan(float(loss[0])) and math.isfinite(float(loss[1]))
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_rows_of_the_largest_vocabulary(dtype, tail):
+    rows, vocab, k = 140, rs.MAX_VOCAB, 64
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(DT[dtype])
+    y = torch.log_softmax(x.float() + torch.randn(rows, vocab, generator=g, device="cuda"), 1).topk(k, dim=1)
+    token, value = y.indices.to(torch.int32), y.values.contiguous()
+    loss, grad = torch.empty(rows, device="cuda"), torch.empty_like(x)
+    rs.reshard_distill_loss(x, (rows, vocab), dtype, token, value, k, loss=loss, dlogits=grad, tail=tail)
+    torch.cuda.synchronize()
+    for r in (0, 70, 139):
+        l, lb, want, bound = lo.distill(lo.cleaned(_f64(x[r]), dtype), 1.0, token[r].cpu().numpy(), _f64(value[r]), tail,
+                                        1.0, EPS[dtype])
+        assert abs(float(loss[r]) - l) <= lb
+        assert np.all(np.abs(_f64(grad[r]) - want) <= bound)

@@ -371,3 +371,31 @@ def test_gradients_that_are_not_finite_stay_so():
     assert not bool(grad[1].isfinite().any())
     assert bool(grad[2].isfinite().all())
     assert bool((grad[3:] == 0).all())       # rows that do not count, or have no finite logit
+
+
+@pytest.mark.parametrize("dtype,ntop", [("fp32", 20), ("bf16", 100), ("fp16", 256)])
+def test_many_rows_of_the_largest_vocabulary(dtype, ntop):
+    """One CTA a row, whose threads note groups of several rounds."""
+    rows, vocab = 140, rs.MAX_VOCAB
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(DT[dtype])
+    target = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    lp, h = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    token, top = (torch.empty(rows, ntop, dtype=torch.int32, device="cuda"), torch.empty(rows, ntop, device="cuda"))
+    state, grad = torch.empty(rows, 4, device="cuda"), torch.empty_like(x)
+    rs.reshard_logprob(x, (rows, vocab), dtype, target=target, logprob=lp, entropy=h, top_token=token,
+                       top_logprob=top, ntop=ntop, state=state)
+    rs.reshard_logprob_grad(x, (rows, vocab), dtype, state, grad, target=target,
+                            dlogprob=torch.ones(rows, device="cuda"))
+    torch.cuda.synchronize()
+    for r in (0, 77, 139):
+        y = lo.cleaned(_f64(x[r]), dtype)
+        for got, (want, bound) in ((lp[r], lo.logprob(y, 1.0, int(target[r]))), (h[r], lo.entropy(y, 1.0))):
+            assert abs(float(got) - want) <= bound
+        best = lo.most_likely(y, ntop)
+        assert np.array_equal(token[r].cpu().numpy(), best)
+        bound = max(lo.logprob(y, 1.0, int(t))[1] for t in best[::10])
+        z, _, normal, _, _ = lo.softmax(y, 1.0)
+        assert np.all(np.abs(_f64(top[r]) - (z[best] - normal)) <= 2 * bound)
+        want, bound = lo.logprob_grad(y, 1.0, int(target[r]), 1.0, 0.0, EPS[dtype])
+        assert np.all(np.abs(_f64(grad[r]) - want) <= bound)
