@@ -1038,7 +1038,7 @@ reshard_status_t reshard_logprob_grad(const void* logits, int32_t dtype, int64_t
  * count: loss and gradient 0.  A token may stand in a list twice: its probabilities add up in the
  * gradient.  Where the student gives a token that has a teacher's probability none, the loss is
  * +inf and the gradient is as above; a row of -inf and NaN alone has loss +inf and gradient 0.
- * The teacher's sums and the loss are held in pairs of float32 (36 bits or more).
+ * The teacher's rest and the loss are held in pairs of float32 (42 bits or more), other sums in float32.
  *
  * logits [rows][ld] of dtype BF16, FP16 or FP32 and any alignment; temperature [rows] or NULL (1);
  * top_token, top_logprob [rows][ldtop]; grad [rows] or NULL (1); loss [rows] or NULL; dlogits

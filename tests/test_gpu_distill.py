@@ -285,3 +285,18 @@ def test_many_rows_of_the_largest_vocabulary(dtype, tail):
                                         1.0, EPS[dtype])
         assert abs(float(loss[r]) - l) <= lb
         assert np.all(np.abs(_f64(grad[r]) - want) <= bound)
+
+
+@pytest.mark.parametrize("k", [1, 2, 64, 256])
+@pytest.mark.parametrize("exponent", [10, 15, 20])
+def test_a_small_rest(k, exponent):
+    """What is left of 1 keeps its digits: its relative bound is 2^-21, 2^-41 of 1 at the smallest."""
+    g = torch.Generator().manual_seed(k + exponent)
+    n, vocab = 4, 5000
+    x = torch.randn(n, vocab, generator=g)
+    token = torch.stack([torch.randperm(vocab, generator=g)[:k] for _ in range(n)]).to(torch.int32)
+    y = torch.log(torch.softmax(torch.randn(n, k, generator=g, dtype=torch.float64) * 2, 1)
+                  * (1 - 2.0 ** -exponent)).float()
+    x.scatter_(1, token.long(), y + 20.0)      # a student that knows most of it
+    _check(x, "fp32", token, y, True)
+    _check(x.bfloat16(), "bf16", token, y, True)
