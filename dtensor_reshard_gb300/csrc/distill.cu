@@ -8,9 +8,14 @@
 // the rows that are on the SMs (two of 256 KB each).  The second pass goes backwards through what the
 // first was told to keep there, and tells it to drop what it has read.
 //
+// Where the rest counts, the sum R over the other tokens is held relative to their own largest logit m_R: a
+// student that is sure of the listed tokens leaves the others a probability below float32's range, but
+// ln p_R = (m_R - m) / T + ln R - ln S is an ordinary number, and so are the others' gradients,
+// e^((l - m_R) / T) times (p_R - q_R) / R.
+//
 // Bound by HBM, and by the tenth of the rows that the L2 has lost by the second pass: 2048 rows of
 // 131072 bf16 with 64 tokens take 190 us (158 of HBM alone, each logit read and written once; 611 MB
-// read where 509 would do, 5.7 TB/s), with the rest as an outcome 208 us.  Measured and dropped: a row
+// read where 509 would do, 5.7 TB/s), with the rest as an outcome 205 us.  Measured and dropped: a row
 // held in the shared memory of four CTAs (291 us) or two (286), whose fixed costs weigh more than a
 // second read; a part of it held in one CTA's (244: it leaves the loads too little of the L1).
 #include "vocab_row.cuh"
@@ -27,6 +32,7 @@ constexpr int kTable = 512;               // of the list's tokens, half full at 
 constexpr int kMarked = 64 * 1024;        // granules of a slice whose listed elements can be marked
 constexpr int kMaxCluster = 8;
 constexpr int kListWarps = RESHARD_MAX_TOP / 32;
+constexpr float kFarthest = 32768.0f;     // T between the row's largest logit and the others' beyond which p_R is 0
 static_assert(RESHARD_MAX_TOP <= kMany && 2 * RESHARD_MAX_TOP <= kTable, "an entry a thread");
 
 struct DistillArgs {
@@ -105,9 +111,9 @@ struct Shared {
   Two list_q[kListWarps];          // sums of the list's warps
   Two list_term[kListWarps];
   int32_t table[kTable];           // its tokens, by a hash: a token that stands there twice meets itself
-  float list_e[kListWarps];
+  float list_top[kListWarps], list_e[kListWarps];
   float warp_top[kWarpsMost], warp_other[kWarpsMost];
-  float part_top, part_other;      // of the CTA: its largest logit, its sum (over other tokens)
+  float part_top, part_other;      // of the CTA: its largest logit, its sum (TAIL: of other tokens)
   float rest;                      // q_R
   uint32_t again;                  // whether one does
   uint32_t endless;                // whether the loss is infinite
@@ -122,6 +128,16 @@ __device__ __forceinline__ void join(float& top, float& other, float c) {
   const float own = top;
   top = warp_max(top);
   other = warp_sum(other * exp2_of(exponent(own, top, c)));
+}
+
+static_assert(kVecs == 4, "marks of a round in a word");
+// The elements of a granule that `bits` name, as -inf.
+template <typename T>
+__device__ __forceinline__ void hide(uint4& v, uint32_t bits) {
+  T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+  for (int i = 0; i < Slice<T>::kPer; ++i)
+    if (bits >> i & 1) e[i] = from_float<T>(-INFINITY);
 }
 
 // Dynamic shared memory (TAIL): a byte a granule whose bits say which of its elements are listed.
@@ -246,10 +262,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
     if (lane == 0) sh.list_q[warp] = all;
   }
   // the sum over all tokens, or (TAIL) those that are not listed, relative to each thread's own
-  // largest logit
-  float m = at_edge, other = edge_counts ? 1.0f : 0.0f;
+  // largest logit of them
+  float m = edge_counts ? at_edge : -INFINITY, other = edge_counts ? 1.0f : 0.0f;
   bool unclean = false;
   auto add = [&](uint4(&v)[kVecs], int round) {
+    if (TAIL) {
+      uint32_t bits = 0;  // a byte a granule
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        const int g = round * kRound + j * kThreads + tid;
+        if (g < row.n) bits |= uint32_t(listed[g]) << 8 * j;
+      }
+      if (bits)
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) hide<T>(v[j], bits >> 8 * j);
+    }
     float largest = largest_or_nan<T>(v);
     if (!(largest < INFINITY)) {
       unclean = true;
@@ -265,17 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
       uint64_t w[kPer / 2];
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) w[i] = exp2_both(mul2(add2(pair(pair_of(e + 2 * i)), minus), c2));
-      if (TAIL) {
-        const int g = round * kRound + j * kThreads + tid;
-        const uint32_t bits = g < row.n ? listed[g] : 0;
-        if (bits) {
-#pragma unroll
-          for (int i = 0; i < kPer / 2; ++i) {
-            const float2 f = tc::unpack2(w[i]);
-            w[i] = pair(make_float2(bits >> (2 * i) & 1 ? 0.0f : f.x, bits >> (2 * i + 1) & 1 ? 0.0f : f.y));
-          }
-        }
-      }
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) s2 = add2(s2, w[i]);
     }
@@ -294,6 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
   if (to) load(v, rounds - 1);
   join(m, other, c);
   if (lane == 0) sh.warp_top[warp] = m, sh.warp_other[warp] = other;
+  if (TAIL && warp < list_warps) {
+    const float list_top = warp_max(clean<T>(to_float(student)));
+    if (lane == 0) sh.list_top[warp] = list_top;
+  }
   __syncthreads();
   const bool again = sh.again != 0;  // tokens stand there twice: what to do once, the first of them does
   bool first = mine >= 0;
@@ -310,9 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
     join(top, other, c);
     tc::cluster_arrive();  // this CTA has read the others' parts
   }
-  const bool empty = !(top > -INFINITY);
+  const float base = top;  // what `other` is relative to
+  if (TAIL) top = fmaxf(top, warp_max(lane < list_warps ? sh.list_top[lane] : -INFINITY));
   const float x = clean<T>(to_float(student));
-  float sum = other, outside = 1.0f, rest = 0.0f;  // S; 1 - q_R / p_R; q_R
+  const bool empty = !(top > -INFINITY);
+  float sum = other, lead = 0.0f, rest = 0.0f;  // S; (p_R - q_R) / R; q_R
   if (TAIL) {
     if (warp < list_warps) {
       const float e = warp_sum(first ? exp2_of(exponent(x, top, c)) : 0.0f);
@@ -322,19 +344,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
       Two left = {1.0f, 0.0f};
       for (int i = 0; i < list_warps; ++i) left = left + -sh.list_q[i];
       // (without other tokens it has nowhere to be)
-      sh.rest = left.high > 0.0f && other > 0.0f ? left.high + left.low : 0.0f;
+      sh.rest = left.high > 0.0f && (base - top) * inverse >= -kFarthest ? left.high + left.low : 0.0f;
     }
     __syncthreads();
+    const float factor = exp2_of(exponent(base, top, c));
+    sum *= factor;
     for (int i = 0; i < list_warps; ++i) sum += sh.list_e[i];
     rest = sh.rest;
-    if (rest > 0.0f) outside = 1.0f - rest * (sum / other);
+    lead = factor / sum;
+    if (rest > 0.0f) lead -= rest / other;
   }
   if (to && empty) {
     put_zeros();
   } else if (to) {
     const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
-    const float slope = factor_of(g * inverse, g), scale = factor_of(slope / sum * outside, g);
-    const uint64_t A = both(scale), minus = both(-top);
+    const float slope = factor_of(g * inverse, g), scale = factor_of(TAIL ? slope * lead : slope / sum, g);
+    const float from_top = base > -INFINITY ? -base : 0.0f;  // (listed tokens are written behind it, whatever comes out)
+    const uint64_t A = both(scale), minus = both(from_top);
     T* begin = to + row.first;
     auto put = [&](uint4(&v)[kVecs], int round) {
       if (unclean) make_clean<T>(v);
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
       load(v, i - 2);
       if (i > 0) put(w, i - 1);
     }
-    if (edge >= 0) to[edge] = from_float<T>(exp2_of(exponent(at_edge, top, c)) * scale);
+    if (edge >= 0) to[edge] = from_float<T>(exp2_of(exponent(at_edge, -from_top, c)) * scale);
     __syncthreads();
   }
   if (warp < list_warps) {
@@ -401,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
   if (tid == 0) {
     Two loss = sh.list_term[0];
     for (int i = 1; i < list_warps; ++i) loss = loss + sh.list_term[i];
-    if (rest > 0.0f) loss = loss + (log_of(rest) + (log_of(sum) + -log_of(other))) * rest;
+    if (rest > 0.0f)
+      loss = loss + (log_of(rest) + (log_of(sum) + -log_of(other)) + -(sum_of(base, -top) * inverse)) * rest;
     a.loss[r] = empty || sh.endless ? INFINITY : loss.high + loss.low;
   }
 }

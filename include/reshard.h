@@ -1028,7 +1028,8 @@ reshard_status_t reshard_logprob_grad(const void* logits, int32_t dtype, int64_t
  * top_logprob[r][j], already at the temperature wanted,
  *   tail == 0:  q_j = exp(y_j) / sum_j exp(y_j),   q_R = 0   (y may be logits then)
  *   tail != 0:  q_j = exp(y_j),   q_R = max(0, 1 - sum_j q_j), the probability of all other tokens,
- *               p_R the student's (q_R counts as 0 where p_R is 0)
+ *               p_R the student's (q_R counts as 0 where p_R is 0: where all other tokens' logits are
+ *               -inf or NaN, or lie more than 2^15 T below the row's largest, as behind a mask)
  *   loss[r]       = sum_j q_j ln(q_j / p_{i_j}) + q_R ln(q_R / p_R)
  *   dlogits[r][i] = grad[r] * dloss[r] / dlogits[r][i]
  *                 = grad[r] / T * (p_i - sum_{j: i_j = i} q_j)       for a token of the list
