@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
     int token = -1;
     float value = -INFINITY;
     if (at < k) {
-      token = __ldg(a.top_token + r * a.ldtop + at);
-      value = __ldg(a.top_logprob + r * a.ldtop + at);
+      token = a.top_token[r * a.ldtop + at];
+      value = a.top_logprob[r * a.ldtop + at];
       if (uint32_t(token) >= uint32_t(row.vocab) || !(value == value)) token = -1, value = -INFINITY;
     }
     if (i == warp) mine = token, y = value;
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
   if (to && empty) {
     put_zeros();
   } else if (to) {
-    const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
+    const float g = a.grad ? a.grad[r] : 1.0f;
     const float slope = factor_of(g * inverse, g), scale = factor_of(TAIL ? slope * lead : slope / sum, g);
     const float from_top = base > -INFINITY ? -base : 0.0f;  // (listed tokens are written behind it, whatever comes out)
     const uint64_t A = both(scale), minus = both(from_top);
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
     const float inv_q = 1.0f / all;
     // the CTA's listed tokens, behind what was just written for them as for others
     if (to && !empty && first && (inside || at_end)) {
-      const float g = a.grad ? __ldg(a.grad + r) : 1.0f;
+      const float g = a.grad ? a.grad[r] : 1.0f;
       const float slope = factor_of(g * inverse, g);
       float mass = q;
       if (again)

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ Sort
   // 32 choices of the warp, the first kKept of them kept; others are read again
   auto choice = [&](uint32_t b) {
     const uint64_t i = uint64_t(b) * 32 + lane;
-    const int e = b < b1 && i < a.n ? __ldg(a.experts + i) : -1;
+    const int e = b < b1 && i < a.n ? a.experts[i] : -1;
     return uint32_t(e) < uint32_t(E) ? e : -1;
   };
   wait_for_previous();
@@ -185,14 +185,18 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const __grid_constant__ D
   for (uint32_t i = 0; i < kDispatchVecs; ++i)
     if (c0 + i * a.lanes < a.vecs) v[i] = __ldcs(x + i * a.lanes);
   const int32_t* slot = a.slot + int64_t(t) * a.topk;
-#pragma unroll 4
-  for (uint32_t j = 0; j < a.topk; ++j) {
-    const uint32_t s = uint32_t(__ldg(slot + j));
-    if (s >= a.nrows) continue;
-    V* to = reinterpret_cast<V*>(a.rows + s * a.ldr) + c0;
+  uint32_t s[kPlaces];
+  load_places(s, slot, 0, a.topk);
+  for (uint32_t j0 = 0; j0 < a.topk; j0 += kPlaces) {
+    if (j0) load_places(s, slot, j0, a.topk);
 #pragma unroll
-    for (uint32_t i = 0; i < kDispatchVecs; ++i)
-      if (c0 + i * a.lanes < a.vecs) to[i * a.lanes] = v[i];
+    for (uint32_t j = 0; j < kPlaces; ++j) {
+      if (s[j] >= a.nrows) continue;
+      V* to = reinterpret_cast<V*>(a.rows + s[j] * a.ldr) + c0;
+#pragma unroll
+      for (uint32_t i = 0; i < kDispatchVecs; ++i)
+        if (c0 + i * a.lanes < a.vecs) to[i * a.lanes] = v[i];
+    }
   }
 }
 
@@ -237,16 +241,21 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
       if (i < mine) e[i].load(x + i * step);
       else if (a.cols % 128 != 0) e[i].load(x, 0);  // zeros beside values
     }
+    uint32_t s[kPlaces];
+    load_places(s, slot, 0, a.topk);
     quantise();
-#pragma unroll 4
-    for (uint32_t j = 0; j < a.topk; ++j) {
-      const uint32_t to = uint32_t(__ldg(slot + j));
-      if (to >= a.nrows) continue;
-      uint8_t* row = a.rows + to * a.ldr + to0;
-      if (scales) a.scale[to * a.lds + my_block] = scale;
+    for (uint32_t j0 = 0; j0 < a.topk; j0 += kPlaces) {
+      if (j0) load_places(s, slot, j0, a.topk);
 #pragma unroll
-      for (int i = 0; i < B; ++i)
-        if (i < mine) *reinterpret_cast<uint2*>(row + i * step) = q[i];
+      for (uint32_t j = 0; j < kPlaces; ++j) {
+        const uint32_t to = s[j];
+        if (to >= a.nrows) continue;
+        uint8_t* row = a.rows + to * a.ldr + to0;
+        if (scales) a.scale[to * a.lds + my_block] = scale;
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          if (i < mine) *reinterpret_cast<uint2*>(row + i * step) = q[i];
+      }
     }
     return;
   }
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(256) dispatch_fp8_kernel(const __grid_constant
   quantise();
 #pragma unroll 1
   for (uint32_t j = 0; j < a.topk; ++j) {
-    const uint32_t to = uint32_t(__ldg(slot + j));
+    const uint32_t to = uint32_t(slot[j]);
     const bool on = to < a.nrows && there;
     uint8_t* row = a.rows + (on ? to * a.ldr + col0 : 0);
     if (on && scales) a.scale[to * a.lds + my_block] = scale;
@@ -392,8 +401,8 @@ __global__ void __launch_bounds__(256, 3) combine_kernel(const __grid_constant__
   auto places = [&](uint32_t j0) {
 #pragma unroll
     for (uint32_t j = 0; j < kTogether; ++j) {
-      const uint32_t s = j0 + j < a.topk ? uint32_t(__ldg(a.slot + first + j0 + j)) : 0xffffffffu;
-      w[j] = s < a.nrows && a.weight ? __ldg(a.weight + first + j0 + j) : 1.0f;
+      const uint32_t s = j0 + j < a.topk ? uint32_t(a.slot[first + j0 + j]) : 0xffffffffu;
+      w[j] = s < a.nrows && a.weight ? a.weight[first + j0 + j] : 1.0f;
       row[j] = s < a.nrows ? a.rows + s * a.ldr : nullptr;
     }
   };
@@ -447,8 +456,8 @@ __global__ void __launch_bounds__(256, 3) combine_grad_kernel(const __grid_const
     float w[kTogether], dot[kTogether];
 #pragma unroll
     for (uint32_t j = 0; j < kTogether; ++j) {
-      s[j] = j < together ? uint32_t(__ldg(a.slot + first + j0 + j)) : 0xffffffffu;
-      w[j] = j < together && a.weight ? __ldg(a.weight + first + j0 + j) : 1.0f;
+      s[j] = j < together ? uint32_t(a.slot[first + j0 + j]) : 0xffffffffu;
+      w[j] = j < together && a.weight ? a.weight[first + j0 + j] : 1.0f;
       dot[j] = 0.0f;
     }
     for (uint32_t c = lane; c < a.vecs; c += LANES) {

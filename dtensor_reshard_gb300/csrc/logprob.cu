@@ -175,7 +175,7 @@ __device__ bool list_reaching(TopSmem& sm, const uint16_t* noted, const Slice<T>
     const int g = (round * kVecs + int(q % kVecs)) * kThreads + int(h % kThreads);
     const bool there = w < all && round < rounds && g < row.n;
     uint4 v = Slice<T>::nothing();
-    if (there) v = __ldg(row.granules() + g);
+    if (there) v = row.granules()[g];
     append_reaching<T>(sm, v, there, row.first + g * Slice<T>::kPer, threshold);
   }
   __syncthreads();
@@ -250,7 +250,7 @@ __device__ __noinline__ void list_again(TopSmem& sm, const Slice<T> row, bool ed
         count = index < to;
         if (count) l[0] = row.at(index);
       } else if (g < row.n) {
-        const uint4 v = __ldg(row.granules() + g);
+        const uint4 v = row.granules()[g];
         const T* e = reinterpret_cast<const T*>(&v);
         index = row.first + g * kPer;
         count = kPer;
@@ -361,12 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     const uint4* p = from + i * kRound;
     if ((i + 1) * kRound <= row.n) {
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) v[j] = TOP ? __ldg(p + j * kThreads) : __ldcs(p + j * kThreads);
+      for (int j = 0; j < kVecs; ++j) v[j] = TOP ? p[j * kThreads] : __ldcs(p + j * kThreads);
     } else {
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         v[j] = Slice<T>::nothing();
-        if (i * kRound + j * kThreads + tid < row.n) v[j] = __ldg(p + j * kThreads);
+        if (i * kRound + j * kThreads + tid < row.n) v[j] = p[j * kThreads];
       }
     }
   };
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
   wait_for_previous();
   uint4 v[kVecs], w[kVecs];
   load(v, 0);
-  const int target = a.target ? __ldg(a.target + r) : 0;
+  const int target = a.target ? a.target[r] : 0;
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   const int edge = rank == 0 ? row.edge() : -1;
   const float at_edge = edge >= 0 ? row.at(edge) : -INFINITY;
@@ -579,9 +579,9 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid
   const int edge = chunk == 0 ? row.edge() : -1;
   let_next_start();
   wait_for_previous();
-  const int target = a.target ? __ldg(a.target + r) : -1;
-  const float4 state = __ldg(a.state + r);  // largest logit, 1 / S, ln S, entropy
-  float g = a.dlogprob && a.target ? __ldg(a.dlogprob + r) : 0.0f, h = a.dentropy ? __ldg(a.dentropy + r) : 0.0f;
+  const int target = a.target ? a.target[r] : -1;
+  const float4 state = a.state[r];  // largest logit, 1 / S, ln S, entropy
+  float g = a.dlogprob && a.target ? a.dlogprob[r] : 0.0f, h = a.dentropy ? a.dentropy[r] : 0.0f;
   if (state.y == 0.0f) g = h = 0.0f;  // no logit of the row counts, or the row does not
   if (g == 0.0f && h == 0.0f) {
 #pragma unroll

@@ -94,12 +94,22 @@ cudaError_t allow_smem(int dev) {
   return ce;
 }
 
-// The next kernel of the stream may start as far as it does not need this one.
+// The next kernel of the stream may start as far as it does not need this one.  What it reads with the
+// kernel in front still running is not read-only for its lifetime: it takes it, behind the wait, by
+// ordinary loads, none that goes through the read-only path (__ldg, ld.global.nc).
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The places of up to kPlaces of a token's choices from the j0-th on, none for those beyond the last: all on
+// their way before what is stored at the first.
+constexpr uint32_t kPlaces = 4;
+__device__ __forceinline__ void load_places(uint32_t (&s)[kPlaces], const int32_t* slot, uint32_t j0, uint32_t topk) {
+#pragma unroll
+  for (uint32_t j = 0; j < kPlaces; ++j) s[j] = j0 + j < topk ? uint32_t(slot[j0 + j]) : 0xffffffffu;
 }
 
 struct Launch {

@@ -95,15 +95,18 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const __grid_constant__ A
     } else {
       v = load_elements(mine, at);
     }
-    for (uint32_t j = 0; j < a.topk; ++j) {
-      const uint32_t s = uint32_t(__ldg(slot + j));
-      if (s < a.nrows) store<T>(a.rows + s * a.ldr + c * uint64_t(16), v, full, mine);
+    for (uint32_t j0 = 0; j0 < a.topk; j0 += kPlaces) {
+      uint32_t s[kPlaces];
+      load_places(s, slot, j0, a.topk);
+#pragma unroll
+      for (uint32_t j = 0; j < kPlaces; ++j)
+        if (s[j] < a.nrows) store<T>(a.rows + s[j] * a.ldr + c * uint64_t(16), v, full, mine);
     }
   }
   const uint32_t e = vecs * 8 + p.lane;
   if (p.first == 0 && e < a.cols)
     for (uint32_t j = 0; j < a.topk; ++j) {
-      const uint32_t s = uint32_t(__ldg(slot + j));
+      const uint32_t s = uint32_t(slot[j]);
       if (s < a.nrows) reinterpret_cast<T*>(a.rows + s * a.ldr)[e] = reinterpret_cast<const T*>(x)[e];
     }
 }
@@ -129,9 +132,9 @@ __global__ void __launch_bounds__(256, 3) combine_kernel(const __grid_constant__
       bool inside = true, on[kTogether];
 #pragma unroll
       for (uint32_t j = 0; j < kTogether; ++j) {
-        const uint32_t s = j0 + j < a.topk ? uint32_t(__ldg(a.slot + first + j0 + j)) : 0xffffffffu;
+        const uint32_t s = j0 + j < a.topk ? uint32_t(a.slot[first + j0 + j]) : 0xffffffffu;
         on[j] = s < a.nrows;
-        w[j] = on[j] && a.weight ? __ldg(a.weight + first + j0 + j) : 1.0f;
+        w[j] = on[j] && a.weight ? a.weight[first + j0 + j] : 1.0f;
         at[j] = a.rows + (on[j] ? s * a.ldr : 0) + c * uint64_t(16);
         inside = inside && (!on[j] || (s > 0 && s + 1 < a.nrows));
       }
@@ -160,9 +163,9 @@ __global__ void __launch_bounds__(256, 3) combine_kernel(const __grid_constant__
   if (p.first != 0 || e >= a.cols) return;
   float sum = 0.0f;
   for (uint32_t j = 0; j < a.topk; ++j) {
-    const uint32_t s = uint32_t(__ldg(a.slot + first + j));
+    const uint32_t s = uint32_t(a.slot[first + j]);
     if (s >= a.nrows) continue;
-    const float w = a.weight ? __ldg(a.weight + first + j) : 1.0f;
+    const float w = a.weight ? a.weight[first + j] : 1.0f;
     sum = fmaf(w, to_float(reinterpret_cast<const T*>(a.rows + s * a.ldr)[e]), sum);
   }
   reinterpret_cast<T*>(out)[e] = from_float<T>(sum);
@@ -185,8 +188,8 @@ __global__ void __launch_bounds__(256, 3) combine_grad_kernel(const __grid_const
     bool inside = dout_inside;
 #pragma unroll
     for (uint32_t j = 0; j < kTogether; ++j) {
-      s[j] = j0 + j < a.topk ? uint32_t(__ldg(a.slot + first + j0 + j)) : 0xffffffffu;
-      w[j] = j0 + j < a.topk && a.weight ? __ldg(a.weight + first + j0 + j) : 1.0f;
+      s[j] = j0 + j < a.topk ? uint32_t(a.slot[first + j0 + j]) : 0xffffffffu;
+      w[j] = j0 + j < a.topk && a.weight ? a.weight[first + j0 + j] : 1.0f;
       dot[j] = 0.0f;
       inside = inside && (s[j] >= a.nrows || (s[j] > 0 && s[j] + 1 < a.nrows));
     }

@@ -39,7 +39,7 @@ constexpr float kLargest = 3.402823466e38f;
 // 1 / T as a factor: 1 for T <= 0 and NaN; never infinite, and never 0 (a logit of -inf has the
 // exponent -inf at any temperature).
 __device__ __forceinline__ float inverse_of(const float* temperature, int64_t r) {
-  const float t = temperature ? __ldg(temperature + r) : 1.0f;
+  const float t = temperature ? temperature[r] : 1.0f;
   return t > 0.0f ? fminf(fmaxf(1.0f / t, 0x1p-126f), kLargest) : 1.0f;
 }
 // A gradient's factor, finite where its gradient g is: 0 times it is 0.

@@ -35,3 +35,14 @@ def test_resident_clusters_are_on_record_for_each_kernel():
     kernels = {(k, y) for k in ("narrow_kernel<16", "narrow_kernel<32", "narrow_kernel<64", "wide_kernel<")
                for y in ("float", "__half", "__nv_bfloat16")}
     assert len(records) == len(kernels), records
+
+
+def test_what_starts_early_reads_by_ordinary_loads():
+    """A kernel that may start while the one in front of it ends must not take what that one writes for
+    read-only during its lifetime: no load by the read-only path in the files of such kernels."""
+    early = ("experts.cu", "shifted_rows.cuh", "logprob.cu", "distill.cu", "vocab_row.cuh", "fp8_block.cuh")
+    texts = {os.path.basename(n): t for n, t in _sources().items()}
+    for name in early:
+        code = "\n".join(line.split("//")[0] for line in texts[name].splitlines())
+        for word in ("__ldg", "ld.global.nc", "__restrict__"):
+            assert word not in code, (name, word)
