@@ -564,6 +564,9 @@ struct GradArgs {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;
+// The most that A and B are, so that A + B z, z down to kLeast, is finite (1 / T can be as large as a float32).
+constexpr float kMostA = 0.75f * kLargest, kMostB = kLargest / 1024;
+static_assert(kMostA - kLeast * kMostB < kLargest, "A + B z");
 
 // dl = g / T (1[target] - p) - h / T p (ln p + H), p = e^z / S: e^z times (A + B z).
 template <typename T, bool ALIKE>
@@ -601,9 +604,9 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid
   if (largest_in<T>(v) == INFINITY) make_finite<T>(v);
   const float inverse = inverse_of(a.temperature, r), c = log2_scale(inverse);
   const float both_of = g + h;  // (NaN or infinite where one of them is)
-  const float slope = inverse * state.y, onehot = factor_of(g * inverse, g);
-  const float a0 = factor_of(-(g + h * (state.w - state.z)) * slope, both_of);
-  const float b0 = factor_of(-h * slope, h) * kLn2;
+  const float slope = inverse * state.y, onehot = factor_of(g * inverse, g, kMostA);
+  const float a0 = factor_of(-(g + h * (state.w - state.z)) * slope, both_of, kMostA);
+  const float b0 = factor_of(-h * slope * kLn2, h, kMostB);
   auto one = [&](float l) {
     const float z = exponent(l, state.x, c);
     return exp2_of(z) * fmaf(z, b0, a0);

@@ -42,9 +42,9 @@ __device__ __forceinline__ float inverse_of(const float* temperature, int64_t r)
   const float t = temperature ? temperature[r] : 1.0f;
   return t > 0.0f ? fminf(fmaxf(1.0f / t, 0x1p-126f), kLargest) : 1.0f;
 }
-// A gradient's factor, finite where its gradient g is: 0 times it is 0.
-__device__ __forceinline__ float factor_of(float x, float g) {
-  return fabsf(g) < INFINITY ? fminf(fmaxf(x, -kLargest), kLargest) : x;
+// A gradient's factor, finite where its gradient g is, and at most `most`: 0 times it is 0.
+__device__ __forceinline__ float factor_of(float x, float g, float most = kLargest) {
+  return fabsf(g) < INFINITY ? fminf(fmaxf(x, -most), most) : x;
 }
 // The same for powers of 2.
 __device__ __forceinline__ float log2_scale(float inverse) {
