@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
   for (int i = tid; i < kTable; i += kThreads) sh.table[i] = -1;
   let_next_start();
   wait_for_previous();
-  policy = to ? keep_policy() : drop_policy();
+  policy = drop_policy();  // (a row that does not count is not read again)
   load(v, 0);
+  if (to) policy = keep_policy();
   if (tid == 0) sh.again = sh.edges = sh.endless = 0;
   __syncthreads();
   // the teacher's list, an entry a thread: tokens outside the vocabulary, and NaN, are none.  Every
