@@ -306,7 +306,8 @@ struct CombineArgs {
 // take apart into a register an element, and their values.
 template <typename T, int W>
 struct Access {
-  static constexpr int kWords = W < 4 ? 1 : W / 4, kElements = W / int(sizeof(T)) > 0 ? W / int(sizeof(T)) : 1;
+  static_assert(W >= int(sizeof(T)), "whole elements");
+  static constexpr int kWords = W < 4 ? 1 : W / 4, kElements = W / int(sizeof(T));
   uint32_t word[kWords];
 
   // Zeros, or what lies at `at` where `on`: one predicated instruction, behind which the next load
@@ -518,14 +519,14 @@ bool all_aligned(int64_t to, std::initializer_list<const void*> pointers, std::i
   return true;
 }
 
-// f(std::integral_constant<int, W>()) with W the widest access, 16 bytes at most.
-template <typename F>
-reshard_status_t by_width(int64_t least, std::initializer_list<const void*> pointers,
-                          std::initializer_list<int64_t> bytes, F&& f) {
+// f(std::integral_constant<int, W>()) with W the widest access, from LEAST bytes, those of an element, to 16.
+template <size_t LEAST, typename F>
+reshard_status_t by_width(std::initializer_list<const void*> pointers, std::initializer_list<int64_t> bytes, F&& f) {
   if (all_aligned(16, pointers, bytes)) return f(std::integral_constant<int, 16>());
   if (all_aligned(8, pointers, bytes)) return f(std::integral_constant<int, 8>());
-  if (least == 4 || all_aligned(4, pointers, bytes)) return f(std::integral_constant<int, 4>());
-  return f(std::integral_constant<int, 2>());
+  if constexpr (LEAST == 2)
+    if (!all_aligned(4, pointers, bytes)) return f(std::integral_constant<int, 2>());
+  return f(std::integral_constant<int, 4>());
 }
 template <int W>
 struct Word;
@@ -667,7 +668,8 @@ extern "C" reshard_status_t reshard_expert_dispatch(const void* x, int32_t dtype
     return cta ? rs::start<rs::shifted::dispatch_kernel<__half, 256, rs::DispatchArgs>>("reshard_expert_dispatch", grid, st, a)
                : rs::start<rs::shifted::dispatch_kernel<__half, 32, rs::DispatchArgs>>("reshard_expert_dispatch", grid, st, a);
   }
-  return rs::by_width(size, {x, rows}, {a.ldx, a.ldr, cols * size}, [&](auto w) {
+  // (accesses know no type: two bytes serve none that is aligned to four)
+  return rs::by_width<2>({x, rows}, {a.ldx, a.ldr, cols * size}, [&](auto w) {
     const int64_t vecs = cols * size / w;
     a.lanes = uint32_t(rs::lanes_of(vecs));
     const int64_t chunks = rs::op::cdiv(vecs, rs::kDispatchVecs * int64_t(a.lanes));
@@ -717,7 +719,7 @@ extern "C" reshard_status_t reshard_expert_combine(const void* rows, int32_t dty
                    : rs::start<rs::shifted::combine_kernel<T, 32, rs::CombineArgs>>("reshard_expert_combine", grid, st, a);
       }
     }
-    return rs::by_width(size, {rows, out}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
+    return rs::by_width<sizeof(T)>({rows, out}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
       const int64_t vecs = cols * size / w, lanes = rs::lanes_of(vecs), groups = rs::op::cdiv(tokens, 256 / lanes);
       // a CTA a whole row, or so much of it that there are some 2048 of them
       int64_t rounds = rs::op::cdiv(vecs, lanes);
@@ -781,7 +783,7 @@ extern "C" reshard_status_t reshard_expert_combine_grad(const void* dout, int32_
         return rs::start<combine_grad_kernel<T, 32, false, CombineArgs>>(what, grid, st, a);
       }
     }
-    return rs::by_width(size, {dout, read, drows}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
+    return rs::by_width<sizeof(T)>({dout, read, drows}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
       a.vecs = uint32_t(cols * size / w);
       const bool cta = a.vecs > 128;  // a CTA a token, else a warp
       const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);

@@ -46,3 +46,11 @@ def test_what_starts_early_reads_by_ordinary_loads():
         code = "\n".join(line.split("//")[0] for line in texts[name].splitlines())
         for word in ("__ldg", "ld.global.nc", "__restrict__"):
             assert word not in code, (name, word)
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="nm lists the library's symbols")
+def test_no_access_narrower_than_an_element():
+    names = subprocess.run(["nm", "-C", rs.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert "combine_kernel<float, 4>" in names and "combine_grad_kernel<float, 4," in names
+    for kernel in ("combine_kernel<float, 2>", "combine_grad_kernel<float, 2,"):
+        assert kernel not in names
