@@ -312,7 +312,7 @@ def _ptr(x) -> int | None:
     if isinstance(x, int):
         return x or None
     data_ptr = getattr(x, "data_ptr", None)
-    return (int(x) if data_ptr is None else data_ptr()) or None
+    return int(x if data_ptr is None else data_ptr()) or None
 
 
 def _ptr_array(xs) -> ctypes.Array:
