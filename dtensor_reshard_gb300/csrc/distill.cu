@@ -32,6 +32,7 @@ constexpr int kTable = 512;               // of the list's tokens, half full at 
 constexpr int kMarked = 64 * 1024;        // granules of a slice whose listed elements can be marked
 constexpr int kMaxCluster = 8;
 constexpr int kListWarps = RESHARD_MAX_TOP / 32;
+constexpr float kShrunk = 0x1p-10f;       // of the loss's terms: they and their sum stay in float32's range
 constexpr float kFarthest = 32768.0f;     // T between the row's largest logit and the others' beyond which p_R is 0
 static_assert(RESHARD_MAX_TOP <= kMany && 2 * RESHARD_MAX_TOP <= kTable, "an entry a thread");
 
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
       const float scaled = q * inv_q;
       if (mine >= 0 && !(scaled <= 0.0f)) {
         const Two z = sum_of(x, -top) * inverse, ln_q = sum_of(y, TAIL ? 0.0f : -y_top);
-        if (z.high > -INFINITY) term = ((ln_q + -z) + (log_of(sum) + -log_of(all))) * scaled;
+        if (z.high > -INFINITY) term = ((ln_q + -z) + (log_of(sum) + -log_of(all))) * (scaled * kShrunk);
         else sh.endless = 1;
       }
       term = sum_of_warp(term);
@@ -429,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_kernel(cons
     Two loss = sh.list_term[0];
     for (int i = 1; i < list_warps; ++i) loss = loss + sh.list_term[i];
     if (rest > 0.0f)
-      loss = loss + (log_of(rest) + (log_of(sum) + -log_of(other)) + -(sum_of(base, -top) * inverse)) * rest;
-    a.loss[r] = empty || sh.endless ? INFINITY : loss.high + loss.low;
+      loss = loss + (log_of(rest) + (log_of(sum) + -log_of(other)) + -(sum_of(base, -top) * inverse)) * (rest * kShrunk);
+    a.loss[r] = empty || sh.endless ? INFINITY : (loss.high + loss.low) * (1.0f / kShrunk);
   }
 }
 
