@@ -14,10 +14,12 @@
 // e^((l - m_R) / T) times (p_R - q_R) / R.
 //
 // Bound by HBM, and by the tenth of the rows that the L2 has lost by the second pass: 2048 rows of
-// 131072 bf16 with 64 tokens take 190 us (158 of HBM alone, each logit read and written once; 611 MB
-// read where 509 would do, 5.7 TB/s), with the rest as an outcome 205 us.  Measured and dropped: a row
+// 131072 bf16 with 64 tokens take 191 us (158 of HBM alone, each logit read and written once; 621 MB
+// read where 509 would do, 5.7 TB/s), with the rest as an outcome 204 us.  Measured and dropped: a row
 // held in the shared memory of four CTAs (291 us) or two (286), whose fixed costs weigh more than a
 // second read; a part of it held in one CTA's (244: it leaves the loads too little of the L1).
+// 64 registers: 16-bit rows with the rest spill 16 bytes, gradients that lie otherwise on 16 bytes than
+// the logits 124 to 160 (317 us, with the rest 341).
 #include "vocab_row.cuh"
 
 namespace rs {
@@ -49,7 +51,10 @@ struct DistillArgs {
 };
 
 // A number as the sum of two float32, the second what the first's rounding left: 48 bits or so in
-// operations that these SMs have many of, where those on float64 take a warp 16 clocks each.
+// operations that these SMs have many of, where those on float64 take a warp 16 clocks each.  Sums by
+// Knuth's exact addition (The Art of Computer Programming 2, 4.2.2), combined as Dekker does (Numerische
+// Mathematik 18, 1971), products with the remainder from one fused operation.  What they are made of here, S, p_R,
+// a probability, 1 / T, is float32: the pairs keep the small difference of the loss's large terms.
 struct Two {
   float high, low;
 };
@@ -72,8 +77,9 @@ __device__ __forceinline__ Two sum_of_warp(Two v) {
     v = v + Two{__shfl_xor_sync(0xffffffffu, v.high, o), __shfl_xor_sync(0xffffffffu, v.low, o)};
   return v;
 }
-// ln x for a positive finite x: of x = m 2^n, m next to 1, by float32 and n ln 2, so that it is off by
-// 2^-24 of ln m and not of ln x.
+// ln x for a positive finite x: of x = m 2^n, m from sqrt(1/2) to sqrt(2) (the usual reduction, as in Cody and
+// Waite, Software Manual for the Elementary Functions, 1980), by float32's logf and n ln 2, so that it is off
+// by 2^-24 of ln m and not of ln x.
 __device__ __forceinline__ Two log_of(float x) {
   int n = 0;
   if (x < 0x1p-126f) x *= 0x1p32f, n = -32;
@@ -86,7 +92,7 @@ __device__ __forceinline__ Two log_of(float x) {
 // e^y within 2^-42 of itself, 0 below e^-87.  With y = n ln 2 + 16 s, ln 2 and 1 / 6 as pairs: e^s - 1 = s +
 // s^2 / 2 + s^3 / 6 + s^4 (1 / 24 + s / 120 + ...), of which the last is 2^-21 of the whole at most and needs
 // float32's digits alone, and four times e^2s - 1 = 2 (e^s - 1) + (e^s - 1)^2.
-// (Float64's exponential took the call 0.1 to 0.3 us longer: 37 rows of 50021 float32 9.6 us, now 9.4.)
+// (Float64's exponential takes a call of 37 rows of 50021 float32 0.1 to 0.3 us longer.)
 __device__ __forceinline__ Two exp_of(float y) {
   if (!(y < 88.0f)) return {expf(y), 0.0f};
   if (y < -87.0f) return {0.0f, 0.0f};
@@ -462,7 +468,7 @@ reshard_status_t launch_distill(const DistillArgs& a, bool tail, int64_t rows, i
                                 (rows * ctas * 8 < int64_t(sms) * 7 && granules > ctas * 2048)))
     ctas *= 2;
   static_assert(RESHARD_MAX_VOCAB / 4 <= kMaxCluster * kMarked, "marks of a slice");
-  // short rows in small CTAs, of which an SM has more (4000 rows of 300 bf16: 20 us, in CTAs of 512
+  // short rows in small CTAs, of which an SM has more (4000 rows of 300 bf16: 21 us, in CTAs of 512
   // threads 70)
   return granules <= kVecs * kFew * 2 && a.ntop <= kFew
              ? launch_threads<T, kFew>(a, tail, rows, ctas, dev, stream)

@@ -3,11 +3,12 @@
 // with weights (reshard_expert_combine, reshard_expert_combine_grad).
 //
 // Beside the sort all of them move rows, each once, and are bound by HBM: 4096 tokens of 7168 bf16 with
-// 8 choices take 81 us to their places (6.4 TB/s), 49 us in 8 bits, 80 us back (6.7 TB/s), and 152 us
-// for both gradients (6.6 TB/s).  Rows that do not start on 16 bytes go in accesses of 8, 4 or 2 bytes:
-// 7170 columns back in 105 us; rows of 16-bit elements that no such access fits in shifted granules
-// (shifted_rows.cuh): 7169 columns back in 121 us, to their places in 113; in 8 bits, rows of columns
-// that are no multiple of 8 take 108 us.
+// 8 choices take 80 us to their places (6.6 TB/s), 49 us in 8 bits, 79 us back (6.7 TB/s), and 150 us
+// for both gradients (6.7 TB/s).  Rows that do not start on 16 bytes go in narrower accesses, or those of
+// 16-bit elements in shifted granules (shifted_rows.cuh): to their places unless 8 bytes fit them (7170
+// columns 102 us, 7169 105), back and in gradients unless 4 bytes do (7170 in accesses of 4 bytes 103 and
+// 199 us, 7169 in granules 119 and 229).  float32 rows off 16 bytes go in accesses of 4: 7169 columns 208,
+// 196 and 381 us, 7168 157, 150 and 291.  In 8 bits, columns that are no multiple of 8 take 117 to 124 us.
 #include <type_traits>
 
 #include "fp8_block.cuh"
@@ -36,7 +37,7 @@ struct SortArgs {
 // places: the expert's next one, and within the 32 by the lanes before with the same expert.  That takes
 // 180 instructions for 32 choices (finding equal experts by a vote a bit no less), which fill one
 // cluster's SMs: several clusters count all of them, and each gives some warps' choices their places
-// (65536 choices of 256 experts: one cluster 13.9 us, eight 7.9; 256 choices: 2.1 us behind another call).
+// (65536 choices of 256 experts: one cluster 13.9 us, eight 7.9, behind another call 5.8; 256 choices 2.5).
 __global__ void __launch_bounds__(1024) sort_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t counted[];  // [warps][nexperts], total [nexperts], first [nexperts]
   __shared__ int32_t warp_sum[32];
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(256, 3) combine_kernel(const __grid_constant__
 
 // drows = weight x dout at the places of a token's choices; dweight = the products of dout with
 // its rows, float32 chains of a lane joined in one order.  dout and each row are read once.  LANES: of a
-// token, a warp or a CTA.
+// token, a warp or a CTA.  (80 registers; with 16-byte accesses and dweight 20 to 36 bytes are spilled.)
 template <typename T, int W, int LANES, bool DOT>
 __global__ void __launch_bounds__(256, 3) combine_grad_kernel(const __grid_constant__ CombineArgs a) {
   using A = Access<T, W>;
@@ -555,13 +556,19 @@ reshard_status_t start(const char* what, int64_t grid, cudaStream_t stream, cons
 
 // Whether rows go in shifted granules: of 16-bit elements, long enough for a warp's worth, and not
 // aligned to `least` bytes.  4096 x 8 rows of 7169 bf16, in accesses of an element and shifted: to their
-// places 128 and 112 us, back 154 and 121, gradients 278 and 230; of 7170, in accesses of two elements
-// and shifted: 124 and 108, 105 and 120, 201 and 225.  So least is 8 to their places, else 4.
+// places 128 and 105 us, back 154 and 119, gradients 278 and 229; of 7170, in accesses of two elements
+// and shifted: 106 and 102, 103 and 120, 199 and 225 (4099 x 6 rows of 4098 to their places 43 and 40).  So
+// least is 8 to their places, else 4.  (Few tokens lose by it, 32 x 8 rows of 7170 2.3 and 9.2 us.)  Rows of
+// 131 columns, 8192 x 4 of them, would gain (18 and 11, 17 and 7, 25 and 13 us), of 255 not (18 and 25, 19
+// and 10, 26 and 26), and few tokens would lose (128: 1.9 and 2.5, 1.8 and 2.4, 2.1 and 3.1): from 256 on.
 bool goes_shifted(int64_t size, int64_t cols, int64_t least, std::initializer_list<const void*> pointers,
                   std::initializer_list<int64_t> bytes) {
   return size == 2 && cols >= 256 && !all_aligned(least, pointers, bytes);
 }
-constexpr int64_t kLongRow = 1024;  // columns from which a CTA has a token, else a warp
+// Columns from which a CTA has a token of them, else a warp.  CTA and warp, 4 choices of 1027 columns: 128
+// tokens to their places 2.9 and 6.1 us, back 2.7 and 5.6, gradients 3.9 and 8.4; 8192 tokens 19 and 20, 25 and
+// 20, 72 and 38.  Of 515: 128 tokens 2.7 and 3.9, 2.5 and 3.7, 3.7 and 5.3; 8192 13 and 11, 19 and 11, 50 and 18.
+constexpr int64_t kLongRow = 1024;
 
 // What the calls on rows have in common.
 reshard_status_t check(int32_t dtype, int64_t tokens, int64_t topk, int64_t cols, int64_t nrows) {
@@ -721,7 +728,8 @@ extern "C" reshard_status_t reshard_expert_combine(const void* rows, int32_t dty
     }
     return rs::by_width<sizeof(T)>({rows, out}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
       const int64_t vecs = cols * size / w, lanes = rs::lanes_of(vecs), groups = rs::op::cdiv(tokens, 256 / lanes);
-      // a CTA a whole row, or so much of it that there are some 2048 of them
+      // a CTA a whole row, or so much of it that there are some 2048 of them (8 choices of 7168 bf16, with 512,
+      // 2048 and 8192: 200 tokens 3.5, 4.2 and 4.2 us, 1000 23.4, 22.9 and 23.9, 2048 42.1, 42.0 and 45.5)
       int64_t rounds = rs::op::cdiv(vecs, lanes);
       if (groups * rounds > 2048) rounds = rs::op::cdiv(groups * rounds, 2048) < rounds ? rs::op::cdiv(groups * rounds, 2048) : rounds;
       else rounds = 1;
@@ -785,7 +793,9 @@ extern "C" reshard_status_t reshard_expert_combine_grad(const void* dout, int32_
     }
     return rs::by_width<sizeof(T)>({dout, read, drows}, {ldr * size, ldo * size, cols * size}, [&](auto w) {
       a.vecs = uint32_t(cols * size / w);
-      const bool cta = a.vecs > 128;  // a CTA a token, else a warp
+      // a CTA a token, else a warp (4 choices: 2048 bf16 columns, 256 accesses, 128 tokens 2.9 and 7.2 us, 8192
+      // tokens 60 and 55; 1024 columns 2.5 and 4.5, 47 and 29)
+      const bool cta = a.vecs > 128;
       const int64_t grid = cta ? tokens : rs::op::cdiv(tokens, 8);
       if (const reshard_status_t s = rs::too_many(grid); s != RESHARD_OK) return s;
       if (dweight && cta) return rs::start<rs::combine_grad_kernel<T, w, 256, true>>(what, grid, st, a);

@@ -5,17 +5,19 @@
 // ln S - U / S.  One pass: a thread carries its own largest logit with S and U relative to it, in
 // float32; differences of logits and 1 / T are rounded once each, exponentials are powers of 2.
 //
-// The pass is bound by HBM: 4096 rows of 131072 bf16 take 144 us (6.7 TB/s; 30000 instructions a row,
-// 62% of the issue slots), and so is the gradient, 152 us for 2048 rows read and written (7.0 TB/s).
+// The pass is bound by HBM: 4096 rows of 131072 bf16, a tenth of which do not count, take 141 us (6.8 TB/s;
+// 30000 instructions a row, 61% of the issue slots), and so is the gradient, 148 us for 2048 such rows, read
+// and written (6.9 TB/s).
 //
 // The most likely tokens: with the pass done, the k-th largest of the threads' own largest logits is
 // reached by k tokens, and by few others (77 of 131072 for k = 64); the groups of granules that reach it,
 // which each thread noted, are read again, their tokens listed, and the list is ranked exactly by
-// comparing all with all.  Nothing of the row's size is sorted or kept.  2048 rows of 131072 bf16 with 64
-// tokens: 95 us (71 of HBM alone: 70% of the issue slots, and a fifth of a row's time at barriers and the list),
-// with 1 token 97, with 128 131, with 256 219 us.  (A threshold from the first granules alone listed 512
-// tokens: 245 us.)  A row whose list overflows, as one of equal logits, goes through the histograms of
-// list_again: 2048 such rows 0.85 ms.
+// comparing all with all.  Nothing of the row's size is sorted or kept.  2048 such rows with 64 tokens: 97 us
+// (71 of HBM alone: 70% of the issue slots, and a fifth of a row's time at barriers and the list), with 1
+// token 90, with none 79; with 128 114, with 256 189: the more of the threads have to reach the threshold, the lower
+// it lies and the more is listed and ranked.  (A threshold from the first granules alone listed 512 tokens for
+// 64: 245 us.)  A row whose list overflows, as one of equal logits, goes through the histograms of list_again:
+// 2048 such rows 0.79 ms.  (61 to 64 registers; float32 with alternatives spills 24 bytes.)
 #include <type_traits>
 
 #include "vocab_row.cuh"

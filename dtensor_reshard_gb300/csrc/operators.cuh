@@ -1,6 +1,6 @@
 // operators.cuh -- pieces shared by the operators that run beside a refit
-// (fp8_quantize.cu, fp8_matmul.cu, sample.cu, balance.cu, experts.cu): element types,
-// reductions and argument checks.
+// (fp8_quantize.cu, fp8_matmul.cu, sample.cu, balance.cu, experts.cu, logprob.cu, distill.cu):
+// element types, reductions, launches and argument checks.
 #pragma once
 
 #include <cuda_bf16.h>

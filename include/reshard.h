@@ -1039,7 +1039,9 @@ reshard_status_t reshard_logprob_grad(const void* logits, int32_t dtype, int64_t
  * count: loss and gradient 0.  A token may stand in a list twice: its probabilities add up in the
  * gradient.  Where the student gives a token that has a teacher's probability none, the loss is
  * +inf and the gradient is as above; a row of -inf and NaN alone has loss +inf and gradient 0.
- * The teacher's rest and the loss are held in pairs of float32 (42 bits or more), other sums in float32.
+ * The teacher's rest is held to 42 bits; the loss's terms are added up in pairs of float32, but what they
+ * are made of, S = sum exp(z), p_R, q and 1 / T, is float32: the loss is off by a few 2^-24 of |z| and ln S.
+ * A loss beyond float32's range is +inf.
  *
  * logits [rows][ld] of dtype BF16, FP16 or FP32 and any alignment; temperature [rows] or NULL (1);
  * top_token, top_logprob [rows][ldtop]; grad [rows] or NULL (1); loss [rows] or NULL; dlogits
